@@ -206,7 +206,7 @@ def _attn_own(s):
     c = s["case"]
     a = M.Attn(scale=c["D"] ** -0.5, cap=c["cap"], causal=c["causal"], window=c["window"], cu_docs=s["cu"],
                prefix=s["prefix"], slopes=s["slopes"])
-    fw = M.attn_fwd(s["q"], s["k"], s["v"], a, ws=s.get("ws"))
+    fw = M.attn_fwd(s["q"], s["k"], s["v"], a, train=c["train"], ws=s.get("ws"))
     s["ws"] = fw["ws"]
     out = {"O": fw["O"], "lse": fw["lse"]}
     if c["train"]:
