@@ -3,7 +3,7 @@
     python -m bwd_lora_mlp_gb300.build          # build unless the library matches the sources
 
 The library is reused only when the digest stored beside it (liblora_mlp.so.digest) equals the
-digest of the current sources (every file of csrc/, the public header, this script) and of the
+digest of the current sources (every file of csrc/, the public headers, this script) and of the
 compiler flags; file times play no part, so a library copied in from elsewhere, or left over from
 other sources, is rebuilt.
 
@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "liblora_mlp.so")
 DIGEST = LIB + ".digest"
 
 SOURCES = ["lm_api.cu", "lm_aux.cu", "lm_gemm_fwd.cu", "lm_gemm_bwd.cu", "lm_gemm2.cu", "lm_gemm2_nf4.cu", "lm_static_ws.cu",
-           "lm_dual.cu"]
+           "lm_dual.cu", "lm_layer_api.cu", "lm_attn.cu", "lm_addnorm.cu", "lm_logprob.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
@@ -43,8 +43,8 @@ def _nvcc() -> str:
 
 
 def _deps() -> list:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "lora_mlp.h"),
-                                                                  os.path.abspath(__file__)]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+    files.append(os.path.abspath(__file__))
     return sorted(f for f in files if os.path.isfile(f))
 
 

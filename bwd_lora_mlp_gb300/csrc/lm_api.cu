@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -10,10 +11,12 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
 #include "lm_internal.h"
+#include "lm_layer.h"
 #include "lora_mlp.h"
 
 using namespace lm;
@@ -57,7 +60,7 @@ struct ProfRec {
     cudaEvent_t a, b;
 };
 std::mutex g_prof_mu;
-bool g_prof_on = false;
+std::atomic<bool> g_prof_on{false};
 std::vector<ProfRec> g_prof;
 std::vector<cudaEvent_t> g_prof_pool;
 
@@ -1102,6 +1105,26 @@ lm_status report_error(lm_status s, const char* fmt, ...) {
     va_end(ap);
     return s;
 }
+
+// What the layer operators' translation units share with this one (lm_layer.h).
+lm_status device_ready(int* sms) { return ready(sms); }
+
+lm_status encode_heads(CUtensorMap* m, const lm_heads& t, int64_t T, int heads, int d, int rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)t.head_stride * 2, (cuuint64_t)t.token_stride * 2};
+    cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows};
+    cuuint32_t es[3] = {1u, 1u, 1u};
+    const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(t.p), dims, strides, box, es,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(LM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %lld tokens x %d heads x %d", (int)r, (long long)T,
+                    heads, d);
+    return LM_OK;
+}
+
+LaunchTag::LaunchTag(const char* tag, cudaStream_t st) : scope_(g_prof_on ? new (std::nothrow) ProfScope(tag, st) : nullptr) {}
+LaunchTag::~LaunchTag() { delete static_cast<ProfScope*>(scope_); }
 }  // namespace lm
 
 // ====================================================================== utilities

@@ -1,0 +1,313 @@
+"""ctypes binding of the layer operators of liblora_mlp.so (include/lora_layer.h): attention over
+packed documents, the residual add with the norms before and after a block, and log probabilities
+of given tokens, forward and backward.
+
+Argument marshalling only, as in lib.py: types and layouts are checked here, sizes and pointers by
+the C entry point of the same name, and every non-zero status raises ``LmError``.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import lib as L
+from .lib import LmError, workspace  # noqa: F401  (re-exported)
+
+HEADER = os.path.join(os.path.dirname(L.PKG), "include", "lora_layer.h")
+LM_BF16, LM_F32 = 0, 1
+LM_I32, LM_I64 = 0, 1
+_DTYPES = {torch.bfloat16: LM_BF16, torch.float32: LM_F32}
+_INDEX = {torch.int32: LM_I32, torch.int64: LM_I64}
+
+_P, _I64, _I32, _SZ, _SZP, _F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t,
+                                 ctypes.POINTER(ctypes.c_size_t), ctypes.c_float)
+
+
+class lm_heads(ctypes.Structure):
+    _fields_ = [("p", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class lm_attn(ctypes.Structure):
+    _fields_ = [("scale", _F), ("cap", _F), ("slopes", _P), ("causal", _I32), ("window", _I32), ("cu_docs", _P),
+                ("prefix", _P), ("n_docs", _I32), ("reserved", _I32)]
+
+
+class lm_addnorm(ctypes.Structure):
+    _fields_ = [("w_in", _P), ("w_post", _P), ("gate", _P), ("alpha", _F), ("eps", _F), ("w_offset", _F),
+                ("h_dtype", _I32), ("w_dtype", _I32), ("reserved", _I32)]
+
+
+_HP = ctypes.POINTER(lm_heads)
+_AP = ctypes.POINTER(lm_attn)
+_NP = ctypes.POINTER(lm_addnorm)
+
+_SIGS = {
+    "attn_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
+    "attn_fwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
+    "attn_bwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _P, _P, _P, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
+    "addnorm_workspace_size": ([_I64, _I64, _SZP], _I32),
+    "addnorm_fwd": ([_I64, _I64, _P, _P, _NP, _P, _P, _P, _P, _P], _I32),
+    "addnorm_bwd": ([_I64, _I64, _P, _P, _P, _P, _P, _P, _NP, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "logprob_fwd": ([_I64, _I64, _I64, _P, _I32, _P, _I32, _F, _I32, _P, _P, _P, _P, _P, _P], _I32),
+    "logprob_bwd": ([_I64, _I64, _I64, _P, _I32, _P, _I32, _F, _P, _P, _P, _P, _P, _I64, _P], _I32),
+}
+
+_fns = {}
+
+
+def header_symbols() -> list:
+    """Names of the entry points declared in include/lora_layer.h."""
+    with open(HEADER) as f:
+        return re.findall(r"LM_API\s+[\w\s\*]+?\b(\w+)\s*\(", f.read())
+
+
+def _fn(name: str):
+    if not _fns:
+        so = L.load()
+        for n, (args, res) in _SIGS.items():
+            fn = getattr(so, n)
+            fn.argtypes, fn.restype = args, res
+            _fns[n] = fn
+    return _fns[name]
+
+
+def call_status(name: str, *args) -> int:
+    """Call an entry point and return its raw status (for tests of the error paths)."""
+    return _fn(name)(*args)
+
+
+def _call(name: str, *args) -> None:
+    st = _fn(name)(*args)
+    if st != L.LM_OK:
+        raise LmError(st, name, L.last_error())
+
+
+def _size(name: str, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _call(name, *args, ctypes.byref(out))
+    return out.value
+
+
+def _shaped(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
+    """Device address of a contiguous tensor of this shape and type (None: a null pointer)."""
+    if t is None:
+        return 0
+    p = L._ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return p
+
+
+# ---------------------------------------------------------------------------------------------
+# attention
+
+
+@dataclass
+class Attn:
+    """What one attention call computes (lm_attn): scores scale * q.k, capped by cap * tanh(. / cap)
+    when cap > 0, less slopes[head] * |i - j| when slopes is given; token i sees the tokens j <= i of
+    its document (all of it when not causal, and always the document's first prefix tokens) nearer
+    than window (0: no limit).  cu_docs: int32 document offsets (n + 1; None: one document), prefix:
+    int32 (n), slopes: float32 (query heads)."""
+    scale: float
+    cap: float = 0.0
+    causal: bool = True
+    window: int = 0
+    cu_docs: Optional[torch.Tensor] = None
+    prefix: Optional[torch.Tensor] = None
+    slopes: Optional[torch.Tensor] = None
+
+    def c_struct(self, hq: int) -> lm_attn:
+        n = 0 if self.cu_docs is None else self.cu_docs.numel() - 1
+        return lm_attn(self.scale, self.cap, _shaped(self.slopes, (hq,), torch.float32, "slopes"), bool(self.causal),
+                       self.window, _shaped(self.cu_docs, (n + 1,), torch.int32, "cu_docs"),
+                       _shaped(self.prefix, (n,), torch.int32, "prefix"), n, 0)
+
+
+def _heads(t: torch.Tensor, T: int, h: int, d: int, name: str) -> lm_heads:
+    """A (T, heads, d) bf16 tensor whose tokens and heads may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if t.shape != (T, h, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (T, h, d), tuple(t.shape)))
+    ts, hs, one = t.stride()
+    if one != 1 and d > 1:
+        raise ValueError("%s must be contiguous in its last dimension" % name)
+    if h == 1:  # the stride of a dimension of size one is not used, and torch may report any value
+        hs = d
+    if T <= 1:
+        ts = h * max(hs, d)
+    return lm_heads(t.data_ptr() if T else L._empty_ptr(t.device), ts, hs)
+
+
+def attn_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
+    return _size("attn_workspace_size", T, hq, hk, d)
+
+
+def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None, stream=None) -> dict:
+    """q (T, hq, d), k and v (T, hk, d) -> O (T, hq, d), lse (hq, T) and, with ``train``, O_lo (T, hq, d int8:
+    more bits of O, for the backward)."""
+    (T, hq, d), hk = q.shape, k.shape[1]
+    dev = q.device
+    O = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev) if O is None else O
+    lse = torch.empty((hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    if train and O_lo is None:
+        O_lo = torch.empty((T, hq, d), dtype=torch.int8, device=dev)
+    ws = workspace(attn_workspace_size(T, hq, hk, d), dev) if ws is None else ws
+    _call("attn_fwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
+          a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, d), torch.int8, "O_lo"),
+          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), L._stream(stream))
+    return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
+
+
+def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None, stream=None) -> dict:
+    """The gradients of q, k and v from dO (T, hq, d) and the forward's result."""
+    (T, hq, d), hk = q.shape, k.shape[1]
+    dev, bf = q.device, torch.bfloat16
+    dQ = torch.empty((T, hq, d), dtype=bf, device=dev) if dQ is None else dQ
+    dK = torch.empty((T, hk, d), dtype=bf, device=dev) if dK is None else dK
+    dV = torch.empty((T, hk, d), dtype=bf, device=dev) if dV is None else dV
+    ws = fwd["ws"] if ws is None else ws
+    _call("attn_bwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
+          _heads(dO, T, hq, d, "dO"), _shaped(fwd["O"], (T, hq, d), bf, "O"),
+          _shaped(fwd["O_lo"], (T, hq, d), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"), a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"),
+          _shaped(dK, (T, hk, d), bf, "dK"), _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"),
+          ws.numel(), L._stream(stream))
+    return {"dQ": dQ, "dK": dK, "dV": dV}
+
+
+# ---------------------------------------------------------------------------------------------
+# residual add and norms
+
+
+@dataclass
+class AddNorm:
+    """h_out = h + alpha * gate * N(y; w_post), x = N(h_out; w_in), N the root-mean-square norm with
+    weight w + w_offset.  Each vector (d values, all bf16 or all float32) may be None: no norm after
+    the block, no gate, no norm before the next block."""
+    w_in: Optional[torch.Tensor] = None
+    w_post: Optional[torch.Tensor] = None
+    gate: Optional[torch.Tensor] = None
+    alpha: float = 1.0
+    eps: float = 1e-5
+    w_offset: float = 0.0
+
+    def c_struct(self, d: int, h_dtype) -> lm_addnorm:
+        dt = next((w.dtype for w in (self.w_in, self.w_post, self.gate) if w is not None), torch.bfloat16)
+        if h_dtype not in _DTYPES or dt not in _DTYPES:
+            raise TypeError("h and the norm's vectors must be bfloat16 or float32, got %s and %s" % (h_dtype, dt))
+        return lm_addnorm(_shaped(self.w_in, (d,), dt, "w_in"), _shaped(self.w_post, (d,), dt, "w_post"),
+                          _shaped(self.gate, (d,), dt, "gate"), self.alpha, self.eps, self.w_offset, _DTYPES[h_dtype],
+                          _DTYPES[dt], 0)
+
+
+def addnorm_workspace_size(T: int, d: int) -> int:
+    return _size("addnorm_workspace_size", T, d)
+
+
+def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
+    """h (T, d) bf16 or float32, y (T, d) bf16 or None -> h (the sum; h itself without y), x (None
+    without w_in), rstd_y, rstd_h."""
+    T, d = h.shape
+    dev, f32, bf = h.device, torch.float32, torch.bfloat16
+    if y is not None and h_out is None:
+        h_out = torch.empty_like(h, memory_format=torch.contiguous_format)
+    if n.w_in is not None and x is None:
+        x = torch.empty((T, d), dtype=bf, device=dev)
+    rstd_y = torch.empty(T, dtype=f32, device=dev) if n.w_post is not None else None
+    rstd_h = torch.empty(T, dtype=f32, device=dev) if n.w_in is not None else None
+    _call("addnorm_fwd", T, d, L._ptr(h, h.dtype, "h"), _shaped(y, (T, d), bf, "y"), n.c_struct(d, h.dtype),
+          _shaped(h_out, (T, d), h.dtype, "h_out"), _shaped(x, (T, d), bf, "x"), _shaped(rstd_y, (T,), f32, "rstd_y"),
+          _shaped(rstd_h, (T,), f32, "rstd_h"), L._stream(stream))
+    return {"h": h if y is None else h_out, "x": x, "rstd_y": rstd_y, "rstd_h": rstd_h}
+
+
+def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None,
+                stream=None) -> dict:
+    """Gradients from those of the sum (dh_out, None: zero) and of x (dx), with the forward's inputs h and
+    y: dh, dy, and with ``weights`` the float32 gradients of the vectors that are there."""
+    T, d = h.shape
+    dev, f32, bf = h.device, torch.float32, torch.bfloat16
+    dh = torch.empty((T, d), dtype=h.dtype, device=dev) if dh is None else dh
+    dy = torch.empty((T, d), dtype=bf, device=dev) if dy is None and y is not None else dy
+
+    def grad(w):
+        return torch.empty(d, dtype=f32, device=dev) if weights and w is not None else None
+
+    dw_in, dw_post, dgate = grad(n.w_in), grad(n.w_post), grad(n.gate)
+    ws = workspace(addnorm_workspace_size(T, d), dev) if ws is None else ws
+    _call("addnorm_bwd", T, d, L._ptr(h, h.dtype, "h"), _shaped(y, (T, d), bf, "y"),
+          _shaped(dh_out, (T, d), h.dtype, "dh_out"), _shaped(dx, (T, d), bf, "dx"),
+          _shaped(fwd["rstd_y"], (T,), f32, "rstd_y"), _shaped(fwd["rstd_h"], (T,), f32, "rstd_h"),
+          n.c_struct(d, h.dtype), _shaped(dh, (T, d), h.dtype, "dh"), _shaped(dy, (T, d), bf, "dy"),
+          _shaped(dw_in, (d,), f32, "dw_in"), _shaped(dw_post, (d,), f32, "dw_post"), _shaped(dgate, (d,), f32, "dgate"),
+          L._ptr(ws, torch.uint8, "ws"), ws.numel(), L._stream(stream))
+    return {"dh": dh, "dy": dy, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
+
+
+# ---------------------------------------------------------------------------------------------
+# log probabilities
+
+
+def _rows2d(t: torch.Tensor, name: str):
+    """(address, row stride, type) of a (T, V) tensor with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TypeError("%s must be a 2D torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in _DTYPES:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    T, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return t.data_ptr() if t.numel() else L._empty_ptr(t.device), t.stride(0) if T > 1 else V, _DTYPES[t.dtype]
+
+
+def _targets(t: torch.Tensor, T: int):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _INDEX:
+        raise TypeError("targets must be an int32 or int64 tensor")
+    return _shaped(t, (T,), t.dtype, "targets"), _INDEX[t.dtype]
+
+
+def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0, stream=None) -> dict:
+    """logits (T, V) bf16 or float32 (rows may be strided), targets (T) -> logp, entropy, lse (T) float32 and,
+    for k > 0, top_ids (T, k) int32 and top_logp (T, k) float32."""
+    T, V = logits.shape
+    p, ld, dt = _rows2d(logits, "logits")
+    tp, ti = _targets(targets, T)
+    dev, f32 = logits.device, torch.float32
+    rows = torch.empty((3, T), dtype=f32, device=dev)
+    logp, entropy, lse = rows.unbind(0)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if k > 0 else None
+    top = torch.empty((T, k), dtype=f32, device=dev) if k > 0 else None
+    _call("logprob_fwd", T, V, ld, p, dt, tp, ti, scale, k, L._ptr(logp), L._ptr(entropy), L._ptr(lse), L._ptr(ids),
+          L._ptr(top), L._stream(stream))
+    return {"logp": logp, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logp": top}
+
+
+def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: float = 1.0, dlogits=None,
+                stream=None) -> dict:
+    """dlogits (T, V), in the logits' type, from the gradients of logp and entropy (T float32; None: zero).
+    ``dlogits`` may be ``logits`` itself."""
+    T, V = logits.shape
+    p, ld, dt = _rows2d(logits, "logits")
+    tp, ti = _targets(targets, T)
+    f32 = torch.float32
+    if dlogits is None:
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+    if dlogits.shape != (T, V) or dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits must have the logits' shape and type")
+    po, ldo, _ = _rows2d(dlogits, "dlogits")
+    _call("logprob_bwd", T, V, ld, p, dt, tp, ti, scale, _shaped(fwd["lse"], (T,), f32, "lse"),
+          _shaped(fwd["entropy"], (T,), f32, "entropy"), _shaped(dlogp, (T,), f32, "dlogp"),
+          _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, L._stream(stream))
+    return {"dlogits": dlogits}
