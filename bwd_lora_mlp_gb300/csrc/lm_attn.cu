@@ -1,10 +1,8 @@
-// Attention over packed documents (include/lora_layer.h), forward and backward: one warp per row,
-// the head's dimensions spread over its lanes.
-//   forward   m, l, o updated key by key:  m' = max(m, s), o = o e^{m-m'} + e^{s-m'} v
-//   backward  P = e^{s - lse}, dz = P (dO.v - delta) (1 - (u/cap)^2), delta = dO.O
+// Attention over packed documents (include/lora_layer.h): who sees whom, and the backward with one
+// warp per row, the head's dimensions spread over its lanes.
+//   P = e^{s - lse}, dz = P (dO.v - delta) (1 - (u/cap)^2), delta = dO.O
 // Bound by the five shuffles that join each dot product.
-#include "lm_layer.h"
-#include "lm_ptx.cuh"
+#include "lm_attn.cuh"
 
 namespace lm {
 
@@ -17,41 +15,28 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // ------------------------------------------------------------------ who sees whom
-__device__ __forceinline__ int clampi(int64_t v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : (int)v; }
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-__global__ void attn_ranges_kernel(lm_attn a, int T, TokRange* out) {
+__global__ void __launch_bounds__(256) attn_ranges_kernel(const __grid_constant__ lm_attn a, int T, TokRange* out) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int t = blockIdx.x * blockDim.x + threadIdx.x;
     if (t >= T) return;
-    int s = 0, e = T, pre = 0;
-    bool in = true;
-    if (a.cu_docs) {
-        // the last document that begins at or before t and is not empty there: the largest m with cu[m] <= t
-        int lo = 0, hi = a.n_docs;  // cu[lo] <= t < cu[hi] where t is inside
-        while (lo + 1 < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu_docs[mid] <= t) lo = mid; else hi = mid;
-        }
-        s = clampi(a.cu_docs[lo], 0, T);
-        e = clampi(a.cu_docs[lo + 1], 0, T);
-        in = s <= t && t < e;
-        if (in && a.prefix) pre = clampi(a.prefix[lo], 0, e - s);
+    // the document: the largest m with cu[m] <= t (empty documents before it are skipped)
+    int m = 0, over = a.n_docs;
+    while (m + 1 < over) {
+        const int mid = (m + over) >> 1;
+        if (a.cu_docs[mid] <= t) m = mid;
+        else over = mid;
     }
-    TokRange r;
-    if (!in) {  // padding: empty intervals at t, which keeps lo and hi non-decreasing over the tokens
-        r.lo = r.hi = r.qlo = r.qhi = t;
-    } else {
-        const int W = a.window > 0 && a.window < T ? a.window : T;
-        r.lo = max(s, t - W + 1);
-        r.hi = a.causal ? min(max(t + 1, s + pre), t + W) : min(e, t + W);
-        r.qlo = a.causal && t >= s + pre ? t : max(s, t - W + 1);
-        r.qhi = min(e, t + W);
-    }
+    const int s = clampi(a.cu_docs[m], 0, T), e = clampi(a.cu_docs[m + 1], 0, T);
+    TokRange r{t, t, t, t};  // padding: empty intervals at t, which keeps all four non-decreasing over the tokens
+    if (s <= t && t < e) r = range_in(t, s, e, a.prefix ? clampi(a.prefix[m], 0, e - s) : 0, T, a.causal, a.window);
     out[t] = r;
 }
 
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st) {
-    attn_ranges_kernel<<<(unsigned)((T + 255) / 256), 256, 0, st>>>(a, (int)T, out);
-    return cudaGetLastError();
+    return launch_pdl(attn_ranges_kernel, dim3((unsigned)((T + 255) / 256)), dim3(256), 0, st, nullptr, 0, a, (int)T, out);
 }
 
 // ------------------------------------------------------------------ one score
@@ -95,45 +80,6 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Lanes& r, float f, 
     }
 }
 
-// The eight bits of a value's fp32 pattern that its bf16 rounding leaves out.
-__device__ __forceinline__ int bits_left(float x) {
-    const uint32_t hi = (pack_bf16x2(x, 0.f) & 0xFFFFu) << 16;
-    return min((int32_t)(__float_as_uint(x) - hi) >> 8, 127);
-}
-
-// ------------------------------------------------------------------ forward
-__global__ void __launch_bounds__(256) attn_fwd_kernel(const __grid_constant__ AttnParams p) {
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, g = h / (p.hq / p.hk);
-    if (i >= p.T) return;
-    const TokRange r = p.rng[i];
-    const Lanes q = load_row(row_of(p.q, i, h), p.d, lane);
-    const float slope = p.slopes ? p.slopes[h] : 0.f;
-    float m = -INFINITY, l = 0.f, bend;
-    Lanes o{};
-    for (int j = r.lo; j < r.hi; ++j) {
-        const float s = score(p, dot(q, load_row(row_of(p.k, j, g), p.d, lane)), slope, i - j, bend);
-        const Lanes v = load_row(row_of(p.v, j, g), p.d, lane);
-        const float mn = fmaxf(m, s), f = expf(m - mn), e = expf(s - mn);
-        l = l * f + e;
-#pragma unroll
-        for (int c = 0; c < kPerLane; ++c) o.x[c] = o.x[c] * f + e * v.x[c];
-        m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t at = ((int64_t)i * p.hq + h) * p.d;
-    store_row(p.out + at, o, inv, p.d, lane);
-    if (p.out_lo)
-        for (int c = 0; c < kPerLane; ++c)
-            if (lane + 32 * c < p.d) p.out_lo[at + lane + 32 * c] = (int8_t)bits_left(o.x[c] * inv);
-    if (lane == 0) p.lse[(int64_t)h * p.T + i] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
-cudaError_t launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
-    attn_fwd_kernel<<<dim3((p.T + 7) / 8, p.hq), 256, 0, st>>>(p);
-    return cudaGetLastError();
-}
-
 // ------------------------------------------------------------------ backward
 // delta_i = dO_i . O_i; 0 where nothing is seen, whatever dO holds there
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* delta) {
@@ -158,7 +104,7 @@ __global__ void __launch_bounds__(256) attn_dq_kernel(const __grid_constant__ At
     const int lane = threadIdx.x & 31;
     const int i = blockIdx.x * 8 + (threadIdx.x >> 5), h = blockIdx.y, g = h / (p.hq / p.hk);
     if (i >= p.T) return;
-    const TokRange r = p.rng[i];
+    const TokRange r = tok_range(p, i);
     const Lanes q = load_row(row_of(p.q, i, h), p.d, lane), dO = load_row(row_of(p.dO, i, h), p.d, lane);
     const float slope = p.slopes ? p.slopes[h] : 0.f;
     const float lse = p.lse_in[(int64_t)h * p.T + i], delta = p.delta[(int64_t)h * p.T + i];
@@ -183,7 +129,7 @@ __global__ void __launch_bounds__(256) attn_dkv_kernel(const __grid_constant__ A
     const int lane = threadIdx.x & 31;
     const int j = blockIdx.x * 8 + (threadIdx.x >> 5), g = blockIdx.y, n = p.hq / p.hk;
     if (j >= p.T) return;
-    const TokRange r = p.rng[j];
+    const TokRange r = tok_range(p, j);
     const Lanes k = load_row(row_of(p.k, j, g), p.d, lane), v = load_row(row_of(p.v, j, g), p.d, lane);
     Lanes dk{}, dv{};
     for (int h = g * n; h < (g + 1) * n; ++h) {

@@ -1,0 +1,140 @@
+// What the attention kernels share: parameters, who sees whom, tensor-memory and TMA forms that the
+// projection kernels do not use, and the score arithmetic.
+#pragma once
+
+#include "lm_gemm.cuh"
+#include "lm_layer.h"
+#include "lm_ptx.cuh"
+
+namespace lm {
+
+constexpr int kTile = 128;             // queries and keys of a score tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// How scores are formed from q.k (ATTN_PLAIN folds the scale into the exponent's multiply-add).
+enum AttnMode : int { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2 };
+
+// ---------------------------------------------------------------- who sees whom
+__host__ __device__ inline TokRange range_in(int t, int s, int e, int pre, int T, int causal, int window) {
+    const int W = window > 0 && window < T ? window : T;  // (T <= 2^20: no sum overflows)
+    TokRange r;
+    r.lo = s > t - W + 1 ? s : t - W + 1;
+    r.hi = e;
+    if (causal) r.hi = t + 1 > s + pre ? t + 1 : s + pre;
+    if (r.hi > t + W) r.hi = t + W;
+    r.qlo = causal && t >= s + pre ? t : r.lo;
+    r.qhi = e < t + W ? e : t + W;
+    return r;
+}
+// of token t < T: from the table, or (one document) from the masks themselves
+__device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
+    if (p.rng) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(p.rng) + t);
+        return TokRange{v.x, v.y, v.z, v.w};
+    }
+    return range_in(t, 0, p.T, 0, p.T, p.causal, p.window);
+}
+
+// ---------------------------------------------------------------- errors
+__device__ __forceinline__ void attn_error(const AttnParams& p, int family, int where) {
+    if (p.err) {
+        atomicExch(p.err, kErrTimeout);
+        p.err[1] = where;
+        p.err[2] = blockIdx.x;
+        p.err[3] = family;
+    }
+}
+
+// ---------------------------------------------------------------- TMA, TMEM
+// The box of 64 dims x 1 head x rows tokens at (dim x, head y, token z).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                            int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: A is 128 rows (lanes) x 16 K values packed two to a column.
+__device__ __forceinline__ void umma_bf16_ts_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate, bool issue) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Waits for this thread's loads; carries the registers so that no use of them moves before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ---------------------------------------------------------------- products of one tile
+// Shared-memory tile of 128 rows x dp dims: dp / 64 boxes of 128 rows x 128 bytes, 128-byte swizzle.
+constexpr uint32_t kBoxBytes = kTile * 128;
+
+// D = A B^T over the tiles' dims: both K-major, `steps` K steps of 16
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool leader) {
+    for (int kk = 0; kk < steps; ++kk) {
+        const uint32_t box = (uint32_t)(kk >> 2) * kBoxBytes;
+        const uint64_t off = (uint64_t)((kk & 3) * 2);
+        umma_bf16_if(d, make_sdesc_sw128(a + box, 16, 1024) + off, make_sdesc_sw128(b + box, 16, 1024) + off, idesc,
+                     kk ? 1u : 0u, leader);
+    }
+}
+
+// ---------------------------------------------------------------- arithmetic
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// tanh x = 1 - 2 / (1 + e^{2x}), given 2 log2(e) x: absolute error a few 2^-24, exact at both ends
+__device__ __forceinline__ float tanh_from_2log2e(float x) { return 1.f - __fdividef(2.f, 1.f + ex2(x)); }
+
+// The eight bits of a value's fp32 pattern that its bf16 rounding leaves out (held to [-128, 127]).
+__device__ __forceinline__ int bits_left(float x, uint32_t bf16_bits) {
+    return min((int32_t)(__float_as_uint(x) - (bf16_bits << 16)) >> 8, 127);
+}
+
+}  // namespace lm

@@ -1,0 +1,398 @@
+// Attention forward (include/lora_layer.h) on the tensor cores.
+//
+// One CTA takes 256 queries of one head as two tiles of 128 and walks the 128-key tiles that any of
+// them sees.  For each query tile w and key tile j:
+//   S_w = Q_w K_j^T                              (tcgen05, both operands in shared memory)
+//   P_w = 2^{S c - m}, l += row sums             (four warps, one thread per query row)
+//   O_w += P_w V_j                               (tcgen05, P_w from tensor memory, where it replaces S_w)
+// The two query tiles take turns: while the tensor cores work on one, the other's four warps form
+// its exponentials, so neither waits for the other as long as 2 x 128 x d x 128 multiply-adds take
+// longer than 128 x 128 exponentials with their loads, maxima, sums and packing.  The running
+// maximum m follows the row only when it has grown by more than 8 (a factor 256 in the weights): the
+// weights then stay below 2^8, exact in their scale, and O_w is rescaled a few times per row
+// instead of once per key tile.  Sums are fp32; P is rounded to bf16 for the second product (as
+// flash-style kernels must), and on tiles with hidden keys the normaliser of O sums the rounded
+// weights, so that short rows keep sum P = 1; lse always comes from the unrounded sums.
+// Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
+// memory: S_0, S_1, O_0, O_1 of 128 columns each.
+#include "lm_attn.cuh"
+
+namespace lm {
+
+constexpr int kFwdThreads = 320;  // two softmax warpgroups, the MMA warp, the loader warp
+constexpr float kRescale = 8.f;
+
+template <int DP>
+struct FwdCfg {
+    static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
+    static constexpr int kSlots = DP == 128 ? 5 : 8;
+    static constexpr int kSmem = 2048 + (2 + kSlots) * kTileBytes;
+};
+
+struct FwdMaps {
+    CUtensorMap q, k, v;
+};
+
+// the key tiles [j0, j1) that the query rows [q0, q0 + 128) may see
+struct TileSpan {
+    int j0, j1;
+    int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
+};
+__device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
+    if (q0 >= p.T) return TileSpan{0, 0, 0, 0};
+    const TokRange a = tok_range(p, q0), b = tok_range(p, min(q0 + kTile, p.T) - 1);
+    if (b.hi <= a.lo) return TileSpan{0, 0, 0, 0};
+    return TileSpan{a.lo / kTile, (b.hi + kTile - 1) / kTile, b.lo, a.hi};
+}
+
+template <int DP, int MODE>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwdMaps maps) {
+    using C = FwdCfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* empty = full + C::kSlots;
+    uint64_t* qfull = empty + C::kSlots;
+    uint64_t* sfull = qfull + 1;   // [2] scores ready
+    uint64_t* pfull = sfull + 2;   // [2] weights written (and the scores read)
+    uint64_t* odone = pfull + 2;   // [2] one more P V product done
+    uint64_t* drain = odone + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint8_t* sq = smem + 1024;
+    uint8_t* ring = sq + 2 * C::kTileBytes;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the longest rows first: under a causal mask the last queries see the most keys
+    const int nqb = (p.T + 2 * kTile - 1) / (2 * kTile);
+    const int h = (int)blockIdx.x % p.hq, q0 = (nqb - 1 - (int)blockIdx.x / p.hq) * 2 * kTile;
+    const int g = h / (p.hq / p.hk);
+
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(qfull), 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&sfull[w]), 1);
+            mbar_init(smem_u32(&pfull[w]), 4);
+            mbar_init(smem_u32(&odone[w]), 1);
+        }
+        mbar_init(smem_u32(drain), 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+    }
+    __syncwarp();
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    const uint32_t tmem = *tmem_slot;
+    const TileSpan span[2] = {key_tiles(p, q0), key_tiles(p, q0 + kTile)};
+    int J0 = span[0].j0, J1 = span[0].j1;
+    if (span[1].j1 > span[1].j0) {
+        J0 = J1 > J0 ? min(J0, span[1].j0) : span[1].j0;
+        J1 = max(J1, span[1].j1);
+    }
+
+    if (warp == 9) {  // ---------------- loader
+        if (lane == 0 && J1 > J0) {
+            bool ok = true;
+            mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
+            for (int w = 0; w < 2; ++w)
+                for (int b = 0; b < DP / 64; ++b)
+                    tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h,
+                                q0 + w * kTile);
+            uint32_t n = 0;
+            for (int j = J0; ok && j < J1; ++j)
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
+                    if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+                    for (int b = 0; b < DP / 64; ++b)
+                        tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
+                                    smem_u32(&full[s]), b * 64, g, j * kTile);
+                }
+            if (!ok) {
+                attn_error(p, 5, 1);
+                *s_abort = 1;
+            }
+            // nothing may land in shared memory after the CTA has gone
+            volatile int never = 0;
+            const bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
+            if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
+        }
+    } else if (warp == 8) {  // ---------------- tensor cores: the whole warp, lane 0 issues
+        const bool leader = lane == 0;
+        const int ksteps = (p.d + 15) / 16;
+        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+        const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
+        // keys of no document hold anything: their rows of V are cleared, 0 x NaN would reach every O
+        int in0 = 0, in1 = p.T;
+        if (p.cu_docs) {
+            in0 = max(0, p.cu_docs[0]);
+            in1 = min(p.T, p.cu_docs[p.n_docs]);
+        }
+        bool ok = J1 <= J0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+        for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
+            const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
+            const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
+            const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
+            if (j > J0) {
+                ok = mbar_wait_warp(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+                const int k0 = (j - 1) * kTile;
+                if (k0 < in0 || k0 + kTile > in1) {
+                    for (int r = lane; r < kTile; r += 32)
+                        if (k0 + r < in0 || k0 + r >= in1)
+                            for (int b = 0; b < DP / 64; ++b)
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4*>(ring + (nv % C::kSlots) * C::kTileBytes + b * kBoxBytes +
+                                                              r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            if (j < J1) {
+                ok = mbar_wait_warp(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
+                if (j > span[w].j0 && j <= span[w].j1) {  // O_w += P_w V_{j-1}
+                    const uint32_t n = (uint32_t)(j - 1 - span[w].j0);
+                    if (!mbar_wait_warp(smem_u32(&pfull[w]), n & 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        umma_bf16_ts_if(to, ts + kk * 8, make_sdesc_sw128(sv, kBoxBytes, 1024) + (uint64_t)(kk * 128), ido,
+                                        (n || kk) ? 1u : 0u, leader);
+                    umma_commit_if(smem_u32(&odone[w]), leader);
+                }
+                if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
+                    mma_rows(ts, smem_u32(sq + w * C::kTileBytes), sk, ksteps, ids, leader);
+                    umma_commit_if(smem_u32(&sfull[w]), leader);
+                }
+            }
+            if (!ok) break;
+            if (j > J0) umma_commit_if(smem_u32(&empty[nv % C::kSlots]), leader);
+            if (j < J1) umma_commit_if(smem_u32(&empty[nk % C::kSlots]), leader);
+        }
+        if (!ok && leader) {
+            attn_error(p, 5, 2);
+            *s_abort = 1;
+        }
+        umma_commit_if(smem_u32(drain), leader);
+        volatile int never = 0;
+        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+        __syncwarp();
+    } else {  // ---------------- softmax: warpgroup w, one thread per query row
+        const int w = warp >> 2;
+        const int i = q0 + w * kTile + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + 2 * kTile + w * DP;
+        TokRange r{0, 0, 0, 0};
+        if (i < p.T) r = tok_range(p, i);
+        const int j0 = span[w].j0, j1 = span[w].j1;
+        const float slope = MODE != ATTN_PLAIN && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+        // scores in units of log 2: x = s c + bias (plain), or cap tanh(s scale / cap) log2 e + bias
+        const float c = MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+        const float cap = p.cap * kLog2e;
+        const float cx = MODE == ATTN_PLAIN ? c : 1.f;
+        float m = -INFINITY, l = 0.f, ln = 0.f;  // running maximum, sum of weights, O's normaliser
+        bool ok = true;
+        for (int j = j0; j < j1; ++j) {
+            if (!mbar_wait_warp(smem_u32(&sfull[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld_x32(ts + b * 32, x[b]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tmem_ld_wait(x[b]);
+            const int k0 = j * kTile;
+            if (MODE != ATTN_PLAIN) {
+                const float dist = (float)(i - k0);
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = __uint_as_float(x[b][e]) * c;
+                        if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
+                        x[b][e] = __float_as_uint(fmaf(-slope, fabsf(dist - (float)(b * 32 + e)), v));
+                    }
+            }
+            const bool hidden = k0 < span[w].lo_max || k0 + kTile > span[w].hi_min;
+            if (hidden) {
+                const int a = r.lo - k0, z = r.hi - k0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (b * 32 + e < a || b * 32 + e >= z) x[b][e] = __float_as_uint(-INFINITY);
+            }
+            float mx[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                mx[b] = __uint_as_float(x[b][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(x[b][e]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cx;
+            const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
+                if (j > j0) {
+                    if (!mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j - 1 - j0) & 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int cc = 0; cc < DP; cc += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32(to + cc, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_x32(to + cc, o);
+                    }
+                    tmem_st_wait();
+                }
+                l *= f;
+                ln *= f;
+                if (grow) m = top;
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+            float s4[4] = {0.f, 0.f, 0.f, 0.f}, r4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t pk[2][32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2(fmaf(__uint_as_float(x[b][e]), cx, -mu));
+                    const float p1 = ex2(fmaf(__uint_as_float(x[b][e + 1]), cx, -mu));
+                    s4[b] += p0 + p1;
+                    pk[b >> 1][(b & 1) * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
+                }
+            const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            float rsum = sum;
+            if (hidden) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r4[(e >> 4) + 2 * b] += bf16lo(pk[b][e]) + bf16hi(pk[b][e]);
+                rsum = (r4[0] + r4[1]) + (r4[2] + r4[3]);
+            }
+            l += sum;
+            ln += rsum;
+            tmem_st_x32(ts, pk[0]);
+            tmem_st_x32(ts + 32, pk[1]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&pfull[w]));
+        }
+        if (ok && j1 > j0) ok = mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j1 - 1 - j0) & 1u, s_abort, p.wait_ns);
+        tc_fence_after();
+        if (!ok) {
+            if (lane == 0) {
+                attn_error(p, 5, 3);
+                *s_abort = 1;
+            }
+        } else {
+            const float inv = ln > 0.f ? 1.f / ln : 0.f;
+            const int64_t at = ((int64_t)i * p.hq + h) * p.d;
+#pragma unroll 1
+            for (int cc = 0; cc < p.d; cc += 16) {
+                uint32_t o[16];
+                if (j1 > j0) {  // (uniform over the warpgroup)
+                    tmem_ld_x16(to + cc, o);
+                    tmem_ld_wait16(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0;
+                }
+                uint32_t v[8];
+                int lo[4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = inv > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
+                    const float b = inv > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
+                    v[e] = pack_bf16x2(a, b);
+                    const int two = (bits_left(a, v[e] & 0xFFFFu) & 255) | (bits_left(b, v[e] >> 16) & 255) << 8;
+                    if (e & 1) lo[e >> 1] |= two << 16;
+                    else lo[e >> 1] = two;
+                }
+                if (i < p.T) {  // d is a multiple of 8: the last 16 columns may be half a chunk
+                    *reinterpret_cast<uint4*>(p.out + at + cc) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + at + cc) = make_uint2(lo[0], lo[1]);
+                    if (cc + 8 < p.d) {
+                        *reinterpret_cast<uint4*>(p.out + at + cc + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                        if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + at + cc + 8) = make_uint2(lo[2], lo[3]);
+                    }
+                }
+            }
+            if (i < p.T) p.lse[(int64_t)h * p.T + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DP, int MODE>
+cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               FwdCfg<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((p.T + 2 * kTile - 1) / (2 * kTile)) * (unsigned)p.hq;
+    return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+}
+
+lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
+    FwdMaps maps;
+    const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs};
+    lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
+    if (s != LM_OK) return s;
+    // the plain form folds the scale into the exponent and needs it positive (the maximum of s c is c max s)
+    const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes || !(p.scale > 0.f) ? ATTN_BIAS : ATTN_PLAIN;
+    cudaError_t e;
+    if (p.d <= 64)
+        e = mode == ATTN_CAP    ? launch_fwd<64, ATTN_CAP>(p, maps, st)
+            : mode == ATTN_BIAS ? launch_fwd<64, ATTN_BIAS>(p, maps, st)
+                                : launch_fwd<64, ATTN_PLAIN>(p, maps, st);
+    else
+        e = mode == ATTN_CAP    ? launch_fwd<128, ATTN_CAP>(p, maps, st)
+            : mode == ATTN_BIAS ? launch_fwd<128, ATTN_BIAS>(p, maps, st)
+                                : launch_fwd<128, ATTN_PLAIN>(p, maps, st);
+    return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn forward launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace lm

@@ -41,7 +41,10 @@ struct AttnParams {
     int32_t T, hq, hk, d;
     float scale, cap;
     const float* slopes;
-    const TokRange* rng;   // T entries
+    const TokRange* rng;   // T entries, or null: one document
+    int32_t causal, window;
+    const int32_t* cu_docs;
+    int32_t n_docs;
     HeadsIn q, k, v, dO;
     const uint16_t* O;
     const int8_t* O_lo;
@@ -55,7 +58,7 @@ struct AttnParams {
     uint64_t wait_ns;
 };
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st);
-cudaError_t launch_attn_fwd(const AttnParams& p, cudaStream_t st);
+lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_delta(const AttnParams& p, float* delta, cudaStream_t st);
 cudaError_t launch_attn_dq(const AttnParams& p, cudaStream_t st);
 cudaError_t launch_attn_dkv(const AttnParams& p, cudaStream_t st);

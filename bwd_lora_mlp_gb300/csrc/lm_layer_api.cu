@@ -124,7 +124,11 @@ AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_he
     p.scale = a->scale;
     p.cap = a->cap;
     p.slopes = a->slopes;
-    p.rng = reinterpret_cast<const TokRange*>(static_cast<char*>(ws) + plan_attn(T, hq).rng);
+    p.rng = a->cu_docs ? reinterpret_cast<const TokRange*>(static_cast<char*>(ws) + plan_attn(T, hq).rng) : nullptr;
+    p.causal = a->causal;
+    p.window = a->window;
+    p.cu_docs = a->cu_docs;
+    p.n_docs = a->n_docs;
     p.q = {q->p, q->token_stride, q->head_stride};
     p.k = {k->p, k->token_stride, k->head_stride};
     p.v = {v->p, v->token_stride, v->head_stride};
@@ -133,7 +137,9 @@ AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_he
     return p;
 }
 
+// the table of who sees whom; one document needs none
 lm_status attn_ranges(const lm_attn* a, const AttnParams& p, cudaStream_t st) {
+    if (!p.rng) return LM_OK;
     LaunchTag tag("attn.ranges", st);
     return launched(launch_attn_ranges(*a, p.T, const_cast<TokRange*>(p.rng), st), "attn ranges launch");
 }
@@ -173,7 +179,7 @@ extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     p.lse = lse;
     LL_TRY(attn_ranges(a, p, st));
     LaunchTag tag("attn.fwd", st);
-    return launched(launch_attn_fwd(p, st), "attn forward launch");
+    return launch_attn_fwd(p, st);
 }
 
 extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
