@@ -29,7 +29,7 @@ LIB = os.path.join(PKG, "liblora_mlp.so")
 DIGEST = LIB + ".digest"
 
 SOURCES = ["lm_api.cu", "lm_aux.cu", "lm_gemm_fwd.cu", "lm_gemm_bwd.cu", "lm_gemm2.cu", "lm_gemm2_nf4.cu", "lm_static_ws.cu",
-           "lm_dual.cu", "lm_layer_api.cu", "lm_attn.cu", "lm_attn_fwd.cu", "lm_addnorm.cu", "lm_logprob.cu"]
+           "lm_dual.cu", "lm_layer_api.cu", "lm_attn.cu", "lm_attn_fwd.cu", "lm_attn_bwd.cu", "lm_addnorm.cu", "lm_logprob.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

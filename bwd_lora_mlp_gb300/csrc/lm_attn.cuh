@@ -56,6 +56,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is 128 rows (lanes) x 16 K values packed two to a column.
 __device__ __forceinline__ void umma_bf16_ts_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                 uint32_t accumulate, bool issue) {
@@ -131,6 +137,27 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // tanh x = 1 - 2 / (1 + e^{2x}), given 2 log2(e) x: absolute error a few 2^-24, exact at both ends
 __device__ __forceinline__ float tanh_from_2log2e(float x) { return 1.f - __fdividef(2.f, 1.f + ex2(x)); }
+
+// This thread's accumulator row, d columns from t on, times f, to bf16 (every lane of the warp comes
+// here; `any` false: the accumulator was never written and the row is zero; `mine`: the row exists).
+__device__ __forceinline__ void store_rows(uint16_t* dst, uint32_t t, int d, float f, bool any, bool mine) {
+#pragma unroll 1
+    for (int c = 0; c < d; c += 16) {
+        uint32_t o[16];
+        if (any) {
+            tmem_ld_x16(t + c, o);
+            tmem_ld_wait16(o);
+        }
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+        if (mine) {  // d is a multiple of 8: the last chunk may be half a chunk
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (c + 8 < d) *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
 
 // The eight bits of a value's fp32 pattern that its bf16 rounding leaves out (held to [-128, 127]).
 __device__ __forceinline__ int bits_left(float x, uint32_t bf16_bits) {

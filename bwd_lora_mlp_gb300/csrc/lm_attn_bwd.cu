@@ -1,0 +1,696 @@
+// Attention backward (include/lora_layer.h) on the tensor cores: two passes over the score tiles,
+// one per owner of the result, so that no sum crosses CTAs and every run gives the same bits.
+//   P = 2^{x - lse log2 e},  dz = P (dO.v - delta) (1 - (u / cap)^2),  delta = dO.O
+//   attn_dkv: a CTA owns 128 keys of one key/value head and walks the query tiles that see them,
+//             over all query heads of the group:  dV += P^T dO,  dK += dz^T Q   (4 products a tile)
+//   attn_dq:  a CTA owns 128 queries of one head and walks their key tiles:  dQ += dz K  (3 products)
+// The scores and dO.v are formed in both, seven products of 128 x 128 x d where one pass with dQ
+// summed by atomics would take five; in exchange there is no fp32 dQ in memory, nothing to clear
+// and no order of arrival.  Scores are formed with the owned rows as tensor-memory lanes (S^T in
+// attn_dkv), so P and dz go back to tensor memory as the left operand of the next product without
+// crossing threads.  Eight warps do the arithmetic (a thread: one row, 64 columns), one issues the
+// products, one loads.
+#include "lm_attn.cuh"
+
+namespace lm {
+
+constexpr int kBwdThreads = 320;
+constexpr int kQStages = 2;  // attn_dkv: query tiles, and dO tiles, in flight
+
+// A = P or dz in tensor memory: columns [0, 64) of the tile packed at t, [64, 128) at t + 64
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, uint32_t idesc, bool first, bool leader) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+        umma_bf16_ts_if(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), make_sdesc_sw128(b, kBoxBytes, 1024) + (uint64_t)(kk * 128),
+                        idesc, first && kk == 0 ? 0u : 1u, leader);
+}
+
+// rows of padding tokens hold anything: they are cleared where they would be a right operand (0 x NaN)
+__device__ __forceinline__ void clear_padding(uint8_t* tile, int boxes, int t0, int in0, int in1, int lane) {
+    if (t0 >= in0 && t0 + kTile <= in1) return;
+    for (int r = lane; r < kTile; r += 32)
+        if (t0 + r < in0 || t0 + r >= in1)
+            for (int b = 0; b < boxes; ++b)
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(tile + b * kBoxBytes + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+__device__ __forceinline__ void inside_tokens(const AttnParams& p, int& in0, int& in1) {
+    in0 = 0;
+    in1 = p.T;
+    if (p.cu_docs) {
+        in0 = max(0, p.cu_docs[0]);
+        in1 = min(p.T, p.cu_docs[p.n_docs]);
+    }
+}
+
+struct ScoreMath {
+    float c, cap, slope;
+};
+template <int MODE>
+__device__ __forceinline__ ScoreMath score_math(const AttnParams& p) {
+    return ScoreMath{MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, 0.f};
+}
+// x - lse in units of log 2; bend = du/dz
+template <int MODE>
+__device__ __forceinline__ float exponent(const ScoreMath& S, float qk, float dist, float nlse, float& bend) {
+    if (MODE == ATTN_PLAIN) return fmaf(qk, S.c, nlse);
+    if (MODE == ATTN_BIAS) return fmaf(-S.slope, fabsf(dist), fmaf(qk, S.c, nlse));
+    const float t = tanh_from_2log2e(qk * S.c);
+    bend = fmaf(-t, t, 1.f);
+    return fmaf(-S.slope, fabsf(dist), fmaf(t, S.cap, nlse));
+}
+
+struct BwdMaps {
+    CUtensorMap q, k, v, dO;
+};
+
+// ------------------------------------------------------------------ delta, and lse in the exponent's units
+// 16 threads a row (token, head): 8 dims each.  Tokens that see nothing get zeros, whatever dO holds.
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* delta, float* nlse) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int sub = threadIdx.x & 15;
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int t = (int)(row / p.hq), h = (int)(row - (int64_t)t * p.hq);
+    if (t >= p.Tp) return;
+    float s = 0.f, nl = 0.f;
+    if (t < p.T) {
+        const float lse = p.lse_in[(int64_t)h * p.T + t];
+        if (lse > -INFINITY || lse != lse) {
+            if (sub * 8 < p.d) {
+                const uint4 a = *reinterpret_cast<const uint4*>(p.dO.p + (int64_t)t * p.dO.ts + (int64_t)h * p.dO.hs + sub * 8);
+                const int64_t at = row * p.d + sub * 8;
+                const uint4 b = *reinterpret_cast<const uint4*>(p.O + at);
+                uint2 lo = make_uint2(0, 0);
+                if (p.O_lo) lo = *reinterpret_cast<const uint2*>(p.O_lo + at);
+                const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t ob = e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16;
+                    const int more = (int)(int8_t)((e < 4 ? lo.x : lo.y) >> (8 * (e & 3)));
+                    s += (e & 1 ? bf16hi(av[e >> 1]) : bf16lo(av[e >> 1])) * __uint_as_float(ob + (uint32_t)(more * 256));
+                }
+            }
+            nl = -lse * kLog2e;
+        }
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (sub == 0) {
+        delta[(int64_t)h * p.Tp + t] = s;
+        nlse[(int64_t)h * p.Tp + t] = nl;
+    }
+}
+
+cudaError_t launch_attn_delta(const AttnParams& p, float* delta, float* nlse, cudaStream_t st) {
+    const int64_t rows = (int64_t)p.Tp * p.hq;
+    return launch_pdl(attn_delta_kernel, dim3((unsigned)(rows / 16)), dim3(256), 0, st, nullptr, 0, p, delta, nlse);
+}
+
+// ------------------------------------------------------------------ dK, dV
+template <int DP>
+struct DkvCfg {
+    static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
+    static constexpr uint32_t kRowBytes = kTile * 4;  // nlse, and delta, of a query tile
+    static constexpr int kSmem = 2048 + (2 + 2 * kQStages) * kTileBytes + kQStages * 2 * kRowBytes;
+};
+
+template <int DP, int MODE>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
+    using C = DkvCfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* qfull = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* qempty = qfull + kQStages;
+    uint64_t* ofull = qempty + kQStages;
+    uint64_t* oempty = ofull + kQStages;
+    uint64_t* kvfull = oempty + kQStages;
+    uint64_t* sfull = kvfull + 1;   // S^T ready
+    uint64_t* pfull = sfull + 1;    // P^T written
+    uint64_t* dpfull = pfull + 1;   // dP^T ready
+    uint64_t* dsfull = dpfull + 1;  // dz^T written
+    uint64_t* drain = dsfull + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint8_t* sk = smem + 1024;
+    uint8_t* sv = sk + C::kTileBytes;
+    uint8_t* sq = sv + C::kTileBytes;
+    uint8_t* so = sq + kQStages * C::kTileBytes;
+    float* srow = reinterpret_cast<float*>(so + kQStages * C::kTileBytes);  // [stage][nlse, delta][128]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = (int)blockIdx.x % p.hk, k0 = (int)blockIdx.x / p.hk * kTile;  // (causal: the first keys are seen by most)
+    const int n = p.hq / p.hk;
+
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kQStages; ++s) {
+            mbar_init(smem_u32(&qfull[s]), 1);
+            mbar_init(smem_u32(&qempty[s]), 1);
+            mbar_init(smem_u32(&ofull[s]), 1);
+            mbar_init(smem_u32(&oempty[s]), 1);
+        }
+        mbar_init(smem_u32(kvfull), 1);
+        mbar_init(smem_u32(sfull), 1);
+        mbar_init(smem_u32(pfull), 8);
+        mbar_init(smem_u32(dpfull), 1);
+        mbar_init(smem_u32(dsfull), 8);
+        mbar_init(smem_u32(drain), 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+        tma_prefetch_map(&maps.dO);
+    }
+    __syncwarp();
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t ts = tmem, tdp = tmem + kTile, tdv = tmem + 2 * kTile, tdk = tdv + DP;
+    const TokRange rf = tok_range(p, k0), rl = tok_range(p, min(k0 + kTile, p.T) - 1);
+    const int qt0 = rf.qlo / kTile, nt = rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0;
+    const int N = nt * n;  // (head of the group, query tile), heads outermost
+
+    if (warp == 9) {  // ---------------- loader
+        if (lane == 0 && N > 0) {
+            bool ok = true;
+            mbar_expect_tx(smem_u32(kvfull), 2 * C::kTileBytes);
+            for (int b = 0; b < DP / 64; ++b) {
+                tma_load_3d(smem_u32(sk + b * kBoxBytes), &maps.k, smem_u32(kvfull), b * 64, g, k0);
+                tma_load_3d(smem_u32(sv + b * kBoxBytes), &maps.v, smem_u32(kvfull), b * 64, g, k0);
+            }
+            uint32_t it = 0, no = 0;  // query and dO tiles asked for
+            for (int hh = 0; ok && hh < n; ++hh)
+                for (int qt = qt0; qt < qt0 + nt; ++qt) {
+                    const int h = g * n + hh;
+                    const uint32_t s = no % kQStages, ph = (no / kQStages) & 1u;
+                    const uint32_t bq = smem_u32(&qfull[s]), bo = smem_u32(&ofull[s]);
+                    if (!mbar_wait(smem_u32(&qempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bq, C::kTileBytes + 2 * C::kRowBytes);
+                    for (int b = 0; b < DP / 64; ++b)
+                        tma_load_3d(smem_u32(sq + s * C::kTileBytes + b * kBoxBytes), &maps.q, bq, b * 64, h, qt * kTile);
+                    const int64_t row = (int64_t)h * p.Tp + qt * kTile;
+                    bulk_load(smem_u32(srow + s * 2 * kTile), p.nlse + row, C::kRowBytes, bq);
+                    bulk_load(smem_u32(srow + s * 2 * kTile + kTile), p.delta + row, C::kRowBytes, bq);
+                    ++it;
+                    if (!mbar_wait(smem_u32(&oempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bo, C::kTileBytes);
+                    for (int b = 0; b < DP / 64; ++b)
+                        tma_load_3d(smem_u32(so + s * C::kTileBytes + b * kBoxBytes), &maps.dO, bo, b * 64, h, qt * kTile);
+                    ++no;
+                }
+            if (!ok) {
+                attn_error(p, 6, 1);
+                *s_abort = 1;
+            }
+            volatile int never = 0;
+            bool in = mbar_wait(smem_u32(kvfull), 0, &never, p.wait_ns);
+            in = drain_fills(smem_u32(&qfull[0]), kQStages, it, p.wait_ns) && in;
+            in = drain_fills(smem_u32(&ofull[0]), kQStages, no, p.wait_ns) && in;
+            if (!in) attn_error(p, 6, 5);
+        }
+    } else if (warp == 8) {  // ---------------- tensor cores
+        const bool leader = lane == 0;
+        const int ksteps = (p.d + 15) / 16;
+        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+        const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // Q and dO are [query][dim]: MN-major
+        int in0, in1;
+        inside_tokens(p, in0, in1);
+        bool ok = N <= 0 || mbar_wait_warp(smem_u32(kvfull), 0, s_abort, p.wait_ns);
+        auto scores = [&](int it) {  // S^T(it) = K Q^T
+            const uint32_t s = (uint32_t)it % kQStages;
+            if (!mbar_wait_warp(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+            clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+            tc_fence_after();
+            mma_rows(ts, smem_u32(sk), smem_u32(sq + s * C::kTileBytes), ksteps, ids, leader);
+            umma_commit_if(smem_u32(sfull), leader);
+            return true;
+        };
+        auto dots = [&](int it) {  // dP^T(it) = V dO^T
+            const uint32_t s = (uint32_t)it % kQStages;
+            if (!mbar_wait_warp(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+            clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+            tc_fence_after();
+            mma_rows(tdp, smem_u32(sv), smem_u32(so + s * C::kTileBytes), ksteps, ids, leader);
+            umma_commit_if(smem_u32(dpfull), leader);
+            return true;
+        };
+        if (ok && N > 0) ok = scores(0) && dots(0);
+        for (int it = 0; ok && it < N; ++it) {
+            const uint32_t s = (uint32_t)it % kQStages;
+            if (!mbar_wait_warp(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            mma_weights(tdv, ts, smem_u32(so + s * C::kTileBytes), idd, it == 0, leader);
+            umma_commit_if(smem_u32(&oempty[s]), leader);
+            if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
+                ok = false;
+                break;
+            }
+            if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            mma_weights(tdk, tdp, smem_u32(sq + s * C::kTileBytes), idd, it == 0, leader);
+            umma_commit_if(smem_u32(&qempty[s]), leader);
+            if (it + 1 < N && !dots(it + 1)) {
+                ok = false;
+                break;
+            }
+        }
+        if (!ok && leader) {
+            attn_error(p, 6, 2);
+            *s_abort = 1;
+        }
+        umma_commit_if(smem_u32(drain), leader);
+        volatile int never = 0;
+        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+        __syncwarp();
+    } else {  // ---------------- arithmetic: one key row, 64 query columns per thread
+        const int half = warp >> 2;
+        const int k = k0 + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tsw = ts + lanes + half * 64, tdpw = tdp + lanes + half * 64;
+        TokRange r{0, 0, 0, 0};
+        if (k < p.T) r = tok_range(p, k);
+        ScoreMath S = score_math<MODE>(p);
+        bool ok = true;
+        int it = 0;
+        for (int hh = 0; ok && hh < n; ++hh) {
+            if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
+            for (int qt = qt0; qt < qt0 + nt; ++qt, ++it) {
+                const int q0 = qt * kTile + half * 64;
+                const float* row = srow + (it % kQStages) * 2 * kTile + half * 64;
+                // every query of the tile sees every key of this one, or some pair is hidden
+                const bool hidden = qt * kTile < rl.qlo || (qt + 1) * kTile > rf.qhi;
+                const int a = r.qlo - q0, z = r.qhi - q0;
+                const float dist = (float)(q0 - k);
+                // the query tile's rows (nlse, delta) come with it; the scores are ready after it is
+                if (!mbar_wait_warp(smem_u32(&qfull[it % kQStages]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns) ||
+                    !mbar_wait_warp(smem_u32(sfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t x[2][32];
+                tmem_ld_x32(tsw, x[0]);
+                tmem_ld_x32(tsw + 32, x[1]);
+                tmem_ld_wait(x[0]);
+                tmem_ld_wait(x[1]);
+                uint32_t pk[32];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 nl = *reinterpret_cast<const float4*>(row + b * 32 + e);
+                        const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+                        float P[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int col = b * 32 + e + f;
+                            float bend = 1.f;
+                            P[f] = ex2(exponent<MODE>(S, __uint_as_float(x[b][e + f]), dist + (float)col, nls[f], bend));
+                            if (hidden && (col < a || col >= z)) P[f] = 0.f;
+                            x[b][e + f] = __float_as_uint(MODE == ATTN_CAP ? P[f] * bend : P[f]);
+                        }
+                        pk[b * 16 + e / 2] = pack_bf16x2(P[0], P[1]);
+                        pk[b * 16 + e / 2 + 1] = pack_bf16x2(P[2], P[3]);
+                    }
+                tmem_st_x32(tsw, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(pfull));
+                if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t y[2][32];
+                tmem_ld_x32(tdpw, y[0]);
+                tmem_ld_x32(tdpw + 32, y[1]);
+                tmem_ld_wait(y[0]);
+                tmem_ld_wait(y[1]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 dl = *reinterpret_cast<const float4*>(row + kTile + b * 32 + e);
+                        const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
+                        float z4[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int col = b * 32 + e + f;
+                            z4[f] = __uint_as_float(x[b][e + f]) * (__uint_as_float(y[b][e + f]) - dls[f]);
+                            if (hidden && (col < a || col >= z)) z4[f] = 0.f;
+                        }
+                        pk[b * 16 + e / 2] = pack_bf16x2(z4[0], z4[1]);
+                        pk[b * 16 + e / 2 + 1] = pack_bf16x2(z4[2], z4[3]);
+                    }
+                tmem_st_x32(tdpw, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(dsfull));
+            }
+        }
+        // warpgroup 0 writes dV, warpgroup 1 dK
+        if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
+        tc_fence_after();
+        if (!ok) {
+            if (lane == 0) {
+                attn_error(p, 6, 3);
+                *s_abort = 1;
+            }
+        } else {
+            store_rows((half ? p.dK : p.dV) + ((int64_t)k * p.hk + g) * p.d, (half ? tdk : tdv) + lanes, p.d,
+                       half ? p.scale : 1.f, N > 0, k < p.T);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ dQ
+template <int DP>
+struct DqCfg {
+    static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
+    static constexpr int kKStages = 3, kVStages = 2;  // S runs one key tile ahead of dz, so K stays longer
+    static constexpr int kSmem = 2048 + (2 + kKStages + kVStages) * kTileBytes;
+};
+
+template <int DP, int MODE>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
+    using C = DqCfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* kempty = kfull + C::kKStages;
+    uint64_t* vfull = kempty + C::kKStages;
+    uint64_t* vempty = vfull + C::kVStages;
+    uint64_t* qfull = vempty + C::kVStages;
+    uint64_t* sfull = qfull + 1;    // [2] S ready
+    uint64_t* dpfull = sfull + 2;   // dP ready
+    uint64_t* dsfull = dpfull + 1;  // dz written (in place of S), dP read
+    uint64_t* drain = dsfull + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint8_t* sq = smem + 1024;
+    uint8_t* so = sq + C::kTileBytes;
+    uint8_t* sk = so + C::kTileBytes;
+    uint8_t* sv = sk + C::kKStages * C::kTileBytes;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nqt = (p.T + kTile - 1) / kTile;
+    const int h = (int)blockIdx.x % p.hq, q0 = (nqt - 1 - (int)blockIdx.x / p.hq) * kTile;  // (the longest rows first)
+    const int g = h / (p.hq / p.hk);
+
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kKStages; ++s) {
+            mbar_init(smem_u32(&kfull[s]), 1);
+            mbar_init(smem_u32(&kempty[s]), 1);
+        }
+        for (int s = 0; s < C::kVStages; ++s) {
+            mbar_init(smem_u32(&vfull[s]), 1);
+            mbar_init(smem_u32(&vempty[s]), 1);
+        }
+        mbar_init(smem_u32(qfull), 1);
+        mbar_init(smem_u32(&sfull[0]), 1);
+        mbar_init(smem_u32(&sfull[1]), 1);
+        mbar_init(smem_u32(dpfull), 1);
+        mbar_init(smem_u32(dsfull), 8);
+        mbar_init(smem_u32(drain), 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&maps.q);
+        tma_prefetch_map(&maps.k);
+        tma_prefetch_map(&maps.v);
+        tma_prefetch_map(&maps.dO);
+    }
+    __syncwarp();
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tdp = tmem + 2 * kTile, tdq = tmem + 3 * kTile;
+    const TokRange rf = tok_range(p, q0), rl = tok_range(p, min(q0 + kTile, p.T) - 1);
+    const int kt0 = rf.lo / kTile, N = rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0;
+
+    if (warp == 9) {  // ---------------- loader
+        if (lane == 0 && N > 0) {
+            bool ok = true;
+            mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
+            for (int b = 0; b < DP / 64; ++b) {
+                tma_load_3d(smem_u32(sq + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h, q0);
+                tma_load_3d(smem_u32(so + b * kBoxBytes), &maps.dO, smem_u32(qfull), b * 64, h, q0);
+            }
+            uint32_t nk = 0, nv = 0;
+            while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, K_2 | V_1, K_3 | V_2, ... as the products take them
+                const bool key = nk < (uint32_t)N && (nk == 0 || nk < nv + 2);
+                const uint32_t i = key ? nk : nv, st = key ? i % C::kKStages : i % C::kVStages;
+                const uint32_t ph = (key ? i / C::kKStages : i / C::kVStages) & 1u;
+                const uint32_t bar = smem_u32(key ? &kfull[st] : &vfull[st]);
+                uint8_t* dst = (key ? sk : sv) + st * C::kTileBytes;
+                if (!mbar_wait(smem_u32(key ? &kempty[st] : &vempty[st]), ph ^ 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(bar, C::kTileBytes);
+                for (int b = 0; b < DP / 64; ++b)
+                    tma_load_3d(smem_u32(dst + b * kBoxBytes), key ? &maps.k : &maps.v, bar, b * 64, g, (kt0 + (int)i) * kTile);
+                if (key) ++nk;
+                else ++nv;
+            }
+            if (!ok) {
+                attn_error(p, 7, 1);
+                *s_abort = 1;
+            }
+            volatile int never = 0;
+            bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
+            in = drain_fills(smem_u32(&kfull[0]), C::kKStages, nk, p.wait_ns) && in;
+            in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
+            if (!in) attn_error(p, 7, 5);
+        }
+    } else if (warp == 8) {  // ---------------- tensor cores
+        const bool leader = lane == 0;
+        const int ksteps = (p.d + 15) / 16;
+        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+        const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
+        int in0, in1;
+        inside_tokens(p, in0, in1);
+        bool ok = N <= 0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+        auto scores = [&](int j) {  // S(j) = Q K^T, in half j & 1
+            const uint32_t s = (uint32_t)j % C::kKStages;
+            if (!mbar_wait_warp(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
+            clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1, lane);
+            tc_fence_after();
+            mma_rows(tmem + (j & 1) * kTile, smem_u32(sq), smem_u32(sk + s * C::kTileBytes), ksteps, ids, leader);
+            umma_commit_if(smem_u32(&sfull[j & 1]), leader);
+            return true;
+        };
+        auto dots = [&](int j) {  // dP(j) = dO V^T
+            const uint32_t s = (uint32_t)j % C::kVStages;
+            if (!mbar_wait_warp(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
+            tc_fence_after();
+            mma_rows(tdp, smem_u32(so), smem_u32(sv + s * C::kTileBytes), ksteps, ids, leader);
+            umma_commit_if(smem_u32(dpfull), leader);
+            umma_commit_if(smem_u32(&vempty[s]), leader);
+            return true;
+        };
+        if (ok && N > 0) ok = scores(0) && dots(0) && (N < 2 || scores(1));
+        for (int j = 0; ok && j < N; ++j) {
+            if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (j + 1 < N && !dots(j + 1)) {
+                ok = false;
+                break;
+            }
+            const uint32_t s = (uint32_t)j % C::kKStages;
+            mma_weights(tdq, tmem + (j & 1) * kTile, smem_u32(sk + s * C::kTileBytes), idd, j == 0, leader);
+            umma_commit_if(smem_u32(&kempty[s]), leader);
+            if (j + 2 < N && !scores(j + 2)) {
+                ok = false;
+                break;
+            }
+        }
+        if (!ok && leader) {
+            attn_error(p, 7, 2);
+            *s_abort = 1;
+        }
+        umma_commit_if(smem_u32(drain), leader);
+        volatile int never = 0;
+        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+        __syncwarp();
+    } else {  // ---------------- arithmetic: one query row, 64 key columns per thread
+        const int half = warp >> 2;
+        const int i = q0 + (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        TokRange r{0, 0, 0, 0};
+        float nlse = 0.f, delta = 0.f;
+        if (i < p.T) {
+            r = tok_range(p, i);
+            nlse = p.nlse[(int64_t)h * p.Tp + i];
+            delta = p.delta[(int64_t)h * p.Tp + i];
+        }
+        ScoreMath S = score_math<MODE>(p);
+        if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[h] * kLog2e;
+        bool ok = true;
+        for (int j = 0; j < N; ++j) {
+            const uint32_t tsw = tmem + lanes + (j & 1) * kTile + half * 64;
+            const int kt = (kt0 + j) * kTile, k0 = kt + half * 64;
+            const bool hidden = kt < rl.lo || kt + kTile > rf.hi;
+            const int a = r.lo - k0, z = r.hi - k0;
+            const float dist = (float)(i - k0);
+            if (!mbar_wait_warp(smem_u32(&sfull[j & 1]), ((uint32_t)j >> 1) & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t x[2][32];
+            tmem_ld_x32(tsw, x[0]);
+            tmem_ld_x32(tsw + 32, x[1]);
+            tmem_ld_wait(x[0]);
+            tmem_ld_wait(x[1]);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float bend = 1.f;
+                    const float P = ex2(exponent<MODE>(S, __uint_as_float(x[b][e]), dist - (float)(b * 32 + e), nlse, bend));
+                    x[b][e] = __float_as_uint(MODE == ATTN_CAP ? P * bend : P);
+                }
+            if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t y[2][32];
+            tmem_ld_x32(tdp + lanes + half * 64, y[0]);
+            tmem_ld_x32(tdp + lanes + half * 64 + 32, y[1]);
+            tmem_ld_wait(y[0]);
+            tmem_ld_wait(y[1]);
+            uint32_t pk[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const int col = b * 32 + e;
+                    float z0 = __uint_as_float(x[b][e]) * (__uint_as_float(y[b][e]) - delta);
+                    float z1 = __uint_as_float(x[b][e + 1]) * (__uint_as_float(y[b][e + 1]) - delta);
+                    if (hidden) {
+                        if (col < a || col >= z) z0 = 0.f;
+                        if (col + 1 < a || col + 1 >= z) z1 = 0.f;
+                    }
+                    pk[b * 16 + e / 2] = pack_bf16x2(z0, z1);
+                }
+            tmem_st_x32(tsw, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(dsfull));
+        }
+        if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
+        tc_fence_after();
+        if (!ok) {
+            if (lane == 0) {
+                attn_error(p, 7, 3);
+                *s_abort = 1;
+            }
+        } else if (half == 0) {
+            store_rows(p.out + ((int64_t)i * p.hq + h) * p.d, tdq + lanes, p.d, p.scale, N > 0, i < p.T);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ launches
+template <int DP, int MODE>
+cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_dkv_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               DkvCfg<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hk;
+    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+}
+template <int DP, int MODE>
+cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               DqCfg<DP>::kSmem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hq;
+    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+}
+
+template <int DP, int MODE>
+cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
+    {
+        LaunchTag tag("attn.dkv", st);
+        const cudaError_t e = launch_dkv<DP, MODE>(p, maps, st);
+        if (e != cudaSuccess) return e;
+    }
+    LaunchTag tag("attn.dq", st);
+    return launch_dq<DP, MODE>(p, maps, st);
+}
+
+lm_status launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
+    BwdMaps maps;
+    const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs}, dO{p.dO.p, p.dO.ts, p.dO.hs};
+    lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.dO, dO, p.T, p.hq, p.d, kTile);
+    if (s != LM_OK) return s;
+    const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes ? ATTN_BIAS : ATTN_PLAIN;
+    cudaError_t e;
+    if (p.d <= 64)
+        e = mode == ATTN_CAP    ? launch_both<64, ATTN_CAP>(p, maps, st)
+            : mode == ATTN_BIAS ? launch_both<64, ATTN_BIAS>(p, maps, st)
+                                : launch_both<64, ATTN_PLAIN>(p, maps, st);
+    else
+        e = mode == ATTN_CAP    ? launch_both<128, ATTN_CAP>(p, maps, st)
+            : mode == ATTN_BIAS ? launch_both<128, ATTN_BIAS>(p, maps, st)
+                                : launch_both<128, ATTN_PLAIN>(p, maps, st);
+    return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn backward launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace lm

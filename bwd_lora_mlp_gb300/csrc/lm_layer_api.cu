@@ -102,15 +102,18 @@ Span heads_span(const lm_heads* t, int64_t T, int heads, int d, const char* name
     return Span{t->p, T ? (size_t)((T - 1) * t->token_stride + (heads - 1) * t->head_stride + d) * 2 : 0, name};
 }
 
+int64_t whole_tiles(int64_t T) { return (T + 127) / 128 * 128; }
+
 struct AttnPlan {
-    size_t rng, delta, total;
+    size_t rng, delta, nlse, total;
 };
 
 AttnPlan plan_attn(int64_t T, int32_t hq) {
     AttnPlan P;
     P.rng = 256;  // after the error word
     P.delta = (P.rng + (size_t)T * sizeof(TokRange) + 255) & ~size_t(255);
-    P.total = (P.delta + (size_t)T * hq * 4 + 255) & ~size_t(255);
+    P.nlse = P.delta + (size_t)whole_tiles(T) * hq * 4;  // (a multiple of 512 bytes)
+    P.total = P.nlse + (size_t)whole_tiles(T) * hq * 4;
     return P;
 }
 
@@ -118,6 +121,7 @@ AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_he
                        const lm_heads* v, const lm_attn* a, void* ws) {
     AttnParams p{};
     p.T = (int32_t)T;
+    p.Tp = (int32_t)whole_tiles(T);
     p.hq = hq;
     p.hk = hk;
     p.d = d;
@@ -218,18 +222,15 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     p.dK = dK;
     p.dV = dV;
     float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + P.delta);
+    float* nlse = reinterpret_cast<float*>(static_cast<char*>(ws) + P.nlse);
     p.delta = delta;
+    p.nlse = nlse;
     LL_TRY(attn_ranges(a, p, st));
     {
         LaunchTag tag("attn.delta", st);
-        LL_TRY(launched(launch_attn_delta(p, delta, st), "attn delta launch"));
+        LL_TRY(launched(launch_attn_delta(p, delta, nlse, st), "attn delta launch"));
     }
-    {
-        LaunchTag tag("attn.dkv", st);
-        LL_TRY(launched(launch_attn_dkv(p, st), "attn dK/dV launch"));
-    }
-    LaunchTag tag("attn.dq", st);
-    return launched(launch_attn_dq(p, st), "attn dQ launch");
+    return launch_attn_bwd(p, st);
 }
 
 // ------------------------------------------------------------------ addnorm
