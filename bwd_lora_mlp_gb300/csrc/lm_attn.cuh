@@ -2,6 +2,8 @@
 // projection kernels do not use, and the score arithmetic.
 #pragma once
 
+#include <type_traits>
+
 #include "lm_gemm.cuh"
 #include "lm_layer.h"
 #include "lm_ptx.cuh"
@@ -73,24 +75,27 @@ __device__ __forceinline__ void umma_bf16_ts_if(uint32_t d_tmem, uint32_t a_tmem
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+// 32 columns of this thread's row into x[AT .. AT + 31].
+template <int AT, int N>
+__device__ __forceinline__ void tmem_ld_f32(uint32_t taddr, float (&x)[N]) {
+    static_assert(AT + 32 <= N, "");
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(x[AT + 0]), "=f"(x[AT + 1]), "=f"(x[AT + 2]), "=f"(x[AT + 3]), "=f"(x[AT + 4]), "=f"(x[AT + 5]), "=f"(x[AT + 6]), "=f"(x[AT + 7]),
+          "=f"(x[AT + 8]), "=f"(x[AT + 9]), "=f"(x[AT + 10]), "=f"(x[AT + 11]), "=f"(x[AT + 12]), "=f"(x[AT + 13]), "=f"(x[AT + 14]), "=f"(x[AT + 15]),
+          "=f"(x[AT + 16]), "=f"(x[AT + 17]), "=f"(x[AT + 18]), "=f"(x[AT + 19]), "=f"(x[AT + 20]), "=f"(x[AT + 21]), "=f"(x[AT + 22]), "=f"(x[AT + 23]),
+          "=f"(x[AT + 24]), "=f"(x[AT + 25]), "=f"(x[AT + 26]), "=f"(x[AT + 27]), "=f"(x[AT + 28]), "=f"(x[AT + 29]), "=f"(x[AT + 30]), "=f"(x[AT + 31])
         : "r"(taddr));
 }
-// Waits for this thread's loads; carries the registers so that no use of them moves before it.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+// Waits for this thread's loads; carries the values so that no use of them moves before it.
+template <int AT, int N>
+__device__ __forceinline__ void tmem_ld_wait_f32(float (&x)[N]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 : "+f"(x[AT + 0]), "+f"(x[AT + 1]), "+f"(x[AT + 2]), "+f"(x[AT + 3]), "+f"(x[AT + 4]), "+f"(x[AT + 5]), "+f"(x[AT + 6]), "+f"(x[AT + 7]),
+                   "+f"(x[AT + 8]), "+f"(x[AT + 9]), "+f"(x[AT + 10]), "+f"(x[AT + 11]), "+f"(x[AT + 12]), "+f"(x[AT + 13]), "+f"(x[AT + 14]), "+f"(x[AT + 15]),
+                   "+f"(x[AT + 16]), "+f"(x[AT + 17]), "+f"(x[AT + 18]), "+f"(x[AT + 19]), "+f"(x[AT + 20]), "+f"(x[AT + 21]), "+f"(x[AT + 22]), "+f"(x[AT + 23]),
+                   "+f"(x[AT + 24]), "+f"(x[AT + 25]), "+f"(x[AT + 26]), "+f"(x[AT + 27]), "+f"(x[AT + 28]), "+f"(x[AT + 29]), "+f"(x[AT + 30]), "+f"(x[AT + 31])
                  :
                  : "memory");
 }
@@ -135,8 +140,28 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // tanh x = 1 - 2 / (1 + e^{2x}), given 2 log2(e) x: absolute error a few 2^-24, exact at both ends
-__device__ __forceinline__ float tanh_from_2log2e(float x) { return 1.f - __fdividef(2.f, 1.f + ex2(x)); }
+__device__ __forceinline__ float tanh_from_2log2e(float x) { return fmaf(-2.f, rcp(1.f + ex2(x)), 1.f); }
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
+// Register budgets of a CTA's warpgroups: what the loader's and the MMA warp's do not need goes to the
+// arithmetic ones.  384 threads start with 168 each; 2 x 208 + 88 is what three threads bring.
+constexpr int kAttnThreads = 384;
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+constexpr int kMathRegs = 208, kIssueRegs = 88;
+static_assert(2 * kMathRegs + kIssueRegs <= 3 * 168, "a register split above the launch's total waits forever");
 
 // This thread's accumulator row, d columns from t on, times f, to bf16 (every lane of the warp comes
 // here; `any` false: the accumulator was never written and the row is zero; `mine`: the row exists).
@@ -159,9 +184,9 @@ __device__ __forceinline__ void store_rows(uint16_t* dst, uint32_t t, int d, flo
     }
 }
 
-// The eight bits of a value's fp32 pattern that its bf16 rounding leaves out (held to [-128, 127]).
+// The next eight bits of a value's fp32 pattern after its bf16 rounding, to the nearest (held to 127).
 __device__ __forceinline__ int bits_left(float x, uint32_t bf16_bits) {
-    return min((int32_t)(__float_as_uint(x) - (bf16_bits << 16)) >> 8, 127);
+    return min(((int32_t)(__float_as_uint(x) - (bf16_bits << 16)) + 128) >> 8, 127);
 }
 
 }  // namespace lm

@@ -14,7 +14,6 @@
 
 namespace lm {
 
-constexpr int kBwdThreads = 320;
 constexpr int kQStages = 2;  // attn_dkv: query tiles, and dO tiles, in flight
 
 // A = P or dz in tensor memory: columns [0, 64) of the tile packed at t, [64, 128) at t + 64
@@ -52,14 +51,23 @@ template <int MODE>
 __device__ __forceinline__ ScoreMath score_math(const AttnParams& p) {
     return ScoreMath{MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, 0.f};
 }
-// x - lse in units of log 2; bend = du/dz
-template <int MODE>
-__device__ __forceinline__ float exponent(const ScoreMath& S, float qk, float dist, float nlse, float& bend) {
-    if (MODE == ATTN_PLAIN) return fmaf(qk, S.c, nlse);
-    if (MODE == ATTN_BIAS) return fmaf(-S.slope, fabsf(dist), fmaf(qk, S.c, nlse));
-    const float t = tanh_from_2log2e(qk * S.c);
-    bend = fmaf(-t, t, 1.f);
-    return fmaf(-S.slope, fabsf(dist), fmaf(t, S.cap, nlse));
+// x - lse in units of log 2 for two neighbouring columns; bend = du/dz.  dist: i - j of the first, and
+// the second's is one more (STEP 1: the columns are queries) or one less (-1: keys).
+template <int MODE, int STEP>
+__device__ __forceinline__ float2 exponents(const ScoreMath& S, float2 qk, float dist, float2 nlse, float2& bend) {
+    float2 y;
+    if (MODE == ATTN_CAP) {
+        const float2 t = make_float2(tanh_from_2log2e(qk.x * S.c), tanh_from_2log2e(qk.y * S.c));
+        bend = __ffma2_rn(make_float2(-t.x, -t.y), t, two(1.f));
+        y = __ffma2_rn(t, two(S.cap), nlse);
+    } else {
+        y = __ffma2_rn(qk, two(S.c), nlse);
+    }
+    if (MODE != ATTN_PLAIN) {
+        y.x = fmaf(-S.slope, fabsf(dist), y.x);
+        y.y = fmaf(-S.slope, fabsf(dist + (float)STEP), y.y);
+    }
+    return y;
 }
 
 struct BwdMaps {
@@ -68,7 +76,7 @@ struct BwdMaps {
 
 // ------------------------------------------------------------------ delta, and lse in the exponent's units
 // 16 threads a row (token, head): 8 dims each.  Tokens that see nothing get zeros, whatever dO holds.
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* delta, float* nlse) {
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* ndelta, float* nlse) {
     griddep_launch_dependents();
     griddep_wait();
     const int sub = threadIdx.x & 15;
@@ -99,26 +107,26 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 #pragma unroll
     for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (sub == 0) {
-        delta[(int64_t)h * p.Tp + t] = s;
+        ndelta[(int64_t)h * p.Tp + t] = -s;
         nlse[(int64_t)h * p.Tp + t] = nl;
     }
 }
 
-cudaError_t launch_attn_delta(const AttnParams& p, float* delta, float* nlse, cudaStream_t st) {
+cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st) {
     const int64_t rows = (int64_t)p.Tp * p.hq;
-    return launch_pdl(attn_delta_kernel, dim3((unsigned)(rows / 16)), dim3(256), 0, st, nullptr, 0, p, delta, nlse);
+    return launch_pdl(attn_delta_kernel, dim3((unsigned)(rows / 16)), dim3(256), 0, st, nullptr, 0, p, ndelta, nlse);
 }
 
 // ------------------------------------------------------------------ dK, dV
 template <int DP>
 struct DkvCfg {
     static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
-    static constexpr uint32_t kRowBytes = kTile * 4;  // nlse, and delta, of a query tile
+    static constexpr uint32_t kRowBytes = kTile * 4;  // nlse, and -delta, of a query tile
     static constexpr int kSmem = 2048 + (2 + 2 * kQStages) * kTileBytes + kQStages * 2 * kRowBytes;
 };
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
     using C = DkvCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint8_t* sv = sk + C::kTileBytes;
     uint8_t* sq = sv + C::kTileBytes;
     uint8_t* so = sq + kQStages * C::kTileBytes;
-    float* srow = reinterpret_cast<float*>(so + kQStages * C::kTileBytes);  // [stage][nlse, delta][128]
+    float* srow = reinterpret_cast<float*>(so + kQStages * C::kTileBytes);  // [stage][nlse, -delta][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = (int)blockIdx.x % p.hk, k0 = (int)blockIdx.x / p.hk * kTile;  // (causal: the first keys are seen by most)
@@ -181,111 +189,115 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int qt0 = rf.qlo / kTile, nt = rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0;
     const int N = nt * n;  // (head of the group, query tile), heads outermost
 
-    if (warp == 9) {  // ---------------- loader
-        if (lane == 0 && N > 0) {
-            bool ok = true;
-            mbar_expect_tx(smem_u32(kvfull), 2 * C::kTileBytes);
-            for (int b = 0; b < DP / 64; ++b) {
-                tma_load_3d(smem_u32(sk + b * kBoxBytes), &maps.k, smem_u32(kvfull), b * 64, g, k0);
-                tma_load_3d(smem_u32(sv + b * kBoxBytes), &maps.v, smem_u32(kvfull), b * 64, g, k0);
-            }
-            uint32_t it = 0, no = 0;  // query and dO tiles asked for
-            for (int hh = 0; ok && hh < n; ++hh)
-                for (int qt = qt0; qt < qt0 + nt; ++qt) {
-                    const int h = g * n + hh;
-                    const uint32_t s = no % kQStages, ph = (no / kQStages) & 1u;
-                    const uint32_t bq = smem_u32(&qfull[s]), bo = smem_u32(&ofull[s]);
-                    if (!mbar_wait(smem_u32(&qempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bq, C::kTileBytes + 2 * C::kRowBytes);
-                    for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(sq + s * C::kTileBytes + b * kBoxBytes), &maps.q, bq, b * 64, h, qt * kTile);
-                    const int64_t row = (int64_t)h * p.Tp + qt * kTile;
-                    bulk_load(smem_u32(srow + s * 2 * kTile), p.nlse + row, C::kRowBytes, bq);
-                    bulk_load(smem_u32(srow + s * 2 * kTile + kTile), p.delta + row, C::kRowBytes, bq);
-                    ++it;
-                    if (!mbar_wait(smem_u32(&oempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bo, C::kTileBytes);
-                    for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(so + s * C::kTileBytes + b * kBoxBytes), &maps.dO, bo, b * 64, h, qt * kTile);
-                    ++no;
+    if (warp >= 8) {
+        regs_down<kIssueRegs>();
+        if (warp == 9) {  // ---------------- loader
+            if (lane == 0 && N > 0) {
+                bool ok = true;
+                mbar_expect_tx(smem_u32(kvfull), 2 * C::kTileBytes);
+                for (int b = 0; b < DP / 64; ++b) {
+                    tma_load_3d(smem_u32(sk + b * kBoxBytes), &maps.k, smem_u32(kvfull), b * 64, g, k0);
+                    tma_load_3d(smem_u32(sv + b * kBoxBytes), &maps.v, smem_u32(kvfull), b * 64, g, k0);
                 }
-            if (!ok) {
-                attn_error(p, 6, 1);
+                uint32_t it = 0, no = 0;  // query and dO tiles asked for
+                for (int hh = 0; ok && hh < n; ++hh)
+                    for (int qt = qt0; qt < qt0 + nt; ++qt) {
+                        const int h = g * n + hh;
+                        const uint32_t s = no % kQStages, ph = (no / kQStages) & 1u;
+                        const uint32_t bq = smem_u32(&qfull[s]), bo = smem_u32(&ofull[s]);
+                        if (!mbar_wait(smem_u32(&qempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(bq, C::kTileBytes + 2 * C::kRowBytes);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(smem_u32(sq + s * C::kTileBytes + b * kBoxBytes), &maps.q, bq, b * 64, h, qt * kTile);
+                        const int64_t row = (int64_t)h * p.Tp + qt * kTile;
+                        bulk_load(smem_u32(srow + s * 2 * kTile), p.nlse + row, C::kRowBytes, bq);
+                        bulk_load(smem_u32(srow + s * 2 * kTile + kTile), p.ndelta + row, C::kRowBytes, bq);
+                        ++it;
+                        if (!mbar_wait(smem_u32(&oempty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(bo, C::kTileBytes);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(smem_u32(so + s * C::kTileBytes + b * kBoxBytes), &maps.dO, bo, b * 64, h, qt * kTile);
+                        ++no;
+                    }
+                if (!ok) {
+                    attn_error(p, 6, 1);
+                    *s_abort = 1;
+                }
+                volatile int never = 0;
+                bool in = mbar_wait(smem_u32(kvfull), 0, &never, p.wait_ns);
+                in = drain_fills(smem_u32(&qfull[0]), kQStages, it, p.wait_ns) && in;
+                in = drain_fills(smem_u32(&ofull[0]), kQStages, no, p.wait_ns) && in;
+                if (!in) attn_error(p, 6, 5);
+            }
+        } else if (warp == 8) {  // ---------------- tensor cores
+            const bool leader = lane == 0;
+            const int ksteps = (p.d + 15) / 16;
+            const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+            const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // Q and dO are [query][dim]: MN-major
+            int in0, in1;
+            inside_tokens(p, in0, in1);
+            bool ok = N <= 0 || mbar_wait_warp(smem_u32(kvfull), 0, s_abort, p.wait_ns);
+            auto scores = [&](int it) {  // S^T(it) = K Q^T
+                const uint32_t s = (uint32_t)it % kQStages;
+                if (!mbar_wait_warp(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+                tc_fence_after();
+                mma_rows(ts, smem_u32(sk), smem_u32(sq + s * C::kTileBytes), ksteps, ids, leader);
+                umma_commit_if(smem_u32(sfull), leader);
+                return true;
+            };
+            auto dots = [&](int it) {  // dP^T(it) = V dO^T
+                const uint32_t s = (uint32_t)it % kQStages;
+                if (!mbar_wait_warp(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+                tc_fence_after();
+                mma_rows(tdp, smem_u32(sv), smem_u32(so + s * C::kTileBytes), ksteps, ids, leader);
+                umma_commit_if(smem_u32(dpfull), leader);
+                return true;
+            };
+            if (ok && N > 0) ok = scores(0) && dots(0);
+            for (int it = 0; ok && it < N; ++it) {
+                const uint32_t s = (uint32_t)it % kQStages;
+                if (!mbar_wait_warp(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                mma_weights(tdv, ts, smem_u32(so + s * C::kTileBytes), idd, it == 0, leader);
+                umma_commit_if(smem_u32(&oempty[s]), leader);
+                if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
+                    ok = false;
+                    break;
+                }
+                if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                mma_weights(tdk, tdp, smem_u32(sq + s * C::kTileBytes), idd, it == 0, leader);
+                umma_commit_if(smem_u32(&qempty[s]), leader);
+                if (it + 1 < N && !dots(it + 1)) {
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok && leader) {
+                attn_error(p, 6, 2);
                 *s_abort = 1;
             }
+            umma_commit_if(smem_u32(drain), leader);
             volatile int never = 0;
-            bool in = mbar_wait(smem_u32(kvfull), 0, &never, p.wait_ns);
-            in = drain_fills(smem_u32(&qfull[0]), kQStages, it, p.wait_ns) && in;
-            in = drain_fills(smem_u32(&ofull[0]), kQStages, no, p.wait_ns) && in;
-            if (!in) attn_error(p, 6, 5);
+            mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+            __syncwarp();
         }
-    } else if (warp == 8) {  // ---------------- tensor cores
-        const bool leader = lane == 0;
-        const int ksteps = (p.d + 15) / 16;
-        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
-        const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // Q and dO are [query][dim]: MN-major
-        int in0, in1;
-        inside_tokens(p, in0, in1);
-        bool ok = N <= 0 || mbar_wait_warp(smem_u32(kvfull), 0, s_abort, p.wait_ns);
-        auto scores = [&](int it) {  // S^T(it) = K Q^T
-            const uint32_t s = (uint32_t)it % kQStages;
-            if (!mbar_wait_warp(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-            clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
-            tc_fence_after();
-            mma_rows(ts, smem_u32(sk), smem_u32(sq + s * C::kTileBytes), ksteps, ids, leader);
-            umma_commit_if(smem_u32(sfull), leader);
-            return true;
-        };
-        auto dots = [&](int it) {  // dP^T(it) = V dO^T
-            const uint32_t s = (uint32_t)it % kQStages;
-            if (!mbar_wait_warp(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-            clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
-            tc_fence_after();
-            mma_rows(tdp, smem_u32(sv), smem_u32(so + s * C::kTileBytes), ksteps, ids, leader);
-            umma_commit_if(smem_u32(dpfull), leader);
-            return true;
-        };
-        if (ok && N > 0) ok = scores(0) && dots(0);
-        for (int it = 0; ok && it < N; ++it) {
-            const uint32_t s = (uint32_t)it % kQStages;
-            if (!mbar_wait_warp(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            mma_weights(tdv, ts, smem_u32(so + s * C::kTileBytes), idd, it == 0, leader);
-            umma_commit_if(smem_u32(&oempty[s]), leader);
-            if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
-                ok = false;
-                break;
-            }
-            if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            mma_weights(tdk, tdp, smem_u32(sq + s * C::kTileBytes), idd, it == 0, leader);
-            umma_commit_if(smem_u32(&qempty[s]), leader);
-            if (it + 1 < N && !dots(it + 1)) {
-                ok = false;
-                break;
-            }
-        }
-        if (!ok && leader) {
-            attn_error(p, 6, 2);
-            *s_abort = 1;
-        }
-        umma_commit_if(smem_u32(drain), leader);
-        volatile int never = 0;
-        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-        __syncwarp();
     } else {  // ---------------- arithmetic: one key row, 64 query columns per thread
+        regs_up<kMathRegs>();
         const int half = warp >> 2;
         const int k = k0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -294,6 +306,69 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (k < p.T) r = tok_range(p, k);
         ScoreMath S = score_math<MODE>(p);
         bool ok = true;
+        // one query tile, its scores ready; tiles with hidden pairs have code of their own
+        auto tile = [&](int it, const float* row, float dist, int a, int z, auto hides) {
+            constexpr bool HIDDEN = decltype(hides)::value;
+            float x[64];
+            uint32_t pk[32];
+            tmem_ld_f32<0>(tsw, x);
+            tmem_ld_f32<32>(tsw + 32, x);
+            tmem_ld_wait_f32<0>(x);
+            tmem_ld_wait_f32<32>(x);
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 nl = *reinterpret_cast<const float4*>(row + e);
+                const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+                for (int f = 0; f < 4; f += 2) {
+                    float2 bend = two(1.f);
+                    const float2 y = exponents<MODE, 1>(S, make_float2(x[e + f], x[e + f + 1]), dist + (float)(e + f),
+                                                     make_float2(nls[f], nls[f + 1]), bend);
+                    float2 P = make_float2(ex2(y.x), ex2(y.y));
+                    if (HIDDEN) {
+                        if (e + f < a || e + f >= z) P.x = 0.f;
+                        if (e + f + 1 < a || e + f + 1 >= z) P.y = 0.f;
+                    }
+                    pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
+                    if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                    x[e + f] = P.x;
+                    x[e + f + 1] = P.y;
+                }
+            }
+            tmem_st_x32(tsw, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(pfull));
+            if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) return false;
+            tc_fence_after();
+            float y[64];
+            tmem_ld_f32<0>(tdpw, y);
+            tmem_ld_f32<32>(tdpw + 32, y);
+            tmem_ld_wait_f32<0>(y);
+            tmem_ld_wait_f32<32>(y);
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 dl = *reinterpret_cast<const float4*>(row + kTile + e);
+                const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+                for (int f = 0; f < 4; f += 2) {
+                    float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
+                    d = __fmul2_rn(d, make_float2(x[e + f], x[e + f + 1]));
+                    if (HIDDEN) {
+                        if (e + f < a || e + f >= z) d.x = 0.f;
+                        if (e + f + 1 < a || e + f + 1 >= z) d.y = 0.f;
+                    }
+                    pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
+                }
+            }
+            tmem_st_x32(tdpw, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(dsfull));
+            return true;
+        };
         int it = 0;
         for (int hh = 0; ok && hh < n; ++hh) {
             if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
@@ -304,73 +379,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const bool hidden = qt * kTile < rl.qlo || (qt + 1) * kTile > rf.qhi;
                 const int a = r.qlo - q0, z = r.qhi - q0;
                 const float dist = (float)(q0 - k);
-                // the query tile's rows (nlse, delta) come with it; the scores are ready after it is
+                // the query tile's rows (nlse, -delta) come with it; the scores are ready after it is
                 if (!mbar_wait_warp(smem_u32(&qfull[it % kQStages]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns) ||
                     !mbar_wait_warp(smem_u32(sfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                uint32_t x[2][32];
-                tmem_ld_x32(tsw, x[0]);
-                tmem_ld_x32(tsw + 32, x[1]);
-                tmem_ld_wait(x[0]);
-                tmem_ld_wait(x[1]);
-                uint32_t pk[32];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 nl = *reinterpret_cast<const float4*>(row + b * 32 + e);
-                        const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
-                        float P[4];
-#pragma unroll
-                        for (int f = 0; f < 4; ++f) {
-                            const int col = b * 32 + e + f;
-                            float bend = 1.f;
-                            P[f] = ex2(exponent<MODE>(S, __uint_as_float(x[b][e + f]), dist + (float)col, nls[f], bend));
-                            if (hidden && (col < a || col >= z)) P[f] = 0.f;
-                            x[b][e + f] = __float_as_uint(MODE == ATTN_CAP ? P[f] * bend : P[f]);
-                        }
-                        pk[b * 16 + e / 2] = pack_bf16x2(P[0], P[1]);
-                        pk[b * 16 + e / 2 + 1] = pack_bf16x2(P[2], P[3]);
-                    }
-                tmem_st_x32(tsw, pk);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(pfull));
-                if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint32_t y[2][32];
-                tmem_ld_x32(tdpw, y[0]);
-                tmem_ld_x32(tdpw + 32, y[1]);
-                tmem_ld_wait(y[0]);
-                tmem_ld_wait(y[1]);
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 dl = *reinterpret_cast<const float4*>(row + kTile + b * 32 + e);
-                        const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
-                        float z4[4];
-#pragma unroll
-                        for (int f = 0; f < 4; ++f) {
-                            const int col = b * 32 + e + f;
-                            z4[f] = __uint_as_float(x[b][e + f]) * (__uint_as_float(y[b][e + f]) - dls[f]);
-                            if (hidden && (col < a || col >= z)) z4[f] = 0.f;
-                        }
-                        pk[b * 16 + e / 2] = pack_bf16x2(z4[0], z4[1]);
-                        pk[b * 16 + e / 2 + 1] = pack_bf16x2(z4[2], z4[3]);
-                    }
-                tmem_st_x32(tdpw, pk);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(dsfull));
+                ok = hidden ? tile(it, row, dist, a, z, std::true_type{}) : tile(it, row, dist, a, z, std::false_type{});
+                if (!ok) break;
             }
         }
         // warpgroup 0 writes dV, warpgroup 1 dK
@@ -404,7 +421,7 @@ struct DqCfg {
 };
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
     using C = DqCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -467,108 +484,152 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const TokRange rf = tok_range(p, q0), rl = tok_range(p, min(q0 + kTile, p.T) - 1);
     const int kt0 = rf.lo / kTile, N = rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0;
 
-    if (warp == 9) {  // ---------------- loader
-        if (lane == 0 && N > 0) {
-            bool ok = true;
-            mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
-            for (int b = 0; b < DP / 64; ++b) {
-                tma_load_3d(smem_u32(sq + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h, q0);
-                tma_load_3d(smem_u32(so + b * kBoxBytes), &maps.dO, smem_u32(qfull), b * 64, h, q0);
+    if (warp >= 8) {
+        regs_down<kIssueRegs>();
+        if (warp == 9) {  // ---------------- loader
+            if (lane == 0 && N > 0) {
+                bool ok = true;
+                mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
+                for (int b = 0; b < DP / 64; ++b) {
+                    tma_load_3d(smem_u32(sq + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h, q0);
+                    tma_load_3d(smem_u32(so + b * kBoxBytes), &maps.dO, smem_u32(qfull), b * 64, h, q0);
+                }
+                uint32_t nk = 0, nv = 0;
+                while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, K_2 | V_1, K_3 | V_2, ... as the products take them
+                    const bool key = nk < (uint32_t)N && (nk == 0 || nk < nv + 2);
+                    const uint32_t i = key ? nk : nv, st = key ? i % C::kKStages : i % C::kVStages;
+                    const uint32_t ph = (key ? i / C::kKStages : i / C::kVStages) & 1u;
+                    const uint32_t bar = smem_u32(key ? &kfull[st] : &vfull[st]);
+                    uint8_t* dst = (key ? sk : sv) + st * C::kTileBytes;
+                    if (!mbar_wait(smem_u32(key ? &kempty[st] : &vempty[st]), ph ^ 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar, C::kTileBytes);
+                    for (int b = 0; b < DP / 64; ++b)
+                        tma_load_3d(smem_u32(dst + b * kBoxBytes), key ? &maps.k : &maps.v, bar, b * 64, g, (kt0 + (int)i) * kTile);
+                    if (key) ++nk;
+                    else ++nv;
+                }
+                if (!ok) {
+                    attn_error(p, 7, 1);
+                    *s_abort = 1;
+                }
+                volatile int never = 0;
+                bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
+                in = drain_fills(smem_u32(&kfull[0]), C::kKStages, nk, p.wait_ns) && in;
+                in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
+                if (!in) attn_error(p, 7, 5);
             }
-            uint32_t nk = 0, nv = 0;
-            while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, K_2 | V_1, K_3 | V_2, ... as the products take them
-                const bool key = nk < (uint32_t)N && (nk == 0 || nk < nv + 2);
-                const uint32_t i = key ? nk : nv, st = key ? i % C::kKStages : i % C::kVStages;
-                const uint32_t ph = (key ? i / C::kKStages : i / C::kVStages) & 1u;
-                const uint32_t bar = smem_u32(key ? &kfull[st] : &vfull[st]);
-                uint8_t* dst = (key ? sk : sv) + st * C::kTileBytes;
-                if (!mbar_wait(smem_u32(key ? &kempty[st] : &vempty[st]), ph ^ 1u, s_abort, p.wait_ns)) {
+        } else if (warp == 8) {  // ---------------- tensor cores
+            const bool leader = lane == 0;
+            const int ksteps = (p.d + 15) / 16;
+            const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+            const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
+            int in0, in1;
+            inside_tokens(p, in0, in1);
+            bool ok = N <= 0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+            auto scores = [&](int j) {  // S(j) = Q K^T, in half j & 1
+                const uint32_t s = (uint32_t)j % C::kKStages;
+                if (!mbar_wait_warp(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1, lane);
+                tc_fence_after();
+                mma_rows(tmem + (j & 1) * kTile, smem_u32(sq), smem_u32(sk + s * C::kTileBytes), ksteps, ids, leader);
+                umma_commit_if(smem_u32(&sfull[j & 1]), leader);
+                return true;
+            };
+            auto dots = [&](int j) {  // dP(j) = dO V^T
+                const uint32_t s = (uint32_t)j % C::kVStages;
+                if (!mbar_wait_warp(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
+                tc_fence_after();
+                mma_rows(tdp, smem_u32(so), smem_u32(sv + s * C::kTileBytes), ksteps, ids, leader);
+                umma_commit_if(smem_u32(dpfull), leader);
+                umma_commit_if(smem_u32(&vempty[s]), leader);
+                return true;
+            };
+            if (ok && N > 0) ok = scores(0) && dots(0) && (N < 2 || scores(1));
+            for (int j = 0; ok && j < N; ++j) {
+                if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
                     ok = false;
                     break;
                 }
-                mbar_expect_tx(bar, C::kTileBytes);
-                for (int b = 0; b < DP / 64; ++b)
-                    tma_load_3d(smem_u32(dst + b * kBoxBytes), key ? &maps.k : &maps.v, bar, b * 64, g, (kt0 + (int)i) * kTile);
-                if (key) ++nk;
-                else ++nv;
+                tc_fence_after();
+                if (j + 1 < N && !dots(j + 1)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t s = (uint32_t)j % C::kKStages;
+                mma_weights(tdq, tmem + (j & 1) * kTile, smem_u32(sk + s * C::kTileBytes), idd, j == 0, leader);
+                umma_commit_if(smem_u32(&kempty[s]), leader);
+                if (j + 2 < N && !scores(j + 2)) {
+                    ok = false;
+                    break;
+                }
             }
-            if (!ok) {
-                attn_error(p, 7, 1);
+            if (!ok && leader) {
+                attn_error(p, 7, 2);
                 *s_abort = 1;
             }
+            umma_commit_if(smem_u32(drain), leader);
             volatile int never = 0;
-            bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
-            in = drain_fills(smem_u32(&kfull[0]), C::kKStages, nk, p.wait_ns) && in;
-            in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
-            if (!in) attn_error(p, 7, 5);
+            mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+            __syncwarp();
         }
-    } else if (warp == 8) {  // ---------------- tensor cores
-        const bool leader = lane == 0;
-        const int ksteps = (p.d + 15) / 16;
-        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
-        const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
-        int in0, in1;
-        inside_tokens(p, in0, in1);
-        bool ok = N <= 0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
-        auto scores = [&](int j) {  // S(j) = Q K^T, in half j & 1
-            const uint32_t s = (uint32_t)j % C::kKStages;
-            if (!mbar_wait_warp(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
-            clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1, lane);
-            tc_fence_after();
-            mma_rows(tmem + (j & 1) * kTile, smem_u32(sq), smem_u32(sk + s * C::kTileBytes), ksteps, ids, leader);
-            umma_commit_if(smem_u32(&sfull[j & 1]), leader);
-            return true;
-        };
-        auto dots = [&](int j) {  // dP(j) = dO V^T
-            const uint32_t s = (uint32_t)j % C::kVStages;
-            if (!mbar_wait_warp(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
-            tc_fence_after();
-            mma_rows(tdp, smem_u32(so), smem_u32(sv + s * C::kTileBytes), ksteps, ids, leader);
-            umma_commit_if(smem_u32(dpfull), leader);
-            umma_commit_if(smem_u32(&vempty[s]), leader);
-            return true;
-        };
-        if (ok && N > 0) ok = scores(0) && dots(0) && (N < 2 || scores(1));
-        for (int j = 0; ok && j < N; ++j) {
-            if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            if (j + 1 < N && !dots(j + 1)) {
-                ok = false;
-                break;
-            }
-            const uint32_t s = (uint32_t)j % C::kKStages;
-            mma_weights(tdq, tmem + (j & 1) * kTile, smem_u32(sk + s * C::kTileBytes), idd, j == 0, leader);
-            umma_commit_if(smem_u32(&kempty[s]), leader);
-            if (j + 2 < N && !scores(j + 2)) {
-                ok = false;
-                break;
-            }
-        }
-        if (!ok && leader) {
-            attn_error(p, 7, 2);
-            *s_abort = 1;
-        }
-        umma_commit_if(smem_u32(drain), leader);
-        volatile int never = 0;
-        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-        __syncwarp();
     } else {  // ---------------- arithmetic: one query row, 64 key columns per thread
+        regs_up<kMathRegs>();
         const int half = warp >> 2;
         const int i = q0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         TokRange r{0, 0, 0, 0};
-        float nlse = 0.f, delta = 0.f;
+        float nlse = 0.f, ndelta = 0.f;
         if (i < p.T) {
             r = tok_range(p, i);
             nlse = p.nlse[(int64_t)h * p.Tp + i];
-            delta = p.delta[(int64_t)h * p.Tp + i];
+            ndelta = p.ndelta[(int64_t)h * p.Tp + i];
         }
         ScoreMath S = score_math<MODE>(p);
         if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[h] * kLog2e;
         bool ok = true;
+        auto tile = [&](int j, uint32_t tsw, float dist, int a, int z, auto hides) {
+            constexpr bool HIDDEN = decltype(hides)::value;
+            float x[64], y[64];
+            tmem_ld_f32<0>(tsw, x);
+            tmem_ld_f32<32>(tsw + 32, x);
+            tmem_ld_wait_f32<0>(x);
+            tmem_ld_wait_f32<32>(x);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                float2 bend = two(1.f);
+                const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(nlse), bend);
+                float2 P = make_float2(ex2(v.x), ex2(v.y));
+                if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                x[e] = P.x;
+                x[e + 1] = P.y;
+            }
+            if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) return false;
+            tc_fence_after();
+            tmem_ld_f32<0>(tdp + lanes + half * 64, y);
+            tmem_ld_f32<32>(tdp + lanes + half * 64 + 32, y);
+            tmem_ld_wait_f32<0>(y);
+            tmem_ld_wait_f32<32>(y);
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(ndelta));
+                d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
+                if (HIDDEN) {
+                    if (e < a || e >= z) d.x = 0.f;
+                    if (e + 1 < a || e + 1 >= z) d.y = 0.f;
+                }
+                pk[e / 2] = pack_bf16x2(d.x, d.y);
+            }
+            tmem_st_x32(tsw, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(dsfull));
+            return true;
+        };
         for (int j = 0; j < N; ++j) {
             const uint32_t tsw = tmem + lanes + (j & 1) * kTile + half * 64;
             const int kt = (kt0 + j) * kTile, k0 = kt + half * 64;
@@ -580,48 +641,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 break;
             }
             tc_fence_after();
-            uint32_t x[2][32];
-            tmem_ld_x32(tsw, x[0]);
-            tmem_ld_x32(tsw + 32, x[1]);
-            tmem_ld_wait(x[0]);
-            tmem_ld_wait(x[1]);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    float bend = 1.f;
-                    const float P = ex2(exponent<MODE>(S, __uint_as_float(x[b][e]), dist - (float)(b * 32 + e), nlse, bend));
-                    x[b][e] = __float_as_uint(MODE == ATTN_CAP ? P * bend : P);
-                }
-            if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t y[2][32];
-            tmem_ld_x32(tdp + lanes + half * 64, y[0]);
-            tmem_ld_x32(tdp + lanes + half * 64 + 32, y[1]);
-            tmem_ld_wait(y[0]);
-            tmem_ld_wait(y[1]);
-            uint32_t pk[32];
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int col = b * 32 + e;
-                    float z0 = __uint_as_float(x[b][e]) * (__uint_as_float(y[b][e]) - delta);
-                    float z1 = __uint_as_float(x[b][e + 1]) * (__uint_as_float(y[b][e + 1]) - delta);
-                    if (hidden) {
-                        if (col < a || col >= z) z0 = 0.f;
-                        if (col + 1 < a || col + 1 >= z) z1 = 0.f;
-                    }
-                    pk[b * 16 + e / 2] = pack_bf16x2(z0, z1);
-                }
-            tmem_st_x32(tsw, pk);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(dsfull));
+            ok = hidden ? tile(j, tsw, dist, a, z, std::true_type{}) : tile(j, tsw, dist, a, z, std::false_type{});
+            if (!ok) break;
         }
         if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
         tc_fence_after();
@@ -650,7 +671,7 @@ cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, cudaStream_t st
                                                DkvCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hk;
-    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 template <int DP, int MODE>
 cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
@@ -658,7 +679,7 @@ cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st)
                                                DqCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hq;
-    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
 template <int DP, int MODE>

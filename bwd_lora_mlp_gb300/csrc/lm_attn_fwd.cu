@@ -10,16 +10,17 @@
 // longer than 128 x 128 exponentials with their loads, maxima, sums and packing.  The running
 // maximum m follows the row only when it has grown by more than 8 (a factor 256 in the weights): the
 // weights then stay below 2^8, exact in their scale, and O_w is rescaled a few times per row
-// instead of once per key tile.  Sums are fp32; P is rounded to bf16 for the second product (as
-// flash-style kernels must), and on tiles with hidden keys the normaliser of O sums the rounded
-// weights, so that short rows keep sum P = 1; lse always comes from the unrounded sums.
+// instead of once per key tile.  Sums are fp32.  P is rounded to bf16 for the second product; on tiles with
+// hidden keys what the rounding left out is multiplied too (as a second left operand, in the other
+// half of S_w's place): rows of few keys have no other weights to average their error with, and the
+// backward takes differences against their O.  That is one more product on the tiles along the
+// diagonal and at document ends; dQ of packed prefixes went from 2.51e-3 to 2.4e-3 of its norm off.
 // Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
 // memory: S_0, S_1, O_0, O_1 of 128 columns each.
 #include "lm_attn.cuh"
 
 namespace lm {
 
-constexpr int kFwdThreads = 320;  // two softmax warpgroups, the MMA warp, the loader warp
 constexpr float kRescale = 8.f;
 
 template <int DP>
@@ -37,6 +38,7 @@ struct FwdMaps {
 struct TileSpan {
     int j0, j1;
     int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
+    __device__ __forceinline__ bool hides(int j) const { return j * kTile < lo_max || (j + 1) * kTile > hi_min; }
 };
 __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
     if (q0 >= p.T) return TileSpan{0, 0, 0, 0};
@@ -46,7 +48,7 @@ __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
 }
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kFwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwdMaps maps) {
     using C = FwdCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -55,8 +57,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t* empty = full + C::kSlots;
     uint64_t* qfull = empty + C::kSlots;
     uint64_t* sfull = qfull + 1;   // [2] scores ready
-    uint64_t* pfull = sfull + 2;   // [2] weights written (and the scores read)
-    uint64_t* odone = pfull + 2;   // [2] one more P V product done
+    uint64_t* pfull = sfull + 2;   // [2][2] weights of the first, of the last 64 keys written (and the scores read)
+    uint64_t* odone = pfull + 4;   // [2] one more P V product done
     uint64_t* drain = odone + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -78,7 +80,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         mbar_init(smem_u32(qfull), 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&sfull[w]), 1);
-            mbar_init(smem_u32(&pfull[w]), 4);
+            mbar_init(smem_u32(&pfull[2 * w]), 4);
+            mbar_init(smem_u32(&pfull[2 * w + 1]), 4);
             mbar_init(smem_u32(&odone[w]), 1);
         }
         mbar_init(smem_u32(drain), 1);
@@ -105,106 +108,119 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         J1 = max(J1, span[1].j1);
     }
 
-    if (warp == 9) {  // ---------------- loader
-        if (lane == 0 && J1 > J0) {
-            bool ok = true;
-            mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
-            for (int w = 0; w < 2; ++w)
-                for (int b = 0; b < DP / 64; ++b)
-                    tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h,
-                                q0 + w * kTile);
-            uint32_t n = 0;
-            for (int j = J0; ok && j < J1; ++j)
-                for (int kv = 0; kv < 2; ++kv, ++n) {
-                    const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
-                    if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+    if (warp >= 8) {
+        regs_down<kIssueRegs>();
+        if (warp == 9) {  // ---------------- loader
+            if (lane == 0 && J1 > J0) {
+                bool ok = true;
+                mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
+                for (int w = 0; w < 2; ++w)
                     for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
-                                    smem_u32(&full[s]), b * 64, g, j * kTile);
+                        tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h,
+                                    q0 + w * kTile);
+                uint32_t n = 0;
+                for (int j = J0; ok && j < J1; ++j)
+                    for (int kv = 0; kv < 2; ++kv, ++n) {
+                        const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
+                        if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
+                                        smem_u32(&full[s]), b * 64, g, j * kTile);
+                    }
+                if (!ok) {
+                    attn_error(p, 5, 1);
+                    *s_abort = 1;
                 }
-            if (!ok) {
-                attn_error(p, 5, 1);
+                // nothing may land in shared memory after the CTA has gone
+                volatile int never = 0;
+                const bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
+                if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
+            }
+        } else if (warp == 8) {  // ---------------- tensor cores: the whole warp, lane 0 issues
+            const bool leader = lane == 0;
+            const int ksteps = (p.d + 15) / 16;
+            const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
+            const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
+            // keys of no document hold anything: their rows of V are cleared, 0 x NaN would reach every O
+            int in0 = 0, in1 = p.T;
+            if (p.cu_docs) {
+                in0 = max(0, p.cu_docs[0]);
+                in1 = min(p.T, p.cu_docs[p.n_docs]);
+            }
+            bool ok = J1 <= J0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+            for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
+                const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
+                const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
+                const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
+                if (j > J0) {
+                    ok = mbar_wait_warp(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+                    if (!ok) break;
+                    const int k0 = (j - 1) * kTile;
+                    if (k0 < in0 || k0 + kTile > in1) {
+                        for (int r = lane; r < kTile; r += 32)
+                            if (k0 + r < in0 || k0 + r >= in1)
+                                for (int b = 0; b < DP / 64; ++b)
+                                    for (int c = 0; c < 8; ++c)
+                                        *reinterpret_cast<uint4*>(ring + (nv % C::kSlots) * C::kTileBytes + b * kBoxBytes +
+                                                                  r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (j < J1) {
+                    ok = mbar_wait_warp(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
+                    if (!ok) break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
+                    if (j > span[w].j0 && j <= span[w].j1) {  // O_w += P_w V_{j-1}
+                        const uint32_t n = (uint32_t)(j - 1 - span[w].j0);
+                        const bool hides = span[w].hides(j - 1);
+#pragma unroll
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = mbar_wait_warp(smem_u32(&pfull[2 * w + half]), n & 1u, s_abort, p.wait_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t a = ts + half * 32;
+                            const uint64_t b = make_sdesc_sw128(sv, kBoxBytes, 1024) + (uint64_t)(half * 512);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16_ts_if(to, a + kk * 8, b + (uint64_t)(kk * 128), ido, (n || half || kk) ? 1u : 0u, leader);
+                            if (hides) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16_ts_if(to, a + 64 + kk * 8, b + (uint64_t)(kk * 128), ido, 1u, leader);
+                            }
+                        }
+                        if (!ok) break;
+                        umma_commit_if(smem_u32(&odone[w]), leader);
+                    }
+                    if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
+                        mma_rows(ts, smem_u32(sq + w * C::kTileBytes), sk, ksteps, ids, leader);
+                        umma_commit_if(smem_u32(&sfull[w]), leader);
+                    }
+                }
+                if (!ok) break;
+                if (j > J0) umma_commit_if(smem_u32(&empty[nv % C::kSlots]), leader);
+                if (j < J1) umma_commit_if(smem_u32(&empty[nk % C::kSlots]), leader);
+            }
+            if (!ok && leader) {
+                attn_error(p, 5, 2);
                 *s_abort = 1;
             }
-            // nothing may land in shared memory after the CTA has gone
+            umma_commit_if(smem_u32(drain), leader);
             volatile int never = 0;
-            const bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
-            if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
+            mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+            __syncwarp();
         }
-    } else if (warp == 8) {  // ---------------- tensor cores: the whole warp, lane 0 issues
-        const bool leader = lane == 0;
-        const int ksteps = (p.d + 15) / 16;
-        const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
-        const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
-        // keys of no document hold anything: their rows of V are cleared, 0 x NaN would reach every O
-        int in0 = 0, in1 = p.T;
-        if (p.cu_docs) {
-            in0 = max(0, p.cu_docs[0]);
-            in1 = min(p.T, p.cu_docs[p.n_docs]);
-        }
-        bool ok = J1 <= J0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
-        for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
-            const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
-            const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
-            const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
-            if (j > J0) {
-                ok = mbar_wait_warp(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
-                if (!ok) break;
-                const int k0 = (j - 1) * kTile;
-                if (k0 < in0 || k0 + kTile > in1) {
-                    for (int r = lane; r < kTile; r += 32)
-                        if (k0 + r < in0 || k0 + r >= in1)
-                            for (int b = 0; b < DP / 64; ++b)
-                                for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4*>(ring + (nv % C::kSlots) * C::kTileBytes + b * kBoxBytes +
-                                                              r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            }
-            if (j < J1) {
-                ok = mbar_wait_warp(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
-                if (!ok) break;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
-                if (j > span[w].j0 && j <= span[w].j1) {  // O_w += P_w V_{j-1}
-                    const uint32_t n = (uint32_t)(j - 1 - span[w].j0);
-                    if (!mbar_wait_warp(smem_u32(&pfull[w]), n & 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_bf16_ts_if(to, ts + kk * 8, make_sdesc_sw128(sv, kBoxBytes, 1024) + (uint64_t)(kk * 128), ido,
-                                        (n || kk) ? 1u : 0u, leader);
-                    umma_commit_if(smem_u32(&odone[w]), leader);
-                }
-                if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
-                    mma_rows(ts, smem_u32(sq + w * C::kTileBytes), sk, ksteps, ids, leader);
-                    umma_commit_if(smem_u32(&sfull[w]), leader);
-                }
-            }
-            if (!ok) break;
-            if (j > J0) umma_commit_if(smem_u32(&empty[nv % C::kSlots]), leader);
-            if (j < J1) umma_commit_if(smem_u32(&empty[nk % C::kSlots]), leader);
-        }
-        if (!ok && leader) {
-            attn_error(p, 5, 2);
-            *s_abort = 1;
-        }
-        umma_commit_if(smem_u32(drain), leader);
-        volatile int never = 0;
-        mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-        __syncwarp();
     } else {  // ---------------- softmax: warpgroup w, one thread per query row
+        regs_up<kMathRegs>();
         const int w = warp >> 2;
         const int i = q0 + w * kTile + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -217,101 +233,96 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float c = MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
         const float cap = p.cap * kLog2e;
         const float cx = MODE == ATTN_PLAIN ? c : 1.f;
-        float m = -INFINITY, l = 0.f, ln = 0.f;  // running maximum, sum of weights, O's normaliser
+        float m = -INFINITY, l = 0.f;  // running maximum, sum of weights
         bool ok = true;
-        for (int j = j0; j < j1; ++j) {
-            if (!mbar_wait_warp(smem_u32(&sfull[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t x[4][32];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld_x32(ts + b * 32, x[b]);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) tmem_ld_wait(x[b]);
+        // one key tile; tiles with hidden keys have code of their own
+        auto tile = [&](int j, auto hides) {
+            constexpr bool HIDDEN = decltype(hides)::value;
+            float x[kTile];
+            tmem_ld_f32<0>(ts, x);
+            tmem_ld_f32<32>(ts + 32, x);
+            tmem_ld_f32<64>(ts + 64, x);
+            tmem_ld_f32<96>(ts + 96, x);
+            tmem_ld_wait_f32<0>(x);
+            tmem_ld_wait_f32<32>(x);
+            tmem_ld_wait_f32<64>(x);
+            tmem_ld_wait_f32<96>(x);
             const int k0 = j * kTile;
             if (MODE != ATTN_PLAIN) {
                 const float dist = (float)(i - k0);
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = __uint_as_float(x[b][e]) * c;
-                        if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
-                        x[b][e] = __float_as_uint(fmaf(-slope, fabsf(dist - (float)(b * 32 + e)), v));
-                    }
+                for (int e = 0; e < kTile; ++e) {
+                    float v = x[e] * c;
+                    if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
+                    x[e] = fmaf(-slope, fabsf(dist - (float)e), v);
+                }
             }
-            const bool hidden = k0 < span[w].lo_max || k0 + kTile > span[w].hi_min;
-            if (hidden) {
+            if (HIDDEN) {
                 const int a = r.lo - k0, z = r.hi - k0;
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (b * 32 + e < a || b * 32 + e >= z) x[b][e] = __float_as_uint(-INFINITY);
+                for (int e = 0; e < kTile; ++e)
+                    if (e < a || e >= z) x[e] = -INFINITY;
             }
             float mx[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                mx[b] = __uint_as_float(x[b][0]);
+                mx[b] = x[b * 32];
 #pragma unroll
-                for (int e = 1; e < 32; ++e) mx[b] = fmaxf(mx[b], __uint_as_float(x[b][e]));
+                for (int e = 1; e < 31; e += 2) mx[b] = fmaxf(fmaxf(mx[b], x[b * 32 + e]), x[b * 32 + e + 1]);
+                mx[b] = fmaxf(mx[b], x[b * 32 + 31]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cx;
             const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
                 if (j > j0) {
-                    if (!mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j - 1 - j0) & 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j - 1 - j0) & 1u, s_abort, p.wait_ns)) return false;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int cc = 0; cc < DP; cc += 32) {
-                        uint32_t o[32];
-                        tmem_ld_x32(to + cc, o);
-                        tmem_ld_wait(o);
+                    for (int cc = 0; cc < DP; cc += 16) {
+                        uint32_t o[16];
+                        tmem_ld_x16(to + cc, o);
+                        tmem_ld_wait16(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st_x32(to + cc, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st_x16(to + cc, o);
                     }
                     tmem_st_wait();
                 }
                 l *= f;
-                ln *= f;
                 if (grow) m = top;
             }
-            const float mu = m == -INFINITY ? 0.f : m;
-            float s4[4] = {0.f, 0.f, 0.f, 0.f}, r4[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t pk[2][32];
+            const float2 c2 = two(cx), mu = two(m == -INFINITY ? 0.f : -m);
+            float2 s2[2] = {two(0.f), two(0.f)};
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int half = 0; half < 2; ++half) {  // 64 keys at a time: their product may begin
+                uint32_t pk[32], rest[32];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(x[b][e]), cx, -mu));
-                    const float p1 = ex2(fmaf(__uint_as_float(x[b][e + 1]), cx, -mu));
-                    s4[b] += p0 + p1;
-                    pk[b >> 1][(b & 1) * 16 + (e >> 1)] = pack_bf16x2(p0, p1);
+                for (int e = 0; e < 64; e += 2) {
+                    const int at = half * 64 + e;
+                    const float2 y = __ffma2_rn(make_float2(x[at], x[at + 1]), c2, mu);
+                    const float2 q = make_float2(ex2(y.x), ex2(y.y));
+                    s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
+                    const uint32_t hi = pack_bf16x2(q.x, q.y);
+                    pk[e >> 1] = hi;
+                    if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
                 }
-            const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            float rsum = sum;
-            if (hidden) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r4[(e >> 4) + 2 * b] += bf16lo(pk[b][e]) + bf16hi(pk[b][e]);
-                rsum = (r4[0] + r4[1]) + (r4[2] + r4[3]);
+                tmem_st_x32(ts + half * 32, pk);
+                if (HIDDEN) tmem_st_x32(ts + 64 + half * 32, rest);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
             }
-            l += sum;
-            ln += rsum;
-            tmem_st_x32(ts, pk[0]);
-            tmem_st_x32(ts + 32, pk[1]);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&pfull[w]));
+            const float2 s = __fadd2_rn(s2[0], s2[1]);
+            l += s.x + s.y;
+            return true;
+        };
+        for (int j = j0; ok && j < j1; ++j) {
+            ok = mbar_wait_warp(smem_u32(&sfull[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            ok = span[w].hides(j) ? tile(j, std::true_type{}) : tile(j, std::false_type{});
         }
         if (ok && j1 > j0) ok = mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j1 - 1 - j0) & 1u, s_abort, p.wait_ns);
         tc_fence_after();
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 *s_abort = 1;
             }
         } else {
-            const float inv = ln > 0.f ? 1.f / ln : 0.f;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t at = ((int64_t)i * p.hq + h) * p.d;
 #pragma unroll 1
             for (int cc = 0; cc < p.d; cc += 16) {
@@ -371,7 +382,7 @@ cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, cudaStream_t st
                                                FwdCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.T + 2 * kTile - 1) / (2 * kTile)) * (unsigned)p.hq;
-    return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
 lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st) {

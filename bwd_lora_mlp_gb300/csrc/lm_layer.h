@@ -49,7 +49,7 @@ struct AttnParams {
     const uint16_t* O;
     const int8_t* O_lo;
     const float* lse_in;
-    const float *delta, *nlse;  // dO.O and -lse log2 e, rows of Tp
+    const float *ndelta, *nlse;  // -dO.O and -lse log2 e, rows of Tp
     int32_t Tp;                 // T rounded up to whole tiles
     uint16_t* out;         // O, or dQ
     int8_t* out_lo;
@@ -60,7 +60,7 @@ struct AttnParams {
 };
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st);
 lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st);
-cudaError_t launch_attn_delta(const AttnParams& p, float* delta, float* nlse, cudaStream_t st);
+cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st);
 lm_status launch_attn_bwd(const AttnParams& p, cudaStream_t st);
 
 // ---- addnorm

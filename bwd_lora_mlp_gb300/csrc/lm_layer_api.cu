@@ -223,7 +223,7 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     p.dV = dV;
     float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + P.delta);
     float* nlse = reinterpret_cast<float*>(static_cast<char*>(ws) + P.nlse);
-    p.delta = delta;
+    p.ndelta = delta;
     p.nlse = nlse;
     LL_TRY(attn_ranges(a, p, st));
     {
