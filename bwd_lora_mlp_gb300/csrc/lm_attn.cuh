@@ -124,13 +124,27 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // Shared-memory tile of 128 rows x dp dims: dp / 64 boxes of 128 rows x 128 bytes, 128-byte swizzle.
 constexpr uint32_t kBoxBytes = kTile * 128;
 
-// D = A B^T over the tiles' dims: both K-major, `steps` K steps of 16
+// The issuing warp's values are made warp-uniform in the compiler's eyes (a broadcast from lane 0) and
+// its descriptors are one 32-bit add each over constants: built anew per product from values the
+// compiler could not prove uniform, an issue took about 150 cycles against the product's own 64, and
+// every kernel here was bound by it.
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Low descriptor word of a tile: start address and leading offset in units of 16 bytes; the high word
+// holds the stride of 8-row groups (1024 bytes), the version and the 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return (addr >> 4) | (1u << 16); }                  // K-major
+__device__ __forceinline__ uint32_t desc_cols(uint32_t addr) { return (addr >> 4) | ((kBoxBytes >> 4) << 16); }    // MN-major
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+    constexpr uint64_t hi = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
+    return hi | lo;
+}
+// D = A B^T over the tiles' dims (both K-major), `steps` of at most DP / 16 K steps
+template <int DP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool leader) {
-    for (int kk = 0; kk < steps; ++kk) {
-        const uint32_t box = (uint32_t)(kk >> 2) * kBoxBytes;
-        const uint64_t off = (uint64_t)((kk & 3) * 2);
-        umma_bf16_if(d, make_sdesc_sw128(a + box, 16, 1024) + off, make_sdesc_sw128(b + box, 16, 1024) + off, idesc,
-                     kk ? 1u : 0u, leader);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t off = (uint32_t)(kk >> 2) * (kBoxBytes >> 4) + (uint32_t)(kk & 3) * 2;
+        if (kk < steps) umma_bf16_if(d, desc(a + off), desc(b + off), idesc, kk ? 1u : 0u, leader);
     }
 }
 

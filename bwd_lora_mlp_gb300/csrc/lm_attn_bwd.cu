@@ -20,8 +20,8 @@ constexpr int kQStages = 2;  // attn_dkv: query tiles, and dO tiles, in flight
 __device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, uint32_t idesc, bool first, bool leader) {
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts_if(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), make_sdesc_sw128(b, kBoxBytes, 1024) + (uint64_t)(kk * 128),
-                        idesc, first && kk == 0 ? 0u : 1u, leader);
+        umma_bf16_ts_if(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), desc(b + kk * 128), idesc, first && kk == 0 ? 0u : 1u,
+                        leader);
 }
 
 // rows of padding tokens hold anything: they are cleared where they would be a right operand (0 x NaN)
@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     griddep_wait();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t ts = tmem, tdp = tmem + kTile, tdv = tmem + 2 * kTile, tdk = tdv + DP;
     const TokRange rf = tok_range(p, k0), rl = tok_range(p, min(k0 + kTile, p.T) - 1);
-    const int qt0 = rf.qlo / kTile, nt = rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0;
+    const int qt0 = uni(rf.qlo / kTile), nt = uni(rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0);
     const int N = nt * n;  // (head of the group, query tile), heads outermost
 
     if (warp >= 8) {
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!mbar_wait_warp(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
                 clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
                 tc_fence_after();
-                mma_rows(ts, smem_u32(sk), smem_u32(sq + s * C::kTileBytes), ksteps, ids, leader);
+                mma_rows<DP>(ts, desc_rows(smem_u32(sk)), desc_rows(smem_u32(sq + s * C::kTileBytes)), ksteps, ids, leader);
                 umma_commit_if(smem_u32(sfull), leader);
                 return true;
             };
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!mbar_wait_warp(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
                 clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
                 tc_fence_after();
-                mma_rows(tdp, smem_u32(sv), smem_u32(so + s * C::kTileBytes), ksteps, ids, leader);
+                mma_rows<DP>(tdp, desc_rows(smem_u32(sv)), desc_rows(smem_u32(so + s * C::kTileBytes)), ksteps, ids, leader);
                 umma_commit_if(smem_u32(dpfull), leader);
                 return true;
             };
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                mma_weights(tdv, ts, smem_u32(so + s * C::kTileBytes), idd, it == 0, leader);
+                mma_weights(tdv, ts, desc_cols(smem_u32(so + s * C::kTileBytes)), idd, it == 0, leader);
                 umma_commit_if(smem_u32(&oempty[s]), leader);
                 if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
                     ok = false;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                mma_weights(tdk, tdp, smem_u32(sq + s * C::kTileBytes), idd, it == 0, leader);
+                mma_weights(tdk, tdp, desc_cols(smem_u32(sq + s * C::kTileBytes)), idd, it == 0, leader);
                 umma_commit_if(smem_u32(&qempty[s]), leader);
                 if (it + 1 < N && !dots(it + 1)) {
                     ok = false;
@@ -479,10 +479,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     griddep_wait();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t tdp = tmem + 2 * kTile, tdq = tmem + 3 * kTile;
     const TokRange rf = tok_range(p, q0), rl = tok_range(p, min(q0 + kTile, p.T) - 1);
-    const int kt0 = rf.lo / kTile, N = rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0;
+    const int kt0 = uni(rf.lo / kTile), N = uni(rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0);
 
     if (warp >= 8) {
         regs_down<kIssueRegs>();
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!mbar_wait_warp(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
                 clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1, lane);
                 tc_fence_after();
-                mma_rows(tmem + (j & 1) * kTile, smem_u32(sq), smem_u32(sk + s * C::kTileBytes), ksteps, ids, leader);
+                mma_rows<DP>(tmem + (j & 1) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps, ids, leader);
                 umma_commit_if(smem_u32(&sfull[j & 1]), leader);
                 return true;
             };
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const uint32_t s = (uint32_t)j % C::kVStages;
                 if (!mbar_wait_warp(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
                 tc_fence_after();
-                mma_rows(tdp, smem_u32(so), smem_u32(sv + s * C::kTileBytes), ksteps, ids, leader);
+                mma_rows<DP>(tdp, desc_rows(smem_u32(so)), desc_rows(smem_u32(sv + s * C::kTileBytes)), ksteps, ids, leader);
                 umma_commit_if(smem_u32(dpfull), leader);
                 umma_commit_if(smem_u32(&vempty[s]), leader);
                 return true;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 }
                 const uint32_t s = (uint32_t)j % C::kKStages;
-                mma_weights(tdq, tmem + (j & 1) * kTile, smem_u32(sk + s * C::kTileBytes), idd, j == 0, leader);
+                mma_weights(tdq, tmem + (j & 1) * kTile, desc_cols(smem_u32(sk + s * C::kTileBytes)), idd, j == 0, leader);
                 umma_commit_if(smem_u32(&kempty[s]), leader);
                 if (j + 2 < N && !scores(j + 2)) {
                     ok = false;

@@ -43,8 +43,9 @@ struct TileSpan {
 __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
     if (q0 >= p.T) return TileSpan{0, 0, 0, 0};
     const TokRange a = tok_range(p, q0), b = tok_range(p, min(q0 + kTile, p.T) - 1);
-    if (b.hi <= a.lo) return TileSpan{0, 0, 0, 0};
-    return TileSpan{a.lo / kTile, (b.hi + kTile - 1) / kTile, b.lo, a.hi};
+    const int lo = uni(a.lo), hi = uni(b.hi);
+    if (hi <= lo) return TileSpan{0, 0, 0, 0};
+    return TileSpan{lo / kTile, (hi + kTile - 1) / kTile, uni(b.lo), uni(a.hi)};
 }
 
 template <int DP, int MODE>
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     griddep_wait();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const TileSpan span[2] = {key_tiles(p, q0), key_tiles(p, q0 + kTile)};
     int J0 = span[0].j0, J1 = span[0].j1;
     if (span[1].j1 > span[1].j0) {
@@ -188,21 +189,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t a = ts + half * 32;
-                            const uint64_t b = make_sdesc_sw128(sv, kBoxBytes, 1024) + (uint64_t)(half * 512);
+                            const uint32_t b = desc_cols(sv) + half * 512;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ts_if(to, a + kk * 8, b + (uint64_t)(kk * 128), ido, (n || half || kk) ? 1u : 0u, leader);
+                                umma_bf16_ts_if(to, a + kk * 8, desc(b + kk * 128), ido, (n || half || kk) ? 1u : 0u, leader);
                             if (hides) {
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    umma_bf16_ts_if(to, a + 64 + kk * 8, b + (uint64_t)(kk * 128), ido, 1u, leader);
+                                    umma_bf16_ts_if(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u, leader);
                             }
                         }
                         if (!ok) break;
                         umma_commit_if(smem_u32(&odone[w]), leader);
                     }
                     if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
-                        mma_rows(ts, smem_u32(sq + w * C::kTileBytes), sk, ksteps, ids, leader);
+                        mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids, leader);
                         umma_commit_if(smem_u32(&sfull[w]), leader);
                     }
                 }
