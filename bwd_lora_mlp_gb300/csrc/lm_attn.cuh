@@ -65,15 +65,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is 128 rows (lanes) x 16 K values packed two to a column.
-__device__ __forceinline__ void umma_bf16_ts_if(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                uint32_t accumulate, bool issue) {
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// True in one lane of the warp.  The issuing role runs inside a branch on it: the compiler then knows
+// that one thread is active and takes descriptors to the uniform registers directly.  Eight products
+// of 64 cycles each are issued in 175 cycles this way, in 390 under `lane == 0` and in 470 to 620 with
+// the whole warp running the loop and a predicate on each (measured alone; the second and third were
+// slower than the tensor cores together with the role's waits, and bound every kernel here).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 // 32 columns of this thread's row into x[AT .. AT + 31].
 template <int AT, int N>
@@ -124,10 +133,7 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // Shared-memory tile of 128 rows x dp dims: dp / 64 boxes of 128 rows x 128 bytes, 128-byte swizzle.
 constexpr uint32_t kBoxBytes = kTile * 128;
 
-// The issuing warp's values are made warp-uniform in the compiler's eyes (a broadcast from lane 0) and
-// its descriptors are one 32-bit add each over constants: built anew per product from values the
-// compiler could not prove uniform, an issue took about 150 cycles against the product's own 64, and
-// every kernel here was bound by it.
+// A value that is the same in the whole warp, made so in the compiler's eyes too.
 __device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Low descriptor word of a tile: start address and leading offset in units of 16 bytes; the high word
@@ -140,11 +146,32 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
 }
 // D = A B^T over the tiles' dims (both K-major), `steps` of at most DP / 16 K steps
 template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool leader) {
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
         const uint32_t off = (uint32_t)(kk >> 2) * (kBoxBytes >> 4) + (uint32_t)(kk & 3) * 2;
-        if (kk < steps) umma_bf16_if(d, desc(a + off), desc(b + off), idesc, kk ? 1u : 0u, leader);
+        if (kk < steps) umma_bf16(d, desc(a + off), desc(b + off), idesc, kk ? 1u : 0u);
+    }
+}
+
+// rows of padding tokens hold anything: they are cleared where they would be a right operand (0 x NaN).
+// The issuing thread does it by itself, about 2 us for a whole tile; at most the two tiles at the ends of
+// the tokens inside any document have such rows.
+__device__ __forceinline__ void clear_padding(uint8_t* tile, int boxes, int t0, int in0, int in1) {
+    if (t0 >= in0 && t0 + kTile <= in1) return;
+    for (int r = 0; r < kTile; ++r)
+        if (t0 + r < in0 || t0 + r >= in1)
+            for (int b = 0; b < boxes; ++b)
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(tile + b * kBoxBytes + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+}
+__device__ __forceinline__ void inside_tokens(const AttnParams& p, int& in0, int& in1) {
+    in0 = 0;
+    in1 = p.T;
+    if (p.cu_docs) {
+        in0 = max(0, p.cu_docs[0]);
+        in1 = min(p.T, p.cu_docs[p.n_docs]);
     }
 }
 

@@ -17,31 +17,10 @@ namespace lm {
 constexpr int kQStages = 2;  // attn_dkv: query tiles, and dO tiles, in flight
 
 // A = P or dz in tensor memory: columns [0, 64) of the tile packed at t, [64, 128) at t + 64
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, uint32_t idesc, bool first, bool leader) {
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, uint32_t idesc, bool first) {
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts_if(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), desc(b + kk * 128), idesc, first && kk == 0 ? 0u : 1u,
-                        leader);
-}
-
-// rows of padding tokens hold anything: they are cleared where they would be a right operand (0 x NaN)
-__device__ __forceinline__ void clear_padding(uint8_t* tile, int boxes, int t0, int in0, int in1, int lane) {
-    if (t0 >= in0 && t0 + kTile <= in1) return;
-    for (int r = lane; r < kTile; r += 32)
-        if (t0 + r < in0 || t0 + r >= in1)
-            for (int b = 0; b < boxes; ++b)
-                for (int c = 0; c < 8; ++c)
-                    *reinterpret_cast<uint4*>(tile + b * kBoxBytes + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    __syncwarp();
-}
-__device__ __forceinline__ void inside_tokens(const AttnParams& p, int& in0, int& in1) {
-    in0 = 0;
-    in1 = p.T;
-    if (p.cu_docs) {
-        in0 = max(0, p.cu_docs[0]);
-        in1 = min(p.T, p.cu_docs[p.n_docs]);
-    }
+        umma_bf16_ts(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), desc(b + kk * 128), idesc, first && kk == 0 ? 0u : 1u);
 }
 
 struct ScoreMath {
@@ -235,66 +214,64 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 in = drain_fills(smem_u32(&ofull[0]), kQStages, no, p.wait_ns) && in;
                 if (!in) attn_error(p, 6, 5);
             }
-        } else if (warp == 8) {  // ---------------- tensor cores
-            const bool leader = lane == 0;
+        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // Q and dO are [query][dim]: MN-major
             int in0, in1;
             inside_tokens(p, in0, in1);
-            bool ok = N <= 0 || mbar_wait_warp(smem_u32(kvfull), 0, s_abort, p.wait_ns);
+            bool ok = N <= 0 || mbar_wait(smem_u32(kvfull), 0, s_abort, p.wait_ns);
             auto scores = [&](int it) {  // S^T(it) = K Q^T
                 const uint32_t s = (uint32_t)it % kQStages;
-                if (!mbar_wait_warp(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+                if (!mbar_wait(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1);
                 tc_fence_after();
-                mma_rows<DP>(ts, desc_rows(smem_u32(sk)), desc_rows(smem_u32(sq + s * C::kTileBytes)), ksteps, ids, leader);
-                umma_commit_if(smem_u32(sfull), leader);
+                mma_rows<DP>(ts, desc_rows(smem_u32(sk)), desc_rows(smem_u32(sq + s * C::kTileBytes)), ksteps, ids);
+                umma_commit(smem_u32(sfull));
                 return true;
             };
             auto dots = [&](int it) {  // dP^T(it) = V dO^T
                 const uint32_t s = (uint32_t)it % kQStages;
-                if (!mbar_wait_warp(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1, lane);
+                if (!mbar_wait(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1);
                 tc_fence_after();
-                mma_rows<DP>(tdp, desc_rows(smem_u32(sv)), desc_rows(smem_u32(so + s * C::kTileBytes)), ksteps, ids, leader);
-                umma_commit_if(smem_u32(dpfull), leader);
+                mma_rows<DP>(tdp, desc_rows(smem_u32(sv)), desc_rows(smem_u32(so + s * C::kTileBytes)), ksteps, ids);
+                umma_commit(smem_u32(dpfull));
                 return true;
             };
             if (ok && N > 0) ok = scores(0) && dots(0);
             for (int it = 0; ok && it < N; ++it) {
                 const uint32_t s = (uint32_t)it % kQStages;
-                if (!mbar_wait_warp(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                if (!mbar_wait(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                mma_weights(tdv, ts, desc_cols(smem_u32(so + s * C::kTileBytes)), idd, it == 0, leader);
-                umma_commit_if(smem_u32(&oempty[s]), leader);
+                mma_weights(tdv, ts, desc_cols(smem_u32(so + s * C::kTileBytes)), idd, it == 0);
+                umma_commit(smem_u32(&oempty[s]));
                 if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
                     ok = false;
                     break;
                 }
-                if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                if (!mbar_wait(smem_u32(dsfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                mma_weights(tdk, tdp, desc_cols(smem_u32(sq + s * C::kTileBytes)), idd, it == 0, leader);
-                umma_commit_if(smem_u32(&qempty[s]), leader);
+                mma_weights(tdk, tdp, desc_cols(smem_u32(sq + s * C::kTileBytes)), idd, it == 0);
+                umma_commit(smem_u32(&qempty[s]));
                 if (it + 1 < N && !dots(it + 1)) {
                     ok = false;
                     break;
                 }
             }
-            if (!ok && leader) {
+            if (!ok) {
                 attn_error(p, 6, 2);
                 *s_abort = 1;
             }
-            umma_commit_if(smem_u32(drain), leader);
+            umma_commit(smem_u32(drain));
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-            __syncwarp();
         }
     } else {  // ---------------- arithmetic: one key row, 64 query columns per thread
         regs_up<kMathRegs>();
@@ -521,35 +498,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
                 if (!in) attn_error(p, 7, 5);
             }
-        } else if (warp == 8) {  // ---------------- tensor cores
-            const bool leader = lane == 0;
+        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
             int in0, in1;
             inside_tokens(p, in0, in1);
-            bool ok = N <= 0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+            bool ok = N <= 0 || mbar_wait(smem_u32(qfull), 0, s_abort, p.wait_ns);
             auto scores = [&](int j) {  // S(j) = Q K^T, in half j & 1
                 const uint32_t s = (uint32_t)j % C::kKStages;
-                if (!mbar_wait_warp(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1, lane);
+                if (!mbar_wait(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
+                clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1);
                 tc_fence_after();
-                mma_rows<DP>(tmem + (j & 1) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps, ids, leader);
-                umma_commit_if(smem_u32(&sfull[j & 1]), leader);
+                mma_rows<DP>(tmem + (j & 1) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps, ids);
+                umma_commit(smem_u32(&sfull[j & 1]));
                 return true;
             };
             auto dots = [&](int j) {  // dP(j) = dO V^T
                 const uint32_t s = (uint32_t)j % C::kVStages;
-                if (!mbar_wait_warp(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
+                if (!mbar_wait(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
                 tc_fence_after();
-                mma_rows<DP>(tdp, desc_rows(smem_u32(so)), desc_rows(smem_u32(sv + s * C::kTileBytes)), ksteps, ids, leader);
-                umma_commit_if(smem_u32(dpfull), leader);
-                umma_commit_if(smem_u32(&vempty[s]), leader);
+                mma_rows<DP>(tdp, desc_rows(smem_u32(so)), desc_rows(smem_u32(sv + s * C::kTileBytes)), ksteps, ids);
+                umma_commit(smem_u32(dpfull));
+                umma_commit(smem_u32(&vempty[s]));
                 return true;
             };
             if (ok && N > 0) ok = scores(0) && dots(0) && (N < 2 || scores(1));
             for (int j = 0; ok && j < N; ++j) {
-                if (!mbar_wait_warp(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
+                if (!mbar_wait(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
                     ok = false;
                     break;
                 }
@@ -559,21 +535,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     break;
                 }
                 const uint32_t s = (uint32_t)j % C::kKStages;
-                mma_weights(tdq, tmem + (j & 1) * kTile, desc_cols(smem_u32(sk + s * C::kTileBytes)), idd, j == 0, leader);
-                umma_commit_if(smem_u32(&kempty[s]), leader);
+                mma_weights(tdq, tmem + (j & 1) * kTile, desc_cols(smem_u32(sk + s * C::kTileBytes)), idd, j == 0);
+                umma_commit(smem_u32(&kempty[s]));
                 if (j + 2 < N && !scores(j + 2)) {
                     ok = false;
                     break;
                 }
             }
-            if (!ok && leader) {
+            if (!ok) {
                 attn_error(p, 7, 2);
                 *s_abort = 1;
             }
-            umma_commit_if(smem_u32(drain), leader);
+            umma_commit(smem_u32(drain));
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-            __syncwarp();
         }
     } else {  // ---------------- arithmetic: one query row, 64 key columns per thread
         regs_up<kMathRegs>();

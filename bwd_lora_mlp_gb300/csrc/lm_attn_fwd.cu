@@ -141,39 +141,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
                 if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
             }
-        } else if (warp == 8) {  // ---------------- tensor cores: the whole warp, lane 0 issues
-            const bool leader = lane == 0;
+        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
-            // keys of no document hold anything: their rows of V are cleared, 0 x NaN would reach every O
-            int in0 = 0, in1 = p.T;
-            if (p.cu_docs) {
-                in0 = max(0, p.cu_docs[0]);
-                in1 = min(p.T, p.cu_docs[p.n_docs]);
-            }
-            bool ok = J1 <= J0 || mbar_wait_warp(smem_u32(qfull), 0, s_abort, p.wait_ns);
+            int in0, in1;
+            inside_tokens(p, in0, in1);
+            bool ok = J1 <= J0 || mbar_wait(smem_u32(qfull), 0, s_abort, p.wait_ns);
             for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
                 const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
                 const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
                 const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
                 if (j > J0) {
-                    ok = mbar_wait_warp(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+                    ok = mbar_wait(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
                     if (!ok) break;
-                    const int k0 = (j - 1) * kTile;
-                    if (k0 < in0 || k0 + kTile > in1) {
-                        for (int r = lane; r < kTile; r += 32)
-                            if (k0 + r < in0 || k0 + r >= in1)
-                                for (int b = 0; b < DP / 64; ++b)
-                                    for (int c = 0; c < 8; ++c)
-                                        *reinterpret_cast<uint4*>(ring + (nv % C::kSlots) * C::kTileBytes + b * kBoxBytes +
-                                                                  r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
+                    clear_padding(ring + (nv % C::kSlots) * C::kTileBytes, DP / 64, (j - 1) * kTile, in0, in1);
                 }
                 if (j < J1) {
-                    ok = mbar_wait_warp(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
+                    ok = mbar_wait(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
                     if (!ok) break;
                 }
                 tc_fence_after();
@@ -185,40 +170,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         const bool hides = span[w].hides(j - 1);
 #pragma unroll
                         for (int half = 0; half < 2 && ok; ++half) {
-                            ok = mbar_wait_warp(smem_u32(&pfull[2 * w + half]), n & 1u, s_abort, p.wait_ns);
+                            ok = mbar_wait(smem_u32(&pfull[2 * w + half]), n & 1u, s_abort, p.wait_ns);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t a = ts + half * 32;
                             const uint32_t b = desc_cols(sv) + half * 512;
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ts_if(to, a + kk * 8, desc(b + kk * 128), ido, (n || half || kk) ? 1u : 0u, leader);
+                                umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, (n || half || kk) ? 1u : 0u);
                             if (hides) {
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    umma_bf16_ts_if(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u, leader);
+                                    umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
                             }
                         }
                         if (!ok) break;
-                        umma_commit_if(smem_u32(&odone[w]), leader);
+                        umma_commit(smem_u32(&odone[w]));
                     }
                     if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
-                        mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids, leader);
-                        umma_commit_if(smem_u32(&sfull[w]), leader);
+                        mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids);
+                        umma_commit(smem_u32(&sfull[w]));
                     }
                 }
                 if (!ok) break;
-                if (j > J0) umma_commit_if(smem_u32(&empty[nv % C::kSlots]), leader);
-                if (j < J1) umma_commit_if(smem_u32(&empty[nk % C::kSlots]), leader);
+                if (j > J0) umma_commit(smem_u32(&empty[nv % C::kSlots]));
+                if (j < J1) umma_commit(smem_u32(&empty[nk % C::kSlots]));
             }
-            if (!ok && leader) {
+            if (!ok) {
                 attn_error(p, 5, 2);
                 *s_abort = 1;
             }
-            umma_commit_if(smem_u32(drain), leader);
+            umma_commit(smem_u32(drain));
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
-            __syncwarp();
         }
     } else {  // ---------------- softmax: warpgroup w, one thread per query row
         regs_up<kMathRegs>();
