@@ -188,6 +188,9 @@ __device__ __forceinline__ float rcp(float x) {
 }
 // tanh x = 1 - 2 / (1 + e^{2x}), given 2 log2(e) x: absolute error a few 2^-24, exact at both ends
 __device__ __forceinline__ float tanh_from_2log2e(float x) { return fmaf(-2.f, rcp(1.f + ex2(x)), 1.f); }
+// Bit e set: column e of a chunk of 32 is in [a, z).
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ uint32_t bits_between(int a, int z) { return bits_below(z) & ~bits_below(a); }
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 
 // Register budgets of a CTA's warpgroups: what the loader's and the MMA warp's do not need goes to the

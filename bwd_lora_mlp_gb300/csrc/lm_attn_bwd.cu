@@ -292,24 +292,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_ld_f32<32>(tsw + 32, x);
             tmem_ld_wait_f32<0>(x);
             tmem_ld_wait_f32<32>(x);
+            uint32_t bits[2] = {~0u, ~0u};
+            if (HIDDEN) {
+                bits[0] = bits_between(a, z);
+                bits[1] = bits_between(a - 32, z - 32);
+            }
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const float4 nl = *reinterpret_cast<const float4*>(row + e);
-                const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+            for (int b = 0; b < 2; ++b) {
+                // (a chunk that none of the warp's keys is seen from has no exponentials)
+                if (HIDDEN && !__any_sync(0xffffffffu, bits[b] != 0u)) {
 #pragma unroll
-                for (int f = 0; f < 4; f += 2) {
-                    float2 bend = two(1.f);
-                    const float2 y = exponents<MODE, 1>(S, make_float2(x[e + f], x[e + f + 1]), dist + (float)(e + f),
-                                                     make_float2(nls[f], nls[f + 1]), bend);
-                    float2 P = make_float2(ex2(y.x), ex2(y.y));
-                    if (HIDDEN) {
-                        if (e + f < a || e + f >= z) P.x = 0.f;
-                        if (e + f + 1 < a || e + f + 1 >= z) P.y = 0.f;
+                    for (int e = 0; e < 32; ++e) x[b * 32 + e] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = 0u;
+                    continue;
+                }
+#pragma unroll
+                for (int e = b * 32; e < b * 32 + 32; e += 4) {
+                    const float4 nl = *reinterpret_cast<const float4*>(row + e);
+                    const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+                    for (int f = 0; f < 4; f += 2) {
+                        float2 bend = two(1.f);
+                        const float2 y = exponents<MODE, 1>(S, make_float2(x[e + f], x[e + f + 1]), dist + (float)(e + f),
+                                                            make_float2(nls[f], nls[f + 1]), bend);
+                        float2 P = make_float2(ex2(y.x), ex2(y.y));
+                        if (HIDDEN) {
+                            if (!(bits[b] >> ((e + f) & 31) & 1u)) P.x = 0.f;
+                            if (!(bits[b] >> ((e + f + 1) & 31) & 1u)) P.y = 0.f;
+                        }
+                        pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
+                        if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                        x[e + f] = P.x;
+                        x[e + f + 1] = P.y;
                     }
-                    pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
-                    if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
-                    x[e + f] = P.x;
-                    x[e + f + 1] = P.y;
                 }
             }
             tmem_st_x32(tsw, pk);
@@ -325,18 +341,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_ld_wait_f32<0>(y);
             tmem_ld_wait_f32<32>(y);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const float4 dl = *reinterpret_cast<const float4*>(row + kTile + e);
-                const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
+            for (int b = 0; b < 2; ++b) {
+                if (HIDDEN && !__any_sync(0xffffffffu, bits[b] != 0u)) continue;  // (pk is zero there)
 #pragma unroll
-                for (int f = 0; f < 4; f += 2) {
-                    float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
-                    d = __fmul2_rn(d, make_float2(x[e + f], x[e + f + 1]));
-                    if (HIDDEN) {
-                        if (e + f < a || e + f >= z) d.x = 0.f;
-                        if (e + f + 1 < a || e + f + 1 >= z) d.y = 0.f;
+                for (int e = b * 32; e < b * 32 + 32; e += 4) {
+                    const float4 dl = *reinterpret_cast<const float4*>(row + kTile + e);
+                    const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+                    for (int f = 0; f < 4; f += 2) {
+                        float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
+                        d = __fmul2_rn(d, make_float2(x[e + f], x[e + f + 1]));
+                        if (HIDDEN) {  // (not 0 x what a padding key's dP holds)
+                            if (!(bits[b] >> ((e + f) & 31) & 1u)) d.x = 0.f;
+                            if (!(bits[b] >> ((e + f + 1) & 31) & 1u)) d.y = 0.f;
+                        }
+                        pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
                     }
-                    pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
                 }
             }
             tmem_st_x32(tdpw, pk);
@@ -572,14 +592,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_ld_f32<32>(tsw + 32, x);
             tmem_ld_wait_f32<0>(x);
             tmem_ld_wait_f32<32>(x);
+            uint32_t bits[2] = {~0u, ~0u};
+            bool some[2] = {true, true};
+            if (HIDDEN) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                float2 bend = two(1.f);
-                const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(nlse), bend);
-                float2 P = make_float2(ex2(v.x), ex2(v.y));
-                if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
-                x[e] = P.x;
-                x[e + 1] = P.y;
+                for (int b = 0; b < 2; ++b) {
+                    bits[b] = bits_between(a - 32 * b, z - 32 * b);
+                    some[b] = __any_sync(0xffffffffu, bits[b] != 0u);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (HIDDEN && !some[b]) continue;
+#pragma unroll
+                for (int e = b * 32; e < b * 32 + 32; e += 2) {
+                    float2 bend = two(1.f);
+                    const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(nlse), bend);
+                    float2 P = make_float2(ex2(v.x), ex2(v.y));
+                    if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                    x[e] = P.x;
+                    x[e + 1] = P.y;
+                }
             }
             if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) return false;
             tc_fence_after();
@@ -589,14 +622,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             tmem_ld_wait_f32<32>(y);
             uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(ndelta));
-                d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
-                if (HIDDEN) {
-                    if (e < a || e >= z) d.x = 0.f;
-                    if (e + 1 < a || e + 1 >= z) d.y = 0.f;
+            for (int b = 0; b < 2; ++b) {
+                if (HIDDEN && !some[b]) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = 0u;
+                    continue;
                 }
-                pk[e / 2] = pack_bf16x2(d.x, d.y);
+#pragma unroll
+                for (int e = b * 32; e < b * 32 + 32; e += 2) {
+                    float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(ndelta));
+                    d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
+                    if (HIDDEN) {
+                        if (!(bits[b] >> (e & 31) & 1u)) d.x = 0.f;
+                        if (!(bits[b] >> ((e + 1) & 31) & 1u)) d.y = 0.f;
+                    }
+                    pk[e / 2] = pack_bf16x2(d.x, d.y);
+                }
             }
             tmem_st_x32(tsw, pk);
             tmem_st_wait();

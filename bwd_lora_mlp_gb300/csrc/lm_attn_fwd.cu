@@ -242,11 +242,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     x[e] = fmaf(-slope, fabsf(dist - (float)e), v);
                 }
             }
+            // on a tile with hidden keys most chunks of 32 keys are seen in full, or not at all, by all rows of
+            // the warp: only the others are masked key by key, and chunks that nobody sees have no exponentials
+            uint32_t some = 15u;
             if (HIDDEN) {
-                const int a = r.lo - k0, z = r.hi - k0;
 #pragma unroll
-                for (int e = 0; e < kTile; ++e)
-                    if (e < a || e >= z) x[e] = -INFINITY;
+                for (int b = 0; b < 4; ++b) {
+                    const uint32_t bits = bits_between(r.lo - k0 - 32 * b, r.hi - k0 - 32 * b);
+                    if (__all_sync(0xffffffffu, bits == ~0u)) continue;
+                    if (!__any_sync(0xffffffffu, bits != 0u)) some &= ~(1u << b);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(bits >> e & 1u)) x[b * 32 + e] = -INFINITY;
+                }
             }
             float mx[4];
 #pragma unroll
@@ -283,14 +291,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int half = 0; half < 2; ++half) {  // 64 keys at a time: their product may begin
                 uint32_t pk[32], rest[32];
 #pragma unroll
-                for (int e = 0; e < 64; e += 2) {
-                    const int at = half * 64 + e;
-                    const float2 y = __ffma2_rn(make_float2(x[at], x[at + 1]), c2, mu);
-                    const float2 q = make_float2(ex2(y.x), ex2(y.y));
-                    s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
-                    const uint32_t hi = pack_bf16x2(q.x, q.y);
-                    pk[e >> 1] = hi;
-                    if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
+                for (int b = 0; b < 2; ++b) {
+                    if (HIDDEN && !(some >> (2 * half + b) & 1u)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[b * 16 + e] = rest[b * 16 + e] = 0u;
+                        continue;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const int at = half * 64 + b * 32 + e;
+                        const float2 y = __ffma2_rn(make_float2(x[at], x[at + 1]), c2, mu);
+                        const float2 q = make_float2(ex2(y.x), ex2(y.y));
+                        s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
+                        const uint32_t hi = pack_bf16x2(q.x, q.y);
+                        pk[b * 16 + (e >> 1)] = hi;
+                        if (HIDDEN) rest[b * 16 + (e >> 1)] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
+                    }
                 }
                 tmem_st_x32(ts + half * 32, pk);
                 if (HIDDEN) tmem_st_x32(ts + 64 + half * 32, rest);
