@@ -207,24 +207,51 @@ __device__ __forceinline__ void regs_down() {
 constexpr int kMathRegs = 208, kIssueRegs = 88;
 static_assert(2 * kMathRegs + kIssueRegs <= 3 * 168, "a register split above the launch's total waits forever");
 
-// This thread's accumulator row, d columns from t on, times f, to bf16 (every lane of the warp comes
-// here; `any` false: the accumulator was never written and the row is zero; `mine`: the row exists).
-__device__ __forceinline__ void store_rows(uint16_t* dst, uint32_t t, int d, float f, bool any, bool mine) {
-#pragma unroll 1
-    for (int c = 0; c < d; c += 16) {
-        uint32_t o[16];
-        if (any) {
-            tmem_ld_x16(t + c, o);
-            tmem_ld_wait16(o);
-        }
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+// Whether every warp of the warpgroup (barrier `id`) came through: a warp that gave up a wait sets the
+// group's flag, and either all of the group go on to the epilogue's barriers or none does.
+__device__ __forceinline__ bool group_ok(bool ok, volatile int* bad, int id) {
+    if (!ok) *bad = 1;
+    group_sync(id);
+    return *bad == 0;
+}
+// Eight packed pairs (16 dims, the c-th of a box's four) of row r to a staged box: 128-byte swizzle.
+__device__ __forceinline__ void stage_pairs(uint8_t* box, int r, int c, const uint32_t (&v)[8]) {
+    uint8_t* row = box + r * 128;
+    *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+}
+// The staged box of 128 tokens x 64 dims to (dim x, head y, token z): all 128 threads of the warpgroup
+// come here after their writes, barrier `id` is theirs; rows past the tensor's end are not written.
+// Rows leave as 128-byte lines (a thread storing its own row would touch a line per lane and chunk: the
+// forward's epilogue took 5000 cycles of a CTA that way).
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const uint8_t* box, int x, int y, int z, int id, bool first) {
+    fence_proxy_async_smem();
+    group_sync(id);
+    if (first) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(smem_u32(box)), "r"(x), "r"(y), "r"(z)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+}
+// 64 dims of this thread's accumulator row (lane r of the warpgroup's 128), times f, to a staged box as
+// bf16.  `any` false: the accumulator was never written and the row is zero (uniform over the warp).
+__device__ __forceinline__ void stage_row(uint8_t* box, int r, uint32_t t, float f, bool any) {
+    float x[64];
+    if (any) {
+        tmem_ld_f32<0>(t, x);
+        tmem_ld_f32<32>(t + 32, x);
+        tmem_ld_wait_f32<0>(x);
+        tmem_ld_wait_f32<32>(x);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
         uint32_t v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
-        if (mine) {  // d is a multiple of 8: the last chunk may be half a chunk
-            *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
-            if (c + 8 < d) *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-        }
+        for (int e = 0; e < 8; ++e) v[e] = any ? pack_bf16x2(x[c * 16 + 2 * e] * f, x[c * 16 + 2 * e + 1] * f) : 0u;
+        stage_pairs(box, r, c, v);
     }
 }
 

@@ -50,7 +50,7 @@ __device__ __forceinline__ float2 exponents(const ScoreMath& S, float2 qk, float
 }
 
 struct BwdMaps {
-    CUtensorMap q, k, v, dO;
+    CUtensorMap q, k, v, dO, dQ, dK, dV;
 };
 
 // ------------------------------------------------------------------ delta, and lse in the exponent's units
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
                 const int64_t at = row * p.d + sub * 8;
                 const uint4 b = *reinterpret_cast<const uint4*>(p.O + at);
                 uint2 lo = make_uint2(0, 0);
-                if (p.O_lo) lo = *reinterpret_cast<const uint2*>(p.O_lo + at);
+                if (p.O_lo) lo = *reinterpret_cast<const uint2*>(p.O_lo + row * p.d16 + sub * 8);
                 const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* drain = dsfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
     uint8_t* sk = smem + 1024;
     uint8_t* sv = sk + C::kTileBytes;
     uint8_t* sq = sv + C::kTileBytes;
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(smem_u32(dpfull), 1);
         mbar_init(smem_u32(dsfull), 8);
         mbar_init(smem_u32(drain), 1);
-        *s_abort = 0;
+        *s_abort = s_bad[0] = s_bad[1] = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -390,14 +391,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // warpgroup 0 writes dV, warpgroup 1 dK
         if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
         tc_fence_after();
-        if (!ok) {
-            if (lane == 0) {
-                attn_error(p, 6, 3);
-                *s_abort = 1;
-            }
+        if (!ok && lane == 0) {
+            attn_error(p, 6, 3);
+            *s_abort = 1;
+        }
+        if (!group_ok(ok, s_bad + half, 1 + half)) {
+            // (nothing is written)
         } else {
-            store_rows((half ? p.dK : p.dV) + ((int64_t)k * p.hk + g) * p.d, (half ? tdk : tdv) + lanes, p.d,
-                       half ? p.scale : 1.f, N > 0, k < p.T);
+            const int r128 = (warp & 3) * 32 + lane;
+            for (int b = 0; b < DP / 64; ++b) {  // (staged where the query tiles were)
+                uint8_t* box = sq + half * C::kTileBytes + b * kBoxBytes;
+                stage_row(box, r128, (half ? tdk : tdv) + lanes + b * 64, half ? p.scale : 1.f, N > 0);
+                store_box(half ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + half, r128 == 0);
+            }
         }
         tc_fence_before();
     }
@@ -434,6 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* drain = dsfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
     uint8_t* sq = smem + 1024;
     uint8_t* so = sq + C::kTileBytes;
     uint8_t* sk = so + C::kTileBytes;
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(smem_u32(dpfull), 1);
         mbar_init(smem_u32(dsfull), 8);
         mbar_init(smem_u32(drain), 1);
-        *s_abort = 0;
+        *s_abort = s_bad[0] = s_bad[1] = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -662,13 +669,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
         tc_fence_after();
-        if (!ok) {
-            if (lane == 0) {
-                attn_error(p, 7, 3);
-                *s_abort = 1;
-            }
-        } else if (half == 0) {
-            store_rows(p.out + ((int64_t)i * p.hq + h) * p.d, tdq + lanes, p.d, p.scale, N > 0, i < p.T);
+        if (!ok && lane == 0) {
+            attn_error(p, 7, 3);
+            *s_abort = 1;
+        }
+        if (!group_ok(ok, s_bad + half, 1 + half)) {
+            // (nothing is written)
+        } else if (half < DP / 64) {  // each warpgroup 64 dims, staged where the queries were
+            const int r128 = (warp & 3) * 32 + lane;
+            uint8_t* box = sq + half * kBoxBytes;
+            stage_row(box, r128, tdq + lanes + half * 64, p.scale, N > 0);
+            store_box(&maps.dQ, box, half * 64, h, q0, 1 + half, r128 == 0);
         }
         tc_fence_before();
     }
@@ -716,6 +727,9 @@ lm_status launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.dO, dO, p.T, p.hq, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.dQ, lm_heads{p.out, (int64_t)p.hq * p.d, p.d}, p.T, p.hq, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.dK, lm_heads{p.dK, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.dV, lm_heads{p.dV, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
     if (s != LM_OK) return s;
     const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes ? ATTN_BIAS : ATTN_PLAIN;
     cudaError_t e;

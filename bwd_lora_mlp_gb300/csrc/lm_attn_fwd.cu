@@ -31,7 +31,7 @@ struct FwdCfg {
 };
 
 struct FwdMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 // the key tiles [j0, j1) that the query rows [q0, q0 + 128) may see
@@ -57,12 +57,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + C::kSlots;
     uint64_t* qfull = empty + C::kSlots;
-    uint64_t* sfull = qfull + 1;   // [2] scores ready
+    uint64_t* sfull = qfull + 2;   // [2] scores ready
     uint64_t* pfull = sfull + 2;   // [2][2] weights of the first, of the last 64 keys written (and the scores read)
-    uint64_t* odone = pfull + 4;   // [2] one more P V product done
+    uint64_t* hdone = pfull + 4;   // [2] the first half of a P V product done (once a tile)
+    uint64_t* odone = hdone + 2;   // [2] the last product of the row tile done (once)
     uint64_t* drain = odone + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
     uint8_t* sq = smem + 1024;
     uint8_t* ring = sq + 2 * C::kTileBytes;
 
@@ -78,19 +80,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        mbar_init(smem_u32(qfull), 1);
         for (int w = 0; w < 2; ++w) {
+            mbar_init(smem_u32(&qfull[w]), 1);
             mbar_init(smem_u32(&sfull[w]), 1);
             mbar_init(smem_u32(&pfull[2 * w]), 4);
             mbar_init(smem_u32(&pfull[2 * w + 1]), 4);
+            mbar_init(smem_u32(&hdone[w]), 1);
             mbar_init(smem_u32(&odone[w]), 1);
         }
         mbar_init(smem_u32(drain), 1);
-        *s_abort = 0;
+        *s_abort = s_bad[0] = s_bad[1] = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
         tma_prefetch_map(&maps.v);
+        tma_prefetch_map(&maps.o);
     }
     __syncwarp();
     if (warp == 8) {
@@ -114,11 +118,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (warp == 9) {  // ---------------- loader
             if (lane == 0 && J1 > J0) {
                 bool ok = true;
-                mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
-                for (int w = 0; w < 2; ++w)
+                auto query = [&](int w) {
+                    mbar_expect_tx(smem_u32(&qfull[w]), C::kTileBytes);
                     for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h,
+                        tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(&qfull[w]), b * 64, h,
                                     q0 + w * kTile);
+                };
+                query(0);  // then K: the first scores wait for these alone
                 uint32_t n = 0;
                 for (int j = J0; ok && j < J1; ++j)
                     for (int kv = 0; kv < 2; ++kv, ++n) {
@@ -131,6 +137,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         for (int b = 0; b < DP / 64; ++b)
                             tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
                                         smem_u32(&full[s]), b * 64, g, j * kTile);
+                        if (n == 0) query(1);
                     }
                 if (!ok) {
                     attn_error(p, 5, 1);
@@ -138,7 +145,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 // nothing may land in shared memory after the CTA has gone
                 volatile int never = 0;
-                const bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
+                bool in = mbar_wait(smem_u32(&qfull[0]), 0, &never, p.wait_ns);
+                if (n > 0) in = mbar_wait(smem_u32(&qfull[1]), 0, &never, p.wait_ns) && in;
                 if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
             }
         } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
             int in0, in1;
             inside_tokens(p, in0, in1);
-            bool ok = J1 <= J0 || mbar_wait(smem_u32(qfull), 0, s_abort, p.wait_ns);
+            bool ok = true;
             for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
                 const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
                 const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
@@ -183,11 +191,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 for (int kk = 0; kk < 4; ++kk)
                                     umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
                             }
+                            if (half == 0) umma_commit(smem_u32(&hdone[w]));
+                            else if (j == span[w].j1) umma_commit(smem_u32(&odone[w]));
                         }
                         if (!ok) break;
-                        umma_commit(smem_u32(&odone[w]));
                     }
                     if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
+                        if (j == span[w].j0) {
+                            ok = mbar_wait(smem_u32(&qfull[w]), 0, s_abort, p.wait_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
                         mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids);
                         umma_commit(smem_u32(&sfull[w]));
                     }
@@ -220,23 +234,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const float cx = MODE == ATTN_PLAIN ? c : 1.f;
         float m = -INFINITY, l = 0.f;  // running maximum, sum of weights
         bool ok = true;
-        // one key tile; tiles with hidden keys have code of their own
-        auto tile = [&](int j, auto hides) {
+        // 64 keys, one step of the running softmax; tiles with hidden keys have code of their own
+        auto step = [&](int j, int half, float(&x)[64], auto hides) {
             constexpr bool HIDDEN = decltype(hides)::value;
-            float x[kTile];
-            tmem_ld_f32<0>(ts, x);
-            tmem_ld_f32<32>(ts + 32, x);
-            tmem_ld_f32<64>(ts + 64, x);
-            tmem_ld_f32<96>(ts + 96, x);
-            tmem_ld_wait_f32<0>(x);
-            tmem_ld_wait_f32<32>(x);
-            tmem_ld_wait_f32<64>(x);
-            tmem_ld_wait_f32<96>(x);
-            const int k0 = j * kTile;
+            const int k0 = j * kTile + half * 64;
             if (MODE != ATTN_PLAIN) {
                 const float dist = (float)(i - k0);
 #pragma unroll
-                for (int e = 0; e < kTile; ++e) {
+                for (int e = 0; e < 64; ++e) {
                     float v = x[e] * c;
                     if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
                     x[e] = fmaf(-slope, fabsf(dist - (float)e), v);
@@ -244,13 +249,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             // on a tile with hidden keys most chunks of 32 keys are seen in full, or not at all, by all rows of
             // the warp: only the others are masked key by key, and chunks that nobody sees have no exponentials
-            uint32_t some = 15u;
+            bool some[2] = {true, true};
             if (HIDDEN) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < 2; ++b) {
                     const uint32_t bits = bits_between(r.lo - k0 - 32 * b, r.hi - k0 - 32 * b);
                     if (__all_sync(0xffffffffu, bits == ~0u)) continue;
-                    if (!__any_sync(0xffffffffu, bits != 0u)) some &= ~(1u << b);
+                    some[b] = __any_sync(0xffffffffu, bits != 0u);
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!(bits >> e & 1u)) x[b * 32 + e] = -INFINITY;
@@ -259,17 +264,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             float mx[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                mx[b] = x[b * 32];
+                mx[b] = x[b * 16];
 #pragma unroll
-                for (int e = 1; e < 31; e += 2) mx[b] = fmaxf(fmaxf(mx[b], x[b * 32 + e]), x[b * 32 + e + 1]);
-                mx[b] = fmaxf(mx[b], x[b * 32 + 31]);
+                for (int e = 1; e < 15; e += 2) mx[b] = fmaxf(fmaxf(mx[b], x[b * 16 + e]), x[b * 16 + e + 1]);
+                mx[b] = fmaxf(mx[b], x[b * 16 + 15]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cx;
             const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
-                if (j > j0) {
-                    if (!mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j - 1 - j0) & 1u, s_abort, p.wait_ns)) return false;
+                if (j > j0 || half) {
+                    // what was multiplied before this half is in O: earlier tiles since these scores are (products
+                    // end in the order they are issued), and the tile's first half once it says so
+                    if (half && !mbar_wait_warp(smem_u32(&hdone[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns)) return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int cc = 0; cc < DP; cc += 16) {
@@ -287,34 +294,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             const float2 c2 = two(cx), mu = two(m == -INFINITY ? 0.f : -m);
             float2 s2[2] = {two(0.f), two(0.f)};
+            uint32_t pk[32], rest[32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {  // 64 keys at a time: their product may begin
-                uint32_t pk[32], rest[32];
+            for (int b = 0; b < 2; ++b) {
+                if (HIDDEN && !some[b]) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (HIDDEN && !(some >> (2 * half + b) & 1u)) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[b * 16 + e] = rest[b * 16 + e] = 0u;
-                        continue;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const int at = half * 64 + b * 32 + e;
-                        const float2 y = __ffma2_rn(make_float2(x[at], x[at + 1]), c2, mu);
-                        const float2 q = make_float2(ex2(y.x), ex2(y.y));
-                        s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
-                        const uint32_t hi = pack_bf16x2(q.x, q.y);
-                        pk[b * 16 + (e >> 1)] = hi;
-                        if (HIDDEN) rest[b * 16 + (e >> 1)] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
-                    }
+                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = rest[b * 16 + e] = 0u;
+                    continue;
                 }
-                tmem_st_x32(ts + half * 32, pk);
-                if (HIDDEN) tmem_st_x32(ts + 64 + half * 32, rest);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 y = __ffma2_rn(make_float2(x[b * 32 + e], x[b * 32 + e + 1]), c2, mu);
+                    const float2 q = make_float2(ex2(y.x), ex2(y.y));
+                    s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
+                    const uint32_t hi = pack_bf16x2(q.x, q.y);
+                    pk[b * 16 + (e >> 1)] = hi;
+                    if (HIDDEN) rest[b * 16 + (e >> 1)] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
+                }
             }
+            tmem_st_x32(ts + half * 32, pk);
+            if (HIDDEN) tmem_st_x32(ts + 64 + half * 32, rest);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
             const float2 s = __fadd2_rn(s2[0], s2[1]);
             l += s.x + s.y;
             return true;
@@ -323,20 +326,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             ok = mbar_wait_warp(smem_u32(&sfull[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            ok = span[w].hides(j) ? tile(j, std::true_type{}) : tile(j, std::false_type{});
-        }
-        if (ok && j1 > j0) ok = mbar_wait_warp(smem_u32(&odone[w]), (uint32_t)(j1 - 1 - j0) & 1u, s_abort, p.wait_ns);
-        tc_fence_after();
-        if (!ok) {
-            if (lane == 0) {
-                attn_error(p, 5, 3);
-                *s_abort = 1;
+            const bool hides = span[w].hides(j);
+            float x0[64], x1[64];
+            tmem_ld_f32<0>(ts, x0);
+            tmem_ld_f32<32>(ts + 32, x0);
+            tmem_ld_wait_f32<0>(x0);
+            tmem_ld_wait_f32<32>(x0);
+            tmem_ld_f32<0>(ts + 64, x1);  // on its way during the first half's arithmetic
+            tmem_ld_f32<32>(ts + 96, x1);
+            if (hides) {  // (the first half writes into the second's columns)
+                tmem_ld_wait_f32<0>(x1);
+                tmem_ld_wait_f32<32>(x1);
+                ok = step(j, 0, x0, std::true_type{}) && step(j, 1, x1, std::true_type{});
+            } else {
+                ok = step(j, 0, x0, std::false_type{});
+                tmem_ld_wait_f32<0>(x1);
+                tmem_ld_wait_f32<32>(x1);
+                ok = ok && step(j, 1, x1, std::false_type{});
             }
+        }
+        if (ok && j1 > j0) ok = mbar_wait_warp(smem_u32(&odone[w]), 0, s_abort, p.wait_ns);
+        tc_fence_after();
+        if (!ok && lane == 0) {
+            attn_error(p, 5, 3);
+            *s_abort = 1;
+        }
+        if (!group_ok(ok, s_bad + w, 1 + w)) {
+            // (nothing is written)
         } else {
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int64_t at = ((int64_t)i * p.hq + h) * p.d;
+            const int row = (warp & 3) * 32 + lane;
+            uint8_t* stage = sq + w * C::kTileBytes;  // (the queries have been read)
+            int8_t* lo = p.out_lo ? p.out_lo + ((int64_t)i * p.hq + h) * p.d16 : nullptr;
 #pragma unroll 1
-            for (int cc = 0; cc < p.d; cc += 16) {
+            for (int cc = 0; cc < DP; cc += 16) {
                 uint32_t o[16];
                 if (j1 > j0) {  // (uniform over the warpgroup)
                     tmem_ld_x16(to + cc, o);
@@ -346,25 +369,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int e = 0; e < 16; ++e) o[e] = 0;
                 }
                 uint32_t v[8];
-                int lo[4];
+                int more[4];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float a = inv > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
                     const float b = inv > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
                     v[e] = pack_bf16x2(a, b);
                     const int two = (bits_left(a, v[e] & 0xFFFFu) & 255) | (bits_left(b, v[e] >> 16) & 255) << 8;
-                    if (e & 1) lo[e >> 1] |= two << 16;
-                    else lo[e >> 1] = two;
+                    if (e & 1) more[e >> 1] |= two << 16;
+                    else more[e >> 1] = two;
                 }
-                if (i < p.T) {  // d is a multiple of 8: the last 16 columns may be half a chunk
-                    *reinterpret_cast<uint4*>(p.out + at + cc) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + at + cc) = make_uint2(lo[0], lo[1]);
-                    if (cc + 8 < p.d) {
-                        *reinterpret_cast<uint4*>(p.out + at + cc + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-                        if (p.out_lo) *reinterpret_cast<uint2*>(p.out_lo + at + cc + 8) = make_uint2(lo[2], lo[3]);
-                    }
-                }
+                stage_pairs(stage + (cc / 64) * kBoxBytes, row, (cc & 63) / 16, v);
+                if (lo && i < p.T && cc < p.d)
+                    *reinterpret_cast<int4*>(lo + cc) = make_int4(more[0], more[1], more[2], more[3]);
             }
+            if (q0 + w * kTile < p.T)  // (uniform over the warpgroup)
+                for (int b = 0; b < DP / 64; ++b)
+                    store_box(&maps.o, stage + b * kBoxBytes, b * 64, h, q0 + w * kTile, 1 + w, row == 0);
             if (i < p.T) p.lse[(int64_t)h * p.T + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
         tc_fence_before();
@@ -392,6 +413,7 @@ lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
     lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
+    if (s == LM_OK) s = encode_heads(&maps.o, lm_heads{p.out, (int64_t)p.hq * p.d, p.d}, p.T, p.hq, p.d, kTile);
     if (s != LM_OK) return s;
     // the plain form folds the scale into the exponent and needs it positive (the maximum of s c is c max s)
     const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes || !(p.scale > 0.f) ? ATTN_BIAS : ATTN_PLAIN;

@@ -38,7 +38,7 @@ struct HeadsIn {
     int64_t ts, hs;
 };
 struct AttnParams {
-    int32_t T, hq, hk, d;
+    int32_t T, hq, hk, d, d16;  // d16: d rounded up to 16
     float scale, cap;
     const float* slopes;
     const TokRange* rng;   // T entries, or null: one document

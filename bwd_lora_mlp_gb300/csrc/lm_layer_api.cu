@@ -125,6 +125,7 @@ AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_he
     p.hq = hq;
     p.hk = hk;
     p.d = d;
+    p.d16 = (d + 15) / 16 * 16;
     p.scale = a->scale;
     p.cap = a->cap;
     p.slopes = a->slopes;
@@ -171,7 +172,7 @@ extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     LL_TRY(need(ws, 32, "ws"));
     const AttnPlan P = plan_attn(T, hq);
     if (ws_bytes < P.total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, P.total);
-    LL_TRY(check_alias({{O, (size_t)T * hq * d * 2, "O"}, {O_lo, (size_t)T * hq * d, "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}, {ws, P.total, "ws"}},
+    LL_TRY(check_alias({{O, (size_t)T * hq * d * 2, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}, {ws, P.total, "ws"}},
                        {heads_span(q, T, hq, d, "q"), heads_span(k, T, hk, d, "k"), heads_span(v, T, hk, d, "v")}));
     if (T == 0) return LM_OK;
     int sms = 0;
@@ -208,7 +209,7 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     const size_t bq = (size_t)T * hq * d * 2, bk = (size_t)T * hk * d * 2;
     LL_TRY(check_alias({{dQ, bq, "dQ"}, {dK, bk, "dK"}, {dV, bk, "dV"}, {ws, P.total, "ws"}},
                        {heads_span(q, T, hq, d, "q"), heads_span(k, T, hk, d, "k"), heads_span(v, T, hk, d, "v"),
-                        heads_span(dO, T, hq, d, "dO"), {O, bq, "O"}, {O_lo, bq / 2, "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}}));
+                        heads_span(dO, T, hq, d, "dO"), {O, bq, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}}));
     if (T == 0) return LM_OK;
     int sms = 0;
     LL_TRY(device_ready(&sms));

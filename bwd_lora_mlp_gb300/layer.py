@@ -149,22 +149,26 @@ def _heads(t: torch.Tensor, T: int, h: int, d: int, name: str) -> lm_heads:
     return lm_heads(t.data_ptr() if T else L._empty_ptr(t.device), ts, hs)
 
 
+def _d16(d: int) -> int:
+    return (d + 15) // 16 * 16
+
+
 def attn_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
     return _size("attn_workspace_size", T, hq, hk, d)
 
 
 def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None, stream=None) -> dict:
-    """q (T, hq, d), k and v (T, hk, d) -> O (T, hq, d), lse (hq, T) and, with ``train``, O_lo (T, hq, d int8:
-    more bits of O, for the backward)."""
+    """q (T, hq, d), k and v (T, hk, d) -> O (T, hq, d), lse (hq, T) and, with ``train``, O_lo (int8: more
+    bits of O, for the backward)."""
     (T, hq, d), hk = q.shape, k.shape[1]
     dev = q.device
     O = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev) if O is None else O
     lse = torch.empty((hq, T), dtype=torch.float32, device=dev) if lse is None else lse
     if train and O_lo is None:
-        O_lo = torch.empty((T, hq, d), dtype=torch.int8, device=dev)
+        O_lo = torch.empty((T, hq, _d16(d)), dtype=torch.int8, device=dev)
     ws = workspace(attn_workspace_size(T, hq, hk, d), dev) if ws is None else ws
     _call("attn_fwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
-          a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, d), torch.int8, "O_lo"),
+          a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, _d16(d)), torch.int8, "O_lo"),
           _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), L._stream(stream))
     return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
 
@@ -179,7 +183,7 @@ def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None
     ws = fwd["ws"] if ws is None else ws
     _call("attn_bwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
           _heads(dO, T, hq, d, "dO"), _shaped(fwd["O"], (T, hq, d), bf, "O"),
-          _shaped(fwd["O_lo"], (T, hq, d), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"), a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"),
+          _shaped(fwd["O_lo"], (T, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"), a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"),
           _shaped(dK, (T, hk, d), bf, "dK"), _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"),
           ws.numel(), L._stream(stream))
     return {"dQ": dQ, "dK": dK, "dV": dV}

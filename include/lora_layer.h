@@ -41,7 +41,7 @@ typedef enum lm_index { LM_I32 = 0, LM_I64 = 1 } lm_index;
  * tokens and heads may be strided (slices of one QKV buffer, head-major layouts): strides in
  * elements, multiples of 8 and at least d, base 16-byte aligned, last dimension contiguous.
  * T <= 2^20.  O (T x hq x d) bf16 and lse (hq x T, natural logarithm) fp32 are contiguous.
- * O_lo (T x hq x d int8, or NULL where no backward follows) takes the next eight bits of O's fp32
+ * O_lo (T x hq x d16 int8, d16 = d rounded up to 16, or NULL where no backward follows) takes the next eight bits of O's fp32
  * pattern: fp32 bits of O = (bits of the bf16 << 16) + (O_lo << 8), to the nearest, O_lo in [-128, 127].
  * The backward takes O, O_lo and lse as the forward left them and writes dQ (T x hq x d), dK and dV
  * (T x hk x d) bf16, contiguous; a key/value head's gradients are summed over its hq / hk query
