@@ -1,113 +1,394 @@
 // Log probabilities of given tokens (include/lora_layer.h), with entropy and top alternatives.
 //   m = max x,  S = sum e^{x-m},  w = sum e^{x-m} (x-m):  lse = m + log S,  H = log S - w / S
-// One CTA per row, a pass for the maximum, one for the sums, and one for each alternative.
+// Forward: one pass over the logits with running m, S, w per thread, joined over the CTA.  A row is
+// one CTA's, or a cluster's of up to eight where there are fewer rows than the device holds CTAs, each
+// taking a segment, joined through distributed shared memory.  The k alternatives: the k-th largest of
+// the threads' own maxima bounds the k-th largest logit from below, so a second look at the segment
+// (in L2 by then) for what is above the bound finds k of them among a few dozen; what is missing are
+// ties at the bound, taken from the lowest index up.  Bound by memory.
+// Backward: one pass, dx = scale (g 1[target] - p (g + gH (log p + H))).
+#include <algorithm>
+
 #include "lm_layer.h"
 #include "lm_ptx.cuh"
 
 namespace lm {
 
-constexpr int kLpThreads = 512;
+constexpr int kThreads = 512;
+constexpr int kMaxCluster = 8;
+constexpr int kCand = 1024;  // alternatives above the bound that fit
+constexpr float kL2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float logit(const LogprobParams& p, int64_t at) {
-    return p.f32 ? static_cast<const float*>(p.logits)[at]
-                 : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.logits)[at] << 16);
+__device__ __forceinline__ float lp_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ int64_t target_of(const LogprobParams& p, int64_t t) {
     const int64_t v = p.i64 ? static_cast<const int64_t*>(p.targets)[t] : static_cast<const int32_t*>(p.targets)[t];
     return v >= 0 && v < p.V ? v : -1;
 }
-// scale * logit, rounded by itself: forward and backward then take the same number, and what cancels
-// in one cancels in the other
-__device__ __forceinline__ float scaled(const LogprobParams& p, int64_t at) { return __fmul_rn(logit(p, at), p.scale); }
 // Larger keys for larger logits; +0 and -0 are equal, every NaN is the largest.
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0xFFFFFFFFu;
     const uint32_t b = __float_as_uint(x + 0.f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-// (key, index) as one number: larger logit first, then the lower index
-__device__ __forceinline__ uint64_t rank_of(float x, int64_t j) {
-    return ((uint64_t)order_key(x) << 32) | (0xFFFFFFFFu - (uint32_t)j);
-}
+// (key, index) as one number: larger logit first, then the lower index; 0 is none
+__device__ __forceinline__ uint64_t rank_of(float x, uint32_t j) { return ((uint64_t)order_key(x) << 32) | (0xFFFFFFFFu - j); }
 
-template <typename T, typename F>
-__device__ T block_all(T x, F op) {
-    __shared__ T part[kLpThreads / 32];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
-    __syncthreads();
-    T s = part[0];
-    for (int i = 1; i < kLpThreads / 32; ++i) s = op(s, part[i]);
-    return s;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) { return (a != a || a > b) ? a : b; }  // NaN wins
-
-__global__ void __launch_bounds__(kLpThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p) {
-    const int64_t t = blockIdx.x, row = t * p.ld;
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < p.V; j += kLpThreads) m = max_nan(scaled(p, row + j), m);
-    m = block_all(m, [](float a, float b) { return max_nan(a, b); });
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float S = 0.f, w = 0.f;
-    for (int64_t j = threadIdx.x; j < p.V; j += kLpThreads) {
-        const float x = scaled(p, row + j) - m0, e = expf(x);
-        S += e;
-        if (x != -INFINITY) w += e * x;
+template <bool F32>
+struct Row {
+    static constexpr int kVec = F32 ? 4 : 8;  // logits of 16 bytes
+    const char* p;
+    __device__ __forceinline__ float at(int64_t j) const {
+        if (F32) return reinterpret_cast<const float*>(p)[j];
+        return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[j] << 16);
     }
-    auto add = [](float a, float b) { return a + b; };
-    S = block_all(S, add);
-    w = block_all(w, add);
-    const float lse = m == -INFINITY ? -INFINITY : m + logf(S);
-    auto logp = [&](int64_t j) { return m == -INFINITY ? -INFINITY : scaled(p, row + j) - lse; };
+    __device__ __forceinline__ void vec(int64_t j, float (&x)[kVec]) const {
+        const uint4 a = *reinterpret_cast<const uint4*>(p + j * (F32 ? 4 : 2));
+        if (F32) {
+            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] = e & 1 ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1]);
+        }
+    }
+    // elements before the first 16-byte boundary at or after element j
+    __device__ __forceinline__ int64_t head(int64_t j) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p + j * (F32 ? 4 : 2)) & 15;
+        return a ? (int64_t)((16 - a) / (F32 ? 4 : 2)) : 0;
+    }
+};
+
+// f(x, first index, count <= vector) over [j0, j1): whole vectors U at a time, then the ragged ends.
+template <int U, bool F32, typename F>
+__device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1, F f) {
+    constexpr int W = Row<F32>::kVec;
+    const int64_t a = min(j1, j0 + row.head(j0)), nv = (j1 - a) / W, b = a + nv * W;
+    int64_t v = threadIdx.x;
+    for (; v + (U - 1) * kThreads < nv; v += U * kThreads) {
+        float x[U][W];
+#pragma unroll
+        for (int u = 0; u < U; ++u) row.vec(a + (v + u * kThreads) * W, x[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) f(x[u], a + (v + u * kThreads) * W, W);
+    }
+    for (; v < nv; v += kThreads) {
+        float x[W];
+        row.vec(a + v * W, x);
+        f(x, a + v * W, W);
+    }
+    // at most W - 1 elements at each end, one a thread
+    const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
+    if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) {
+        float x[W];
+        x[0] = row.at(j);
+        f(x, j, 1);
+    }
+}
+
+// Running softmax sums; max_nan keeps a NaN, and the sums of a row with one are NaN.
+__device__ __forceinline__ float max_nan(float a, float b) { return (a != a || a > b) ? a : b; }
+struct Sums {
+    float m, S, w;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
+    Sums r;
+    r.m = max_nan(a.m, b.m);
+    if (r.m == -INFINITY) return Sums{-INFINITY, 0.f, 0.f};
+    const float da = a.m - r.m, db = b.m - r.m;  // (one is 0)
+    const float fa = lp_ex2(da * kL2e), fb = lp_ex2(db * kL2e);
+    r.S = a.S * fa + b.S * fb;
+    // w moves with the maximum: sum e^{x-m} (x-m); an empty part has da = -inf and counts nothing
+    r.w = (a.S > 0.f ? fa * fmaf(a.S, da, a.w) : 0.f) + (b.S > 0.f ? fb * fmaf(b.S, db, b.w) : 0.f);
+    if (a.m != a.m || b.m != b.m) r.S = r.w = r.m;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// this CTA's shared variable at the same place in CTA 0 of the cluster
+template <typename T>
+__device__ __forceinline__ void st_first(T* p, T v) {
+    const uint32_t a = map_to_rank(smem_u32(p), 0);
+    if constexpr (sizeof(T) == 8) asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(a), "l"((uint64_t)v) : "memory");
+    else asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(__float_as_uint(v)) : "memory");
+}
+
+struct LpShared {
+    Sums warp[kThreads / 32];
+    float seg[kMaxCluster][3];
+    uint64_t cand[kCand];
+    uint64_t best[kMaxCluster * kMaxTop];  // the segments' alternatives (in CTA 0: of all)
+    uint64_t mine[kMaxTop];
+    uint64_t red[kThreads / 32];
+    int count;
+    int ties[kThreads / 32];
+};
+
+// The k best of [j0, j1) (fewer if it is shorter: the rest are 0) to sm.mine, best first.
+template <bool F32>
+__device__ void segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, uint32_t own_max, LpShared& sm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < kMaxTop) sm.mine[tid] = 0;
+    if (tid == 0) sm.count = 0;
+    // the k-th largest of the threads' maxima, from the top bit down; for fp32 its upper half is a bound too
+    uint32_t bound = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t t = bound | (1u << bit);
+        if (__syncthreads_count(own_max >= t) >= k) bound = t;
+    }
+    if (!F32 && bound >= 0x80000000u) {
+        // (exact: the low 16 bits of a positive bf16 key are zero)
+    } else if (!F32) {
+        bound |= 0xFFFFu;  // (and of a negative one they are ones)
+        if (__syncthreads_count(own_max >= bound) < k) bound &= 0xFFFF0000u;
+    }
+    scan<4>(row, j0, j1, [&](const float* x, int64_t j, int n) {
+#pragma unroll
+        for (int e = 0; e < Row<F32>::kVec; ++e)
+            if (e < n && order_key(x[e]) > bound) {
+                const int at = atomicAdd(&sm.count, 1);
+                if (at < kCand) sm.cand[at] = rank_of(x[e], (uint32_t)(j + e));
+            }
+    });
+    __syncthreads();
+    const int n = sm.count;
+    if (n > kCand) {  // far more than k logits above the bound: k searches of the segment
+        uint64_t last = ~0ull;
+        for (int i = 0; i < k; ++i) {
+            uint64_t b = 0;
+            scan<4>(row, j0, j1, [&](const float* x, int64_t j, int c) {
+#pragma unroll
+                for (int e = 0; e < Row<F32>::kVec; ++e)
+                    if (e < c) {
+                        const uint64_t r = rank_of(x[e], (uint32_t)(j + e));
+                        if (r < last && r > b) b = r;
+                    }
+            });
+#pragma unroll
+            for (int o = 16; o; o >>= 1) b = max(b, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)b, o));
+            __syncthreads();
+            if (lane == 0) sm.red[warp] = b;
+            __syncthreads();
+            last = 0;
+            for (int q = 0; q < kThreads / 32; ++q) last = max(last, sm.red[q]);
+            if (tid == 0) sm.mine[i] = last;
+        }
+        __syncthreads();
+        return;
+    }
+    // each candidate's place is the number of better ones (whatever order they came in)
+    for (int c = tid; c < n; c += kThreads) {
+        const uint64_t r = sm.cand[c];
+        int place = 0;
+        for (int q = 0; q < n; ++q) place += sm.cand[q] > r;
+        if (place < k) sm.mine[place] = r;
+    }
+    // what is missing lies at the bound itself: the lowest indices first, a stretch of the segment at a time
+    int have = min(n, k);
+    for (int64_t j = j0; have < k && j < j1; j += kThreads) {
+        const bool tie = j + tid < j1 && order_key(row.at(j + tid)) == bound;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        __syncthreads();
+        if (lane == 0) sm.ties[warp] = __popc(votes);
+        __syncthreads();
+        int before = have, total = 0;
+        for (int q = 0; q < kThreads / 32; ++q) {
+            if (q < warp) before += sm.ties[q];
+            total += sm.ties[q];
+        }
+        const int place = before + __popc(votes & ((1u << lane) - 1u));
+        if (tie && place < k) sm.mine[place] = rank_of(row.at(j + tid), (uint32_t)(j + tid));
+        have += total;
+    }
+    __syncthreads();
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
+    __shared__ LpShared sm;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t t = blockIdx.x / cluster;
+    const int part = cluster > 1 ? (int)cluster_rank() : 0;
+    const Row<F32> row{static_cast<const char*>(p.logits) + t * p.ld * (F32 ? 4 : 2)};
+    // segments of whole 64-element stretches
+    const int64_t len = ((p.V + cluster - 1) / cluster + 63) / 64 * 64;
+    const int64_t j0 = min(p.V, part * len), j1 = min(p.V, j0 + len);
+    constexpr int W = Row<F32>::kVec;
+    Sums s{-INFINITY, 0.f, 0.f};
+    float own = -INFINITY;  // the thread's largest logit (NaN the largest)
+    const bool plain = p.scale == 1.f;
+    scan<4>(row, j0, j1, [&](float* x, int64_t, int n) {
+        float big = x[0];
+        if (n == W) {
+#pragma unroll
+            for (int e = 1; e < W; ++e) big = max_nan(x[e], big);
+        } else {
+#pragma unroll
+            for (int e = 1; e < W; ++e) x[e] = -INFINITY;
+        }
+        own = max_nan(big, own);
+        if (!plain) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) x[e] = __fmul_rn(x[e], p.scale);
+            big = __fmul_rn(big, p.scale);
+        }
+        if (!(big <= s.m)) {  // (a NaN comes here too)
+            const float f = s.m == -INFINITY ? 0.f : lp_ex2((s.m - big) * kL2e);
+            s.w = s.S > 0.f ? f * fmaf(s.S, s.m - big, s.w) : 0.f;
+            s.S *= f;
+            s.m = big;
+        }
+        if (s.m == -INFINITY) return;
+        float2 S2 = make_float2(s.S, 0.f), w2 = make_float2(s.w, 0.f);
+#pragma unroll
+        for (int e = 0; e < W; e += 2) {
+            const float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-s.m, -s.m));
+            const float2 q = __fmul2_rn(d, make_float2(kL2e, kL2e));
+            const float2 y = make_float2(lp_ex2(q.x), lp_ex2(q.y));
+            S2 = __fadd2_rn(S2, y);
+            // (d = -inf has y = 0; the product with the largest finite number is 0 as well)
+            w2 = __ffma2_rn(y, make_float2(fmaxf(d.x, -3e38f), fmaxf(d.y, -3e38f)), w2);
+        }
+        s.S = S2.x + S2.y;
+        s.w = w2.x + w2.y;
+    });
+    if (s.m != s.m) s.S = s.w = s.m;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const Sums q{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.S, o), __shfl_xor_sync(0xffffffffu, s.w, o)};
+        s = (threadIdx.x & o) ? join(q, s) : join(s, q);  // (the same operands in the same order in both lanes)
+    }
+    if ((threadIdx.x & 31) == 0) sm.warp[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = sm.warp[0];
+    for (int i = 1; i < kThreads / 32; ++i) s = join(s, sm.warp[i]);
+    if (p.k) segment_top(row, j0, j1, p.k, order_key(own) & (j0 < j1 ? ~0u : 0u), sm);
+    if (cluster > 1) {
+        if (threadIdx.x == 0) {
+            st_first(&sm.seg[part][0], s.m);
+            st_first(&sm.seg[part][1], s.S);
+            st_first(&sm.seg[part][2], s.w);
+        }
+        if (threadIdx.x < p.k) st_first(&sm.best[part * p.k + threadIdx.x], sm.mine[threadIdx.x]);
+        cluster_sync();
+        if (part) return;
+        s = Sums{sm.seg[0][0], sm.seg[0][1], sm.seg[0][2]};
+        for (int i = 1; i < cluster; ++i) s = join(s, Sums{sm.seg[i][0], sm.seg[i][1], sm.seg[i][2]});
+        const int n = cluster * p.k;
+        if (threadIdx.x < n) {
+            const uint64_t r = sm.best[threadIdx.x];
+            int place = 0;
+            for (int q = 0; q < n; ++q) place += sm.best[q] > r;
+            if (r && place < p.k) sm.mine[place] = r;
+        }
+        __syncthreads();
+    }
+    const bool empty = s.m == -INFINITY;
+    const float lse = empty ? -INFINITY : s.m + logf(s.S);
+    auto logp = [&](int64_t j) { return empty ? -INFINITY : __fmul_rn(row.at(j), p.scale) - lse; };
     if (threadIdx.x == 0) {
         const int64_t at = target_of(p, t);
         p.lse[t] = lse;
         p.logp[t] = at < 0 ? 0.f : logp(at);
-        if (p.entropy) p.entropy[t] = m == -INFINITY ? 0.f : logf(S) - w / S;
+        if (p.entropy) p.entropy[t] = empty ? 0.f : logf(s.S) - s.w / s.S;
     }
-    uint64_t last = ~0ull;
-    for (int i = 0; i < p.k; ++i) {
-        uint64_t best = 0;
-        for (int64_t j = threadIdx.x; j < p.V; j += kLpThreads) {
-            const uint64_t r = rank_of(logit(p, row + j), j);
-            if (r < last && r > best) best = r;
-        }
-        last = block_all(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-        if (threadIdx.x == 0) {
-            const uint32_t j = 0xFFFFFFFFu - (uint32_t)last;
-            p.top_ids[t * p.k + i] = (int32_t)j;
-            p.top_logp[t * p.k + i] = logp(j);
-        }
+    if (threadIdx.x < p.k) {
+        const uint32_t j = 0xFFFFFFFFu - (uint32_t)sm.mine[threadIdx.x];
+        p.top_ids[t * p.k + threadIdx.x] = (int32_t)j;
+        p.top_logp[t * p.k + threadIdx.x] = logp(j);
     }
 }
 
+template <bool F32>
+static cudaError_t fwd_launch(const LogprobParams& p, cudaStream_t st) {
+    // A CTA per row fills the device from about two rows an SM on; with fewer, a row is shared, as long as
+    // a CTA's segment keeps every thread a few vectors.  (4 rows of 131072 fp32: 8 CTAs a row.)
+    int c = 1;
+    while (c < kMaxCluster && p.T * c * 2 <= 304 && p.V / (c * 2) >= kThreads * 8) c *= 2;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim = {(unsigned)c, 1, 1};
+    return launch_pdl(logprob_fwd_kernel<F32>, dim3((unsigned)(p.T * c)), dim3(kThreads), 0, st, &a, 1, p, c);
+}
 cudaError_t launch_logprob_fwd(const LogprobParams& p, cudaStream_t st) {
-    logprob_fwd_kernel<<<(unsigned)p.T, kLpThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return p.f32 ? fwd_launch<true>(p, st) : fwd_launch<false>(p, st);
 }
 
-__global__ void __launch_bounds__(kLpThreads) logprob_bwd_kernel(const __grid_constant__ LogprobParams p) {
-    const int64_t t = blockIdx.x, row = t * p.ld, at = target_of(p, t);
+// ------------------------------------------------------------------ backward
+constexpr int kBwdThreads = 256;
+constexpr int kBwdVecs = 8;  // 16-byte vectors of a thread: a CTA takes a stretch of 2048 of them
+
+template <bool F32>
+__global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_constant__ LogprobParams p, unsigned per_row) {
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int W = Row<F32>::kVec;
+    const int64_t t = blockIdx.x / per_row;
+    const Row<F32> row{static_cast<const char*>(p.logits) + t * p.ld * (F32 ? 4 : 2)};
+    char* out = static_cast<char*>(p.dlogits) + t * p.ld_out * (F32 ? 4 : 2);
+    const int64_t at = target_of(p, t);
     const float lse = p.lse_in[t], gH = p.dentropy ? p.dentropy[t] : 0.f, H = p.dentropy ? p.entropy_in[t] : 0.f;
     const float g = p.dlogp && at >= 0 ? p.dlogp[t] : 0.f;
-    for (int64_t j = threadIdx.x; j < p.V; j += kLpThreads) {
-        const float lp = scaled(p, row + j) - lse;
-        const float e = expf(lp);
-        float d = lse == -INFINITY || e == 0.f ? 0.f : -e * (g + gH * (lp + H));
-        if (j == at && lse != -INFINITY) d += g;
-        d *= p.scale;
-        const int64_t o = t * p.ld_out + j;
-        if (p.f32) static_cast<float*>(p.dlogits)[o] = d;
-        else static_cast<uint16_t*>(p.dlogits)[o] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
+    auto grad = [&](float x, int64_t j) {
+        const float lp = __fmul_rn(x, p.scale) - lse, e = lp_ex2(lp * kL2e);
+        float d = e == 0.f ? 0.f : -e * fmaf(gH, lp + H, g);
+        if (j == at) d += g;
+        return lse == -INFINITY ? 0.f : d * p.scale;
+    };
+    auto put = [&](int64_t j, float d) {
+        if (F32) reinterpret_cast<float*>(out)[j] = d;
+        else reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
+    };
+    // stretches begin at the row's first 16-byte boundary; the first CTA also takes what is before it
+    const int64_t a = min(p.V, row.head(0)), n = (int64_t)kBwdThreads * kBwdVecs * W;
+    const int64_t s0 = a + (blockIdx.x - t * per_row) * n, s1 = min(p.V, s0 + n);
+    if (s0 == a && threadIdx.x < a) put(threadIdx.x, grad(row.at(threadIdx.x), threadIdx.x));
+    if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15) == 0) {
+        float x[kBwdVecs][W];
+#pragma unroll
+        for (int u = 0; u < kBwdVecs; ++u) {
+            const int64_t j = s0 + (u * kBwdThreads + threadIdx.x) * W;
+            if (j + W <= s1) row.vec(j, x[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBwdVecs; ++u) {
+            const int64_t j = s0 + (u * kBwdThreads + threadIdx.x) * W;
+            if (j + W <= s1) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) x[u][e] = grad(x[u][e], j + e);
+                uint4 v;
+                if (F32) v = make_uint4(__float_as_uint(x[u][0]), __float_as_uint(x[u][1]), __float_as_uint(x[u][2]), __float_as_uint(x[u][3]));
+                else v = make_uint4(pack_bf16x2(x[u][0], x[u][1]), pack_bf16x2(x[u][2], x[u][3]),
+                                    pack_bf16x2(x[u][W - 4], x[u][W - 3]), pack_bf16x2(x[u][W - 2], x[u][W - 1]));
+                *reinterpret_cast<uint4*>(out + j * (F32 ? 4 : 2)) = v;
+            } else {
+                for (int64_t i = j; i < s1; ++i) put(i, grad(row.at(i), i));
+            }
+        }
+    } else {  // the rows of the two tensors lie differently: element by element
+        for (int64_t j = s0 + threadIdx.x; j < s1; j += kBwdThreads) put(j, grad(row.at(j), j));
     }
 }
 
+template <bool F32>
+static cudaError_t bwd_launch(const LogprobParams& p, cudaStream_t st) {
+    const int64_t n = (int64_t)kBwdThreads * kBwdVecs * Row<F32>::kVec;
+    const int64_t per_row = (p.V + n - 1) / n;
+    if (p.T * per_row > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(logprob_bwd_kernel<F32>, dim3((unsigned)(p.T * per_row)), dim3(kBwdThreads), 0, st, nullptr, 0, p,
+                      (unsigned)per_row);
+}
 cudaError_t launch_logprob_bwd(const LogprobParams& p, cudaStream_t st) {
-    logprob_bwd_kernel<<<(unsigned)p.T, kLpThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return p.f32 ? bwd_launch<true>(p, st) : bwd_launch<false>(p, st);
 }
 
 }  // namespace lm
