@@ -4,8 +4,7 @@
 // one CTA's, or a cluster's of up to eight where there are fewer rows than the device holds CTAs, each
 // taking a segment, joined through distributed shared memory.  The k alternatives: the k-th largest of
 // the threads' own maxima bounds the k-th largest logit from below, so a second look at the segment
-// (in L2 by then) for what is above the bound finds k of them among a few dozen; what is missing are
-// ties at the bound, taken from the lowest index up.  Bound by memory.
+// (in L2 by then) for what reaches the bound finds k of them among a few dozen.  Bound by memory.
 // Backward: one pass, dx = scale (g 1[target] - p (g + gH (log p + H))).
 #include <algorithm>
 
@@ -45,16 +44,6 @@ struct Row {
         if (F32) return reinterpret_cast<const float*>(p)[j];
         return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[j] << 16);
     }
-    __device__ __forceinline__ void vec(int64_t j, float (&x)[kVec]) const {
-        const uint4 a = *reinterpret_cast<const uint4*>(p + j * (F32 ? 4 : 2));
-        if (F32) {
-            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
-        } else {
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) x[e] = e & 1 ? bf16hi(w[e >> 1]) : bf16lo(w[e >> 1]);
-        }
-    }
     // elements before the first 16-byte boundary at or after element j
     __device__ __forceinline__ int64_t head(int64_t j) const {
         const uintptr_t a = reinterpret_cast<uintptr_t>(p + j * (F32 ? 4 : 2)) & 15;
@@ -62,35 +51,51 @@ struct Row {
     }
 };
 
-// f(x, first index, count <= vector) over [j0, j1): whole vectors U at a time, then the ragged ends.
-template <int U, bool F32, typename F>
-__device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1, F f) {
+// f(x, index of vector 0) over [j0, j1) in batches of U whole vectors of a thread (vector u lies
+// u kThreads vectors on; n of them are there), the next batch loading meanwhile, and one(x, index) for
+// the single elements before the first and after the last 16-byte boundary.
+template <int U, bool F32, typename F, typename G>
+__device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1, F f, G one) {
     constexpr int W = Row<F32>::kVec;
-    const int64_t a = min(j1, j0 + row.head(j0)), nv = (j1 - a) / W, b = a + nv * W;
-    int64_t v = threadIdx.x;
-    for (; v + (U - 1) * kThreads < nv; v += U * kThreads) {
+    const int64_t a = min(j1, j0 + row.head(j0));
+    const int nv = (int)((j1 - a) / W);
+    const char* base = row.p + a * (F32 ? 4 : 2);
+    uint4 next[U];
+    auto load = [&](int v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * kThreads < nv) next[u] = *reinterpret_cast<const uint4*>(base + (int64_t)(v + u * kThreads) * 16);
+    };
+    load(threadIdx.x);
+    for (int v = threadIdx.x; v < nv; v += U * kThreads) {
         float x[U][W];
 #pragma unroll
-        for (int u = 0; u < U; ++u) row.vec(a + (v + u * kThreads) * W, x[u]);
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {next[u].x, next[u].y, next[u].z, next[u].w};
 #pragma unroll
-        for (int u = 0; u < U; ++u) f(x[u], a + (v + u * kThreads) * W, W);
+            for (int e = 0; e < W; ++e)
+                x[u][e] = F32 ? __uint_as_float(w[e % 4]) : e & 1 ? bf16hi(w[e / 2 % 4]) : bf16lo(w[e / 2 % 4]);
+        }
+        if (v + (U - 1) * kThreads >= nv)  // (the last batch of some threads: what is not there counts nothing)
+#pragma unroll
+            for (int u = 1; u < U; ++u)
+                if (v + u * kThreads >= nv)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) x[u][e] = -INFINITY;
+        load(v + U * kThreads);
+        f(x, a + (int64_t)v * W, nv - v);
     }
-    for (; v < nv; v += kThreads) {
-        float x[W];
-        row.vec(a + v * W, x);
-        f(x, a + v * W, W);
-    }
-    // at most W - 1 elements at each end, one a thread
+    const int64_t b = a + (int64_t)nv * W;
     const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
-    if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) {
-        float x[W];
-        x[0] = row.at(j);
-        f(x, j, 1);
-    }
+    if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
 }
 
 // Running softmax sums; max_nan keeps a NaN, and the sums of a row with one are NaN.
-__device__ __forceinline__ float max_nan(float a, float b) { return (a != a || a > b) ? a : b; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 struct Sums {
     float m, S, w;
 };
@@ -133,45 +138,60 @@ struct LpShared {
 
 // The k best of [j0, j1) (fewer if it is shorter: the rest are 0) to sm.mine, best first.
 template <bool F32>
-__device__ void segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, uint32_t own_max, LpShared& sm) {
+__device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, uint32_t own_max, LpShared& sm) {
+    constexpr int W = Row<F32>::kVec;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < kMaxTop) sm.mine[tid] = 0;
     if (tid == 0) sm.count = 0;
-    // the k-th largest of the threads' maxima, from the top bit down; for fp32 its upper half is a bound too
+    // the k-th largest of the threads' maxima from the top bit down (16 bits: that of a bf16, but for the
+    // sixteen ones of a negative one's key; for fp32 a little below it, a bound as good)
     uint32_t bound = 0;
 #pragma unroll 1
     for (int bit = 31; bit >= 16; --bit) {
         const uint32_t t = bound | (1u << bit);
         if (__syncthreads_count(own_max >= t) >= k) bound = t;
     }
-    if (!F32 && bound >= 0x80000000u) {
-        // (exact: the low 16 bits of a positive bf16 key are zero)
-    } else if (!F32) {
-        bound |= 0xFFFFu;  // (and of a negative one they are ones)
-        if (__syncthreads_count(own_max >= bound) < k) bound &= 0xFFFF0000u;
-    }
-    scan<4>(row, j0, j1, [&](const float* x, int64_t j, int n) {
+    const float least = bound & 0x80000000u ? __uint_as_float(bound & 0x7FFFFFFFu) : __uint_as_float(~bound);
+    // what is at or above the bound (or NaN), above it only in a second try
+    auto collect = [&](bool strict) {
+        auto take = [&](float x, int64_t j) {
+            if (x < least || (strict && x == least)) return;
+            const int at = atomicAdd(&sm.count, 1);
+            if (at < kCand) sm.cand[at] = rank_of(x, (uint32_t)j);
+        };
+        scan<2>(row, j0, j1, [&](const float (&x)[2][W], int64_t j, int n) {
 #pragma unroll
-        for (int e = 0; e < Row<F32>::kVec; ++e)
-            if (e < n && order_key(x[e]) > bound) {
-                const int at = atomicAdd(&sm.count, 1);
-                if (at < kCand) sm.cand[at] = rank_of(x[e], (uint32_t)(j + e));
+            for (int u = 0; u < 2; ++u) {
+                float big = x[u][0];
+#pragma unroll
+                for (int e = 1; e < W; ++e) big = fmaxf(big, x[u][e]);  // (NaN when all are; else seen below or not larger)
+                bool any = !(big < least) && u * kThreads < n;
+#pragma unroll
+                for (int e = 0; e < W; ++e) any = any || x[u][e] != x[u][e];
+                if (any)
+#pragma unroll 1
+                    for (int e = 0; e < W; ++e) take(row.at(j + (int64_t)u * kThreads * W + e), j + (int64_t)u * kThreads * W + e);
             }
-    });
-    __syncthreads();
-    const int n = sm.count;
-    if (n > kCand) {  // far more than k logits above the bound: k searches of the segment
+        }, take);
+        __syncthreads();
+        return sm.count;
+    };
+    int n = collect(false);
+    const bool ties = n > kCand;
+    if (ties) {  // many equal to the bound: only what is above it, and then from the lowest index up
+        __syncthreads();
+        if (tid == 0) sm.count = 0;
+        __syncthreads();
+        n = collect(true);
+    }
+    if (n > kCand) {  // a few threads hold most of the largest: k searches of the segment
         uint64_t last = ~0ull;
         for (int i = 0; i < k; ++i) {
             uint64_t b = 0;
-            scan<4>(row, j0, j1, [&](const float* x, int64_t j, int c) {
-#pragma unroll
-                for (int e = 0; e < Row<F32>::kVec; ++e)
-                    if (e < c) {
-                        const uint64_t r = rank_of(x[e], (uint32_t)(j + e));
-                        if (r < last && r > b) b = r;
-                    }
-            });
+            for (int64_t j = j0 + tid; j < j1; j += kThreads) {
+                const uint64_t r = rank_of(row.at(j), (uint32_t)j);
+                if (r < last && r > b) b = r;
+            }
 #pragma unroll
             for (int o = 16; o; o >>= 1) b = max(b, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)b, o));
             __syncthreads();
@@ -191,28 +211,29 @@ __device__ void segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, 
         for (int q = 0; q < n; ++q) place += sm.cand[q] > r;
         if (place < k) sm.mine[place] = r;
     }
-    // what is missing lies at the bound itself: the lowest indices first, a stretch of the segment at a time
-    int have = min(n, k);
-    for (int64_t j = j0; have < k && j < j1; j += kThreads) {
-        const bool tie = j + tid < j1 && order_key(row.at(j + tid)) == bound;
-        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-        __syncthreads();
-        if (lane == 0) sm.ties[warp] = __popc(votes);
-        __syncthreads();
-        int before = have, total = 0;
-        for (int q = 0; q < kThreads / 32; ++q) {
-            if (q < warp) before += sm.ties[q];
-            total += sm.ties[q];
+    if (ties) {
+        int have = min(n, k);
+        for (int64_t j = j0; have < k && j < j1; j += kThreads) {
+            const bool tie = j + tid < j1 && row.at(j + tid) == least;
+            const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+            __syncthreads();
+            if (lane == 0) sm.ties[warp] = __popc(votes);
+            __syncthreads();
+            int before = have, total = 0;
+            for (int q = 0; q < kThreads / 32; ++q) {
+                if (q < warp) before += sm.ties[q];
+                total += sm.ties[q];
+            }
+            const int place = before + __popc(votes & ((1u << lane) - 1u));
+            if (tie && place < k) sm.mine[place] = rank_of(least, (uint32_t)(j + tid));
+            have += total;
         }
-        const int place = before + __popc(votes & ((1u << lane) - 1u));
-        if (tie && place < k) sm.mine[place] = rank_of(row.at(j + tid), (uint32_t)(j + tid));
-        have += total;
     }
     __syncthreads();
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
     __shared__ LpShared sm;
     griddep_launch_dependents();
     griddep_wait();
@@ -226,40 +247,51 @@ __global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(const __grid_cons
     Sums s{-INFINITY, 0.f, 0.f};
     float own = -INFINITY;  // the thread's largest logit (NaN the largest)
     const bool plain = p.scale == 1.f;
-    scan<4>(row, j0, j1, [&](float* x, int64_t, int n) {
-        float big = x[0];
-        if (n == W) {
+    auto rise = [&](float big) {  // the running maximum follows, and the sums with it
+        const float f = s.m == -INFINITY ? 0.f : lp_ex2((s.m - big) * kL2e);
+        s.w = s.S > 0.f ? f * fmaf(s.S, s.m - big, s.w) : 0.f;
+        s.S *= f;
+        s.m = big;
+    };
+    constexpr int U = 4;
+    scan<U>(row, j0, j1, [&](float (&x)[U][W], int64_t, int) {
+        float big = x[0][0];
 #pragma unroll
-            for (int e = 1; e < W; ++e) big = max_nan(x[e], big);
-        } else {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 1; e < W; ++e) x[e] = -INFINITY;
-        }
+            for (int e = u ? 0 : 1; e < W; ++e) big = max_nan(x[u][e], big);
         own = max_nan(big, own);
         if (!plain) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) x[e] = __fmul_rn(x[e], p.scale);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < W; ++e) x[u][e] = __fmul_rn(x[u][e], p.scale);
             big = __fmul_rn(big, p.scale);
         }
-        if (!(big <= s.m)) {  // (a NaN comes here too)
-            const float f = s.m == -INFINITY ? 0.f : lp_ex2((s.m - big) * kL2e);
-            s.w = s.S > 0.f ? f * fmaf(s.S, s.m - big, s.w) : 0.f;
-            s.S *= f;
-            s.m = big;
-        }
+        if (!(big <= s.m)) rise(big);  // (a NaN comes here too)
         if (s.m == -INFINITY) return;
-        float2 S2 = make_float2(s.S, 0.f), w2 = make_float2(s.w, 0.f);
+        float2 S2[2] = {make_float2(s.S, 0.f), make_float2(0.f, 0.f)}, w2[2] = {make_float2(s.w, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < W; e += 2) {
-            const float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-s.m, -s.m));
-            const float2 q = __fmul2_rn(d, make_float2(kL2e, kL2e));
-            const float2 y = make_float2(lp_ex2(q.x), lp_ex2(q.y));
-            S2 = __fadd2_rn(S2, y);
-            // (d = -inf has y = 0; the product with the largest finite number is 0 as well)
-            w2 = __ffma2_rn(y, make_float2(fmaxf(d.x, -3e38f), fmaxf(d.y, -3e38f)), w2);
-        }
-        s.S = S2.x + S2.y;
-        s.w = w2.x + w2.y;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+                const float2 d = __fadd2_rn(make_float2(x[u][e], x[u][e + 1]), make_float2(-s.m, -s.m));
+                const float2 q = __fmul2_rn(d, make_float2(kL2e, kL2e));
+                const float2 y = make_float2(lp_ex2(q.x), lp_ex2(q.y));
+                S2[u & 1] = __fadd2_rn(S2[u & 1], y);
+                // (0 x -inf is none: where y is 0, any finite number does)
+                w2[u & 1] = __ffma2_rn(y, make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), w2[u & 1]);
+            }
+        s.S = (S2[0].x + S2[0].y) + (S2[1].x + S2[1].y);
+        s.w = (w2[0].x + w2[0].y) + (w2[1].x + w2[1].y);
+    }, [&](float x, int64_t) {
+        own = max_nan(x, own);
+        x = __fmul_rn(x, p.scale);
+        if (!(x <= s.m)) rise(x);
+        if (x == -INFINITY) return;
+        const float y = lp_ex2((x - s.m) * kL2e);
+        s.S += y;
+        s.w = fmaf(y, fmaxf(x - s.m, -1e30f), s.w);
     });
     if (s.m != s.m) s.S = s.w = s.m;
 #pragma unroll
@@ -338,12 +370,14 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_c
     const int64_t at = target_of(p, t);
     const float lse = p.lse_in[t], gH = p.dentropy ? p.dentropy[t] : 0.f, H = p.dentropy ? p.entropy_in[t] : 0.f;
     const float g = p.dlogp && at >= 0 ? p.dlogp[t] : 0.f;
-    auto grad = [&](float x, int64_t j) {
-        const float lp = __fmul_rn(x, p.scale) - lse, e = lp_ex2(lp * kL2e);
-        float d = e == 0.f ? 0.f : -e * fmaf(gH, lp + H, g);
-        if (j == at) d += g;
-        return lse == -INFINITY ? 0.f : d * p.scale;
+    const bool empty = lse == -INFINITY;
+    const float k0 = -p.scale * fmaf(gH, H, g), k1 = -p.scale * gH, at_target = p.scale * g;
+    // scale (-p (g + gH (log p + H))); p = 0 where log p = -inf (0 x any finite number)
+    auto soft = [&](float x) {
+        const float lp = __fmul_rn(x, p.scale) - lse;
+        return empty ? 0.f : lp_ex2(lp * kL2e) * fmaf(k1, fmaxf(lp, -1e30f), k0);
     };
+    auto grad = [&](float x, int64_t j) { return soft(x) + (j == at && !empty ? at_target : 0.f); };
     auto put = [&](int64_t j, float d) {
         if (F32) reinterpret_cast<float*>(out)[j] = d;
         else reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
@@ -353,22 +387,45 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_c
     const int64_t s0 = a + (blockIdx.x - t * per_row) * n, s1 = min(p.V, s0 + n);
     if (s0 == a && threadIdx.x < a) put(threadIdx.x, grad(row.at(threadIdx.x), threadIdx.x));
     if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15) == 0) {
-        float x[kBwdVecs][W];
+        uint4 raw[kBwdVecs];
 #pragma unroll
         for (int u = 0; u < kBwdVecs; ++u) {
             const int64_t j = s0 + (u * kBwdThreads + threadIdx.x) * W;
-            if (j + W <= s1) row.vec(j, x[u]);
+            if (j + W <= s1) raw[u] = *reinterpret_cast<const uint4*>(row.p + j * (F32 ? 4 : 2));
         }
 #pragma unroll
         for (int u = 0; u < kBwdVecs; ++u) {
             const int64_t j = s0 + (u * kBwdThreads + threadIdx.x) * W;
             if (j + W <= s1) {
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                float d[W];
 #pragma unroll
-                for (int e = 0; e < W; ++e) x[u][e] = grad(x[u][e], j + e);
+                for (int e = 0; e < W; ++e)
+                    d[e] = F32 ? __uint_as_float(w[e % 4]) : e & 1 ? bf16hi(w[e / 2 % 4]) : bf16lo(w[e / 2 % 4]);
+                if (empty) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) d[e] = 0.f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) {
+                        const float2 lp = __fadd2_rn(__fmul2_rn(make_float2(d[e], d[e + 1]), make_float2(p.scale, p.scale)),
+                                                     make_float2(-lse, -lse));
+                        const float2 q = __fmul2_rn(lp, make_float2(kL2e, kL2e));
+                        const float2 c = __ffma2_rn(make_float2(k1, k1), make_float2(fmaxf(lp.x, -1e30f), fmaxf(lp.y, -1e30f)),
+                                                    make_float2(k0, k0));
+                        const float2 r = __fmul2_rn(make_float2(lp_ex2(q.x), lp_ex2(q.y)), c);
+                        d[e] = r.x;
+                        d[e + 1] = r.y;
+                    }
+                    if ((uint64_t)(at - j) < (uint64_t)W) {  // the target is one of these
+#pragma unroll
+                        for (int e = 0; e < W; ++e) d[e] += at - j == e ? at_target : 0.f;
+                    }
+                }
                 uint4 v;
-                if (F32) v = make_uint4(__float_as_uint(x[u][0]), __float_as_uint(x[u][1]), __float_as_uint(x[u][2]), __float_as_uint(x[u][3]));
-                else v = make_uint4(pack_bf16x2(x[u][0], x[u][1]), pack_bf16x2(x[u][2], x[u][3]),
-                                    pack_bf16x2(x[u][W - 4], x[u][W - 3]), pack_bf16x2(x[u][W - 2], x[u][W - 1]));
+                if (F32) v = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+                else v = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[W - 4], d[W - 3]),
+                                    pack_bf16x2(d[W - 2], d[W - 1]));
                 *reinterpret_cast<uint4*>(out + j * (F32 ? 4 : 2)) = v;
             } else {
                 for (int64_t i = j; i < s1; ++i) put(i, grad(row.at(i), i));

@@ -67,13 +67,12 @@ def header_symbols() -> list:
 
 
 def _fn(name: str):
-    if not _fns:
-        so = L.load()
-        for n, (args, res) in _SIGS.items():
-            fn = getattr(so, n)
-            fn.argtypes, fn.restype = args, res
-            _fns[n] = fn
-    return _fns[name]
+    fn = _fns.get(name)
+    if fn is None:
+        fn = getattr(L.load(), name)
+        fn.argtypes, fn.restype = _SIGS[name]
+        _fns[name] = fn
+    return fn
 
 
 def call_status(name: str, *args) -> int:
@@ -93,14 +92,33 @@ def _size(name: str, *args) -> int:
     return out.value
 
 
+def _refuse(t, shape, dtype, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
 def _shaped(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
     """Device address of a contiguous tensor of this shape and type (None: a null pointer)."""
     if t is None:
         return 0
-    p = L._ptr(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    return p
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, shape, dtype, name)
+    return t.data_ptr() or L._empty_ptr(t.device)
+
+
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+def _stream(stream) -> int:
+    """The raw stream: the current one without building a Stream object (3 us of a call's 20)."""
+    return _raw_stream(_device()) if stream is None else L._stream(stream)
 
 
 # ---------------------------------------------------------------------------------------------
@@ -169,7 +187,7 @@ def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, 
     ws = workspace(attn_workspace_size(T, hq, hk, d), dev) if ws is None else ws
     _call("attn_fwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
           a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, _d16(d)), torch.int8, "O_lo"),
-          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), L._stream(stream))
+          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
     return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
 
 
@@ -185,7 +203,7 @@ def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None
           _heads(dO, T, hq, d, "dO"), _shaped(fwd["O"], (T, hq, d), bf, "O"),
           _shaped(fwd["O_lo"], (T, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"), a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"),
           _shaped(dK, (T, hk, d), bf, "dK"), _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"),
-          ws.numel(), L._stream(stream))
+          ws.numel(), _stream(stream))
     return {"dQ": dQ, "dK": dK, "dV": dV}
 
 
@@ -206,12 +224,14 @@ class AddNorm:
     w_offset: float = 0.0
 
     def c_struct(self, d: int, h_dtype) -> lm_addnorm:
-        dt = next((w.dtype for w in (self.w_in, self.w_post, self.gate) if w is not None), torch.bfloat16)
-        if h_dtype not in _DTYPES or dt not in _DTYPES:
-            raise TypeError("h and the norm's vectors must be bfloat16 or float32, got %s and %s" % (h_dtype, dt))
-        return lm_addnorm(_shaped(self.w_in, (d,), dt, "w_in"), _shaped(self.w_post, (d,), dt, "w_post"),
-                          _shaped(self.gate, (d,), dt, "gate"), self.alpha, self.eps, self.w_offset, _DTYPES[h_dtype],
-                          _DTYPES[dt], 0)
+        w = self.w_in if self.w_in is not None else self.w_post if self.w_post is not None else self.gate
+        wt = torch.bfloat16 if w is None else w.dtype
+        hc, wc = _DTYPES.get(h_dtype), _DTYPES.get(wt)
+        if hc is None or wc is None:
+            raise TypeError("h and the norm's vectors must be bfloat16 or float32, got %s and %s" % (h_dtype, wt))
+        shape = (d,)
+        return lm_addnorm(_shaped(self.w_in, shape, wt, "w_in"), _shaped(self.w_post, shape, wt, "w_post"),
+                          _shaped(self.gate, shape, wt, "gate"), self.alpha, self.eps, self.w_offset, hc, wc, 0)
 
 
 def addnorm_workspace_size(T: int, d: int) -> int:
@@ -223,15 +243,16 @@ def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
     without w_in), rstd_y, rstd_h."""
     T, d = h.shape
     dev, f32, bf = h.device, torch.float32, torch.bfloat16
+    td = (T, d)
     if y is not None and h_out is None:
-        h_out = torch.empty_like(h, memory_format=torch.contiguous_format)
+        h_out = torch.empty(td, dtype=h.dtype, device=dev)
     if n.w_in is not None and x is None:
-        x = torch.empty((T, d), dtype=bf, device=dev)
+        x = torch.empty(td, dtype=bf, device=dev)
     rstd_y = torch.empty(T, dtype=f32, device=dev) if n.w_post is not None else None
     rstd_h = torch.empty(T, dtype=f32, device=dev) if n.w_in is not None else None
-    _call("addnorm_fwd", T, d, L._ptr(h, h.dtype, "h"), _shaped(y, (T, d), bf, "y"), n.c_struct(d, h.dtype),
-          _shaped(h_out, (T, d), h.dtype, "h_out"), _shaped(x, (T, d), bf, "x"), _shaped(rstd_y, (T,), f32, "rstd_y"),
-          _shaped(rstd_h, (T,), f32, "rstd_h"), L._stream(stream))
+    _call("addnorm_fwd", T, d, _shaped(h, td, h.dtype, "h"), _shaped(y, td, bf, "y"), n.c_struct(d, h.dtype),
+          _shaped(h_out, td, h.dtype, "h_out"), _shaped(x, td, bf, "x"), _shaped(rstd_y, (T,), f32, "rstd_y"),
+          _shaped(rstd_h, (T,), f32, "rstd_h"), _stream(stream))
     return {"h": h if y is None else h_out, "x": x, "rstd_y": rstd_y, "rstd_h": rstd_h}
 
 
@@ -249,12 +270,12 @@ def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, d
 
     dw_in, dw_post, dgate = grad(n.w_in), grad(n.w_post), grad(n.gate)
     ws = workspace(addnorm_workspace_size(T, d), dev) if ws is None else ws
-    _call("addnorm_bwd", T, d, L._ptr(h, h.dtype, "h"), _shaped(y, (T, d), bf, "y"),
+    _call("addnorm_bwd", T, d, _shaped(h, (T, d), h.dtype, "h"), _shaped(y, (T, d), bf, "y"),
           _shaped(dh_out, (T, d), h.dtype, "dh_out"), _shaped(dx, (T, d), bf, "dx"),
           _shaped(fwd["rstd_y"], (T,), f32, "rstd_y"), _shaped(fwd["rstd_h"], (T,), f32, "rstd_h"),
           n.c_struct(d, h.dtype), _shaped(dh, (T, d), h.dtype, "dh"), _shaped(dy, (T, d), bf, "dy"),
           _shaped(dw_in, (d,), f32, "dw_in"), _shaped(dw_post, (d,), f32, "dw_post"), _shaped(dgate, (d,), f32, "dgate"),
-          L._ptr(ws, torch.uint8, "ws"), ws.numel(), L._stream(stream))
+          L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
     return {"dh": dh, "dy": dy, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
 
 
@@ -289,12 +310,11 @@ def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0, stream=None) ->
     p, ld, dt = _rows2d(logits, "logits")
     tp, ti = _targets(targets, T)
     dev, f32 = logits.device, torch.float32
-    rows = torch.empty((3, T), dtype=f32, device=dev)
-    logp, entropy, lse = rows.unbind(0)
+    logp, entropy, lse = (torch.empty(T, dtype=f32, device=dev) for _ in range(3))
     ids = torch.empty((T, k), dtype=torch.int32, device=dev) if k > 0 else None
     top = torch.empty((T, k), dtype=f32, device=dev) if k > 0 else None
     _call("logprob_fwd", T, V, ld, p, dt, tp, ti, scale, k, L._ptr(logp), L._ptr(entropy), L._ptr(lse), L._ptr(ids),
-          L._ptr(top), L._stream(stream))
+          L._ptr(top), _stream(stream))
     return {"logp": logp, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logp": top}
 
 
@@ -313,5 +333,5 @@ def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: fl
     po, ldo, _ = _rows2d(dlogits, "dlogits")
     _call("logprob_bwd", T, V, ld, p, dt, tp, ti, scale, _shaped(fwd["lse"], (T,), f32, "lse"),
           _shaped(fwd["entropy"], (T,), f32, "entropy"), _shaped(dlogp, (T,), f32, "dlogp"),
-          _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, L._stream(stream))
+          _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, _stream(stream))
     return {"dlogits": dlogits}
