@@ -131,12 +131,10 @@ struct RowGroup {
     }
 };
 
-// ------------------------------------------------------------------ forward
-template <int NV, bool H32, int MOST>
+template <int NV, bool H32, bool W32, int MOST>
 __global__ void __launch_bounds__(MOST, 1024 / MOST)
     addnorm_fwd_kernel(const __grid_constant__ AddNormParams p, int warps, int rows) {
     constexpr int kHp = H32 ? 2 : 1, kPieces = kHp + 1, kStages = fwd_stages(NV);
-    constexpr bool KEEP = NV == 1;  // the weights in registers
     __shared__ float red[2 * 32];
     extern __shared__ uint4 smem_raw[];  // [stage][vector][piece][thread]
     griddep_launch_dependents();
@@ -149,24 +147,8 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST)
     bool on[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) c[k] = (R.lane + k * warps * 32) * 8;
-    F8 w_post[NV], ag[NV], w_in[NV];
-    auto weights_y = [&](int k) {
-        if (p.w_post) w_post[k] = weight8(p.w_post, c[k], p.w_f32, p.w_offset);
-        if (p.gate) ag[k] = weight8(p.gate, c[k], p.w_f32, 0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ag[k].v[e] = p.gate ? __fmul2_rn(ag[k].v[e], both(p.alpha)) : both(p.alpha);
-    };
-    auto weight_in = [&](int k) {
-        if (p.w_in) w_in[k] = weight8(p.w_in, c[k], p.w_f32, p.w_offset);
-    };
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        on[k] = c[k] < p.d;
-        if (KEEP && on[k]) {
-            weights_y(k);
-            weight_in(k);
-        }
-    }
+    for (int k = 0; k < NV; ++k) on[k] = c[k] < p.d;
     const int64_t stride = (int64_t)gridDim.x * rows, hop = stride * p.d;
     int64_t t = (int64_t)blockIdx.x * rows + R.grp;
     int64_t next = t * p.d + c[0];  // the first element that is asked for next
@@ -217,12 +199,18 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST)
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (on[k]) {
-                    if (!KEEP) weights_y(k);
-                    if (p.w_post)
+                    if (p.w_post) {
+                        const F8 w = weight8(p.w_post, c[k], W32, p.w_offset);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[k].v[e] = __fmul2_rn(__fmul2_rn(y[k].v[e], ry2), w_post[k].v[e]);
+                        for (int e = 0; e < 4; ++e) y[k].v[e] = __fmul2_rn(__fmul2_rn(y[k].v[e], ry2), w.v[e]);
+                    }
+                    if (p.gate) {
+                        const F8 w = weight8(p.gate, c[k], W32, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) h[k].v[e] = __ffma2_rn(ag[k].v[e], y[k].v[e], h[k].v[e]);
+                        for (int e = 0; e < 4; ++e) y[k].v[e] = __fmul2_rn(y[k].v[e], w.v[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[k].v[e] = __ffma2_rn(both(p.alpha), y[k].v[e], h[k].v[e]);
                     store8<H32>(p.h_out, at + c[k], h[k]);
                 }
         }
@@ -239,20 +227,22 @@ __global__ void __launch_bounds__(MOST, 1024 / MOST)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (on[k]) {
-                if (!KEEP) weight_in(k);
+                const F8 w = weight8(p.w_in, c[k], W32, p.w_offset);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[k].v[e] = __fmul2_rn(__fmul2_rn(h[k].v[e], rh2), w_in[k].v[e]);
+                for (int e = 0; e < 4; ++e) h[k].v[e] = __fmul2_rn(__fmul2_rn(h[k].v[e], rh2), w.v[e]);
                 store8<false>(p.x, at + c[k], h[k]);
             }
     }
 }
 
 // ------------------------------------------------------------------ backward
-// Sums over tokens of a CTA's rows to part[CTA][wanted sum][d].  POST: y is normed; GATE: it is gated.
-template <int NV, bool H32, bool POST, bool GATE, int MOST>
+// Sums over tokens of a CTA's rows to part[CTA][wanted sum][d].  POST: y is normed; GATE: it is gated.  W32
+// (the weights' type) counts where the weights are read row by row, NV == 2.
+template <int NV, bool H32, bool W32, bool POST, bool GATE, int MOST>
 __global__ void __launch_bounds__(MOST, 1) addnorm_bwd_kernel(const __grid_constant__ AddNormParams p, int warps, int rows) {
     constexpr int kHp = H32 ? 2 : 1, kPieces = 2 * kHp + 2, kStages = bwd_stages(NV, H32, MOST);
     constexpr bool KEEP = NV == 1;
+    const bool w32 = KEEP ? p.w_f32 : W32;
     __shared__ float red[2 * 32];
     extern __shared__ uint4 smem_raw[];
     griddep_launch_dependents();
@@ -268,15 +258,15 @@ __global__ void __launch_bounds__(MOST, 1) addnorm_bwd_kernel(const __grid_const
     for (int k = 0; k < NV; ++k) c[k] = (R.lane + k * warps * 32) * 8;
     F8 w_post[NV], ag[NV], w_in[NV], a_in[NV], a_post[NV], a_gate[NV];
     auto weights_y = [&](int k) {
-        if (POST) w_post[k] = weight8(p.w_post, c[k], p.w_f32, p.w_offset);
+        if (POST) w_post[k] = weight8(p.w_post, c[k], w32, p.w_offset);
         if (GATE) {
-            ag[k] = weight8(p.gate, c[k], p.w_f32, 0.f);
+            ag[k] = weight8(p.gate, c[k], w32, 0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ag[k].v[e] = __fmul2_rn(ag[k].v[e], alpha);
         }
     };
     auto weight_in = [&](int k) {
-        if (p.w_in) w_in[k] = weight8(p.w_in, c[k], p.w_f32, p.w_offset);
+        if (p.w_in) w_in[k] = weight8(p.w_in, c[k], w32, p.w_offset);
     };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -461,17 +451,18 @@ static cudaError_t launch_rows(K kernel, int grid, const RowPlan& P, size_t smem
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     return e == cudaSuccess ? launch_pdl(kernel, dim3(grid), dim3(P.threads), smem, st, nullptr, 0, p, P.warps, P.rows) : e;
 }
-template <int NV, bool H32, int MOST>
+template <int NV, bool H32, bool W32, int MOST>
 static cudaError_t fwd_launch(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
     const size_t smem = (size_t)fwd_stages(NV) * NV * (H32 ? 3 : 2) * P.threads * 16;
     const int grid = (int)std::min<int64_t>(1024 / MOST * kSms, (p.T + P.rows - 1) / P.rows);
-    return launch_rows(addnorm_fwd_kernel<NV, H32, MOST>, grid, P, smem, p, st);
+    return launch_rows(addnorm_fwd_kernel<NV, H32, W32, MOST>, grid, P, smem, p, st);
 }
 template <int NV, int MOST>
 static cudaError_t fwd_types(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
-    return p.h_f32 ? fwd_launch<NV, true, MOST>(p, P, st) : fwd_launch<NV, false, MOST>(p, P, st);
+    if (p.h_f32) return p.w_f32 ? fwd_launch<NV, true, true, MOST>(p, P, st) : fwd_launch<NV, true, false, MOST>(p, P, st);
+    return p.w_f32 ? fwd_launch<NV, false, true, MOST>(p, P, st) : fwd_launch<NV, false, false, MOST>(p, P, st);
 }
-template <int NV, bool H32, bool POST, bool GATE, int MOST>
+template <int NV, bool H32, bool W32, bool POST, bool GATE, int MOST>
 static cudaError_t bwd_launch(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
     const int grid = bwd_grid(p.T, P);
     JoinOut outs{};
@@ -480,20 +471,22 @@ static cudaError_t bwd_launch(const AddNormParams& p, const RowPlan& P, cudaStre
         if (o) outs.out[nsums++] = o;
     const size_t pieces = (size_t)bwd_stages(NV, H32, MOST) * NV * (H32 ? 6 : 4) * P.threads * 16;
     const size_t join = (size_t)nsums * NV * P.threads * 32;
-    cudaError_t e = launch_rows(addnorm_bwd_kernel<NV, H32, POST, GATE, MOST>, grid, P, std::max(pieces, join), p, st);
+    cudaError_t e = launch_rows(addnorm_bwd_kernel<NV, H32, W32, POST, GATE, MOST>, grid, P, std::max(pieces, join), p, st);
     if (e == cudaSuccess && nsums)
         e = launch_pdl(addnorm_join_kernel, dim3((unsigned)(p.d / 32), (unsigned)nsums), dim3(256), 0, st, nullptr, 0,
                        (const float*)p.part, p.d, grid, outs);
     return e;
 }
-template <int NV, bool H32, int MOST>
+template <int NV, bool H32, bool W32, int MOST>
 static cudaError_t bwd_forms(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
-    if (p.w_post) return p.gate ? bwd_launch<NV, H32, true, true, MOST>(p, P, st) : bwd_launch<NV, H32, true, false, MOST>(p, P, st);
-    return p.gate ? bwd_launch<NV, H32, false, true, MOST>(p, P, st) : bwd_launch<NV, H32, false, false, MOST>(p, P, st);
+    if (p.w_post) return p.gate ? bwd_launch<NV, H32, W32, true, true, MOST>(p, P, st) : bwd_launch<NV, H32, W32, true, false, MOST>(p, P, st);
+    return p.gate ? bwd_launch<NV, H32, W32, false, true, MOST>(p, P, st) : bwd_launch<NV, H32, W32, false, false, MOST>(p, P, st);
 }
 template <int NV, int MOST>
 static cudaError_t bwd_types(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
-    return p.h_f32 ? bwd_forms<NV, true, MOST>(p, P, st) : bwd_forms<NV, false, MOST>(p, P, st);
+    if constexpr (NV == 2)
+        if (p.w_f32) return p.h_f32 ? bwd_forms<NV, true, true, MOST>(p, P, st) : bwd_forms<NV, false, true, MOST>(p, P, st);
+    return p.h_f32 ? bwd_forms<NV, true, false, MOST>(p, P, st) : bwd_forms<NV, false, false, MOST>(p, P, st);
 }
 
 cudaError_t launch_addnorm_fwd(const AddNormParams& p, cudaStream_t st) {
