@@ -8,19 +8,24 @@
 // summed by atomics would take five; in exchange there is no fp32 dQ in memory, nothing to clear
 // and no order of arrival.  Scores are formed with the owned rows as tensor-memory lanes (S^T in
 // attn_dkv), so P and dz go back to tensor memory as the left operand of the next product without
-// crossing threads.  Eight warps do the arithmetic (a thread: one row, 64 columns), one issues the
-// products, one loads.
+// crossing threads.  The arithmetic is on the way from one product to the next (S to P to the next S in
+// attn_dkv), so its latency counts, not only its rate: sixteen warps with 32 columns a thread against
+// eight with 64 took 8192 causal tokens from DKV0 to DKV1 us and DQ0 to DQ1.
 #include "lm_attn.cuh"
 
 namespace lm {
 
+// Sixteen arithmetic warps (four warpgroups, a thread: one row, 32 columns) and a warpgroup for the
+// loader's and the issuer's warps: 640 threads start with 96 registers each.
+constexpr int kBwdThreads = 640, kBwdMath = 16, kBwdMathRegs = 104, kBwdIssueRegs = 64;
+static_assert(4 * kBwdMathRegs + kBwdIssueRegs <= 5 * 96, "a register split above the launch's total waits forever");
 constexpr int kQStages = 2;  // attn_dkv: query tiles, and dO tiles, in flight
 
-// A = P or dz in tensor memory: columns [0, 64) of the tile packed at t, [64, 128) at t + 64
+// A = P or dz in tensor memory: each 32 columns of the tile packed at the first 16 of their place
 __device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, uint32_t idesc, bool first) {
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk)
-        umma_bf16_ts(d, t + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), desc(b + kk * 128), idesc, first && kk == 0 ? 0u : 1u);
+        umma_bf16_ts(d, t + (uint32_t)((kk >> 1) * 32 + (kk & 1) * 8), desc(b + kk * 128), idesc, first && kk == 0 ? 0u : 1u);
 }
 
 struct ScoreMath {
@@ -105,7 +110,7 @@ struct DkvCfg {
 };
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
     using C = DkvCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* drain = dsfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
+    volatile int* s_bad = s_abort + 1;  // [4] a warp of the warpgroup gave up
     uint8_t* sk = smem + 1024;
     uint8_t* sv = sk + C::kTileBytes;
     uint8_t* sq = sv + C::kTileBytes;
@@ -143,11 +148,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mbar_init(smem_u32(kvfull), 1);
         mbar_init(smem_u32(sfull), 1);
-        mbar_init(smem_u32(pfull), 8);
+        mbar_init(smem_u32(pfull), kBwdMath);
         mbar_init(smem_u32(dpfull), 1);
-        mbar_init(smem_u32(dsfull), 8);
+        mbar_init(smem_u32(dsfull), kBwdMath);
         mbar_init(smem_u32(drain), 1);
-        *s_abort = s_bad[0] = s_bad[1] = 0;
+        *s_abort = s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tma_prefetch_map(&maps.dO);
     }
     __syncwarp();
-    if (warp == 8) {
+    if (warp == kBwdMath) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -169,9 +174,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int qt0 = uni(rf.qlo / kTile), nt = uni(rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0);
     const int N = nt * n;  // (head of the group, query tile), heads outermost
 
-    if (warp >= 8) {
-        regs_down<kIssueRegs>();
-        if (warp == 9) {  // ---------------- loader
+    if (warp >= kBwdMath) {
+        regs_down<kBwdIssueRegs>();
+        if (warp == kBwdMath + 1) {  // ---------------- loader
             if (lane == 0 && N > 0) {
                 bool ok = true;
                 mbar_expect_tx(smem_u32(kvfull), 2 * C::kTileBytes);
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 in = drain_fills(smem_u32(&ofull[0]), kQStages, no, p.wait_ns) && in;
                 if (!in) attn_error(p, 6, 5);
             }
-        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
+        } else if (warp == kBwdMath && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // Q and dO are [query][dim]: MN-major
@@ -274,12 +279,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
         }
-    } else {  // ---------------- arithmetic: one key row, 64 query columns per thread
-        regs_up<kMathRegs>();
-        const int half = warp >> 2;
+    } else {  // ---------------- arithmetic: one key row, 32 query columns per thread
+        regs_up<kBwdMathRegs>();
+        const int part = warp >> 2;
         const int k = k0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tsw = ts + lanes + half * 64, tdpw = tdp + lanes + half * 64;
+        const uint32_t tsw = ts + lanes + part * 32, tdpw = tdp + lanes + part * 32;
         TokRange r{0, 0, 0, 0};
         if (k < p.T) r = tok_range(p, k);
         ScoreMath S = score_math<MODE>(p);
@@ -287,29 +292,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // one query tile, its scores ready; tiles with hidden pairs have code of their own
         auto tile = [&](int it, const float* row, float dist, int a, int z, auto hides) {
             constexpr bool HIDDEN = decltype(hides)::value;
-            float x[64];
-            uint32_t pk[32];
+            float x[32];
+            uint32_t pk[16];
             tmem_ld_f32<0>(tsw, x);
-            tmem_ld_f32<32>(tsw + 32, x);
+            const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
+            const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
             tmem_ld_wait_f32<0>(x);
-            tmem_ld_wait_f32<32>(x);
-            uint32_t bits[2] = {~0u, ~0u};
-            if (HIDDEN) {
-                bits[0] = bits_between(a, z);
-                bits[1] = bits_between(a - 32, z - 32);
-            }
+            if (some) {  // (a chunk that none of the warp's keys is seen from has no exponentials)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                // (a chunk that none of the warp's keys is seen from has no exponentials)
-                if (HIDDEN && !__any_sync(0xffffffffu, bits[b] != 0u)) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[b * 32 + e] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = 0u;
-                    continue;
-                }
-#pragma unroll
-                for (int e = b * 32; e < b * 32 + 32; e += 4) {
+                for (int e = 0; e < 32; e += 4) {
                     const float4 nl = *reinterpret_cast<const float4*>(row + e);
                     const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
@@ -319,8 +310,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                             make_float2(nls[f], nls[f + 1]), bend);
                         float2 P = make_float2(ex2(y.x), ex2(y.y));
                         if (HIDDEN) {
-                            if (!(bits[b] >> ((e + f) & 31) & 1u)) P.x = 0.f;
-                            if (!(bits[b] >> ((e + f + 1) & 31) & 1u)) P.y = 0.f;
+                            if (!(bits >> (e + f) & 1u)) P.x = 0.f;
+                            if (!(bits >> (e + f + 1) & 1u)) P.y = 0.f;
                         }
                         pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
                         if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
@@ -328,24 +319,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         x[e + f + 1] = P.y;
                     }
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = 0u;
             }
-            tmem_st_x32(tsw, pk);
+            tmem_st_x16(tsw, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(pfull));
             if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) return false;
             tc_fence_after();
-            float y[64];
-            tmem_ld_f32<0>(tdpw, y);
-            tmem_ld_f32<32>(tdpw + 32, y);
-            tmem_ld_wait_f32<0>(y);
-            tmem_ld_wait_f32<32>(y);
+            if (some) {
+                float y[32];
+                tmem_ld_f32<0>(tdpw, y);
+                tmem_ld_wait_f32<0>(y);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (HIDDEN && !__any_sync(0xffffffffu, bits[b] != 0u)) continue;  // (pk is zero there)
-#pragma unroll
-                for (int e = b * 32; e < b * 32 + 32; e += 4) {
+                for (int e = 0; e < 32; e += 4) {
                     const float4 dl = *reinterpret_cast<const float4*>(row + kTile + e);
                     const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
@@ -353,14 +343,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
                         d = __fmul2_rn(d, make_float2(x[e + f], x[e + f + 1]));
                         if (HIDDEN) {  // (not 0 x what a padding key's dP holds)
-                            if (!(bits[b] >> ((e + f) & 31) & 1u)) d.x = 0.f;
-                            if (!(bits[b] >> ((e + f + 1) & 31) & 1u)) d.y = 0.f;
+                            if (!(bits >> (e + f) & 1u)) d.x = 0.f;
+                            if (!(bits >> (e + f + 1) & 1u)) d.y = 0.f;
                         }
                         pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
                     }
                 }
             }
-            tmem_st_x32(tdpw, pk);
+            tmem_st_x16(tdpw, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -371,8 +361,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int hh = 0; ok && hh < n; ++hh) {
             if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
             for (int qt = qt0; qt < qt0 + nt; ++qt, ++it) {
-                const int q0 = qt * kTile + half * 64;
-                const float* row = srow + (it % kQStages) * 2 * kTile + half * 64;
+                const int q0 = qt * kTile + part * 32;
+                const float* row = srow + (it % kQStages) * 2 * kTile + part * 32;
                 // every query of the tile sees every key of this one, or some pair is hidden
                 const bool hidden = qt * kTile < rl.qlo || (qt + 1) * kTile > rf.qhi;
                 const int a = r.qlo - q0, z = r.qhi - q0;
@@ -388,27 +378,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (!ok) break;
             }
         }
-        // warpgroup 0 writes dV, warpgroup 1 dK
+        // DP / 64 warpgroups write dV, as many dK, a box of 64 dims each
         if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
         tc_fence_after();
         if (!ok && lane == 0) {
             attn_error(p, 6, 3);
             *s_abort = 1;
         }
-        if (!group_ok(ok, s_bad + half, 1 + half)) {
-            // (nothing is written)
-        } else {
-            const int r128 = (warp & 3) * 32 + lane;
-            for (int b = 0; b < DP / 64; ++b) {  // (staged where the query tiles were)
-                uint8_t* box = sq + half * C::kTileBytes + b * kBoxBytes;
-                stage_row(box, r128, (half ? tdk : tdv) + lanes + b * 64, half ? p.scale : 1.f, N > 0);
-                store_box(half ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + half, r128 == 0);
-            }
+        constexpr int kBoxes = DP / 64;
+        if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes) {  // (staged where the query tiles were)
+            const int r128 = (warp & 3) * 32 + lane, b = part % kBoxes;
+            const bool key = part >= kBoxes;
+            uint8_t* box = sq + part * kBoxBytes;
+            stage_row(box, r128, (key ? tdk : tdv) + lanes + b * 64, key ? p.scale : 1.f, N > 0);
+            store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kBwdMath) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -424,7 +412,7 @@ struct DqCfg {
 };
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
     using C = DqCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -440,7 +428,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t* drain = dsfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
+    volatile int* s_bad = s_abort + 1;  // [4] a warp of the warpgroup gave up
     uint8_t* sq = smem + 1024;
     uint8_t* so = sq + C::kTileBytes;
     uint8_t* sk = so + C::kTileBytes;
@@ -465,9 +453,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(smem_u32(&sfull[0]), 1);
         mbar_init(smem_u32(&sfull[1]), 1);
         mbar_init(smem_u32(dpfull), 1);
-        mbar_init(smem_u32(dsfull), 8);
+        mbar_init(smem_u32(dsfull), kBwdMath);
         mbar_init(smem_u32(drain), 1);
-        *s_abort = s_bad[0] = s_bad[1] = 0;
+        *s_abort = s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -475,7 +463,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tma_prefetch_map(&maps.dO);
     }
     __syncwarp();
-    if (warp == 8) {
+    if (warp == kBwdMath) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -488,9 +476,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const TokRange rf = tok_range(p, q0), rl = tok_range(p, min(q0 + kTile, p.T) - 1);
     const int kt0 = uni(rf.lo / kTile), N = uni(rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0);
 
-    if (warp >= 8) {
-        regs_down<kIssueRegs>();
-        if (warp == 9) {  // ---------------- loader
+    if (warp >= kBwdMath) {
+        regs_down<kBwdIssueRegs>();
+        if (warp == kBwdMath + 1) {  // ---------------- loader
             if (lane == 0 && N > 0) {
                 bool ok = true;
                 mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
@@ -499,8 +487,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tma_load_3d(smem_u32(so + b * kBoxBytes), &maps.dO, smem_u32(qfull), b * 64, h, q0);
                 }
                 uint32_t nk = 0, nv = 0;
-                while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, K_2 | V_1, K_3 | V_2, ... as the products take them
-                    const bool key = nk < (uint32_t)N && (nk == 0 || nk < nv + 2);
+                while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, V_1, ... (V_j asked for after K_{j+1} came 22 % later)
+                    const bool key = nk == nv;
                     const uint32_t i = key ? nk : nv, st = key ? i % C::kKStages : i % C::kVStages;
                     const uint32_t ph = (key ? i / C::kKStages : i / C::kVStages) & 1u;
                     const uint32_t bar = smem_u32(key ? &kfull[st] : &vfull[st]);
@@ -525,7 +513,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
                 if (!in) attn_error(p, 7, 5);
             }
-        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
+        } else if (warp == kBwdMath && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
@@ -577,9 +565,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
         }
-    } else {  // ---------------- arithmetic: one query row, 64 key columns per thread
-        regs_up<kMathRegs>();
-        const int half = warp >> 2;
+    } else {  // ---------------- arithmetic: one query row, 32 key columns per thread
+        regs_up<kBwdMathRegs>();
+        const int part = warp >> 2;
         const int i = q0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         TokRange r{0, 0, 0, 0};
@@ -594,25 +582,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         bool ok = true;
         auto tile = [&](int j, uint32_t tsw, float dist, int a, int z, auto hides) {
             constexpr bool HIDDEN = decltype(hides)::value;
-            float x[64], y[64];
+            float x[32], y[32];
+            uint32_t pk[16];
             tmem_ld_f32<0>(tsw, x);
-            tmem_ld_f32<32>(tsw + 32, x);
+            const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
+            const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
             tmem_ld_wait_f32<0>(x);
-            tmem_ld_wait_f32<32>(x);
-            uint32_t bits[2] = {~0u, ~0u};
-            bool some[2] = {true, true};
-            if (HIDDEN) {
+            if (some) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    bits[b] = bits_between(a - 32 * b, z - 32 * b);
-                    some[b] = __any_sync(0xffffffffu, bits[b] != 0u);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (HIDDEN && !some[b]) continue;
-#pragma unroll
-                for (int e = b * 32; e < b * 32 + 32; e += 2) {
+                for (int e = 0; e < 32; e += 2) {
                     float2 bend = two(1.f);
                     const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(nlse), bend);
                     float2 P = make_float2(ex2(v.x), ex2(v.y));
@@ -623,30 +601,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) return false;
             tc_fence_after();
-            tmem_ld_f32<0>(tdp + lanes + half * 64, y);
-            tmem_ld_f32<32>(tdp + lanes + half * 64 + 32, y);
-            tmem_ld_wait_f32<0>(y);
-            tmem_ld_wait_f32<32>(y);
-            uint32_t pk[32];
+            if (some) {
+                tmem_ld_f32<0>(tdp + lanes + part * 32, y);
+                tmem_ld_wait_f32<0>(y);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (HIDDEN && !some[b]) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = 0u;
-                    continue;
-                }
-#pragma unroll
-                for (int e = b * 32; e < b * 32 + 32; e += 2) {
+                for (int e = 0; e < 32; e += 2) {
                     float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(ndelta));
                     d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
                     if (HIDDEN) {
-                        if (!(bits[b] >> (e & 31) & 1u)) d.x = 0.f;
-                        if (!(bits[b] >> ((e + 1) & 31) & 1u)) d.y = 0.f;
+                        if (!(bits >> e & 1u)) d.x = 0.f;
+                        if (!(bits >> (e + 1) & 1u)) d.y = 0.f;
                     }
                     pk[e / 2] = pack_bf16x2(d.x, d.y);
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = 0u;
             }
-            tmem_st_x32(tsw, pk);
+            tmem_st_x16(tsw, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -654,8 +626,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             return true;
         };
         for (int j = 0; j < N; ++j) {
-            const uint32_t tsw = tmem + lanes + (j & 1) * kTile + half * 64;
-            const int kt = (kt0 + j) * kTile, k0 = kt + half * 64;
+            const uint32_t tsw = tmem + lanes + (j & 1) * kTile + part * 32;
+            const int kt = (kt0 + j) * kTile, k0 = kt + part * 32;
             const bool hidden = kt < rl.lo || kt + kTile > rf.hi;
             const int a = r.lo - k0, z = r.hi - k0;
             const float dist = (float)(i - k0);
@@ -673,18 +645,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             attn_error(p, 7, 3);
             *s_abort = 1;
         }
-        if (!group_ok(ok, s_bad + half, 1 + half)) {
-            // (nothing is written)
-        } else if (half < DP / 64) {  // each warpgroup 64 dims, staged where the queries were
+        // DP / 64 warpgroups write a box of 64 dims each, staged where the queries were
+        if (group_ok(ok, s_bad + part, 1 + part) && part < DP / 64) {
             const int r128 = (warp & 3) * 32 + lane;
-            uint8_t* box = sq + half * kBoxBytes;
-            stage_row(box, r128, tdq + lanes + half * 64, p.scale, N > 0);
-            store_box(&maps.dQ, box, half * 64, h, q0, 1 + half, r128 == 0);
+            uint8_t* box = sq + part * kBoxBytes;
+            stage_row(box, r128, tdq + lanes + part * 64, p.scale, N > 0);
+            store_box(&maps.dQ, box, part * 64, h, q0, 1 + part, r128 == 0);
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kBwdMath) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -698,7 +669,7 @@ cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, cudaStream_t st
                                                DkvCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hk;
-    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 template <int DP, int MODE>
 cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
@@ -706,7 +677,7 @@ cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st)
                                                DqCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hq;
-    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
 template <int DP, int MODE>
