@@ -108,6 +108,57 @@ __device__ __forceinline__ void tmem_ld_wait_f32(float (&x)[N]) {
                  :
                  : "memory");
 }
+template <int AT, int N>
+__device__ __forceinline__ void tmem_ld_wait16_f32(float (&x)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[AT + 0]), "+f"(x[AT + 1]), "+f"(x[AT + 2]), "+f"(x[AT + 3]), "+f"(x[AT + 4]), "+f"(x[AT + 5]), "+f"(x[AT + 6]), "+f"(x[AT + 7]),
+                   "+f"(x[AT + 8]), "+f"(x[AT + 9]), "+f"(x[AT + 10]), "+f"(x[AT + 11]), "+f"(x[AT + 12]), "+f"(x[AT + 13]), "+f"(x[AT + 14]), "+f"(x[AT + 15])
+                 :
+                 : "memory");
+}
+// The same with a row's columns over four lanes: 16 rows of the warp's quarter (taddr names the first,
+// 0 or 16 of the 32), 8 columns a group of four values: lane T holds row T / 4, columns 2 (T % 4) and
+// one more, then the same of row T / 4 + 8.  A row's maximum then takes two shuffles, and two warps share
+// a quarter's rows instead of its columns.
+template <int AT, int N>
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, float (&x)[N]) {
+    static_assert(AT + 32 <= N, "");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(x[AT + 0]), "=f"(x[AT + 1]), "=f"(x[AT + 2]), "=f"(x[AT + 3]), "=f"(x[AT + 4]), "=f"(x[AT + 5]), "=f"(x[AT + 6]), "=f"(x[AT + 7]),
+          "=f"(x[AT + 8]), "=f"(x[AT + 9]), "=f"(x[AT + 10]), "=f"(x[AT + 11]), "=f"(x[AT + 12]), "=f"(x[AT + 13]), "=f"(x[AT + 14]), "=f"(x[AT + 15]),
+          "=f"(x[AT + 16]), "=f"(x[AT + 17]), "=f"(x[AT + 18]), "=f"(x[AT + 19]), "=f"(x[AT + 20]), "=f"(x[AT + 21]), "=f"(x[AT + 22]), "=f"(x[AT + 23]),
+          "=f"(x[AT + 24]), "=f"(x[AT + 25]), "=f"(x[AT + 26]), "=f"(x[AT + 27]), "=f"(x[AT + 28]), "=f"(x[AT + 29]), "=f"(x[AT + 30]), "=f"(x[AT + 31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag16(uint32_t taddr, const float (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+        "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+        : "memory");
+}
+template <int AT, int N>
+__device__ __forceinline__ void tmem_ld_frag16(uint32_t taddr, float (&x)[N]) {
+    static_assert(AT + 16 <= N, "");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(x[AT + 0]), "=f"(x[AT + 1]), "=f"(x[AT + 2]), "=f"(x[AT + 3]), "=f"(x[AT + 4]), "=f"(x[AT + 5]), "=f"(x[AT + 6]), "=f"(x[AT + 7]),
+          "=f"(x[AT + 8]), "=f"(x[AT + 9]), "=f"(x[AT + 10]), "=f"(x[AT + 11]), "=f"(x[AT + 12]), "=f"(x[AT + 13]), "=f"(x[AT + 14]), "=f"(x[AT + 15])
+        : "r"(taddr));
+}
+// Packed pairs (bf16) of such groups: lane T holds the pair 2 (T % 4) of row T / 4, then of row T / 4 + 8.
+__device__ __forceinline__ void tmem_st_pairs16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

@@ -1,19 +1,19 @@
 // Attention forward (include/lora_layer.h) on the tensor cores.
 //
-// One CTA takes 256 queries of one head as two tiles of 128 and walks the 128-key tiles that any of
-// them sees.  For each query tile w and key tile j:
+// One CTA per SM stays and takes items of 256 queries of one head as two tiles of 128, walking the
+// 128-key tiles that any of them sees.  For each query tile w and key tile j:
 //   S_w = Q_w K_j^T                              (tcgen05, both operands in shared memory)
-//   P_w = 2^{S c - m}, l += row sums             (four warps, one thread per query row)
+//   P_w = 2^{S c - m}, l += row sums             (eight warps)
 //   O_w += P_w V_j                               (tcgen05, P_w from tensor memory, where it replaces S_w)
-// The two query tiles take turns: while the tensor cores work on one, the other's four warps form
-// its exponentials, so neither waits for the other as long as 2 x 128 x d x 128 multiply-adds take
-// longer than 128 x 128 exponentials with their loads, maxima, sums and packing.  The running
-// maximum m follows the row only when it has grown by more than 8 (a factor 256 in the weights): the
-// weights then stay below 2^8, exact in their scale, and O_w is rescaled a few times per row
-// instead of once per key tile.  Sums are fp32.  P is rounded to bf16 for the second product; on tiles with
-// hidden keys what the rounding left out is multiplied too (as a second left operand, in the other
-// half of S_w's place): rows of few keys have no other weights to average their error with, and the
-// backward takes differences against their O.  That is one more product on the tiles along the
+// The two query tiles take turns: while the tensor cores work on one, the other's warps form its
+// exponentials.  The first scores of the next item are formed while this one's rows are written.  The
+// weights go to the tensor cores 64 keys at a time, so the second product starts half a tile early.
+// The running maximum m follows the row only when it has grown by more than 8 (a factor 256 in the
+// weights): the weights then stay below 2^8, exact in their scale, and O_w is rescaled a few times per
+// row instead of once per key tile.  Sums are fp32.  P is rounded to bf16 for the second product; on
+// tiles with hidden keys what the rounding left out is multiplied too (as a second left operand, in the
+// other half of S_w's place): rows of few keys have no other weights to average their error with, and
+// the backward takes differences against their O.  That is one more product on the tiles along the
 // diagonal and at document ends; dQ of packed prefixes went from 2.51e-3 to 2.4e-3 of its norm off.
 // Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
 // memory: S_0, S_1, O_0, O_1 of 128 columns each.
@@ -22,58 +22,90 @@
 namespace lm {
 
 constexpr float kRescale = 8.f;
+// Sixteen softmax warps and a warpgroup for the loader's and the issuer's: 640 threads start with 96
+// registers each.
+constexpr int kFwdThreads = 640, kFwdMath = 16, kFwdMathRegs = 104, kFwdIssueRegs = 64;
+static_assert(4 * kFwdMathRegs + kFwdIssueRegs <= 5 * 96, "a register split above the launch's total waits forever");
 
 template <int DP>
 struct FwdCfg {
     static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
     static constexpr int kSlots = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 2048 + (2 + kSlots) * kTileBytes;
+    static constexpr int kSmem = 3072 + (2 + kSlots) * kTileBytes;
 };
 
 struct FwdMaps {
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, k, v;
 };
 
 // the key tiles [j0, j1) that the query rows [q0, q0 + 128) may see
 struct TileSpan {
     int j0, j1;
     int lo_max, hi_min;  // keys in [lo_max, hi_min) are seen by every row
+    __device__ __forceinline__ bool any() const { return j1 > j0; }
     __device__ __forceinline__ bool hides(int j) const { return j * kTile < lo_max || (j + 1) * kTile > hi_min; }
+    __device__ __forceinline__ bool has(int j) const { return j >= j0 && j < j1; }
 };
 __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
     if (q0 >= p.T) return TileSpan{0, 0, 0, 0};
     const TokRange a = tok_range(p, q0), b = tok_range(p, min(q0 + kTile, p.T) - 1);
-    const int lo = uni(a.lo), hi = uni(b.hi);
-    if (hi <= lo) return TileSpan{0, 0, 0, 0};
-    return TileSpan{lo / kTile, (hi + kTile - 1) / kTile, uni(b.lo), uni(a.hi)};
+    if (b.hi <= a.lo) return TileSpan{0, 0, 0, 0};
+    return TileSpan{a.lo / kTile, (b.hi + kTile - 1) / kTile, b.lo, a.hi};
+}
+// Item k of this CTA: the heavier items first (under a causal mask the last queries see the most keys),
+// dealt out forwards and backwards in turn, so that every CTA gets about the same work.
+struct Item {
+    int h, q0;
+    TileSpan span[2];
+    int J0, J1;
+    bool valid;
+};
+__device__ __forceinline__ Item item_of(const AttnParams& p, int k) {
+    const int nqb = (p.T + 2 * kTile - 1) / (2 * kTile), G = (int)gridDim.x;
+    const int idx = k & 1 ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
+    Item it;
+    it.valid = idx < nqb * p.hq;
+    it.h = idx % p.hq;
+    it.q0 = (nqb - 1 - idx / p.hq) * 2 * kTile;
+    it.span[0] = it.span[1] = TileSpan{0, 0, 0, 0};
+    it.J0 = it.J1 = 0;
+    if (it.valid) {
+        it.span[0] = key_tiles(p, it.q0);
+        it.span[1] = key_tiles(p, it.q0 + kTile);
+        it.J0 = it.span[0].any() ? it.span[0].j0 : it.span[1].j0;
+        if (it.span[1].any()) it.J0 = min(it.J0, it.span[1].j0);
+        it.J1 = max(it.span[0].j1, it.span[1].j1);
+    }
+    return it;
+}
+__device__ __forceinline__ int rounds_of(const AttnParams& p) {
+    const int n = (p.T + 2 * kTile - 1) / (2 * kTile) * p.hq;
+    return (n + (int)gridDim.x - 1) / (int)gridDim.x;
 }
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwdMaps maps) {
     using C = FwdCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + C::kSlots;
-    uint64_t* qfull = empty + C::kSlots;
-    uint64_t* sfull = qfull + 2;   // [2] scores ready
-    uint64_t* pfull = sfull + 2;   // [2][2] weights of the first, of the last 64 keys written (and the scores read)
-    uint64_t* hdone = pfull + 4;   // [2] the first half of a P V product done (once a tile)
-    uint64_t* odone = hdone + 2;   // [2] the last product of the row tile done (once)
-    uint64_t* drain = odone + 2;
+    uint64_t* qfull = empty + C::kSlots;  // [2] the item's queries are there
+    uint64_t* qempty = qfull + 2;         // [2] and are done with
+    uint64_t* sfull = qempty + 2;         // [2] scores ready
+    uint64_t* pfull = sfull + 2;          // [2][2] weights of the first, of the last 64 keys written
+    uint64_t* hdone = pfull + 4;          // [2] the first half of a P V product done (once a tile)
+    uint64_t* odone = hdone + 2;          // [2] the last product of the item done
+    uint64_t* lready = odone + 2;         // [2][4] the quarter's row sums exchanged
+    uint64_t* drain = lready + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* s_bad = s_abort + 1;  // [2] a warp of the warpgroup gave up
-    uint8_t* sq = smem + 1024;
+    float* s_inv = reinterpret_cast<float*>(smem + 1024);  // [2][128] 1 / l
+    uint8_t* sq = smem + 2048;
     uint8_t* ring = sq + 2 * C::kTileBytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the longest rows first: under a causal mask the last queries see the most keys
-    const int nqb = (p.T + 2 * kTile - 1) / (2 * kTile);
-    const int h = (int)blockIdx.x % p.hq, q0 = (nqb - 1 - (int)blockIdx.x / p.hq) * 2 * kTile;
-    const int g = h / (p.hq / p.hk);
-
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
@@ -82,22 +114,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&qfull[w]), 1);
+            mbar_init(smem_u32(&qempty[w]), 1);
             mbar_init(smem_u32(&sfull[w]), 1);
-            mbar_init(smem_u32(&pfull[2 * w]), 4);
-            mbar_init(smem_u32(&pfull[2 * w + 1]), 4);
+            mbar_init(smem_u32(&pfull[2 * w]), 8);
+            mbar_init(smem_u32(&pfull[2 * w + 1]), 8);
             mbar_init(smem_u32(&hdone[w]), 1);
             mbar_init(smem_u32(&odone[w]), 1);
+            for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&lready[4 * w + q]), 2);
         }
         mbar_init(smem_u32(drain), 1);
-        *s_abort = s_bad[0] = s_bad[1] = 0;
+        *s_abort = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
         tma_prefetch_map(&maps.v);
-        tma_prefetch_map(&maps.o);
     }
     __syncwarp();
-    if (warp == 8) {
+    if (warp == kFwdMath) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -106,109 +139,128 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_after();
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
-    const TileSpan span[2] = {key_tiles(p, q0), key_tiles(p, q0 + kTile)};
-    int J0 = span[0].j0, J1 = span[0].j1;
-    if (span[1].j1 > span[1].j0) {
-        J0 = J1 > J0 ? min(J0, span[1].j0) : span[1].j0;
-        J1 = max(J1, span[1].j1);
-    }
+    const int rounds = rounds_of(p), group = p.hq / p.hk;
 
-    if (warp >= 8) {
-        regs_down<kIssueRegs>();
-        if (warp == 9) {  // ---------------- loader
-            if (lane == 0 && J1 > J0) {
+    if (warp >= kFwdMath) {
+        regs_down<kFwdIssueRegs>();
+        if (warp == kFwdMath + 1) {  // ---------------- loader
+            if (lane == 0) {
                 bool ok = true;
-                auto query = [&](int w) {
-                    mbar_expect_tx(smem_u32(&qfull[w]), C::kTileBytes);
-                    for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, smem_u32(&qfull[w]), b * 64, h,
-                                    q0 + w * kTile);
-                };
-                query(0);  // then K: the first scores wait for these alone
-                uint32_t n = 0;
-                for (int j = J0; ok && j < J1; ++j)
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
-                        if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+                uint32_t n = 0, nq[2] = {0, 0};  // tiles and queries asked for
+                for (int k = 0; ok && k < rounds; ++k) {
+                    const Item it = item_of(p, k);
+                    auto query = [&](int w) {
+                        if (!it.span[w].any()) return true;
+                        if (!mbar_wait(smem_u32(&qempty[w]), (nq[w] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;
+                        const uint32_t bar = smem_u32(&qfull[w]);
+                        mbar_expect_tx(bar, C::kTileBytes);
                         for (int b = 0; b < DP / 64; ++b)
-                            tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
-                                        smem_u32(&full[s]), b * 64, g, j * kTile);
-                        if (n == 0) query(1);
-                    }
+                            tma_load_3d(smem_u32(sq + w * C::kTileBytes + b * kBoxBytes), &maps.q, bar, b * 64, it.h,
+                                        it.q0 + w * kTile);
+                        ++nq[w];
+                        return true;
+                    };
+                    ok = query(0);  // then K, then the other queries: the first scores wait for what they need
+                    for (int j = it.J0; ok && j < it.J1; ++j)
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
+                            if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+                            for (int b = 0; b < DP / 64; ++b)
+                                tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
+                                            smem_u32(&full[s]), b * 64, it.h / group, j * kTile);
+                            ++n;
+                            if (j == it.J0 && kv == 0 && !query(1)) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                }
                 if (!ok) {
                     attn_error(p, 5, 1);
                     *s_abort = 1;
                 }
                 // nothing may land in shared memory after the CTA has gone
                 volatile int never = 0;
-                bool in = mbar_wait(smem_u32(&qfull[0]), 0, &never, p.wait_ns);
-                if (n > 0) in = mbar_wait(smem_u32(&qfull[1]), 0, &never, p.wait_ns) && in;
-                if (!drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns) || !in) attn_error(p, 5, 5);
+                bool in = drain_fills(smem_u32(&full[0]), C::kSlots, n, p.wait_ns);
+                for (int w = 0; w < 2; ++w)
+                    if (nq[w]) in = mbar_wait(smem_u32(&qfull[w]), (nq[w] - 1u) & 1u, &never, p.wait_ns) && in;
+                if (!in) attn_error(p, 5, 5);
             }
-        } else if (warp == 8 && elect_one()) {  // ---------------- tensor cores
+        } else if (warp == kFwdMath && elect_one()) {  // ---------------- tensor cores
             const int ksteps = (p.d + 15) / 16;
             const uint32_t ids = make_idesc_bf16(kTile, kTile, false, false);
             const uint32_t ido = make_idesc_bf16(kTile, ksteps * 16, false, true);  // V is [key][dim]: MN-major
             int in0, in1;
             inside_tokens(p, in0, in1);
             bool ok = true;
-            for (int j = J0; ok && j <= J1 && J1 > J0; ++j) {
-                const uint32_t nk = 2 * (j - J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
-                const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
-                const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
-                if (j > J0) {
-                    ok = mbar_wait(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
-                    if (!ok) break;
-                    clear_padding(ring + (nv % C::kSlots) * C::kTileBytes, DP / 64, (j - 1) * kTile, in0, in1);
-                }
-                if (j < J1) {
-                    ok = mbar_wait(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
-                    if (!ok) break;
-                }
-                tc_fence_after();
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
-                    if (j > span[w].j0 && j <= span[w].j1) {  // O_w += P_w V_{j-1}
-                        const uint32_t n = (uint32_t)(j - 1 - span[w].j0);
-                        const bool hides = span[w].hides(j - 1);
-#pragma unroll
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = mbar_wait(smem_u32(&pfull[2 * w + half]), n & 1u, s_abort, p.wait_ns);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t a = ts + half * 32;
-                            const uint32_t b = desc_cols(sv) + half * 512;
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, (n || half || kk) ? 1u : 0u);
-                            if (hides) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
-                            }
-                            if (half == 0) umma_commit(smem_u32(&hdone[w]));
-                            else if (j == span[w].j1) umma_commit(smem_u32(&odone[w]));
-                        }
+            uint32_t n = 0, nt[2] = {0, 0}, nq[2] = {0, 0};  // ring position of K_{J0}; tiles, items of each query tile
+            Item next = item_of(p, 0);
+            for (int k = 0; ok && k < rounds; ++k) {
+                const Item it = next;
+                next = item_of(p, k + 1);
+                if (it.J1 <= it.J0) continue;
+                for (int j = it.J0; ok && j <= it.J1; ++j) {
+                    const uint32_t nk = n + 2 * (uint32_t)(j - it.J0), nv = nk - 1;  // ring positions of K_j and V_{j-1}
+                    const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
+                    const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
+                    if (j > it.J0) {
+                        ok = mbar_wait(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+                        if (!ok) break;
+                        clear_padding(ring + (nv % C::kSlots) * C::kTileBytes, DP / 64, (j - 1) * kTile, in0, in1);
+                    }
+                    if (j < it.J1) {
+                        ok = mbar_wait(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
                         if (!ok) break;
                     }
-                    if (j >= span[w].j0 && j < span[w].j1) {  // S_w = Q_w K_j^T
-                        if (j == span[w].j0) {
-                            ok = mbar_wait(smem_u32(&qfull[w]), 0, s_abort, p.wait_ns);
+                    tc_fence_after();
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
+                        const TileSpan& sp = it.span[w];
+                        if (j > it.J0 && sp.has(j - 1)) {  // O_w += P_w V_{j-1}
+                            const bool first = j - 1 == sp.j0, hides = sp.hides(j - 1);
+#pragma unroll
+                            for (int half = 0; half < 2 && ok; ++half) {
+                                ok = mbar_wait(smem_u32(&pfull[2 * w + half]), (nt[w] - 1u) & 1u, s_abort, p.wait_ns);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint32_t a = ts + half * 32;
+                                const uint32_t b = desc_cols(sv) + half * 512;
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, first && !half && !kk ? 0u : 1u);
+                                if (hides) {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
+                                }
+                                if (half == 0) umma_commit(smem_u32(&hdone[w]));
+                                else if (j == sp.j1) umma_commit(smem_u32(&odone[w]));
+                            }
                             if (!ok) break;
-                            tc_fence_after();
                         }
-                        mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids);
-                        umma_commit(smem_u32(&sfull[w]));
+                        if (sp.has(j)) {  // S_w = Q_w K_j^T
+                            if (j == sp.j0) {
+                                ok = mbar_wait(smem_u32(&qfull[w]), nq[w] & 1u, s_abort, p.wait_ns);
+                                if (!ok) break;
+                                ++nq[w];
+                                tc_fence_after();
+                            }
+                            mma_rows<DP>(ts, desc_rows(smem_u32(sq + w * C::kTileBytes)), desc_rows(sk), ksteps, ids);
+                            umma_commit(smem_u32(&sfull[w]));
+                            ++nt[w];
+                            if (j + 1 == sp.j1) umma_commit(smem_u32(&qempty[w]));
+                        }
                     }
+                    if (!ok) break;
+                    if (j > it.J0) umma_commit(smem_u32(&empty[nv % C::kSlots]));
+                    if (j < it.J1) umma_commit(smem_u32(&empty[nk % C::kSlots]));
                 }
-                if (!ok) break;
-                if (j > J0) umma_commit(smem_u32(&empty[nv % C::kSlots]));
-                if (j < J1) umma_commit(smem_u32(&empty[nk % C::kSlots]));
+                n += 2 * (uint32_t)(it.J1 - it.J0);
             }
             if (!ok) {
                 attn_error(p, 5, 2);
@@ -218,180 +270,218 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
         }
-    } else {  // ---------------- softmax: warpgroup w, one thread per query row
-        regs_up<kMathRegs>();
-        const int w = warp >> 2;
-        const int i = q0 + w * kTile + (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + w * kTile, to = tmem + lanes + 2 * kTile + w * DP;
-        TokRange r{0, 0, 0, 0};
-        if (i < p.T) r = tok_range(p, i);
-        const int j0 = span[w].j0, j1 = span[w].j1;
-        const float slope = MODE != ATTN_PLAIN && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+    } else {  // ---------------- softmax: 16 query rows a warp, two of them (and a quarter of each) a thread
+        regs_up<kFwdMathRegs>();
+        const int w = warp >> 3, quarter = warp & 3, sub = (warp >> 2) & 1;
+        const int row0 = quarter * 32 + sub * 16 + (lane >> 2), c0 = 2 * (lane & 3);  // rows row0, row0 + 8
+        const uint32_t half_lanes = (uint32_t)(quarter * 32 + sub * 16) << 16, all_lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + half_lanes + w * kTile, to = tmem + half_lanes + 2 * kTile + w * DP;
         // scores in units of log 2: x = s c + bias (plain), or cap tanh(s scale / cap) log2 e + bias
         const float c = MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
         const float cap = p.cap * kLog2e;
         const float cx = MODE == ATTN_PLAIN ? c : 1.f;
-        float m = -INFINITY, l = 0.f;  // running maximum, sum of weights
+        uint32_t nt = 0, nq = 0;
         bool ok = true;
-        // 64 keys, one step of the running softmax; tiles with hidden keys have code of their own
-        auto step = [&](int j, int half, float(&x)[64], auto hides) {
-            constexpr bool HIDDEN = decltype(hides)::value;
-            const int k0 = j * kTile + half * 64;
-            if (MODE != ATTN_PLAIN) {
-                const float dist = (float)(i - k0);
+        Item next = item_of(p, 0);
+        for (int k = 0; ok && k < rounds; ++k) {
+            const Item it = next;
+            next = item_of(p, k + 1);
+            if (!it.valid) continue;
+            const TileSpan sp = w ? it.span[1] : it.span[0];
+            const int i0 = it.q0 + w * kTile + row0;
+            int lo[2] = {0, 0}, hi[2] = {0, 0};
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
-                    float v = x[e] * c;
-                    if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
-                    x[e] = fmaf(-slope, fabsf(dist - (float)e), v);
+            for (int r = 0; r < 2; ++r)
+                if (i0 + 8 * r < p.T) {
+                    const TokRange t = tok_range(p, i0 + 8 * r);
+                    lo[r] = t.lo - c0;  // (in terms of this lane's first column)
+                    hi[r] = t.hi - c0;
                 }
-            }
-            // on a tile with hidden keys most chunks of 32 keys are seen in full, or not at all, by all rows of
-            // the warp: only the others are masked key by key, and chunks that nobody sees have no exponentials
-            bool some[2] = {true, true};
-            if (HIDDEN) {
+            const float slope = MODE != ATTN_PLAIN && p.slopes ? p.slopes[it.h] * kLog2e : 0.f;
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // running maxima, this lane's sums of weights
+            // 64 keys, one step of the running softmax; tiles with hidden keys have code of their own.
+            // x[4 g + 2 r + e]: row r, key k0 + 8 g + c0 + e
+            auto step = [&](int j, int half, float(&x)[32], auto hides) {
+                constexpr bool HIDDEN = decltype(hides)::value;
+                const int k0 = j * kTile + half * 64;
+                if (MODE != ATTN_PLAIN) {
+                    const float dist = (float)(i0 - k0 - c0);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t bits = bits_between(r.lo - k0 - 32 * b, r.hi - k0 - 32 * b);
-                    if (__all_sync(0xffffffffu, bits == ~0u)) continue;
-                    some[b] = __any_sync(0xffffffffu, bits != 0u);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!(bits >> e & 1u)) x[b * 32 + e] = -INFINITY;
-                }
-            }
-            float mx[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                mx[b] = x[b * 16];
-#pragma unroll
-                for (int e = 1; e < 15; e += 2) mx[b] = fmaxf(fmaxf(mx[b], x[b * 16 + e]), x[b * 16 + e + 1]);
-                mx[b] = fmaxf(mx[b], x[b * 16 + 15]);
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cx;
-            const bool grow = top > m + kRescale || (m == -INFINITY && top > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
-                const float f = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(m - top);
-                if (j > j0 || half) {
-                    // what was multiplied before this half is in O: earlier tiles since these scores are (products
-                    // end in the order they are issued), and the tile's first half once it says so
-                    if (half && !mbar_wait_warp(smem_u32(&hdone[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns)) return false;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int cc = 0; cc < DP; cc += 16) {
-                        uint32_t o[16];
-                        tmem_ld_x16(to + cc, o);
-                        tmem_ld_wait16(o);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st_x16(to + cc, o);
+                    for (int e = 0; e < 32; ++e) {
+                        float v = x[e] * c;
+                        if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
+                        x[e] = fmaf(-slope, fabsf(dist + (float)((e & 2) * 4 - (e >> 2) * 8 - (e & 1))), v);
                     }
-                    tmem_st_wait();
                 }
-                l *= f;
-                if (grow) m = top;
-            }
-            const float2 c2 = two(cx), mu = two(m == -INFINITY ? 0.f : -m);
-            float2 s2[2] = {two(0.f), two(0.f)};
-            uint32_t pk[32], rest[32];
+                if (HIDDEN) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (HIDDEN && !some[b]) {
+                    for (int b = 0; b < 2; ++b) {
+                        // (bits of this lane's keys: 8 g + e of the chunk's 32, from its first column on)
+                        const uint32_t b0 = bits_between(lo[0] - k0 - 32 * b, hi[0] - k0 - 32 * b);
+                        const uint32_t b1 = bits_between(lo[1] - k0 - 32 * b, hi[1] - k0 - 32 * b);
+                        if (__all_sync(0xffffffffu, ((b0 & b1) | ~0x03030303u) == ~0u)) continue;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[b * 16 + e] = rest[b * 16 + e] = 0u;
-                    continue;
+                        for (int e = 0; e < 16; ++e)
+                            if (!((e & 2 ? b1 : b0) >> ((e >> 2) * 8 + (e & 1)) & 1u)) x[b * 16 + e] = -INFINITY;
+                    }
                 }
+                float top[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(x[2 * r], x[2 * r + 1]);
+#pragma unroll
+                    for (int g = 1; g < 8; ++g) top[r] = fmaxf(fmaxf(top[r], x[4 * g + 2 * r]), x[4 * g + 2 * r + 1]);
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)) * cx;
+                }
+                bool grow[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) grow[r] = top[r] > m[r] + kRescale || (m[r] == -INFINITY && top[r] > -INFINITY);
+                if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
+                    float f[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) f[r] = !grow[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - top[r]);
+                    if (j > sp.j0 || half) {
+                        // what was multiplied before this half is in O: earlier tiles since these scores are (products
+                        // end in the order they are issued), and the tile's first half once it says so
+                        if (half && !mbar_wait_warp(smem_u32(&hdone[w]), nt & 1u, s_abort, p.wait_ns)) return false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < DP; cc += 32) {
+                            float o[16];
+                            tmem_ld_frag16<0>(to + cc, o);
+                            tmem_ld_wait16_f32<0>(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f[(e >> 1) & 1];
+                            tmem_st_frag16(to + cc, o);
+                        }
+                        tmem_st_wait();
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        l[r] *= f[r];
+                        if (grow[r]) m[r] = top[r];
+                    }
+                }
+                const float2 c2 = two(cx);
+                const float2 mu[2] = {two(m[0] == -INFINITY ? 0.f : -m[0]), two(m[1] == -INFINITY ? 0.f : -m[1])};
+                float2 s2[2] = {two(0.f), two(0.f)};
+                uint32_t pk[16], rest[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float2 y = __ffma2_rn(make_float2(x[b * 32 + e], x[b * 32 + e + 1]), c2, mu);
+                    const int r = (e >> 1) & 1;
+                    const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), c2, mu[r]);
                     const float2 q = make_float2(ex2(y.x), ex2(y.y));
-                    s2[(e >> 1) & 1] = __fadd2_rn(s2[(e >> 1) & 1], q);
-                    const uint32_t hi = pack_bf16x2(q.x, q.y);
-                    pk[b * 16 + (e >> 1)] = hi;
-                    if (HIDDEN) rest[b * 16 + (e >> 1)] = pack_bf16x2(q.x - bf16lo(hi), q.y - bf16hi(hi));
+                    s2[r] = __fadd2_rn(s2[r], q);
+                    const uint32_t hi2 = pack_bf16x2(q.x, q.y);
+                    pk[e >> 1] = hi2;
+                    if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi2), q.y - bf16hi(hi2));
+                }
+                tmem_st_pairs16(ts + half * 32, pk);
+                if (HIDDEN) tmem_st_pairs16(ts + 64 + half * 32, rest);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
+                l[0] += s2[0].x + s2[0].y;
+                l[1] += s2[1].x + s2[1].y;
+                return true;
+            };
+            for (int j = sp.j0; ok && j < sp.j1; ++j, ++nt) {
+                ok = mbar_wait_warp(smem_u32(&sfull[w]), nt & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const bool hides = sp.hides(j);
+                float x0[32], x1[32];
+                tmem_ld_frag32<0>(ts, x0);
+                tmem_ld_wait_f32<0>(x0);
+                tmem_ld_frag32<0>(ts + 64, x1);  // on its way during the first half's arithmetic
+                if (hides) {  // (the first half writes into the second's columns)
+                    tmem_ld_wait_f32<0>(x1);
+                    ok = step(j, 0, x0, std::true_type{}) && step(j, 1, x1, std::true_type{});
+                } else {
+                    ok = step(j, 0, x0, std::false_type{});
+                    tmem_ld_wait_f32<0>(x1);
+                    ok = ok && step(j, 1, x1, std::false_type{});
                 }
             }
-            tmem_st_x32(ts + half * 32, pk);
-            if (HIDDEN) tmem_st_x32(ts + 64 + half * 32, rest);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
-            const float2 s = __fadd2_rn(s2[0], s2[1]);
-            l += s.x + s.y;
-            return true;
-        };
-        for (int j = j0; ok && j < j1; ++j) {
-            ok = mbar_wait_warp(smem_u32(&sfull[w]), (uint32_t)(j - j0) & 1u, s_abort, p.wait_ns);
             if (!ok) break;
-            tc_fence_after();
-            const bool hides = span[w].hides(j);
-            float x0[64], x1[64];
-            tmem_ld_f32<0>(ts, x0);
-            tmem_ld_f32<32>(ts + 32, x0);
-            tmem_ld_wait_f32<0>(x0);
-            tmem_ld_wait_f32<32>(x0);
-            tmem_ld_f32<0>(ts + 64, x1);  // on its way during the first half's arithmetic
-            tmem_ld_f32<32>(ts + 96, x1);
-            if (hides) {  // (the first half writes into the second's columns)
-                tmem_ld_wait_f32<0>(x1);
-                tmem_ld_wait_f32<32>(x1);
-                ok = step(j, 0, x0, std::true_type{}) && step(j, 1, x1, std::true_type{});
-            } else {
-                ok = step(j, 0, x0, std::false_type{});
-                tmem_ld_wait_f32<0>(x1);
-                tmem_ld_wait_f32<32>(x1);
-                ok = ok && step(j, 1, x1, std::false_type{});
+            // ---- the item's rows: sums over a row's four lanes, then 1 / l to the quarter's two warps
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if ((lane & 3) == 0) {
+                    s_inv[w * kTile + row0 + 8 * r] = l[r] > 0.f ? 1.f / l[r] : 0.f;
+                    if (i0 + 8 * r < p.T)
+                        p.lse[(int64_t)it.h * p.T + i0 + 8 * r] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&lready[4 * w + quarter]));
+            // (this barrier completes twice an item: the sums are there; both warps have read them)
+            ok = mbar_wait_warp(smem_u32(&lready[4 * w + quarter]), 0, s_abort, p.wait_ns);
+            if (!ok) break;
+            const int row = quarter * 32 + lane, i = it.q0 + w * kTile + row;
+            const float inv = s_inv[w * kTile + row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&lready[4 * w + quarter]));
+            if (sp.any()) {
+                ok = mbar_wait_warp(smem_u32(&odone[w]), nq & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+                ++nq;
+                tc_fence_after();
+            }
+            // each of the quarter's warps writes half of the dims, a thread one row of them
+            const int64_t at = (int64_t)i * p.hq + it.h;
+            uint16_t* out = p.out + at * p.d;
+            int8_t* out_lo = p.out_lo ? p.out_lo + at * p.d16 : nullptr;
+#pragma unroll 1
+            for (int cc = sub * (DP / 2); cc < (sub + 1) * (DP / 2); cc += 16) {
+                float o[16];
+                if (sp.any()) {  // (uniform over the query tile's warps)
+                    uint32_t raw[16];
+                    tmem_ld_x16(tmem + all_lanes + 2 * kTile + w * DP + cc, raw);
+                    tmem_ld_wait16(raw);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = inv > 0.f ? __uint_as_float(raw[e]) * inv : 0.f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = 0.f;
+                }
+                uint32_t v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+                if (i < p.T && cc < p.d) {
+                    if ((p.d & 15) == 0) {
+                        st_global_v8(out + cc, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+                    } else {  // (d = 8 modulo 16: rows lie on 16 bytes, and the last chunk is half there)
+                        *reinterpret_cast<uint4*>(out + cc) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (cc + 8 < p.d) *reinterpret_cast<uint4*>(out + cc + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                    if (out_lo) {
+                        int more[4];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int pair = (bits_left(o[2 * e], v[e] & 0xFFFFu) & 255) | (bits_left(o[2 * e + 1], v[e] >> 16) & 255) << 8;
+                            if (e & 1) more[e >> 1] |= pair << 16;
+                            else more[e >> 1] = pair;
+                        }
+                        *reinterpret_cast<int4*>(out_lo + cc) = make_int4(more[0], more[1], more[2], more[3]);
+                    }
+                }
+            }
+            tc_fence_before();  // (the next item's products may overwrite O once the weights say so)
+            ok = mbar_wait_warp(smem_u32(&lready[4 * w + quarter]), 1, s_abort, p.wait_ns);
         }
-        if (ok && j1 > j0) ok = mbar_wait_warp(smem_u32(&odone[w]), 0, s_abort, p.wait_ns);
-        tc_fence_after();
         if (!ok && lane == 0) {
             attn_error(p, 5, 3);
             *s_abort = 1;
         }
-        if (!group_ok(ok, s_bad + w, 1 + w)) {
-            // (nothing is written)
-        } else {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int row = (warp & 3) * 32 + lane;
-            uint8_t* stage = sq + w * C::kTileBytes;  // (the queries have been read)
-            int8_t* lo = p.out_lo ? p.out_lo + ((int64_t)i * p.hq + h) * p.d16 : nullptr;
-#pragma unroll 1
-            for (int cc = 0; cc < DP; cc += 16) {
-                uint32_t o[16];
-                if (j1 > j0) {  // (uniform over the warpgroup)
-                    tmem_ld_x16(to + cc, o);
-                    tmem_ld_wait16(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = 0;
-                }
-                uint32_t v[8];
-                int more[4];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = inv > 0.f ? __uint_as_float(o[2 * e]) * inv : 0.f;
-                    const float b = inv > 0.f ? __uint_as_float(o[2 * e + 1]) * inv : 0.f;
-                    v[e] = pack_bf16x2(a, b);
-                    const int two = (bits_left(a, v[e] & 0xFFFFu) & 255) | (bits_left(b, v[e] >> 16) & 255) << 8;
-                    if (e & 1) more[e >> 1] |= two << 16;
-                    else more[e >> 1] = two;
-                }
-                stage_pairs(stage + (cc / 64) * kBoxBytes, row, (cc & 63) / 16, v);
-                if (lo && i < p.T && cc < p.d)
-                    *reinterpret_cast<int4*>(lo + cc) = make_int4(more[0], more[1], more[2], more[3]);
-            }
-            if (q0 + w * kTile < p.T)  // (uniform over the warpgroup)
-                for (int b = 0; b < DP / 64; ++b)
-                    store_box(&maps.o, stage + b * kBoxBytes, b * 64, h, q0 + w * kTile, 1 + w, row == 0);
-            if (i < p.T) p.lse[(int64_t)h * p.T + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kFwdMath) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -399,33 +489,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 }
 
 template <int DP, int MODE>
-cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, cudaStream_t st) {
+cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, int sms, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                FwdCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.T + 2 * kTile - 1) / (2 * kTile)) * (unsigned)p.hq;
-    return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kAttnThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    const int64_t items = (int64_t)((p.T + 2 * kTile - 1) / (2 * kTile)) * p.hq;
+    const unsigned grid = (unsigned)(items < sms ? items : sms);
+    return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
-lm_status launch_attn_fwd(const AttnParams& p, cudaStream_t st) {
+lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
     FwdMaps maps;
     const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs};
     lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
-    if (s == LM_OK) s = encode_heads(&maps.o, lm_heads{p.out, (int64_t)p.hq * p.d, p.d}, p.T, p.hq, p.d, kTile);
     if (s != LM_OK) return s;
     // the plain form folds the scale into the exponent and needs it positive (the maximum of s c is c max s)
     const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes || !(p.scale > 0.f) ? ATTN_BIAS : ATTN_PLAIN;
     cudaError_t e;
     if (p.d <= 64)
-        e = mode == ATTN_CAP    ? launch_fwd<64, ATTN_CAP>(p, maps, st)
-            : mode == ATTN_BIAS ? launch_fwd<64, ATTN_BIAS>(p, maps, st)
-                                : launch_fwd<64, ATTN_PLAIN>(p, maps, st);
+        e = mode == ATTN_CAP    ? launch_fwd<64, ATTN_CAP>(p, maps, sms, st)
+            : mode == ATTN_BIAS ? launch_fwd<64, ATTN_BIAS>(p, maps, sms, st)
+                                : launch_fwd<64, ATTN_PLAIN>(p, maps, sms, st);
     else
-        e = mode == ATTN_CAP    ? launch_fwd<128, ATTN_CAP>(p, maps, st)
-            : mode == ATTN_BIAS ? launch_fwd<128, ATTN_BIAS>(p, maps, st)
-                                : launch_fwd<128, ATTN_PLAIN>(p, maps, st);
+        e = mode == ATTN_CAP    ? launch_fwd<128, ATTN_CAP>(p, maps, sms, st)
+            : mode == ATTN_BIAS ? launch_fwd<128, ATTN_BIAS>(p, maps, sms, st)
+                                : launch_fwd<128, ATTN_PLAIN>(p, maps, sms, st);
     return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn forward launch: %s", cudaGetErrorString(e));
 }
 

@@ -184,7 +184,7 @@ extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     p.lse = lse;
     LL_TRY(attn_ranges(a, p, st));
     LaunchTag tag("attn.fwd", st);
-    return launch_attn_fwd(p, st);
+    return launch_attn_fwd(p, sms, st);
 }
 
 extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
