@@ -95,8 +95,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t* qempty = qfull + 2;         // [2] and are done with
     uint64_t* sfull = qempty + 2;         // [2] scores ready
     uint64_t* pfull = sfull + 2;          // [2][2] weights of the first, of the last 64 keys written
-    uint64_t* hdone = pfull + 4;          // [2] the first half of a P V product done (once a tile)
-    uint64_t* odone = hdone + 2;          // [2] the last product of the item done
+    uint64_t* odone = pfull + 4;          // [2] the last product of the item done
     uint64_t* lready = odone + 2;         // [2][4] the quarter's row sums exchanged
     uint64_t* drain = lready + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -118,7 +117,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(smem_u32(&sfull[w]), 1);
             mbar_init(smem_u32(&pfull[2 * w]), 8);
             mbar_init(smem_u32(&pfull[2 * w + 1]), 8);
-            mbar_init(smem_u32(&hdone[w]), 1);
             mbar_init(smem_u32(&odone[w]), 1);
             for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&lready[4 * w + q]), 2);
         }
@@ -238,8 +236,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                     for (int kk = 0; kk < 4; ++kk)
                                         umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
                                 }
-                                if (half == 0) umma_commit(smem_u32(&hdone[w]));
-                                else if (j == sp.j1) umma_commit(smem_u32(&odone[w]));
+                                if (half && j == sp.j1) umma_commit(smem_u32(&odone[w]));
                             }
                             if (!ok) break;
                         }
@@ -299,15 +296,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             const float slope = MODE != ATTN_PLAIN && p.slopes ? p.slopes[it.h] * kLog2e : 0.f;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // running maxima, this lane's sums of weights
-            // 64 keys, one step of the running softmax; tiles with hidden keys have code of their own.
-            // x[4 g + 2 r + e]: row r, key k0 + 8 g + c0 + e
-            auto step = [&](int j, int half, float(&x)[32], auto hides) {
+            // one key tile; tiles with hidden keys have code of their own.  x[4 g + 2 r + e]: row r, key
+            // 8 g + c0 + e of the tile
+            auto tile = [&](int j, auto hides) {
                 constexpr bool HIDDEN = decltype(hides)::value;
-                const int k0 = j * kTile + half * 64;
+                const int k0 = j * kTile;
+                float x[64];
+                tmem_ld_frag32<0>(ts, x);
+                tmem_ld_frag32<32>(ts + 64, x);
+                tmem_ld_wait_f32<0>(x);
+                tmem_ld_wait_f32<32>(x);
                 if (MODE != ATTN_PLAIN) {
                     const float dist = (float)(i0 - k0 - c0);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 64; ++e) {
                         float v = x[e] * c;
                         if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
                         x[e] = fmaf(-slope, fabsf(dist + (float)((e & 2) * 4 - (e >> 2) * 8 - (e & 1))), v);
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
                 if (HIDDEN) {
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
+                    for (int b = 0; b < 4; ++b) {
                         // (bits of this lane's keys: 8 g + e of the chunk's 32, from its first column on)
                         const uint32_t b0 = bits_between(lo[0] - k0 - 32 * b, hi[0] - k0 - 32 * b);
                         const uint32_t b1 = bits_between(lo[1] - k0 - 32 * b, hi[1] - k0 - 32 * b);
@@ -328,24 +330,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 float top[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    top[r] = fmaxf(x[2 * r], x[2 * r + 1]);
+                    float a = fmaxf(x[2 * r], x[2 * r + 1]), b = fmaxf(x[32 + 2 * r], x[32 + 2 * r + 1]);
 #pragma unroll
-                    for (int g = 1; g < 8; ++g) top[r] = fmaxf(fmaxf(top[r], x[4 * g + 2 * r]), x[4 * g + 2 * r + 1]);
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2)) * cx;
+                    for (int g = 1; g < 8; ++g) {
+                        a = fmaxf(fmaxf(a, x[4 * g + 2 * r]), x[4 * g + 2 * r + 1]);
+                        b = fmaxf(fmaxf(b, x[32 + 4 * g + 2 * r]), x[32 + 4 * g + 2 * r + 1]);
+                    }
+                    top[r] = fmaxf(a, b);
                 }
+#pragma unroll
+                for (int o = 1; o <= 2; ++o)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
                 bool grow[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) grow[r] = top[r] > m[r] + kRescale || (m[r] == -INFINITY && top[r] > -INFINITY);
+                for (int r = 0; r < 2; ++r) {
+                    top[r] *= cx;
+                    grow[r] = top[r] > m[r] + kRescale || (m[r] == -INFINITY && top[r] > -INFINITY);
+                }
                 if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
                     float f[2];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) f[r] = !grow[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - top[r]);
-                    if (j > sp.j0 || half) {
-                        // what was multiplied before this half is in O: earlier tiles since these scores are (products
-                        // end in the order they are issued), and the tile's first half once it says so
-                        if (half && !mbar_wait_warp(smem_u32(&hdone[w]), nt & 1u, s_abort, p.wait_ns)) return false;
-                        tc_fence_after();
+                    for (int r = 0; r < 2; ++r) {
+                        f[r] = !grow[r] ? 1.f : m[r] == -INFINITY ? 0.f : ex2(m[r] - top[r]);
+                        l[r] *= f[r];
+                        if (grow[r]) m[r] = top[r];
+                    }
+                    // the earlier tiles are in O since these scores are there: products end in the order they
+                    // are issued
+                    if (j > sp.j0) {
 #pragma unroll 1
                         for (int cc = 0; cc < DP; cc += 32) {
                             float o[16];
@@ -357,53 +370,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         }
                         tmem_st_wait();
                     }
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        l[r] *= f[r];
-                        if (grow[r]) m[r] = top[r];
-                    }
                 }
                 const float2 c2 = two(cx);
                 const float2 mu[2] = {two(m[0] == -INFINITY ? 0.f : -m[0]), two(m[1] == -INFINITY ? 0.f : -m[1])};
                 float2 s2[2] = {two(0.f), two(0.f)};
-                uint32_t pk[16], rest[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int r = (e >> 1) & 1;
-                    const float2 y = __ffma2_rn(make_float2(x[e], x[e + 1]), c2, mu[r]);
-                    const float2 q = make_float2(ex2(y.x), ex2(y.y));
-                    s2[r] = __fadd2_rn(s2[r], q);
-                    const uint32_t hi2 = pack_bf16x2(q.x, q.y);
-                    pk[e >> 1] = hi2;
-                    if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi2), q.y - bf16hi(hi2));
+                for (int half = 0; half < 2; ++half) {  // 64 keys at a time: their product may begin
+                    uint32_t pk[16], rest[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const int r = (e >> 1) & 1;
+                        const float2 y = __ffma2_rn(make_float2(x[half * 32 + e], x[half * 32 + e + 1]), c2, mu[r]);
+                        const float2 q = make_float2(ex2(y.x), ex2(y.y));
+                        s2[r] = __fadd2_rn(s2[r], q);
+                        const uint32_t hi2 = pack_bf16x2(q.x, q.y);
+                        pk[e >> 1] = hi2;
+                        if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi2), q.y - bf16hi(hi2));
+                    }
+                    tmem_st_pairs16(ts + half * 32, pk);
+                    if (HIDDEN) tmem_st_pairs16(ts + 64 + half * 32, rest);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
                 }
-                tmem_st_pairs16(ts + half * 32, pk);
-                if (HIDDEN) tmem_st_pairs16(ts + 64 + half * 32, rest);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&pfull[2 * w + half]));
                 l[0] += s2[0].x + s2[0].y;
                 l[1] += s2[1].x + s2[1].y;
-                return true;
             };
-            for (int j = sp.j0; ok && j < sp.j1; ++j, ++nt) {
+            for (int j = sp.j0; j < sp.j1; ++j, ++nt) {
                 ok = mbar_wait_warp(smem_u32(&sfull[w]), nt & 1u, s_abort, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
-                const bool hides = sp.hides(j);
-                float x0[32], x1[32];
-                tmem_ld_frag32<0>(ts, x0);
-                tmem_ld_wait_f32<0>(x0);
-                tmem_ld_frag32<0>(ts + 64, x1);  // on its way during the first half's arithmetic
-                if (hides) {  // (the first half writes into the second's columns)
-                    tmem_ld_wait_f32<0>(x1);
-                    ok = step(j, 0, x0, std::true_type{}) && step(j, 1, x1, std::true_type{});
-                } else {
-                    ok = step(j, 0, x0, std::false_type{});
-                    tmem_ld_wait_f32<0>(x1);
-                    ok = ok && step(j, 1, x1, std::false_type{});
-                }
+                if (sp.hides(j)) tile(j, std::true_type{});
+                else tile(j, std::false_type{});
             }
             if (!ok) break;
             // ---- the item's rows: sums over a row's four lanes, then 1 / l to the quarter's two warps
