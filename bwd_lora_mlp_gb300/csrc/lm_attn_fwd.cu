@@ -10,11 +10,10 @@
 // weights go to the tensor cores 64 keys at a time, so the second product starts half a tile early.
 // The running maximum m follows the row only when it has grown by more than 8 (a factor 256 in the
 // weights): the weights then stay below 2^8, exact in their scale, and O_w is rescaled a few times per
-// row instead of once per key tile.  Sums are fp32.  P is rounded to bf16 for the second product; on
-// tiles with hidden keys what the rounding left out is multiplied too (as a second left operand, in the
-// other half of S_w's place): rows of few keys have no other weights to average their error with, and
-// the backward takes differences against their O.  That is one more product on the tiles along the
-// diagonal and at document ends; dQ of packed prefixes went from 2.51e-3 to 2.4e-3 of its norm off.
+// row instead of once per key tile.  Sums are fp32.  P is rounded to bf16 for the second product; for
+// query tiles with rows of few keys (the first tokens of a document) what the rounding left out is
+// multiplied too, as a second left operand in the other half of S_w's place: such rows have no other
+// weights to average their error with, and the backward takes differences against their O.
 // Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
 // memory: S_0, S_1, O_0, O_1 of 128 columns each.
 #include "lm_attn.cuh"
@@ -45,6 +44,8 @@ struct TileSpan {
     __device__ __forceinline__ bool any() const { return j1 > j0; }
     __device__ __forceinline__ bool hides(int j) const { return j * kTile < lo_max || (j + 1) * kTile > hi_min; }
     __device__ __forceinline__ bool has(int j) const { return j >= j0 && j < j1; }
+    // some row may see fewer keys than a tile has: what its weights' rounding left out is multiplied too
+    __device__ __forceinline__ bool short_rows() const { return hi_min - lo_max < kTile; }
 };
 __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0) {
     if (q0 >= p.T) return TileSpan{0, 0, 0, 0};
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
                         const TileSpan& sp = it.span[w];
                         if (j > it.J0 && sp.has(j - 1)) {  // O_w += P_w V_{j-1}
-                            const bool first = j - 1 == sp.j0, hides = sp.hides(j - 1);
+                            const bool first = j - 1 == sp.j0, both = sp.short_rows();
 #pragma unroll
                             for (int half = 0; half < 2 && ok; ++half) {
                                 ok = mbar_wait(smem_u32(&pfull[2 * w + half]), (nt[w] - 1u) & 1u, s_abort, p.wait_ns);
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
                                     umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, first && !half && !kk ? 0u : 1u);
-                                if (hides) {
+                                if (both) {
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
                                         umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
@@ -298,8 +299,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // running maxima, this lane's sums of weights
             // one key tile; tiles with hidden keys have code of their own.  x[4 g + 2 r + e]: row r, key
             // 8 g + c0 + e of the tile
-            auto tile = [&](int j, auto hides) {
-                constexpr bool HIDDEN = decltype(hides)::value;
+            auto tile = [&](int j, auto hides, auto few) {
+                constexpr bool HIDDEN = decltype(hides)::value, REST = decltype(few)::value;
                 const int k0 = j * kTile;
                 float x[64];
                 tmem_ld_frag32<0>(ts, x);
@@ -385,10 +386,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         s2[r] = __fadd2_rn(s2[r], q);
                         const uint32_t hi2 = pack_bf16x2(q.x, q.y);
                         pk[e >> 1] = hi2;
-                        if (HIDDEN) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi2), q.y - bf16hi(hi2));
+                        if (REST) rest[e >> 1] = pack_bf16x2(q.x - bf16lo(hi2), q.y - bf16hi(hi2));
                     }
                     tmem_st_pairs16(ts + half * 32, pk);
-                    if (HIDDEN) tmem_st_pairs16(ts + 64 + half * 32, rest);
+                    if (REST) tmem_st_pairs16(ts + 64 + half * 32, rest);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -401,8 +402,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 ok = mbar_wait_warp(smem_u32(&sfull[w]), nt & 1u, s_abort, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
-                if (sp.hides(j)) tile(j, std::true_type{});
-                else tile(j, std::false_type{});
+                if (sp.short_rows()) tile(j, std::true_type{}, std::true_type{});
+                else if (sp.hides(j)) tile(j, std::true_type{}, std::false_type{});
+                else tile(j, std::false_type{}, std::false_type{});
             }
             if (!ok) break;
             // ---- the item's rows: sums over a row's four lanes, then 1 / l to the quarter's two warps
