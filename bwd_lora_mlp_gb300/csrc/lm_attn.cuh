@@ -287,6 +287,30 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, const uint8_t*
         asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
     }
 }
+// N (a multiple of 16) dims from dim c0 on of this thread's accumulator row (at t), times f, to bf16 at
+// dst.  `any` false: the accumulator was never written and the row is zero (uniform over the warp).
+template <int N>
+__device__ __forceinline__ void store_dims(uint16_t* dst, uint32_t t, int c0, int d, float f, bool any, bool mine) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t o[16], v[8];
+        if (any) {
+            tmem_ld_x16(t + c0 + c, o);
+            tmem_ld_wait16(o);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f) : 0u;
+        if (!mine || c0 + c >= d) continue;
+        uint16_t* q = dst + c0 + c;
+        if ((d & 15) == 0) {
+            st_global_v8(q, v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]);
+        } else {  // (d = 8 modulo 16: rows lie on 16 bytes, and the last chunk is half there)
+            *reinterpret_cast<uint4*>(q) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (c0 + c + 8 < d) *reinterpret_cast<uint4*>(q + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
 // 64 dims of this thread's accumulator row (lane r of the warpgroup's 128), times f, to a staged box as
 // bf16.  `any` false: the accumulator was never written and the row is zero (uniform over the warp).
 __device__ __forceinline__ void stage_row(uint8_t* box, int r, uint32_t t, float f, bool any) {

@@ -55,7 +55,7 @@ __device__ __forceinline__ float2 exponents(const ScoreMath& S, float2 qk, float
 }
 
 struct BwdMaps {
-    CUtensorMap q, k, v, dO, dQ, dK, dV;
+    CUtensorMap q, k, v, dO, dK, dV;
 };
 
 // ------------------------------------------------------------------ delta, and lse in the exponent's units
@@ -410,6 +410,27 @@ struct DqCfg {
     static constexpr int kKStages = 3, kVStages = 2;  // S runs one key tile ahead of dz, so K stays longer
     static constexpr int kSmem = 2048 + (2 + kKStages + kVStages) * kTileBytes;
 };
+// Item k of this CTA, 128 queries of one head: dealt out like the forward's (the heavier ones first,
+// forwards and backwards in turn).  CTAs stay: the next item's operands load and its first scores are
+// formed while this one's rows are written (10 thousand cycles an item otherwise, as much as five tiles).
+struct DqItem {
+    int h, q0, kt0, N;    // key tiles [kt0, kt0 + N)
+    int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row
+    bool valid;
+};
+__device__ __forceinline__ DqItem dq_item(const AttnParams& p, int k) {
+    const int nqt = (p.T + kTile - 1) / kTile, G = (int)gridDim.x;
+    const int idx = k & 1 ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
+    DqItem it{idx % p.hq, (nqt - 1 - idx / p.hq) * kTile, 0, 0, 0, 0, idx < nqt * p.hq};
+    if (it.valid) {
+        const TokRange rf = tok_range(p, it.q0), rl = tok_range(p, min(it.q0 + kTile, p.T) - 1);
+        it.kt0 = rf.lo / kTile;
+        it.N = rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - it.kt0 : 0;
+        it.lo_max = rl.lo;
+        it.hi_min = rf.hi;
+    }
+    return it;
+}
 
 template <int DP, int MODE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -421,24 +442,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint64_t* kempty = kfull + C::kKStages;
     uint64_t* vfull = kempty + C::kKStages;
     uint64_t* vempty = vfull + C::kVStages;
-    uint64_t* qfull = vempty + C::kVStages;
-    uint64_t* sfull = qfull + 1;    // [2] S ready
-    uint64_t* dpfull = sfull + 2;   // dP ready
-    uint64_t* dsfull = dpfull + 1;  // dz written (in place of S), dP read
-    uint64_t* drain = dsfull + 1;
+    uint64_t* qfull = vempty + C::kVStages;  // [2] the item's Q, dO
+    uint64_t* qempty = qfull + 2;
+    uint64_t* sfull = qempty + 2;    // [2] S ready
+    uint64_t* dpfull = sfull + 2;    // dP ready
+    uint64_t* dsfull = dpfull + 1;   // dz written (in place of S), dP read
+    uint64_t* dqdone = dsfull + 1;   // the item's last product done
+    uint64_t* drain = dqdone + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* s_bad = s_abort + 1;  // [4] a warp of the warpgroup gave up
     uint8_t* sq = smem + 1024;
     uint8_t* so = sq + C::kTileBytes;
     uint8_t* sk = so + C::kTileBytes;
     uint8_t* sv = sk + C::kKStages * C::kTileBytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nqt = (p.T + kTile - 1) / kTile;
-    const int h = (int)blockIdx.x % p.hq, q0 = (nqt - 1 - (int)blockIdx.x / p.hq) * kTile;  // (the longest rows first)
-    const int g = h / (p.hq / p.hk);
-
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kKStages; ++s) {
@@ -449,13 +467,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mbar_init(smem_u32(&vfull[s]), 1);
             mbar_init(smem_u32(&vempty[s]), 1);
         }
-        mbar_init(smem_u32(qfull), 1);
-        mbar_init(smem_u32(&sfull[0]), 1);
-        mbar_init(smem_u32(&sfull[1]), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&qfull[s]), 1);
+            mbar_init(smem_u32(&qempty[s]), 1);
+            mbar_init(smem_u32(&sfull[s]), 1);
+        }
         mbar_init(smem_u32(dpfull), 1);
         mbar_init(smem_u32(dsfull), kBwdMath);
+        mbar_init(smem_u32(dqdone), 1);
         mbar_init(smem_u32(drain), 1);
-        *s_abort = s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0;
+        *s_abort = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -473,44 +494,56 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t tdp = tmem + 2 * kTile, tdq = tmem + 3 * kTile;
-    const TokRange rf = tok_range(p, q0), rl = tok_range(p, min(q0 + kTile, p.T) - 1);
-    const int kt0 = uni(rf.lo / kTile), N = uni(rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - kt0 : 0);
+    const int rounds = ((p.T + kTile - 1) / kTile * p.hq + (int)gridDim.x - 1) / (int)gridDim.x;
 
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
         if (warp == kBwdMath + 1) {  // ---------------- loader
-            if (lane == 0 && N > 0) {
+            if (lane == 0) {
                 bool ok = true;
-                mbar_expect_tx(smem_u32(qfull), 2 * C::kTileBytes);
-                for (int b = 0; b < DP / 64; ++b) {
-                    tma_load_3d(smem_u32(sq + b * kBoxBytes), &maps.q, smem_u32(qfull), b * 64, h, q0);
-                    tma_load_3d(smem_u32(so + b * kBoxBytes), &maps.dO, smem_u32(qfull), b * 64, h, q0);
-                }
-                uint32_t nk = 0, nv = 0;
-                while (ok && nv < (uint32_t)N) {  // K_0, V_0, K_1, V_1, ... (V_j asked for after K_{j+1} came 22 % later)
-                    const bool key = nk == nv;
-                    const uint32_t i = key ? nk : nv, st = key ? i % C::kKStages : i % C::kVStages;
-                    const uint32_t ph = (key ? i / C::kKStages : i / C::kVStages) & 1u;
-                    const uint32_t bar = smem_u32(key ? &kfull[st] : &vfull[st]);
-                    uint8_t* dst = (key ? sk : sv) + st * C::kTileBytes;
-                    if (!mbar_wait(smem_u32(key ? &kempty[st] : &vempty[st]), ph ^ 1u, s_abort, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar, C::kTileBytes);
-                    for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(smem_u32(dst + b * kBoxBytes), key ? &maps.k : &maps.v, bar, b * 64, g, (kt0 + (int)i) * kTile);
-                    if (key) ++nk;
-                    else ++nv;
+                uint32_t nk = 0, nv = 0, nq[2] = {0, 0};  // tiles asked for
+                for (int r = 0; ok && r < rounds; ++r) {
+                    const DqItem it = dq_item(p, r);
+                    auto query = [&](int which) {  // Q, then dO
+                        if (!mbar_wait(smem_u32(&qempty[which]), (nq[which] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;
+                        const uint32_t bar = smem_u32(&qfull[which]);
+                        mbar_expect_tx(bar, C::kTileBytes);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(smem_u32((which ? so : sq) + b * kBoxBytes), which ? &maps.dO : &maps.q, bar, b * 64, it.h,
+                                        it.q0);
+                        ++nq[which];
+                        return true;
+                    };
+                    for (int j = 0; ok && j < it.N; ++j)
+                        for (int kv = 0; kv < 2; ++kv) {  // Q, K_0, dO, V_0, K_1, V_1, ...
+                            if (j == 0 && !query(kv)) {
+                                ok = false;
+                                break;
+                            }
+                            uint32_t& n = kv ? nv : nk;
+                            const uint32_t st = kv ? n % C::kVStages : n % C::kKStages;
+                            const uint32_t ph = (kv ? n / C::kVStages : n / C::kKStages) & 1u;
+                            const uint32_t bar = smem_u32(kv ? &vfull[st] : &kfull[st]);
+                            if (!mbar_wait(smem_u32(kv ? &vempty[st] : &kempty[st]), ph ^ 1u, s_abort, p.wait_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_expect_tx(bar, C::kTileBytes);
+                            for (int b = 0; b < DP / 64; ++b)
+                                tma_load_3d(smem_u32((kv ? sv : sk) + st * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k, bar,
+                                            b * 64, it.h / (p.hq / p.hk), (it.kt0 + j) * kTile);
+                            ++n;
+                        }
                 }
                 if (!ok) {
                     attn_error(p, 7, 1);
                     *s_abort = 1;
                 }
                 volatile int never = 0;
-                bool in = mbar_wait(smem_u32(qfull), 0, &never, p.wait_ns);
-                in = drain_fills(smem_u32(&kfull[0]), C::kKStages, nk, p.wait_ns) && in;
+                bool in = drain_fills(smem_u32(&kfull[0]), C::kKStages, nk, p.wait_ns);
                 in = drain_fills(smem_u32(&vfull[0]), C::kVStages, nv, p.wait_ns) && in;
+                for (int s = 0; s < 2; ++s)
+                    if (nq[s]) in = mbar_wait(smem_u32(&qfull[s]), (nq[s] - 1u) & 1u, &never, p.wait_ns) && in;
                 if (!in) attn_error(p, 7, 5);
             }
         } else if (warp == kBwdMath && elect_one()) {  // ---------------- tensor cores
@@ -519,43 +552,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t idd = make_idesc_bf16(kTile, ksteps * 16, false, true);  // K is [key][dim]: MN-major
             int in0, in1;
             inside_tokens(p, in0, in1);
-            bool ok = N <= 0 || mbar_wait(smem_u32(qfull), 0, s_abort, p.wait_ns);
-            auto scores = [&](int j) {  // S(j) = Q K^T, in half j & 1
-                const uint32_t s = (uint32_t)j % C::kKStages;
-                if (!mbar_wait(smem_u32(&kfull[s]), ((uint32_t)j / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(sk + s * C::kTileBytes, DP / 64, (kt0 + j) * kTile, in0, in1);
-                tc_fence_after();
-                mma_rows<DP>(tmem + (j & 1) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps, ids);
-                umma_commit(smem_u32(&sfull[j & 1]));
-                return true;
-            };
-            auto dots = [&](int j) {  // dP(j) = dO V^T
-                const uint32_t s = (uint32_t)j % C::kVStages;
-                if (!mbar_wait(smem_u32(&vfull[s]), ((uint32_t)j / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
-                tc_fence_after();
-                mma_rows<DP>(tdp, desc_rows(smem_u32(so)), desc_rows(smem_u32(sv + s * C::kTileBytes)), ksteps, ids);
-                umma_commit(smem_u32(dpfull));
-                umma_commit(smem_u32(&vempty[s]));
-                return true;
-            };
-            if (ok && N > 0) ok = scores(0) && dots(0) && (N < 2 || scores(1));
-            for (int j = 0; ok && j < N; ++j) {
-                if (!mbar_wait(smem_u32(dsfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) {
-                    ok = false;
-                    break;
+            bool ok = true;
+            uint32_t base = 0, items = 0;  // tiles and items with tiles before this one
+            DqItem next = dq_item(p, 0);
+            for (int r = 0; ok && r < rounds; ++r) {
+                const DqItem it = next;
+                next = dq_item(p, r + 1);
+                if (it.N <= 0) continue;
+                auto scores = [&](int j) {  // S(j) = Q K^T, in buffer t & 1
+                    const uint32_t t = base + (uint32_t)j, s = t % C::kKStages;
+                    if (!mbar_wait(smem_u32(&kfull[s]), (t / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
+                    clear_padding(sk + s * C::kTileBytes, DP / 64, (it.kt0 + j) * kTile, in0, in1);
+                    tc_fence_after();
+                    mma_rows<DP>(tmem + (t & 1u) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps,
+                                 ids);
+                    umma_commit(smem_u32(&sfull[t & 1u]));
+                    if (j == it.N - 1) umma_commit(smem_u32(&qempty[0]));
+                    return true;
+                };
+                auto dots = [&](int j) {  // dP(j) = dO V^T
+                    const uint32_t t = base + (uint32_t)j, s = t % C::kVStages;
+                    if (!mbar_wait(smem_u32(&vfull[s]), (t / C::kVStages) & 1u, s_abort, p.wait_ns)) return false;
+                    tc_fence_after();
+                    mma_rows<DP>(tdp, desc_rows(smem_u32(so)), desc_rows(smem_u32(sv + s * C::kTileBytes)), ksteps, ids);
+                    umma_commit(smem_u32(dpfull));
+                    umma_commit(smem_u32(&vempty[s]));
+                    if (j == it.N - 1) umma_commit(smem_u32(&qempty[1]));
+                    return true;
+                };
+                ok = mbar_wait(smem_u32(&qfull[0]), items & 1u, s_abort, p.wait_ns) && scores(0) &&
+                     mbar_wait(smem_u32(&qfull[1]), items & 1u, s_abort, p.wait_ns) && dots(0) && (it.N < 2 || scores(1));
+                for (int j = 0; ok && j < it.N; ++j) {
+                    const uint32_t t = base + (uint32_t)j, s = t % C::kKStages;
+                    if (!mbar_wait(smem_u32(dsfull), t & 1u, s_abort, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (j + 1 < it.N && !dots(j + 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_weights(tdq, tmem + (t & 1u) * kTile, desc_cols(smem_u32(sk + s * C::kTileBytes)), idd, j == 0);
+                    umma_commit(smem_u32(&kempty[s]));
+                    if (j == it.N - 1) umma_commit(smem_u32(dqdone));
+                    if (j + 2 < it.N && !scores(j + 2)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                tc_fence_after();
-                if (j + 1 < N && !dots(j + 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t s = (uint32_t)j % C::kKStages;
-                mma_weights(tdq, tmem + (j & 1) * kTile, desc_cols(smem_u32(sk + s * C::kTileBytes)), idd, j == 0);
-                umma_commit(smem_u32(&kempty[s]));
-                if (j + 2 < N && !scores(j + 2)) {
-                    ok = false;
-                    break;
-                }
+                base += (uint32_t)it.N;
+                ++items;
             }
             if (!ok) {
                 attn_error(p, 7, 2);
@@ -567,90 +614,108 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     } else {  // ---------------- arithmetic: one query row, 32 key columns per thread
         regs_up<kBwdMathRegs>();
-        const int part = warp >> 2;
-        const int i = q0 + (warp & 3) * 32 + lane;
+        const int part = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        TokRange r{0, 0, 0, 0};
-        float nlse = 0.f, ndelta = 0.f;
-        if (i < p.T) {
-            r = tok_range(p, i);
-            nlse = p.nlse[(int64_t)h * p.Tp + i];
-            ndelta = p.ndelta[(int64_t)h * p.Tp + i];
-        }
-        ScoreMath S = score_math<MODE>(p);
-        if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[h] * kLog2e;
-        bool ok = true;
-        auto tile = [&](int j, uint32_t tsw, float dist, int a, int z, auto hides) {
-            constexpr bool HIDDEN = decltype(hides)::value;
-            float x[32], y[32];
-            uint32_t pk[16];
-            tmem_ld_f32<0>(tsw, x);
-            const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
-            const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
-            tmem_ld_wait_f32<0>(x);
-            if (some) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float2 bend = two(1.f);
-                    const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(nlse), bend);
-                    float2 P = make_float2(ex2(v.x), ex2(v.y));
-                    if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
-                    x[e] = P.x;
-                    x[e + 1] = P.y;
-                }
-            }
-            if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)j & 1u, s_abort, p.wait_ns)) return false;
-            tc_fence_after();
-            if (some) {
-                tmem_ld_f32<0>(tdp + lanes + part * 32, y);
-                tmem_ld_wait_f32<0>(y);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(ndelta));
-                    d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
-                    if (HIDDEN) {
-                        if (!(bits >> e & 1u)) d.x = 0.f;
-                        if (!(bits >> (e + 1) & 1u)) d.y = 0.f;
-                    }
-                    pk[e / 2] = pack_bf16x2(d.x, d.y);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) pk[e] = 0u;
-            }
-            tmem_st_x16(tsw, pk);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(dsfull));
-            return true;
+        struct RowOf {
+            int lo, hi;
+            float nlse, ndelta;
         };
-        for (int j = 0; j < N; ++j) {
-            const uint32_t tsw = tmem + lanes + (j & 1) * kTile + part * 32;
-            const int kt = (kt0 + j) * kTile, k0 = kt + part * 32;
-            const bool hidden = kt < rl.lo || kt + kTile > rf.hi;
-            const int a = r.lo - k0, z = r.hi - k0;
-            const float dist = (float)(i - k0);
-            if (!mbar_wait_warp(smem_u32(&sfull[j & 1]), ((uint32_t)j >> 1) & 1u, s_abort, p.wait_ns)) {
-                ok = false;
-                break;
+        auto row_of = [&](const DqItem& it) {
+            RowOf r{0, 0, 0.f, 0.f};
+            const int i = it.q0 + row;
+            if (it.valid && i < p.T) {
+                const TokRange t = tok_range(p, i);
+                r.lo = t.lo;
+                r.hi = t.hi;
+                r.nlse = p.nlse[(int64_t)it.h * p.Tp + i];
+                r.ndelta = p.ndelta[(int64_t)it.h * p.Tp + i];
             }
-            tc_fence_after();
-            ok = hidden ? tile(j, tsw, dist, a, z, std::true_type{}) : tile(j, tsw, dist, a, z, std::false_type{});
+            return r;
+        };
+        ScoreMath S = score_math<MODE>(p);
+        bool ok = true;
+        uint32_t t = 0, items = 0;  // tiles; items with tiles
+        DqItem next = dq_item(p, 0);
+        RowOf next_row = row_of(next);
+        for (int r = 0; ok && r < rounds; ++r) {
+            const DqItem it = next;
+            const RowOf R = next_row;
+            next = dq_item(p, r + 1);
+            next_row = row_of(next);
+            if (!it.valid) continue;
+            if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[it.h] * kLog2e;
+            auto tile = [&](uint32_t tsw, float dist, int a, int z, auto hides) {
+                constexpr bool HIDDEN = decltype(hides)::value;
+                float x[32], y[32];
+                uint32_t pk[16];
+                tmem_ld_f32<0>(tsw, x);
+                const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
+                const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
+                tmem_ld_wait_f32<0>(x);
+                if (some) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 bend = two(1.f);
+                        const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(R.nlse), bend);
+                        float2 P = make_float2(ex2(v.x), ex2(v.y));
+                        if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                        x[e] = P.x;
+                        x[e + 1] = P.y;
+                    }
+                }
+                if (!mbar_wait_warp(smem_u32(dpfull), t & 1u, s_abort, p.wait_ns)) return false;
+                tc_fence_after();
+                if (some) {
+                    tmem_ld_f32<0>(tdp + lanes + part * 32, y);
+                    tmem_ld_wait_f32<0>(y);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 d = __fadd2_rn(make_float2(y[e], y[e + 1]), two(R.ndelta));
+                        d = __fmul2_rn(d, make_float2(x[e], x[e + 1]));
+                        if (HIDDEN) {
+                            if (!(bits >> e & 1u)) d.x = 0.f;
+                            if (!(bits >> (e + 1) & 1u)) d.y = 0.f;
+                        }
+                        pk[e / 2] = pack_bf16x2(d.x, d.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                }
+                tmem_st_x16(tsw, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(dsfull));
+                return true;
+            };
+            for (int j = 0; j < it.N; ++j, ++t) {
+                const uint32_t tsw = tmem + lanes + (t & 1u) * kTile + part * 32;
+                const int kt = (it.kt0 + j) * kTile, k0 = kt + part * 32;
+                const bool hidden = kt < it.lo_max || kt + kTile > it.hi_min;
+                const float dist = (float)(it.q0 + row - k0);
+                ok = mbar_wait_warp(smem_u32(&sfull[t & 1u]), (t >> 1) & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                ok = hidden ? tile(tsw, dist, R.lo - k0, R.hi - k0, std::true_type{})
+                            : tile(tsw, dist, 0, 0, std::false_type{});
+                if (!ok) break;
+            }
             if (!ok) break;
+            if (it.N > 0) {
+                ok = mbar_wait_warp(smem_u32(dqdone), items & 1u, s_abort, p.wait_ns);
+                if (!ok) break;
+                ++items;
+                tc_fence_after();
+            }
+            // each warpgroup a quarter of the dims, a thread one row of them
+            const int i = it.q0 + row;
+            store_dims<DP / 4>(p.out + ((int64_t)i * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d, p.scale, it.N > 0, i < p.T);
+            tc_fence_before();  // (the next item's products may overwrite dQ once dz says so)
         }
-        if (ok && N > 0) ok = mbar_wait_warp(smem_u32(drain), 0, s_abort, p.wait_ns);
-        tc_fence_after();
         if (!ok && lane == 0) {
             attn_error(p, 7, 3);
             *s_abort = 1;
-        }
-        // DP / 64 warpgroups write a box of 64 dims each, staged where the queries were
-        if (group_ok(ok, s_bad + part, 1 + part) && part < DP / 64) {
-            const int r128 = (warp & 3) * 32 + lane;
-            uint8_t* box = sq + part * kBoxBytes;
-            stage_row(box, r128, tdq + lanes + part * 64, p.scale, N > 0);
-            store_box(&maps.dQ, box, part * 64, h, q0, 1 + part, r128 == 0);
         }
         tc_fence_before();
     }
@@ -672,46 +737,46 @@ cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, cudaStream_t st
     return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 template <int DP, int MODE>
-cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
+cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                DqCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hq;
+    const int64_t items = (int64_t)((p.T + kTile - 1) / kTile) * p.hq;
+    const unsigned grid = (unsigned)(items < sms ? items : sms);
     return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
 template <int DP, int MODE>
-cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
+cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
     {
         LaunchTag tag("attn.dkv", st);
         const cudaError_t e = launch_dkv<DP, MODE>(p, maps, st);
         if (e != cudaSuccess) return e;
     }
     LaunchTag tag("attn.dq", st);
-    return launch_dq<DP, MODE>(p, maps, st);
+    return launch_dq<DP, MODE>(p, maps, sms, st);
 }
 
-lm_status launch_attn_bwd(const AttnParams& p, cudaStream_t st) {
+lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
     BwdMaps maps;
     const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs}, dO{p.dO.p, p.dO.ts, p.dO.hs};
     lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.dO, dO, p.T, p.hq, p.d, kTile);
-    if (s == LM_OK) s = encode_heads(&maps.dQ, lm_heads{p.out, (int64_t)p.hq * p.d, p.d}, p.T, p.hq, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.dK, lm_heads{p.dK, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.dV, lm_heads{p.dV, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
     if (s != LM_OK) return s;
     const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes ? ATTN_BIAS : ATTN_PLAIN;
     cudaError_t e;
     if (p.d <= 64)
-        e = mode == ATTN_CAP    ? launch_both<64, ATTN_CAP>(p, maps, st)
-            : mode == ATTN_BIAS ? launch_both<64, ATTN_BIAS>(p, maps, st)
-                                : launch_both<64, ATTN_PLAIN>(p, maps, st);
+        e = mode == ATTN_CAP    ? launch_both<64, ATTN_CAP>(p, maps, sms, st)
+            : mode == ATTN_BIAS ? launch_both<64, ATTN_BIAS>(p, maps, sms, st)
+                                : launch_both<64, ATTN_PLAIN>(p, maps, sms, st);
     else
-        e = mode == ATTN_CAP    ? launch_both<128, ATTN_CAP>(p, maps, st)
-            : mode == ATTN_BIAS ? launch_both<128, ATTN_BIAS>(p, maps, st)
-                                : launch_both<128, ATTN_PLAIN>(p, maps, st);
+        e = mode == ATTN_CAP    ? launch_both<128, ATTN_CAP>(p, maps, sms, st)
+            : mode == ATTN_BIAS ? launch_both<128, ATTN_BIAS>(p, maps, sms, st)
+                                : launch_both<128, ATTN_PLAIN>(p, maps, sms, st);
     return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn backward launch: %s", cudaGetErrorString(e));
 }
 

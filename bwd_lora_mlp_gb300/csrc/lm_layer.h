@@ -61,7 +61,7 @@ struct AttnParams {
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st);
 lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st);
-lm_status launch_attn_bwd(const AttnParams& p, cudaStream_t st);
+lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st);
 
 // ---- addnorm
 struct AddNormParams {

@@ -231,7 +231,7 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
         LaunchTag tag("attn.delta", st);
         LL_TRY(launched(launch_attn_delta(p, delta, nlse, st), "attn delta launch"));
     }
-    return launch_attn_bwd(p, st);
+    return launch_attn_bwd(p, sms, st);
 }
 
 // ------------------------------------------------------------------ addnorm
