@@ -290,12 +290,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ScoreMath S = score_math<MODE>(p);
         bool ok = true;
         // one query tile, its scores ready; tiles with hidden pairs have code of their own
-        auto tile = [&](int it, const float* row, float dist, int a, int z, auto hides) {
+        auto tile = [&](int it, const float* row, float dist, uint32_t bits, auto hides) {
             constexpr bool HIDDEN = decltype(hides)::value;
             float x[32];
             uint32_t pk[16];
             tmem_ld_f32<0>(tsw, x);
-            const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
             const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
             tmem_ld_wait_f32<0>(x);
             if (some) {  // (a chunk that none of the warp's keys is seen from has no exponentials)
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const float* row = srow + (it % kQStages) * 2 * kTile + part * 32;
                 // every query of the tile sees every key of this one, or some pair is hidden
                 const bool hidden = qt * kTile < rl.qlo || (qt + 1) * kTile > rf.qhi;
-                const int a = r.qlo - q0, z = r.qhi - q0;
+                const uint32_t bits = hidden ? bits_between(r.qlo - q0, r.qhi - q0) : ~0u;
                 const float dist = (float)(q0 - k);
                 // the query tile's rows (nlse, -delta) come with it; the scores are ready after it is
                 if (!mbar_wait_warp(smem_u32(&qfull[it % kQStages]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns) ||
@@ -374,7 +373,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     break;
                 }
                 tc_fence_after();
-                ok = hidden ? tile(it, row, dist, a, z, std::true_type{}) : tile(it, row, dist, a, z, std::false_type{});
+                // (a warp whose keys are seen from all of its columns has nothing to mask)
+                ok = __all_sync(0xffffffffu, bits == ~0u) ? tile(it, row, dist, bits, std::false_type{})
+                                                         : tile(it, row, dist, bits, std::true_type{});
                 if (!ok) break;
             }
         }
@@ -644,12 +645,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             next_row = row_of(next);
             if (!it.valid) continue;
             if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[it.h] * kLog2e;
-            auto tile = [&](uint32_t tsw, float dist, int a, int z, auto hides) {
+            auto tile = [&](uint32_t tsw, float dist, uint32_t bits, auto hides) {
                 constexpr bool HIDDEN = decltype(hides)::value;
                 float x[32], y[32];
                 uint32_t pk[16];
                 tmem_ld_f32<0>(tsw, x);
-                const uint32_t bits = HIDDEN ? bits_between(a, z) : ~0u;
                 const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
                 tmem_ld_wait_f32<0>(x);
                 if (some) {
@@ -697,8 +697,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = mbar_wait_warp(smem_u32(&sfull[t & 1u]), (t >> 1) & 1u, s_abort, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
-                ok = hidden ? tile(tsw, dist, R.lo - k0, R.hi - k0, std::true_type{})
-                            : tile(tsw, dist, 0, 0, std::false_type{});
+                const uint32_t bits = hidden ? bits_between(R.lo - k0, R.hi - k0) : ~0u;
+                // (a warp whose rows see all of its columns has nothing to mask)
+                ok = __all_sync(0xffffffffu, bits == ~0u) ? tile(tsw, dist, bits, std::false_type{})
+                                                         : tile(tsw, dist, bits, std::true_type{});
                 if (!ok) break;
             }
             if (!ok) break;
