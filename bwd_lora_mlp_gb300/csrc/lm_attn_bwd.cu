@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
         if (warp == kBwdMath + 1) {  // ---------------- loader
-            if (lane == 0 && N > 0) {
+            if (lane == 0 && N > 0 && !(p.starve & K_ATTN_DKV)) {
                 bool ok = true;
                 mbar_expect_tx(smem_u32(kvfull), 2 * C::kTileBytes);
                 for (int b = 0; b < DP / 64; ++b) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) {
                 bool ok = true;
                 uint32_t nk = 0, nv = 0, nq[2] = {0, 0};  // tiles asked for
-                for (int r = 0; ok && r < rounds; ++r) {
+                for (int r = p.starve & K_ATTN_DQ ? rounds : 0; ok && r < rounds; ++r) {
                     const DqItem it = dq_item(p, r);
                     auto query = [&](int which) {  // Q, then dO
                         if (!mbar_wait(smem_u32(&qempty[which]), (nq[which] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;

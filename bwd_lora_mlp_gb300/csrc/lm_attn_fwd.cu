@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) {
                 bool ok = true;
                 uint32_t n = 0, nq[2] = {0, 0};  // tiles and queries asked for
-                for (int k = 0; ok && k < rounds; ++k) {
+                for (int k = p.starve & K_ATTN_FWD ? rounds : 0; ok && k < rounds; ++k) {
                     const Item it = item_of(p, k);
                     auto query = [&](int w) {
                         if (!it.span[w].any()) return true;

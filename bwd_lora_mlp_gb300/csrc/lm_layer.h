@@ -57,7 +57,9 @@ struct AttnParams {
     uint16_t *dK, *dV;
     int32_t* err;
     uint64_t wait_ns;
+    int32_t starve;        // kernels whose loaders ask for nothing (attn_debug_inject)
 };
+enum AttnKernel : int { K_ATTN_FWD = 1, K_ATTN_DKV = 2, K_ATTN_DQ = 4 };
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st);
 lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st);
 cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st);

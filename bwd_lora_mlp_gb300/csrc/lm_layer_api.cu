@@ -61,6 +61,10 @@ lm_status check_alias(std::initializer_list<Span> outs, std::initializer_list<Sp
 }
 
 // ------------------------------------------------------------------ attention
+// test hook (attn_debug_inject)
+thread_local int32_t g_starve = 0;
+thread_local uint64_t g_wait_ns = 0;
+
 constexpr int64_t kMaxTokens = int64_t(1) << 20;
 
 lm_status check_attn_shape(int64_t T, int32_t hq, int32_t hk, int32_t d) {
@@ -138,7 +142,8 @@ AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_he
     p.k = {k->p, k->token_stride, k->head_stride};
     p.v = {v->p, v->token_stride, v->head_stride};
     p.err = static_cast<int32_t*>(ws);
-    p.wait_ns = kDefaultWaitNs;
+    p.wait_ns = g_wait_ns ? g_wait_ns : kDefaultWaitNs;
+    p.starve = g_starve;
     return p;
 }
 
@@ -158,6 +163,13 @@ extern "C" lm_status attn_workspace_size(int64_t T, int32_t hq, int32_t hk, int3
     return LM_OK;
 }
 
+extern "C" lm_status attn_debug_inject(int32_t kernel_mask, uint64_t wait_ns) {
+    if (kernel_mask < 0 || kernel_mask > 7) return report_error(LM_ERR_SHAPE, "kernel_mask = %d is not in [0, 7]", kernel_mask);
+    g_starve = kernel_mask;
+    g_wait_ns = wait_ns;
+    return LM_OK;
+}
+
 extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
                               const lm_heads* v, const lm_attn* a, uint16_t* O, int8_t* O_lo, float* lse, void* ws,
                               size_t ws_bytes, lm_stream stream) {
@@ -172,7 +184,8 @@ extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     LL_TRY(need(ws, 32, "ws"));
     const AttnPlan P = plan_attn(T, hq);
     if (ws_bytes < P.total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, P.total);
-    LL_TRY(check_alias({{O, (size_t)T * hq * d * 2, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}, {ws, P.total, "ws"}},
+    LL_TRY(check_alias({{O, (size_t)T * hq * d * 2, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"},
+                        {lse, (size_t)T * hq * 4, "lse"}, {ws, P.total, "ws"}},
                        {heads_span(q, T, hq, d, "q"), heads_span(k, T, hk, d, "k"), heads_span(v, T, hk, d, "v")}));
     if (T == 0) return LM_OK;
     int sms = 0;
@@ -189,8 +202,8 @@ extern "C" lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
 
 extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
                               const lm_heads* v, const lm_heads* dO, const uint16_t* O, const int8_t* O_lo,
-                              const float* lse, const lm_attn* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws, size_t ws_bytes,
-                              lm_stream stream) {
+                              const float* lse, const lm_attn* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws,
+                              size_t ws_bytes, lm_stream stream) {
     LL_TRY(check_attn_shape(T, hq, hk, d));
     LL_TRY(check_attn(a));
     LL_TRY(check_heads(q, T, hq, d, "q"));
@@ -209,7 +222,8 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     const size_t bq = (size_t)T * hq * d * 2, bk = (size_t)T * hk * d * 2;
     LL_TRY(check_alias({{dQ, bq, "dQ"}, {dK, bk, "dK"}, {dV, bk, "dV"}, {ws, P.total, "ws"}},
                        {heads_span(q, T, hq, d, "q"), heads_span(k, T, hk, d, "k"), heads_span(v, T, hk, d, "v"),
-                        heads_span(dO, T, hq, d, "dO"), {O, bq, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"}, {lse, (size_t)T * hq * 4, "lse"}}));
+                        heads_span(dO, T, hq, d, "dO"), {O, bq, "O"}, {O_lo, (size_t)T * hq * ((d + 15) / 16 * 16), "O_lo"},
+                        {lse, (size_t)T * hq * 4, "lse"}}));
     if (T == 0) return LM_OK;
     int sms = 0;
     LL_TRY(device_ready(&sms));

@@ -3,11 +3,14 @@ packed documents, the residual add with the norms before and after a block, and 
 of given tokens, forward and backward.
 
 Argument marshalling only, as in lib.py: types and layouts are checked here, sizes and pointers by
-the C entry point of the same name, and every non-zero status raises ``LmError``.
+the C entry point of the same name, and every non-zero status raises ``LmError``.  Every operator
+takes ``stream`` (a torch stream or a raw handle; None: the current one): its results and workspace
+are allocated on the stream that its kernels run on.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -48,6 +51,7 @@ _NP = ctypes.POINTER(lm_addnorm)
 
 _SIGS = {
     "attn_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
+    "attn_debug_inject": ([_I32, ctypes.c_uint64], _I32),
     "attn_fwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
     "attn_bwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _P, _P, _P, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
     "addnorm_workspace_size": ([_I64, _I64, _SZP], _I32),
@@ -116,9 +120,24 @@ def _shaped(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
 _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _stream(stream) -> int:
-    """The raw stream: the current one without building a Stream object (3 us of a call's 20)."""
-    return _raw_stream(_device()) if stream is None else L._stream(stream)
+def _stream() -> int:
+    """The current raw stream, without building a Stream object (3 us of a call's 20)."""
+    return _raw_stream(_device())
+
+
+def _on_stream(op):
+    """The operator with a ``stream`` argument: that stream is the current one for the whole call, so that
+    what it allocates and zeroes is ordered before its kernels."""
+    @functools.wraps(op)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return op(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = L._stream(stream)
+            stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return op(*args, **kw)
+    return call
 
 
 # ---------------------------------------------------------------------------------------------
@@ -175,7 +194,8 @@ def attn_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
     return _size("attn_workspace_size", T, hq, hk, d)
 
 
-def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None, stream=None) -> dict:
+@_on_stream
+def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None) -> dict:
     """q (T, hq, d), k and v (T, hk, d) -> O (T, hq, d), lse (hq, T) and, with ``train``, O_lo (int8: more
     bits of O, for the backward)."""
     (T, hq, d), hk = q.shape, k.shape[1]
@@ -187,11 +207,12 @@ def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, 
     ws = workspace(attn_workspace_size(T, hq, hk, d), dev) if ws is None else ws
     _call("attn_fwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
           a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, _d16(d)), torch.int8, "O_lo"),
-          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
 
 
-def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None, stream=None) -> dict:
+@_on_stream
+def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None) -> dict:
     """The gradients of q, k and v from dO (T, hq, d) and the forward's result."""
     (T, hq, d), hk = q.shape, k.shape[1]
     dev, bf = q.device, torch.bfloat16
@@ -201,9 +222,9 @@ def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None
     ws = fwd["ws"] if ws is None else ws
     _call("attn_bwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
           _heads(dO, T, hq, d, "dO"), _shaped(fwd["O"], (T, hq, d), bf, "O"),
-          _shaped(fwd["O_lo"], (T, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"), a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"),
-          _shaped(dK, (T, hk, d), bf, "dK"), _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"),
-          ws.numel(), _stream(stream))
+          _shaped(fwd["O_lo"], (T, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"),
+          a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"), _shaped(dK, (T, hk, d), bf, "dK"),
+          _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"dQ": dQ, "dK": dK, "dV": dV}
 
 
@@ -238,7 +259,8 @@ def addnorm_workspace_size(T: int, d: int) -> int:
     return _size("addnorm_workspace_size", T, d)
 
 
-def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
+@_on_stream
+def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None) -> dict:
     """h (T, d) bf16 or float32, y (T, d) bf16 or None -> h (the sum; h itself without y), x (None
     without w_in), rstd_y, rstd_h."""
     T, d = h.shape
@@ -252,12 +274,12 @@ def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
     rstd_h = torch.empty(T, dtype=f32, device=dev) if n.w_in is not None else None
     _call("addnorm_fwd", T, d, _shaped(h, td, h.dtype, "h"), _shaped(y, td, bf, "y"), n.c_struct(d, h.dtype),
           _shaped(h_out, td, h.dtype, "h_out"), _shaped(x, td, bf, "x"), _shaped(rstd_y, (T,), f32, "rstd_y"),
-          _shaped(rstd_h, (T,), f32, "rstd_h"), _stream(stream))
+          _shaped(rstd_h, (T,), f32, "rstd_h"), _stream())
     return {"h": h if y is None else h_out, "x": x, "rstd_y": rstd_y, "rstd_h": rstd_h}
 
 
-def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None,
-                stream=None) -> dict:
+@_on_stream
+def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None) -> dict:
     """Gradients from those of the sum (dh_out, None: zero) and of x (dx), with the forward's inputs h and
     y: dh, dy, and with ``weights`` the float32 gradients of the vectors that are there."""
     T, d = h.shape
@@ -275,7 +297,7 @@ def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, d
           _shaped(fwd["rstd_y"], (T,), f32, "rstd_y"), _shaped(fwd["rstd_h"], (T,), f32, "rstd_h"),
           n.c_struct(d, h.dtype), _shaped(dh, (T, d), h.dtype, "dh"), _shaped(dy, (T, d), bf, "dy"),
           _shaped(dw_in, (d,), f32, "dw_in"), _shaped(dw_post, (d,), f32, "dw_post"), _shaped(dgate, (d,), f32, "dgate"),
-          L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+          L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"dh": dh, "dy": dy, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
 
 
@@ -303,7 +325,8 @@ def _targets(t: torch.Tensor, T: int):
     return _shaped(t, (T,), t.dtype, "targets"), _INDEX[t.dtype]
 
 
-def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0, stream=None) -> dict:
+@_on_stream
+def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0) -> dict:
     """logits (T, V) bf16 or float32 (rows may be strided), targets (T) -> logp, entropy, lse (T) float32 and,
     for k > 0, top_ids (T, k) int32 and top_logp (T, k) float32."""
     T, V = logits.shape
@@ -314,12 +337,12 @@ def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0, stream=None) ->
     ids = torch.empty((T, k), dtype=torch.int32, device=dev) if k > 0 else None
     top = torch.empty((T, k), dtype=f32, device=dev) if k > 0 else None
     _call("logprob_fwd", T, V, ld, p, dt, tp, ti, scale, k, L._ptr(logp), L._ptr(entropy), L._ptr(lse), L._ptr(ids),
-          L._ptr(top), _stream(stream))
+          L._ptr(top), _stream())
     return {"logp": logp, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logp": top}
 
 
-def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: float = 1.0, dlogits=None,
-                stream=None) -> dict:
+@_on_stream
+def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: float = 1.0, dlogits=None) -> dict:
     """dlogits (T, V), in the logits' type, from the gradients of logp and entropy (T float32; None: zero).
     ``dlogits`` may be ``logits`` itself."""
     T, V = logits.shape
@@ -333,5 +356,5 @@ def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: fl
     po, ldo, _ = _rows2d(dlogits, "dlogits")
     _call("logprob_bwd", T, V, ld, p, dt, tp, ti, scale, _shaped(fwd["lse"], (T,), f32, "lse"),
           _shaped(fwd["entropy"], (T,), f32, "entropy"), _shaped(dlogp, (T,), f32, "dlogp"),
-          _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, _stream(stream))
+          _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, _stream())
     return {"dlogits": dlogits}

@@ -41,15 +41,20 @@ typedef enum lm_index { LM_I32 = 0, LM_I64 = 1 } lm_index;
  * tokens and heads may be strided (slices of one QKV buffer, head-major layouts): strides in
  * elements, multiples of 8 and at least d, base 16-byte aligned, last dimension contiguous.
  * T <= 2^20.  O (T x hq x d) bf16 and lse (hq x T, natural logarithm) fp32 are contiguous.
- * O_lo (T x hq x d16 int8, d16 = d rounded up to 16, or NULL where no backward follows) takes the next eight bits of O's fp32
- * pattern: fp32 bits of O = (bits of the bf16 << 16) + (O_lo << 8), to the nearest, O_lo in [-128, 127].
+ * O_lo (T x hq x d16 int8, d16 = d rounded up to 16, or NULL where no backward follows) takes the
+ * next eight bits of O's fp32 pattern: fp32 bits of O = (bits of the bf16 << 16) + (O_lo << 8), to the
+ * nearest, O_lo in [-128, 127].
  * The backward takes O, O_lo and lse as the forward left them and writes dQ (T x hq x d), dK and dV
  * (T x hk x d) bf16, contiguous; a key/value head's gradients are summed over its hq / hk query
  * heads in fp32.  The slopes are constants (no gradient).  P and the score gradients are rounded
  * to bf16 for the second products, as are the outputs; every sum is fp32.  dO_i . O_i cancels most of
  * dO_i . v_j where few keys matter, which is why the backward takes O with O_lo's bits (O_lo may be
- * NULL there too: the first tokens of a document then have gradients good to a per cent or two).  The workspace begins
- * with the error word (lm_workspace_reset, lm_workspace_check); the same one serves both calls. */
+ * NULL there too: the first tokens of a document then have gradients good to a per cent or two).
+ * The workspace begins with the error word (lm_workspace_reset, lm_workspace_check); the same one
+ * serves both calls.  Kernel families in its reports: 5 forward, 6 dK and dV, 7 dQ.
+ * attn_debug_inject is a test hook like lm_debug_inject, for this thread's following calls: the
+ * loaders of the masked kernels (1 forward, 2 dK and dV, 4 dQ) ask for nothing, so their waits run out
+ * after wait_ns (0: the default); attn_debug_inject(0, 0) restores normal operation. */
 typedef struct lm_heads {
     const uint16_t* p;
     int64_t token_stride;
@@ -69,13 +74,14 @@ typedef struct lm_attn {
 } lm_attn;
 
 LM_API lm_status attn_workspace_size(int64_t T, int32_t hq, int32_t hk, int32_t d, size_t* bytes);
+LM_API lm_status attn_debug_inject(int32_t kernel_mask, uint64_t wait_ns);
 LM_API lm_status attn_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
                           const lm_heads* v, const lm_attn* a, uint16_t* O, int8_t* O_lo, float* lse, void* ws,
                           size_t ws_bytes, lm_stream stream);
 LM_API lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
                           const lm_heads* v, const lm_heads* dO, const uint16_t* O, const int8_t* O_lo,
-                          const float* lse, const lm_attn* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws, size_t ws_bytes,
-                          lm_stream stream);
+                          const float* lse, const lm_attn* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws,
+                          size_t ws_bytes, lm_stream stream);
 
 /* ---- residual add with the norms before and after a block ----------------------------------
  *   N(a; w) = a * rsqrt(mean(a^2) + eps) * (w + w_offset)     (over a row's d values)
