@@ -33,10 +33,10 @@ static RowPlan plan_rows(int d, int one) {
     P.threads = P.rows * P.warps * 32;
     return P;
 }
-constexpr int kFwdOne = 8192, kBwdOne = 4096;
+constexpr int kFwdOne = 2048, kBwdOne = 4096;
 // Rows on their way: as many as the shared memory holds beside a first-level cache for the weights that
 // are not in registers.
-constexpr int fwd_stages(int nv) { return nv == 1 ? 3 : 1; }
+constexpr int fwd_stages(int nv, int most) { return nv == 1 ? 3 : most <= 512 ? 2 : 1; }
 constexpr int bwd_stages(int nv, bool h32, int most) { return nv == 1 ? 3 : most <= 512 && !h32 ? 2 : 1; }
 
 // ------------------------------------------------------------------ eight columns, as pairs
@@ -134,7 +134,7 @@ struct RowGroup {
 template <int NV, bool H32, bool W32, int MOST>
 __global__ void __launch_bounds__(MOST, 1024 / MOST)
     addnorm_fwd_kernel(const __grid_constant__ AddNormParams p, int warps, int rows) {
-    constexpr int kHp = H32 ? 2 : 1, kPieces = kHp + 1, kStages = fwd_stages(NV);
+    constexpr int kHp = H32 ? 2 : 1, kPieces = kHp + 1, kStages = fwd_stages(NV, MOST);
     __shared__ float red[2 * 32];
     extern __shared__ uint4 smem_raw[];  // [stage][vector][piece][thread]
     griddep_launch_dependents();
@@ -453,7 +453,7 @@ static cudaError_t launch_rows(K kernel, int grid, const RowPlan& P, size_t smem
 }
 template <int NV, bool H32, bool W32, int MOST>
 static cudaError_t fwd_launch(const AddNormParams& p, const RowPlan& P, cudaStream_t st) {
-    const size_t smem = (size_t)fwd_stages(NV) * NV * (H32 ? 3 : 2) * P.threads * 16;
+    const size_t smem = (size_t)fwd_stages(NV, MOST) * NV * (H32 ? 3 : 2) * P.threads * 16;
     const int grid = (int)std::min<int64_t>(1024 / MOST * kSms, (p.T + P.rows - 1) / P.rows);
     return launch_rows(addnorm_fwd_kernel<NV, H32, W32, MOST>, grid, P, smem, p, st);
 }
@@ -491,7 +491,7 @@ static cudaError_t bwd_types(const AddNormParams& p, const RowPlan& P, cudaStrea
 
 cudaError_t launch_addnorm_fwd(const AddNormParams& p, cudaStream_t st) {
     const RowPlan P = plan_rows(p.d, kFwdOne);
-    if (P.nv == 2) return fwd_types<2, 1024>(p, P, st);
+    if (P.nv == 2) return P.threads <= 512 ? fwd_types<2, 512>(p, P, st) : fwd_types<2, 1024>(p, P, st);
     return P.threads <= 512 ? fwd_types<1, 512>(p, P, st) : fwd_types<1, 1024>(p, P, st);
 }
 cudaError_t launch_addnorm_bwd(const AddNormParams& p, cudaStream_t st) {

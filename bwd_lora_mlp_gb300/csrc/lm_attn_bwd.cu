@@ -59,46 +59,60 @@ struct BwdMaps {
 };
 
 // ------------------------------------------------------------------ delta, and lse in the exponent's units
-// 16 threads a row (token, head): 8 dims each.  Tokens that see nothing get zeros, whatever dO holds.
+// A CTA takes 16 tokens and kDeltaHeads heads: 16 threads a token, 8 dims each, all heads' loads in flight at
+// once.  The results lie by head, so they are exchanged and leave 16 tokens at a time.  Tokens that see
+// nothing get zeros, whatever dO holds.
+constexpr int kDeltaHeads = 4;
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* ndelta, float* nlse) {
+    __shared__ float s_delta[kDeltaHeads][16], s_nlse[kDeltaHeads][16];
     griddep_launch_dependents();
     griddep_wait();
-    const int sub = threadIdx.x & 15;
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-    const int t = (int)(row / p.hq), h = (int)(row - (int64_t)t * p.hq);
-    if (t >= p.Tp) return;
-    float s = 0.f, nl = 0.f;
-    if (t < p.T) {
-        const float lse = p.lse_in[(int64_t)h * p.T + t];
-        if (lse > -INFINITY || lse != lse) {
-            if (sub * 8 < p.d) {
-                const uint4 a = *reinterpret_cast<const uint4*>(p.dO.p + (int64_t)t * p.dO.ts + (int64_t)h * p.dO.hs + sub * 8);
-                const int64_t at = row * p.d + sub * 8;
-                const uint4 b = *reinterpret_cast<const uint4*>(p.O + at);
-                uint2 lo = make_uint2(0, 0);
-                if (p.O_lo) lo = *reinterpret_cast<const uint2*>(p.O_lo + row * p.d16 + sub * 8);
-                const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    const int sub = threadIdx.x & 15, mine = threadIdx.x >> 4;
+    const int t0 = (int)blockIdx.x * 16, t = t0 + mine, h0 = (int)blockIdx.y * kDeltaHeads;
+    float lse[kDeltaHeads];
+    uint4 a[kDeltaHeads], b[kDeltaHeads];
+    uint2 lo[kDeltaHeads];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t ob = e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16;
-                    const int more = (int)(int8_t)((e < 4 ? lo.x : lo.y) >> (8 * (e & 3)));
-                    s += (e & 1 ? bf16hi(av[e >> 1]) : bf16lo(av[e >> 1])) * __uint_as_float(ob + (uint32_t)(more * 256));
-                }
-            }
-            nl = -lse * kLog2e;
+    for (int r = 0; r < kDeltaHeads; ++r) {
+        const int h = h0 + r;
+        a[r] = b[r] = make_uint4(0, 0, 0, 0);
+        lo[r] = make_uint2(0, 0);
+        lse[r] = -INFINITY;
+        if (t >= p.T || h >= p.hq) continue;
+        lse[r] = p.lse_in[(int64_t)h * p.T + t];
+        if (sub * 8 >= p.d) continue;
+        const int64_t row = (int64_t)t * p.hq + h;
+        a[r] = *reinterpret_cast<const uint4*>(p.dO.p + (int64_t)t * p.dO.ts + (int64_t)h * p.dO.hs + sub * 8);
+        b[r] = *reinterpret_cast<const uint4*>(p.O + row * p.d + sub * 8);
+        if (p.O_lo) lo[r] = *reinterpret_cast<const uint2*>(p.O_lo + row * p.d16 + sub * 8);
+    }
+#pragma unroll
+    for (int r = 0; r < kDeltaHeads; ++r) {
+        const bool sees = lse[r] > -INFINITY || lse[r] != lse[r];
+        const uint32_t av[4] = {a[r].x, a[r].y, a[r].z, a[r].w}, bv[4] = {b[r].x, b[r].y, b[r].z, b[r].w};
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t ob = e & 1 ? bv[e >> 1] & 0xFFFF0000u : bv[e >> 1] << 16;
+            const int more = (int)(int8_t)((e < 4 ? lo[r].x : lo[r].y) >> (8 * (e & 3)));
+            s += (e & 1 ? bf16hi(av[e >> 1]) : bf16lo(av[e >> 1])) * __uint_as_float(ob + (uint32_t)(more * 256));
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (sub == 0) {
+            s_delta[r][mine] = sees ? -s : 0.f;
+            s_nlse[r][mine] = sees ? -lse[r] * kLog2e : 0.f;
         }
     }
-#pragma unroll
-    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (sub == 0) {
-        ndelta[(int64_t)h * p.Tp + t] = -s;
-        nlse[(int64_t)h * p.Tp + t] = nl;
-    }
+    __syncthreads();
+    const int r = mine % kDeltaHeads, which = mine / kDeltaHeads;
+    if (which < 2 && h0 + r < p.hq)
+        (which ? nlse : ndelta)[(int64_t)(h0 + r) * p.Tp + t0 + sub] = which ? s_nlse[r][sub] : s_delta[r][sub];
 }
 
 cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st) {
-    const int64_t rows = (int64_t)p.Tp * p.hq;
-    return launch_pdl(attn_delta_kernel, dim3((unsigned)(rows / 16)), dim3(256), 0, st, nullptr, 0, p, ndelta, nlse);
+    const dim3 grid((unsigned)(p.Tp / 16), (unsigned)((p.hq + kDeltaHeads - 1) / kDeltaHeads));  // (Tp: whole 128-token tiles)
+    return launch_pdl(attn_delta_kernel, grid, dim3(256), 0, st, nullptr, 0, p, ndelta, nlse);
 }
 
 // ------------------------------------------------------------------ dK, dV

@@ -99,17 +99,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 struct Sums {
     float m, S, w;
 };
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
-    Sums r;
-    r.m = max_nan(a.m, b.m);
-    if (r.m == -INFINITY) return Sums{-INFINITY, 0.f, 0.f};
-    const float da = a.m - r.m, db = b.m - r.m;  // (one is 0)
-    const float fa = lp_ex2(da * kL2e), fb = lp_ex2(db * kL2e);
-    r.S = a.S * fa + b.S * fb;
-    // w moves with the maximum: sum e^{x-m} (x-m); an empty part has da = -inf and counts nothing
-    r.w = (a.S > 0.f ? fa * fmaf(a.S, da, a.w) : 0.f) + (b.S > 0.f ? fb * fmaf(b.S, db, b.w) : 0.f);
-    if (a.m != a.m || b.m != b.m) r.S = r.w = r.m;
-    return r;
+// The sums of the parts held by N neighbouring lanes (N a power of two), the same in all of them: the largest
+// maximum first, every part brought to it once, then plain sums in a fixed order.
+template <int N>
+__device__ __forceinline__ Sums join(Sums s) {
+    float m = s.m;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float d = s.m - m, f = lp_ex2(d * kL2e);
+    // w moves with the maximum: sum e^{x-m} (x-m); an empty part has d = -inf (or NaN) and counts nothing
+    const bool any = s.S > 0.f;
+    s.w = any ? f * fmaf(s.S, d, s.w) : 0.f;
+    s.S = any ? s.S * f : 0.f;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+        s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+        s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    }
+    if (m != m) s.S = s.w = m;
+    s.m = m;
+    return s;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -159,7 +168,8 @@ __device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_
             const int at = atomicAdd(&sm.count, 1);
             if (at < kCand) sm.cand[at] = rank_of(x, (uint32_t)j);
         };
-        scan<2>(row, j0, j1, [&](const float (&x)[2][W], int64_t j, int n) {
+        // (what reaches the bound is in a thread whose own largest does)
+        if (own_max >= bound) scan<2>(row, j0, j1, [&](const float (&x)[2][W], int64_t j, int n) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 float big = x[u][0];
@@ -294,15 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_c
         s.w = fmaf(y, fmaxf(x - s.m, -1e30f), s.w);
     });
     if (s.m != s.m) s.S = s.w = s.m;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const Sums q{__shfl_xor_sync(0xffffffffu, s.m, o), __shfl_xor_sync(0xffffffffu, s.S, o), __shfl_xor_sync(0xffffffffu, s.w, o)};
-        s = (threadIdx.x & o) ? join(q, s) : join(s, q);  // (the same operands in the same order in both lanes)
-    }
+    s = join<32>(s);
     if ((threadIdx.x & 31) == 0) sm.warp[threadIdx.x >> 5] = s;
     __syncthreads();
-    s = sm.warp[0];
-    for (int i = 1; i < kThreads / 32; ++i) s = join(s, sm.warp[i]);
+    s = join<kThreads / 32>(sm.warp[threadIdx.x & (kThreads / 32 - 1)]);
     if (p.k) segment_top(row, j0, j1, p.k, order_key(own) & (j0 < j1 ? ~0u : 0u), sm);
     if (cluster > 1) {
         if (threadIdx.x == 0) {
@@ -313,8 +318,9 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_c
         if (threadIdx.x < p.k) st_first(&sm.best[part * p.k + threadIdx.x], sm.mine[threadIdx.x]);
         cluster_sync();
         if (part) return;
-        s = Sums{sm.seg[0][0], sm.seg[0][1], sm.seg[0][2]};
-        for (int i = 1; i < cluster; ++i) s = join(s, Sums{sm.seg[i][0], sm.seg[i][1], sm.seg[i][2]});
+        const int i = threadIdx.x & (kMaxCluster - 1);
+        s = i < cluster ? Sums{sm.seg[i][0], sm.seg[i][1], sm.seg[i][2]} : Sums{-INFINITY, 0.f, 0.f};
+        s = join<kMaxCluster>(s);
         const int n = cluster * p.k;
         if (threadIdx.x < n) {
             const uint64_t r = sm.best[threadIdx.x];
