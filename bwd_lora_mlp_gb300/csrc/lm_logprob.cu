@@ -7,6 +7,7 @@
 // (in L2 by then) for what reaches the bound finds k of them among a few dozen.  Bound by memory.
 // Backward: one pass, dx = scale (g 1[target] - p (g + gH (log p + H))).
 #include <algorithm>
+#include <type_traits>
 
 #include "lm_layer.h"
 #include "lm_ptx.cuh"
@@ -51,7 +52,7 @@ struct Row {
     }
 };
 
-// f(x, index of vector 0) over [j0, j1) in batches of U whole vectors of a thread (vector u lies
+// f(v, index of vector 0) over [j0, j1) in batches of U whole vectors of a thread (vector u lies
 // u kThreads vectors on; n of them are there), the next batch loading meanwhile, and one(x, index) for
 // the single elements before the first and after the last 16-byte boundary.
 template <int U, bool F32, typename F, typename G>
@@ -68,26 +69,26 @@ __device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1
     };
     load(threadIdx.x);
     for (int v = threadIdx.x; v < nv; v += U * kThreads) {
-        float x[U][W];
+        uint32_t w[U][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t w[4] = {next[u].x, next[u].y, next[u].z, next[u].w};
-#pragma unroll
-            for (int e = 0; e < W; ++e)
-                x[u][e] = F32 ? __uint_as_float(w[e % 4]) : e & 1 ? bf16hi(w[e / 2 % 4]) : bf16lo(w[e / 2 % 4]);
-        }
+        for (int u = 0; u < U; ++u) w[u][0] = next[u].x, w[u][1] = next[u].y, w[u][2] = next[u].z, w[u][3] = next[u].w;
         if (v + (U - 1) * kThreads >= nv)  // (the last batch of some threads: what is not there counts nothing)
 #pragma unroll
             for (int u = 1; u < U; ++u)
                 if (v + u * kThreads >= nv)
 #pragma unroll
-                    for (int e = 0; e < W; ++e) x[u][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) w[u][e] = F32 ? 0xFF800000u : 0xFF80FF80u;
         load(v + U * kThreads);
-        f(x, a + (int64_t)v * W, nv - v);
+        f(w, a + (int64_t)v * W, nv - v);
     }
     const int64_t b = a + (int64_t)nv * W;
     const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
     if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
+}
+// logit e of a vector
+template <bool F32>
+__device__ __forceinline__ float logit(const uint32_t (&w)[4], int e) {
+    return F32 ? __uint_as_float(w[e % 4]) : e & 1 ? bf16hi(w[e / 2 % 4]) : bf16lo(w[e / 2 % 4]);
 }
 
 // Running softmax sums; max_nan keeps a NaN, and the sums of a row with one are NaN.
@@ -95,6 +96,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+// the same of two pairs of bf16
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// the largest logit of a batch (NaN if there is one)
+template <int U, bool F32>
+__device__ __forceinline__ float largest(const uint32_t (&w)[U][4]) {
+    if (F32) {
+        float big = __uint_as_float(w[0][0]);
+#pragma unroll
+        for (int i = 1; i < 4 * U; ++i) big = max_nan(big, __uint_as_float(w[i / 4][i % 4]));
+        return big;
+    }
+    uint32_t big = w[0][0];
+#pragma unroll
+    for (int i = 1; i < 4 * U; ++i) big = max2_nan(big, w[i / 4][i % 4]);
+    return max_nan(bf16lo(big), bf16hi(big));
 }
 struct Sums {
     float m, S, w;
@@ -169,16 +190,11 @@ __device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_
             if (at < kCand) sm.cand[at] = rank_of(x, (uint32_t)j);
         };
         // (what reaches the bound is in a thread whose own largest does)
-        if (own_max >= bound) scan<2>(row, j0, j1, [&](const float (&x)[2][W], int64_t j, int n) {
+        if (own_max >= bound) scan<4>(row, j0, j1, [&](const uint32_t (&w)[4][4], int64_t j, int n) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float big = x[u][0];
-#pragma unroll
-                for (int e = 1; e < W; ++e) big = fmaxf(big, x[u][e]);  // (NaN when all are; else seen below or not larger)
-                bool any = !(big < least) && u * kThreads < n;
-#pragma unroll
-                for (int e = 0; e < W; ++e) any = any || x[u][e] != x[u][e];
-                if (any)
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t one[1][4] = {{w[u][0], w[u][1], w[u][2], w[u][3]}};
+                if (u * kThreads < n && !(largest<1, F32>(one) < least))
 #pragma unroll 1
                     for (int e = 0; e < W; ++e) take(row.at(j + (int64_t)u * kThreads * W + e), j + (int64_t)u * kThreads * W + e);
             }
@@ -264,36 +280,39 @@ __global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_c
         s.m = big;
     };
     constexpr int U = 4;
-    scan<U>(row, j0, j1, [&](float (&x)[U][W], int64_t, int) {
-        float big = x[0][0];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = u ? 0 : 1; e < W; ++e) big = max_nan(x[u][e], big);
+    scan<U>(row, j0, j1, [&](uint32_t (&w)[U][4], int64_t, int) {
+        float big = largest<U, F32>(w);
         own = max_nan(big, own);
-        if (!plain) {
+        if (!plain) big = __fmul_rn(big, p.scale);
+        if (!(big <= s.m)) rise(big);  // (a NaN comes here too)
+        if (s.m == -INFINITY) return;
+        auto add = [&](auto is_easy) {
+            constexpr bool EASY = decltype(is_easy)::value;
+            float2 S2[2] = {make_float2(s.S, 0.f), make_float2(0.f, 0.f)}, w2[2] = {make_float2(s.w, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < W; ++e) x[u][e] = __fmul_rn(x[u][e], p.scale);
-            big = __fmul_rn(big, p.scale);
+                for (int e = 0; e < W; e += 2) {
+                    float2 x = make_float2(logit<F32>(w[u], e), logit<F32>(w[u], e + 1));
+                    if (!EASY) x = __fmul2_rn(x, make_float2(p.scale, p.scale));
+                    const float2 d = __fadd2_rn(x, make_float2(-s.m, -s.m));
+                    const float2 q = __fmul2_rn(d, make_float2(kL2e, kL2e));
+                    const float2 y = make_float2(lp_ex2(q.x), lp_ex2(q.y));
+                    S2[u & 1] = __fadd2_rn(S2[u & 1], y);
+                    // (0 x -inf is none: where y is 0, any finite number does)
+                    w2[u & 1] = __ffma2_rn(y, EASY ? d : make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), w2[u & 1]);
+                }
+            s.S = (S2[0].x + S2[0].y) + (S2[1].x + S2[1].y);
+            s.w = (w2[0].x + w2[0].y) + (w2[1].x + w2[1].y);
+        };
+        // bf16 as they are, m of an ordinary size: -inf made the lowest number in pairs, its difference is finite
+        if (!F32 && plain && fabsf(s.m) < 1e36f) {
+#pragma unroll
+            for (int i = 0; i < 4 * U; ++i) w[i / 4][i % 4] = max2_nan(w[i / 4][i % 4], 0xFF7FFF7Fu);
+            add(std::true_type{});
+        } else {
+            add(std::false_type{});
         }
-        if (!(big <= s.m)) rise(big);  // (a NaN comes here too)
-        if (s.m == -INFINITY) return;
-        float2 S2[2] = {make_float2(s.S, 0.f), make_float2(0.f, 0.f)}, w2[2] = {make_float2(s.w, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < W; e += 2) {
-                const float2 d = __fadd2_rn(make_float2(x[u][e], x[u][e + 1]), make_float2(-s.m, -s.m));
-                const float2 q = __fmul2_rn(d, make_float2(kL2e, kL2e));
-                const float2 y = make_float2(lp_ex2(q.x), lp_ex2(q.y));
-                S2[u & 1] = __fadd2_rn(S2[u & 1], y);
-                // (0 x -inf is none: where y is 0, any finite number does)
-                w2[u & 1] = __ffma2_rn(y, make_float2(fmaxf(d.x, -1e30f), fmaxf(d.y, -1e30f)), w2[u & 1]);
-            }
-        s.S = (S2[0].x + S2[0].y) + (S2[1].x + S2[1].y);
-        s.w = (w2[0].x + w2[0].y) + (w2[1].x + w2[1].y);
     }, [&](float x, int64_t) {
         own = max_nan(x, own);
         x = __fmul_rn(x, p.scale);
