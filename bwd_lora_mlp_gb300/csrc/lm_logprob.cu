@@ -14,7 +14,7 @@
 
 namespace lm {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
 constexpr int kCand = 1024;  // alternatives above the bound that fit
 constexpr float kL2e = 1.4426950408889634f;
@@ -259,7 +259,7 @@ __device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 2) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
     __shared__ LpShared sm;
     griddep_launch_dependents();
     griddep_wait();
@@ -370,7 +370,7 @@ static cudaError_t fwd_launch(const LogprobParams& p, cudaStream_t st) {
     // A CTA per row fills the device from about two rows an SM on; with fewer, a row is shared, as long as
     // a CTA's segment keeps every thread a few vectors.  (4 rows of 131072 fp32: 8 CTAs a row.)
     int c = 1;
-    while (c < kMaxCluster && p.T * c * 2 <= 304 && p.V / (c * 2) >= kThreads * 8) c *= 2;
+    while (c < kMaxCluster && p.T * c * 2 <= 152 * 1024 / kThreads && p.V / (c * 2) >= kThreads * 8) c *= 2;
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeClusterDimension;
     a.val.clusterDim = {(unsigned)c, 1, 1};
