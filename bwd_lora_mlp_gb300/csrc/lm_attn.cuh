@@ -64,6 +64,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                  : "memory");
 }
+// Four floats to another CTA's shared memory (an address of map_to_rank).
+__device__ __forceinline__ void st_peer4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is 128 rows (lanes) x 16 K values packed two to a column.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
@@ -182,9 +186,11 @@ constexpr uint32_t kBoxBytes = kTile * 128;
 __device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Low descriptor word of a tile: start address and leading offset in units of 16 bytes; the high word
-// holds the stride of 8-row groups (1024 bytes), the version and the 128-byte swizzle.
-__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return (addr >> 4) | (1u << 16); }                  // K-major
-__device__ __forceinline__ uint32_t desc_cols(uint32_t addr) { return (addr >> 4) | ((kBoxBytes >> 4) << 16); }    // MN-major
+// holds the stride of 8-row groups (1024 bytes), the version and the 128-byte swizzle.  (In a cluster an
+// address says which CTA's it is above the bits of its place.)
+__device__ __forceinline__ uint32_t desc_at(uint32_t addr) { return (addr >> 4) & 0x3FFFu; }
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return desc_at(addr) | (1u << 16); }                // K-major
+__device__ __forceinline__ uint32_t desc_cols(uint32_t addr) { return desc_at(addr) | ((kBoxBytes >> 4) << 16); }  // MN-major
 __device__ __forceinline__ uint64_t desc(uint32_t lo) {
     constexpr uint64_t hi = (uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32;
     return hi | lo;

@@ -121,11 +121,16 @@ struct DkvCfg {
     static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
     static constexpr uint32_t kRowBytes = kTile * 4;  // nlse, and -delta, of a query tile
     static constexpr int kSmem = 2048 + (2 + 2 * kQStages) * kTileBytes + kQStages * 2 * kRowBytes;
+    // CTAs that may share a key tile: the others' sums have to fit where the query and dO tiles were
+    static constexpr int kMaxSplit = DP == 128 ? 4 : 2;
+    static_assert((kMaxSplit - 1) * (2 * (DP / 64) / kMaxSplit) * kTile * 64 * 4 <= 2 * kQStages * kTileBytes, "");
 };
 
-template <int DP, int MODE>
+// SHARED: a cluster of `ctas` CTAs shares the key tile.
+template <int DP, int MODE, bool SHARED>
 __global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
+    attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps, int ctas) {
+    const int split = SHARED ? ctas : 1;
     using C = DkvCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -150,8 +155,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     float* srow = reinterpret_cast<float*>(so + kQStages * C::kTileBytes);  // [stage][nlse, -delta][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = (int)blockIdx.x % p.hk, k0 = (int)blockIdx.x / p.hk * kTile;  // (causal: the first keys are seen by most)
-    const int n = p.hq / p.hk;
+    // (under a causal mask the first keys, seen by most, come first)
+    const int item = (int)blockIdx.x / split, rank = (int)blockIdx.x % split;
+    const int g = item % p.hk, n = p.hq / p.hk;
 
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
@@ -186,9 +192,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t ts = tmem, tdp = tmem + kTile, tdv = tmem + 2 * kTile, tdk = tdv + DP;
+    const int k0 = item / p.hk * kTile;
     const TokRange rf = tok_range(p, k0), rl = tok_range(p, min(k0 + kTile, p.T) - 1);
     const int qt0 = uni(rf.qlo / kTile), nt = uni(rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0);
-    const int N = nt * n;  // (head of the group, query tile), heads outermost
+    // (head of the group, query tile) pairs, heads outermost: this CTA's are [first, first + N)
+    auto begin = [&](int r) { return (int)((int64_t)nt * n * r / split); };
+    const int first = SHARED ? begin(rank) : 0, N = SHARED ? begin(rank + 1) - first : nt * n;
+    const int hh0 = SHARED && nt ? first / nt : 0, qi0 = SHARED && nt ? first % nt : 0;
 
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
@@ -201,8 +211,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tma_load_3d(smem_u32(sv + b * kBoxBytes), &maps.v, smem_u32(kvfull), b * 64, g, k0);
                 }
                 uint32_t it = 0, no = 0;  // query and dO tiles asked for
-                for (int hh = 0; ok && hh < n; ++hh)
-                    for (int qt = qt0; qt < qt0 + nt; ++qt) {
+                for (int hh = hh0; ok && (SHARED ? no < (uint32_t)N : hh < n); ++hh)
+                    for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || no < (uint32_t)N); ++qt) {
                         const int h = g * n + hh;
                         const uint32_t s = no % kQStages, ph = (no / kQStages) & 1u;
                         const uint32_t bq = smem_u32(&qfull[s]), bo = smem_u32(&ofull[s]);
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             auto scores = [&](int it) {  // S^T(it) = K Q^T
                 const uint32_t s = (uint32_t)it % kQStages;
                 if (!mbar_wait(smem_u32(&qfull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1);
+                clear_padding(sq + s * C::kTileBytes, DP / 64, (qt0 + (first + it) % nt) * kTile, in0, in1);
                 tc_fence_after();
                 mma_rows<DP>(ts, desc_rows(smem_u32(sk)), desc_rows(smem_u32(sq + s * C::kTileBytes)), ksteps, ids);
                 umma_commit(smem_u32(sfull));
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             auto dots = [&](int it) {  // dP^T(it) = V dO^T
                 const uint32_t s = (uint32_t)it % kQStages;
                 if (!mbar_wait(smem_u32(&ofull[s]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns)) return false;
-                clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + it % nt) * kTile, in0, in1);
+                clear_padding(so + s * C::kTileBytes, DP / 64, (qt0 + (first + it) % nt) * kTile, in0, in1);
                 tc_fence_after();
                 mma_rows<DP>(tdp, desc_rows(smem_u32(sv)), desc_rows(smem_u32(so + s * C::kTileBytes)), ksteps, ids);
                 umma_commit(smem_u32(dpfull));
@@ -295,6 +305,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             umma_commit(smem_u32(drain));
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+        }
+        __syncwarp();
+        if (SHARED) {  // (the arithmetic warps' two meetings of the cluster)
+            cluster_sync();
+            cluster_sync();
         }
     } else {  // ---------------- arithmetic: half of the warps form P^T, the others dz^T; one key row, 64 queries a thread
         regs_up<kBwdMathRegs>();
@@ -403,9 +418,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return true;
         };
         int it = 0;
-        for (int hh = 0; ok && hh < n; ++hh) {
+        for (int hh = hh0; ok && (SHARED ? it < N : hh < n); ++hh) {
             if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
-            for (int qt = qt0; qt < qt0 + nt; ++qt, ++it) {
+            for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || it < N); ++qt, ++it) {
                 const int q0 = qt * kTile + half * 64;
                 const float* row = srow + (it % kQStages) * 2 * kTile + half * 64;
                 // every query of the tile sees every key of this one, or some pair is hidden
@@ -437,13 +452,69 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             attn_error(p, 6, 3);
             *s_abort = 1;
         }
+        // (b's box, of 64 dims of dV or dK, is the (b % split)-th CTA's to write)
         constexpr int kBoxes = DP / 64;
-        if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes) {  // (staged where the query tiles were)
-            const int r128 = (warp & 3) * 32 + lane, b = part % kBoxes;
-            const bool key = part >= kBoxes;
-            uint8_t* box = sq + part * kBoxBytes;
-            stage_row(box, r128, (key ? tdk : tdv) + lanes + b * 64, key ? p.scale : 1.f, N > 0);
-            store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
+        const int r128 = (warp & 3) * 32 + lane, b = part % kBoxes, owner = part % split;
+        const bool key = part >= kBoxes;
+        const uint32_t acc = (key ? tdk : tdv) + lanes + b * 64;
+        uint8_t* box = sk + part * kBoxBytes;  // (staged where the keys and values were)
+        if (!SHARED) {
+            if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes) {
+                stage_row(box, r128, acc, key ? p.scale : 1.f, N > 0);
+                store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
+            }
+        } else {
+            // Every CTA's products are done before sums arrive where its query tiles were, and all sums have
+            // arrived before any CTA reads them or leaves.  A place holds 64 values of 128 rows, by peer and box.
+            auto place = [&](int from, int to) {
+                return sq + ((from - (from > to ? 1 : 0)) * (2 * kBoxes / split) + part / split) * (kTile * 64 * 4);
+            };
+            __syncwarp();
+            cluster_sync();
+            if (part < 2 * kBoxes && owner != rank && N > 0) {
+                const uint32_t to = map_to_rank(smem_u32(place(rank, owner)), owner) + r128 * 16;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x[32];
+                    tmem_ld_f32<0>(acc + c * 32, x);
+                    tmem_ld_wait_f32<0>(x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) st_peer4(to + (c * 8 + e / 4) * (kTile * 16), x[e], x[e + 1], x[e + 2], x[e + 3]);
+                }
+            }
+            __syncwarp();
+            cluster_sync();
+            if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes && owner == rank) {
+                const float f = key ? p.scale : 1.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {  // 16 dims: this CTA's and the others', in their order
+                    float s[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) s[e] = 0.f;
+                    for (int from = 0; from < split; ++from) {
+                        if (begin(from + 1) == begin(from)) continue;
+                        if (from == rank) {
+                            uint32_t o[16];
+                            tmem_ld_x16(acc + c * 16, o);
+                            tmem_ld_wait16(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) s[e] += __uint_as_float(o[e]);
+                        } else {
+                            const float4* q = reinterpret_cast<const float4*>(place(from, rank)) + r128;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 v = q[(c * 4 + e) * kTile];
+                                s[4 * e] += v.x, s[4 * e + 1] += v.y, s[4 * e + 2] += v.z, s[4 * e + 3] += v.w;
+                            }
+                        }
+                    }
+                    uint32_t v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = pack_bf16x2(s[2 * e] * f, s[2 * e + 1] * f);
+                    stage_pairs(box, r128, c, v);
+                }
+                store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
+            }
         }
         tc_fence_before();
     }
@@ -781,13 +852,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ------------------------------------------------------------------ launches
-template <int DP, int MODE>
-cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_dkv_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int DP, int MODE, bool SHARED>
+cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int items, int split, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_dkv_kernel<DP, MODE, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                DkvCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.T + kTile - 1) / kTile) * (unsigned)p.hk;
-    return launch_pdl(attn_dkv_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {(unsigned)split, 1, 1};
+    return launch_pdl(attn_dkv_kernel<DP, MODE, SHARED>, dim3((unsigned)(items * split)), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st,
+                      &cluster, SHARED ? 1 : 0, p, maps, split);
+}
+template <int DP, int MODE>
+cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
+    // A key tile is shared where there are fewer of them than SMs and the (head, query tile) pairs that see one
+    // are many: down to 4 a CTA while the SMs take all CTAs at once, from 32 a CTA up to two CTAs an SM.  A join
+    // costs about six pairs.  (32 query heads on 8, 128 dims: 512 tokens 33 -> 25 us with four CTAs a tile, 1024
+    // 57 -> 40 with two and 45 with four, 2048 103 -> 72 with two; 8 heads on 1, 8192 tokens 731 -> 217 with
+    // four.  16 heads on 16, 1024 tokens: 21 with one, 29 with two.)
+    const int tiles = (p.T + kTile - 1) / kTile, items = tiles * p.hk;
+    const int reach = p.window > 0 && p.window / kTile + 2 < tiles ? p.window / kTile + 2 : tiles;
+    int split = 1;
+    while (split < DkvCfg<DP>::kMaxSplit) {
+        const int pairs = p.hq / p.hk * reach / split, after = items * split * 2;
+        if (!(after <= sms && pairs >= 8) && !(after <= 2 * sms && pairs >= 32)) break;
+        split *= 2;
+    }
+    return split > 1 ? launch_dkv<DP, MODE, true>(p, maps, items, split, st) : launch_dkv<DP, MODE, false>(p, maps, items, 1, st);
 }
 template <int DP, int MODE>
 cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
@@ -803,7 +894,7 @@ template <int DP, int MODE>
 cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
     {
         LaunchTag tag("attn.dkv", st);
-        const cudaError_t e = launch_dkv<DP, MODE>(p, maps, st);
+        const cudaError_t e = launch_dkv<DP, MODE>(p, maps, sms, st);
         if (e != cudaSuccess) return e;
     }
     LaunchTag tag("attn.dq", st);

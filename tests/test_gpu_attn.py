@@ -232,3 +232,15 @@ def test_offsets_past_32_bits():
             check("dQ", host64(got["dQ"][sl, h])[inner], ref["dQ"][inner, 0], REL)
     del q, dO, got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,hq,hk,d", [(2600, 8, 8, 64), (1300, 16, 8, 128), (520, 8, 2, 128), (260, 5, 1, 128), (700, 6, 2, 40)])
+@pytest.mark.parametrize("docs", [False, True])
+def test_key_tiles_of_one_two_and_four_ctas(T, hq, hk, d, docs):
+    """dK and dV where there are more key tiles than SMs, fewer, and far fewer (their sums then meet from two
+    or four CTAs), with documents whose key tiles are taken out of order."""
+    mask = dict(cu_docs=[0, 3, 3, T // 7, T // 7 + 1, T // 2, T - 9]) if docs else {}
+    args, a, ref = _case(T, hq, hk, d, seed=11, **mask)
+    got, again = _run(*args, a), _run(*args, a)
+    _compare(got, ref)
+    assert all(torch.equal(got[n], again[n]) for n in got)
