@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t ts = tmem, tdp = tmem + kTile, tdv = tmem + 2 * kTile, tdk = tdv + DP;
-    const int k0 = item / p.hk * kTile;
+    const int k0 = uni(item / p.hk * kTile);
     const TokRange rf = tok_range(p, k0), rl = tok_range(p, min(k0 + kTile, p.T) - 1);
     const int qt0 = uni(rf.qlo / kTile), nt = uni(rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0);
     // (head of the group, query tile) pairs, heads outermost: this CTA's are [first, first + N)
