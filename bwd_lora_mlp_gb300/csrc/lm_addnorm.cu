@@ -4,13 +4,15 @@
 //             dy = r_y (dn w_post - y r_y^2 mean(dn w_post y)),
 //             dw_in = sum dx h' r_h,  dw_post = sum dn y r_y,  dgate = sum alpha g n
 // Bound by memory as long as a row's arithmetic takes less than its bytes: each tensor of the row is
-// read and written once.  A thread holds 8 neighbouring columns, the same ones for every row its CTA
-// walks, so the row stays in registers between its two means, the weights are read and made fp32 once,
-// and the backward's three sums over tokens are registers too.  Each thread copies its own 16-byte pieces
-// of the next rows to shared memory asynchronously, so reads are in flight while a row is normalised.
-// Small rows share a CTA; its row groups join their sums at its end and a second kernel joins the CTAs',
-// both in order.  (The weights and sums in shared memory instead: 1000 bytes of it moved per thread and
-// row, its pipe as busy as the memory, 108 us against KBWD for 8192 x 4096 backward.)
+// read and written once.  A thread holds 8 or 16 columns, the same ones for every row its CTA walks, so the
+// row stays in registers between its two means, and the backward's weights and its three sums over tokens
+// are registers too (up to 4096 columns).  Each thread copies its own 16-byte pieces of the next rows to
+// shared memory asynchronously, so reads are in flight while a row is normalised.  Small rows share a
+// CTA; its row groups join their sums at its end and a second kernel joins the CTAs', both in order.
+// Measured: 8192 x 4096 with all of it, forward 51 us, 5.3 TB/s (0.78 of the copy rate), backward 88 us,
+// 4.6 TB/s (0.67); 3001 x 8192 with an fp32 stream 63 and 104 us (4.7 and 4.2 TB/s).  What is left is the
+// two means a row, a barrier each.  (Weights and sums in shared memory: 1000 bytes of it moved per thread
+// and row, its pipe as busy as the memory, 108 us for the 8192 x 4096 backward.)
 #include <algorithm>
 
 #include "lm_layer.h"
@@ -33,9 +35,12 @@ static RowPlan plan_rows(int d, int one) {
     P.threads = P.rows * P.warps * 32;
     return P;
 }
+// Two vectors a thread halve what the means cost per column.  The forward has registers for it: 8192 x 4096
+// 61 us with one, 51 with two; at 2048 columns one vector is already a CTA of two rows.  The backward's
+// weights and sums do not fit then: 88 us with one, 139 with two; it takes two only where one does not fit.
 constexpr int kFwdOne = 2048, kBwdOne = 4096;
 // Rows on their way: as many as the shared memory holds beside a first-level cache for the weights that
-// are not in registers.
+// are not in registers.  (8192 x 4096 forward: 51 us with two, 56 with three and less cache.)
 constexpr int fwd_stages(int nv, int most) { return nv == 1 ? 3 : most <= 512 ? 2 : 1; }
 constexpr int bwd_stages(int nv, bool h32, int most) { return nv == 1 ? 3 : most <= 512 && !h32 ? 2 : 1; }
 

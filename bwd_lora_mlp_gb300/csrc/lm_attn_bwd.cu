@@ -8,9 +8,15 @@
 // summed by atomics would take five; in exchange there is no fp32 dQ in memory, nothing to clear
 // and no order of arrival.  Scores are formed with the owned rows as tensor-memory lanes (S^T in
 // attn_dkv), so P and dz go back to tensor memory as the left operand of the next product without
-// crossing threads.  The arithmetic is on the way from one product to the next (S to P to the next S in
-// attn_dkv), so its latency counts, not only its rate: sixteen warps with 32 columns a thread against
-// eight with 64 took 8192 causal tokens from DKV0 to DKV1 us and DQ0 to DQ1.
+// crossing threads.
+// attn_dkv is bound by the way from one product to the next: S to P to the next S, whose place P takes,
+// and the same for dP and dz.  So half of the sixteen arithmetic warps form P and the others dz from it
+// (rounded as the product takes it, which is one rounding more in dz), a tile apart; all sixteen doing
+// one after the other took 788 us for 8192 causal tokens with 32 query heads on 8 of 128 dims, this way
+// 699: 1.57 PFLOP/s, 0.82 of the burst rate.  attn_dq has room for a second score tile and runs its three
+// products at 0.94 of it, 460 us.  (One CTA an item took 479 there, dK and dV's K and V order asked for as
+// it is used 623 before that; P and dz handed over in two halves cost 110 us in attn_dkv: a store to tensor
+// memory and its wait take 300 cycles while the tensor cores multiply from shared memory.)
 #include "lm_attn.cuh"
 
 namespace lm {
@@ -61,7 +67,8 @@ struct BwdMaps {
 // ------------------------------------------------------------------ delta, and lse in the exponent's units
 // A CTA takes 16 tokens and kDeltaHeads heads: 16 threads a token, 8 dims each, all heads' loads in flight at
 // once.  The results lie by head, so they are exchanged and leave 16 tokens at a time.  Tokens that see
-// nothing get zeros, whatever dO holds.
+// nothing get zeros, whatever dO holds.  (8192 tokens, 32 heads of 128: 33 us, 5.0 TB/s; a token and head at a
+// time, the results scattered, 37.)
 constexpr int kDeltaHeads = 4;
 __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* ndelta, float* nlse) {
     __shared__ float s_delta[kDeltaHeads][16], s_nlse[kDeltaHeads][16];
