@@ -10,13 +10,15 @@
 // attn_dkv), so P and dz go back to tensor memory as the left operand of the next product without
 // crossing threads.
 // attn_dkv is bound by the way from one product to the next: S to P to the next S, whose place P takes,
-// and the same for dP and dz.  So half of the sixteen arithmetic warps form P and the others dz from it
-// (rounded as the product takes it, which is one rounding more in dz), a tile apart; all sixteen doing
-// one after the other took 788 us for 8192 causal tokens with 32 query heads on 8 of 128 dims, this way
-// 699: 1.57 PFLOP/s, 0.82 of the burst rate.  attn_dq has room for a second score tile and runs its three
-// products at 0.94 of it, 460 us.  (One CTA an item took 479 there, dK and dV's K and V order asked for as
-// it is used 623 before that; P and dz handed over in two halves cost 110 us in attn_dkv: a store to tensor
-// memory and its wait take 300 cycles while the tensor cores multiply from shared memory.)
+// and the same for dP and dz; sixteen warps share each step, 32 columns a thread.  8192 causal tokens, 32
+// query heads on 8 of 128 dims: 788 us, 1.40 PFLOP/s, 0.73 of the burst rate.  attn_dq has room for a second
+// score tile and runs its three products at 0.94 of it, 458 us.
+// Tried in attn_dkv: eight warps that form P and eight that form dz from its bf16 rounding, a tile apart,
+// 699 us there, but dK's error 2.9e-3 against 2.4e-3, and 133 against 119 for capped prefixes, 62 against 58
+// for a biased window; the same with P in f16 for dz, 748 and 208 against 192 for packed documents; two groups
+// of eight that take every other tile, 771 and 223; P and dz handed over in two halves, 897 (a store to tensor
+// memory and its wait take 300 cycles while the tensor cores multiply from shared memory).  In attn_dq: one
+// CTA an item instead of CTAs that stay, 479; K and V asked for in another order than they are used, 623.
 #include "lm_attn.cuh"
 
 namespace lm {
@@ -148,8 +150,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint64_t* kvfull = oempty + kQStages;
     uint64_t* sfull = kvfull + 1;   // S^T ready
     uint64_t* pfull = sfull + 1;    // P^T written
-    uint64_t* pread = pfull + 1;    // and read by the warps that form dz^T
-    uint64_t* dpfull = pread + 1;   // dP^T ready
+    uint64_t* dpfull = pfull + 1;   // dP^T ready
     uint64_t* dsfull = dpfull + 1;  // dz^T written
     uint64_t* drain = dsfull + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -176,10 +177,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         mbar_init(smem_u32(kvfull), 1);
         mbar_init(smem_u32(sfull), 1);
-        mbar_init(smem_u32(pfull), kBwdMath / 2);
-        mbar_init(smem_u32(pread), kBwdMath / 2);
+        mbar_init(smem_u32(pfull), kBwdMath);
         mbar_init(smem_u32(dpfull), 1);
-        mbar_init(smem_u32(dsfull), kBwdMath / 2);
+        mbar_init(smem_u32(dsfull), kBwdMath);
         mbar_init(smem_u32(drain), 1);
         *s_abort = s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0;
         fence_mbar_init();
@@ -288,8 +288,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_fence_after();
                 mma_weights(tdv, ts, desc_cols(smem_u32(so + s * C::kTileBytes)), idd, it == 0);
                 umma_commit(smem_u32(&oempty[s]));
-                // (P(it) has been read by then: by the product, they run in order, and by the warps)
-                if (it + 1 < N && !(mbar_wait(smem_u32(pread), (uint32_t)it & 1u, s_abort, p.wait_ns) && scores(it + 1))) {
+                if (it + 1 < N && !scores(it + 1)) {  // (P(it) has been read by then: products run in order)
                     ok = false;
                     break;
                 }
@@ -318,106 +317,77 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             cluster_sync();
             cluster_sync();
         }
-    } else {  // ---------------- arithmetic: half of the warps form P^T, the others dz^T; one key row, 64 queries a thread
+    } else {  // ---------------- arithmetic: one key row, 32 query columns per thread
         regs_up<kBwdMathRegs>();
-        const int part = warp >> 2, half = part & 1;
+        const int part = warp >> 2;
         const int k = k0 + (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tsw = ts + lanes + half * 64, tdpw = tdp + lanes + half * 64;
-        constexpr int kBent = MODE == ATTN_CAP ? 16 : 0;  // capped scores: P du/dz lies beside P
+        const uint32_t tsw = ts + lanes + part * 32, tdpw = tdp + lanes + part * 32;
         TokRange r{0, 0, 0, 0};
         if (k < p.T) r = tok_range(p, k);
         ScoreMath S = score_math<MODE>(p);
         bool ok = true;
-        // the weights of one query tile, its scores ready; tiles with hidden pairs have code of their own
-        auto weights = [&](int it, const float* row, float dist, const uint32_t (&bits)[2], auto hides) {
+        // one query tile, its scores ready; tiles with hidden pairs have code of their own
+        auto tile = [&](int it, const float* row, float dist, uint32_t bits, auto hides) {
             constexpr bool HIDDEN = decltype(hides)::value;
-            float x[64];
+            float x[32];
+            uint32_t pk[16];
             tmem_ld_f32<0>(tsw, x);
-            tmem_ld_f32<32>(tsw + 32, x);
+            const bool some = !HIDDEN || __any_sync(0xffffffffu, bits != 0u);
             tmem_ld_wait_f32<0>(x);
-            tmem_ld_wait_f32<32>(x);
+            if (some) {  // (a chunk that none of the warp's keys is seen from has no exponentials)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16], pb[16];
-                if (!HIDDEN || __any_sync(0xffffffffu, bits[c] != 0u)) {  // (else: no exponentials)
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 nl = *reinterpret_cast<const float4*>(row + e);
+                    const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 nl = *reinterpret_cast<const float4*>(row + c * 32 + e);
-                        const float nls[4] = {nl.x, nl.y, nl.z, nl.w};
-#pragma unroll
-                        for (int f = 0; f < 4; f += 2) {
-                            float2 bend = two(1.f);
-                            const float2 y = exponents<MODE, 1>(S, make_float2(x[c * 32 + e + f], x[c * 32 + e + f + 1]),
-                                                                dist + (float)(c * 32 + e + f), make_float2(nls[f], nls[f + 1]), bend);
-                            float2 P = make_float2(ex2(y.x), ex2(y.y));
-                            if (HIDDEN) {
-                                if (!(bits[c] >> (e + f) & 1u)) P.x = 0.f;
-                                if (!(bits[c] >> (e + f + 1) & 1u)) P.y = 0.f;
-                            }
-                            pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
-                            if (MODE == ATTN_CAP) {
-                                P = __fmul2_rn(P, bend);
-                                pb[(e + f) / 2] = pack_bf16x2(P.x, P.y);
-                            }
+                    for (int f = 0; f < 4; f += 2) {
+                        float2 bend = two(1.f);
+                        const float2 y = exponents<MODE, 1>(S, make_float2(x[e + f], x[e + f + 1]), dist + (float)(e + f),
+                                                            make_float2(nls[f], nls[f + 1]), bend);
+                        float2 P = make_float2(ex2(y.x), ex2(y.y));
+                        if (HIDDEN) {
+                            if (!(bits >> (e + f) & 1u)) P.x = 0.f;
+                            if (!(bits >> (e + f + 1) & 1u)) P.y = 0.f;
                         }
+                        pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
+                        if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                        x[e + f] = P.x;
+                        x[e + f + 1] = P.y;
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = pb[e] = 0u;
                 }
-                tmem_st_x16(tsw + c * 32, pk);
-                if (MODE == ATTN_CAP) tmem_st_x16(tsw + c * 32 + kBent, pb);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = 0u;
             }
+            tmem_st_x16(tsw, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(pfull));
-        };
-        // its score gradients from the rounded weights
-        auto gradients = [&](int it, const float* row, const uint32_t (&bits)[2], auto hides) {
-            constexpr bool HIDDEN = decltype(hides)::value;
-            if (!mbar_wait_warp(smem_u32(pfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) return false;
-            tc_fence_after();
-            uint32_t P0[16], P1[16];
-            tmem_ld_x16(tsw + kBent, P0);
-            tmem_ld_x16(tsw + 32 + kBent, P1);
-            tmem_ld_wait16(P0);
-            tmem_ld_wait16(P1);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(pread));
             if (!mbar_wait_warp(smem_u32(dpfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) return false;
             tc_fence_after();
+            if (some) {
+                float y[32];
+                tmem_ld_f32<0>(tdpw, y);
+                tmem_ld_wait_f32<0>(y);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
-                if (!HIDDEN || __any_sync(0xffffffffu, bits[c] != 0u)) {
-                    float y[32];
-                    tmem_ld_f32<0>(tdpw + c * 32, y);
-                    tmem_ld_wait_f32<0>(y);
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 dl = *reinterpret_cast<const float4*>(row + kTile + e);
+                    const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 dl = *reinterpret_cast<const float4*>(row + kTile + c * 32 + e);
-                        const float dls[4] = {dl.x, dl.y, dl.z, dl.w};
-#pragma unroll
-                        for (int f = 0; f < 4; f += 2) {
-                            const uint32_t w = c ? P1[(e + f) / 2] : P0[(e + f) / 2];
-                            float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
-                            d = __fmul2_rn(d, make_float2(bf16lo(w), bf16hi(w)));
-                            if (HIDDEN) {  // (not 0 x what a padding key's dP holds)
-                                if (!(bits[c] >> (e + f) & 1u)) d.x = 0.f;
-                                if (!(bits[c] >> (e + f + 1) & 1u)) d.y = 0.f;
-                            }
-                            pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
+                    for (int f = 0; f < 4; f += 2) {
+                        float2 d = __fadd2_rn(make_float2(y[e + f], y[e + f + 1]), make_float2(dls[f], dls[f + 1]));
+                        d = __fmul2_rn(d, make_float2(x[e + f], x[e + f + 1]));
+                        if (HIDDEN) {  // (not 0 x what a padding key's dP holds)
+                            if (!(bits >> (e + f) & 1u)) d.x = 0.f;
+                            if (!(bits >> (e + f + 1) & 1u)) d.y = 0.f;
                         }
+                        pk[(e + f) / 2] = pack_bf16x2(d.x, d.y);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
                 }
-                tmem_st_x16(tdpw + c * 32, pk);
             }
+            tmem_st_x16(tdpw, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -428,28 +398,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int hh = hh0; ok && (SHARED ? it < N : hh < n); ++hh) {
             if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
             for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || it < N); ++qt, ++it) {
-                const int q0 = qt * kTile + half * 64;
-                const float* row = srow + (it % kQStages) * 2 * kTile + half * 64;
+                const int q0 = qt * kTile + part * 32;
+                const float* row = srow + (it % kQStages) * 2 * kTile + part * 32;
                 // every query of the tile sees every key of this one, or some pair is hidden
                 const bool hidden = qt * kTile < rl.qlo || (qt + 1) * kTile > rf.qhi;
-                uint32_t bits[2] = {~0u, ~0u};
-                if (hidden)
-                    for (int c = 0; c < 2; ++c) bits[c] = bits_between(r.qlo - q0 - 32 * c, r.qhi - q0 - 32 * c);
-                // (a warp whose keys are seen from all of its columns has nothing to mask)
-                const bool clear = __all_sync(0xffffffffu, (bits[0] & bits[1]) == ~0u);
+                const uint32_t bits = hidden ? bits_between(r.qlo - q0, r.qhi - q0) : ~0u;
+                const float dist = (float)(q0 - k);
                 // the query tile's rows (nlse, -delta) come with it; the scores are ready after it is
-                ok = mbar_wait_warp(smem_u32(&qfull[it % kQStages]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns);
-                if (!ok) break;
-                if (part < 2) {
-                    ok = mbar_wait_warp(smem_u32(sfull), (uint32_t)it & 1u, s_abort, p.wait_ns);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (clear) weights(it, row, (float)(q0 - k), bits, std::false_type{});
-                    else weights(it, row, (float)(q0 - k), bits, std::true_type{});
-                } else {
-                    ok = clear ? gradients(it, row, bits, std::false_type{}) : gradients(it, row, bits, std::true_type{});
-                    if (!ok) break;
+                if (!mbar_wait_warp(smem_u32(&qfull[it % kQStages]), ((uint32_t)it / kQStages) & 1u, s_abort, p.wait_ns) ||
+                    !mbar_wait_warp(smem_u32(sfull), (uint32_t)it & 1u, s_abort, p.wait_ns)) {
+                    ok = false;
+                    break;
                 }
+                tc_fence_after();
+                // (a warp whose keys are seen from all of its columns has nothing to mask)
+                ok = __all_sync(0xffffffffu, bits == ~0u) ? tile(it, row, dist, bits, std::false_type{})
+                                                         : tile(it, row, dist, bits, std::true_type{});
+                if (!ok) break;
             }
         }
         // DP / 64 warpgroups write dV, as many dK, a box of 64 dims each
