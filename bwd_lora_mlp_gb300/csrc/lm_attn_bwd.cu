@@ -839,9 +839,9 @@ template <int DP, int MODE>
 cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
     // A key tile is shared where there are fewer of them than SMs and the (head, query tile) pairs that see one
     // are many: down to 4 a CTA while the SMs take all CTAs at once, from 32 a CTA up to two CTAs an SM.  A join
-    // costs about six pairs.  (32 query heads on 8, 128 dims: 512 tokens 33 -> 25 us with four CTAs a tile, 1024
-    // 57 -> 40 with two and 45 with four, 2048 103 -> 72 with two; 8 heads on 1, 8192 tokens 731 -> 217 with
-    // four.  16 heads on 16, 1024 tokens: 21 with one, 29 with two.)
+    // costs about six pairs.  (32 query heads on 8, 128 dims: 512 tokens 35 -> 24 us with four CTAs a tile, 27 with
+    // two; 1024 62 -> 39 with two, 44 with four; 2048 116 -> 68 with two, 104 with four; 8 heads on 1, 8192 tokens
+    // 848 -> 207 with four.  16 heads on 16, 1024 tokens: 20 with one, 29 with two.)
     const int tiles = (p.T + kTile - 1) / kTile, items = tiles * p.hk;
     const int reach = p.window > 0 && p.window / kTile + 2 < tiles ? p.window / kTile + 2 : tiles;
     int split = 1;

@@ -130,8 +130,8 @@ __device__ __forceinline__ Sums join(Sums s) {
     float m = s.m;
 #pragma unroll
     for (int o = N / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float d = s.m - m, f = lp_ex2(d * kL2e);
-    // w moves with the maximum: sum e^{x-m} (x-m); an empty part has d = -inf (or NaN) and counts nothing
+    const float d = fmaxf(s.m - m, -1e30f), f = lp_ex2(d * kL2e);  // (where f is 0, any finite d does)
+    // w moves with the maximum: sum e^{x-m} (x-m); an empty part counts nothing
     const bool any = s.S > 0.f;
     s.w = any ? f * fmaf(s.S, d, s.w) : 0.f;
     s.S = any ? s.S * f : 0.f;
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(
     float own = -INFINITY;  // the thread's largest logit (NaN the largest)
     const bool plain = p.scale == 1.f;
     auto rise = [&](float big) {  // the running maximum follows, and the sums with it
-        const float f = s.m == -INFINITY ? 0.f : lp_ex2((s.m - big) * kL2e);
-        s.w = s.S > 0.f ? f * fmaf(s.S, s.m - big, s.w) : 0.f;
+        const float d = fmaxf(s.m - big, -1e30f), f = s.m == -INFINITY ? 0.f : lp_ex2(d * kL2e);  // (f 0: no 0 x inf)
+        s.w = s.S > 0.f ? f * fmaf(s.S, d, s.w) : 0.f;
         s.S *= f;
         s.m = big;
     };

@@ -125,7 +125,8 @@ LM_API lm_status addnorm_bwd(int64_t T, int64_t d, const void* h, const uint16_t
  * (T x k int32) and top_logp (T x k fp32), the row's k largest logits from the largest down, equal
  * ones by the lower index first, and their log probabilities (k == 0: both NULL).  A NaN logit
  * counts as the largest.  Logits of -inf have p = 0 and count nothing in the entropy; a row of
- * nothing else has lse = logp = top_logp = -inf, entropy 0 and gradient 0.
+ * nothing else has lse = logp = top_logp = -inf, entropy 0 and gradient 0.  logp and p are formed with
+ * lse as fp32 holds it: log p is off by up to 2^-24 |lse|.
  * The backward: dlogits_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + entropy)),
  * in the logits' type (T x V, row stride ld_out >= V), from the forward's lse and entropy; dlogp and
  * dentropy T fp32, each may be NULL (zero; entropy is needed with dentropy).  dlogits may be the

@@ -196,3 +196,35 @@ def test_offsets_past_32_bits():
     check("dlogits", host64(d[rows]), O.logprob_backward(f, tn, host64(gl[rows])), BF16_REL)
     del x, d
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.5])
+def test_masks_of_the_types_lowest_value_and_huge_logits(scale):
+    """bf16 rows whose masked logits are the type's lowest value or -inf, both, nothing else, or lie next to
+    huge ones; the entropy is of what is left."""
+    low, inf = torch.finfo(torch.bfloat16).min, float("inf")
+    x, t, _, _ = _case(7, 3001, torch.bfloat16, 21)
+    x[0, ::2], x[0, 1::2] = -inf, low      # the lowest value is what is left
+    t[0] = 5
+    x[1, ::3] = low
+    t[1] = 1
+    x[2, :], x[2, 2000] = low, 3e38
+    t[2] = 2000
+    x[3, :], x[3, 10:20] = -2e36, 2e36
+    t[3] = 12
+    x[4, :], x[4, 7:9] = -inf, 1e37
+    t[4] = 8
+    x[5, :] = low
+    t[5] = 0
+    x[6, ::2], x[6, 1::4] = -inf, low
+    t[6] = 3
+    fw = M.logprob_fwd(x, t, 1, scale)
+    rf = O.logprob_forward(host64(x), t.cpu().numpy(), 1, scale)
+    for n in ("logp", "entropy", "top_logp"):
+        _near(n, fw[n], rf[n])
+    assert np.array_equal(fw["top_ids"].cpu().numpy(), rf["top_ids"])
+    lse, want = host64(fw["lse"]), rf["lse"]
+    assert np.all(np.abs(lse - want) <= np.maximum(ABS, 2.0 ** -23 * np.abs(want)))  # (one rounding to fp32)
+    d = M.logprob_bwd(x, t, fw, torch.ones(7, device="cuda"), None, scale)["dlogits"]
+    # (rows 0, 3, 4, 5: lse cannot hold the logarithm of how many equal logits there are beside 1e36 of them)
+    assert torch.isfinite(d).all() and torch.all(d[[1, 2, 6]].sum(1).abs() < 0.1)
