@@ -14,8 +14,11 @@ constexpr int kTile = 128;             // queries and keys of a score tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// How scores are formed from q.k (ATTN_PLAIN folds the scale into the exponent's multiply-add).
-enum AttnMode : int { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2 };
+// How scores are formed from q.k: bit 0 slopes, bit 1 the cap.  Without slopes the factor of the scores is
+// part of the exponent's multiply-add.
+enum AttnMode : int { ATTN_PLAIN = 0, ATTN_BIAS = 1, ATTN_CAP = 2, ATTN_CAP_BIAS = 3 };
+constexpr bool biased(int mode) { return mode & 1; }
+constexpr bool capped(int mode) { return mode & 2; }
 
 // ---------------------------------------------------------------- who sees whom
 __host__ __device__ inline TokRange range_in(int t, int s, int e, int pre, int T, int causal, int window) {
@@ -237,8 +240,13 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// tanh x = 1 - 2 / (1 + e^{2x}), given 2 log2(e) x: absolute error a few 2^-24, exact at both ends
-__device__ __forceinline__ float tanh_from_2log2e(float x) { return fmaf(-2.f, rcp(1.f + ex2(x)), 1.f); }
+// Capped scores: tanh x = 1 + 2 n with n = -1 / (1 + e^{2x}), exact at both ends, and 1 - tanh^2 x =
+// -4 (n + n^2).  The kernels work with n: the factors 2 cap and -4 go into multiplications that are there
+// anyway, and the constant cap into lse.  Given 2 log2(e) x; n's absolute error is a few 2^-25.
+__device__ __forceinline__ float2 cap_n(float2 x) {
+    const float2 a = __ffma2_rn(make_float2(ex2(x.x), ex2(x.y)), make_float2(-1.f, -1.f), make_float2(-1.f, -1.f));
+    return make_float2(rcp(a.x), rcp(a.y));
+}
 // Bit e set: column e of a chunk of 32 is in [a, z).
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ uint32_t bits_between(int a, int z) { return bits_below(z) & ~bits_below(a); }

@@ -37,29 +37,35 @@ __device__ __forceinline__ void mma_weights(uint32_t d, uint32_t t, uint32_t b, 
 }
 
 struct ScoreMath {
-    float c, cap, slope;
+    float c, cap2, slope;
 };
 template <int MODE>
 __device__ __forceinline__ ScoreMath score_math(const AttnParams& p) {
-    return ScoreMath{MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, 0.f};
+    return ScoreMath{capped(MODE) ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e, 2.f * p.cap * kLog2e, 0.f};
 }
-// x - lse in units of log 2 for two neighbouring columns; bend = du/dz.  dist: i - j of the first, and
-// the second's is one more (STEP 1: the columns are queries) or one less (-1: keys).
+// x - lse in units of log 2 for two neighbouring columns (nlse holds the constant cap of capped scores);
+// bend = -1/4 du/dz.  dist: i - j of the first, and the second's is one more (STEP 1: the columns are queries)
+// or one less (-1: keys).
 template <int MODE, int STEP>
 __device__ __forceinline__ float2 exponents(const ScoreMath& S, float2 qk, float dist, float2 nlse, float2& bend) {
     float2 y;
-    if (MODE == ATTN_CAP) {
-        const float2 t = make_float2(tanh_from_2log2e(qk.x * S.c), tanh_from_2log2e(qk.y * S.c));
-        bend = __ffma2_rn(make_float2(-t.x, -t.y), t, two(1.f));
-        y = __ffma2_rn(t, two(S.cap), nlse);
+    if (capped(MODE)) {
+        const float2 n = cap_n(__fmul2_rn(qk, two(S.c)));
+        bend = __ffma2_rn(n, n, n);
+        y = __ffma2_rn(n, two(S.cap2), nlse);
     } else {
         y = __ffma2_rn(qk, two(S.c), nlse);
     }
-    if (MODE != ATTN_PLAIN) {
+    if (biased(MODE)) {
         y.x = fmaf(-S.slope, fabsf(dist), y.x);
         y.y = fmaf(-S.slope, fabsf(dist + (float)STEP), y.y);
     }
     return y;
+}
+// what dz K and dz^T Q are multiplied by in the end
+template <int MODE>
+__device__ __forceinline__ float gradient_scale(const AttnParams& p) {
+    return capped(MODE) ? -4.f * p.scale : p.scale;
 }
 
 struct BwdMaps {
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
         for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (sub == 0) {
             s_delta[r][mine] = sees ? -s : 0.f;
-            s_nlse[r][mine] = sees ? -lse[r] * kLog2e : 0.f;
+            s_nlse[r][mine] = sees ? (p.cap - lse[r]) * kLog2e : 0.f;  // (the cap: exponents)
         }
     }
     __syncthreads();
@@ -351,7 +357,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                             if (!(bits >> (e + f + 1) & 1u)) P.y = 0.f;
                         }
                         pk[(e + f) / 2] = pack_bf16x2(P.x, P.y);
-                        if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                        if (capped(MODE)) P = __fmul2_rn(P, bend);
                         x[e + f] = P.x;
                         x[e + f + 1] = P.y;
                     }
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         };
         int it = 0;
         for (int hh = hh0; ok && (SHARED ? it < N : hh < n); ++hh) {
-            if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[g * n + hh] * kLog2e;
+            if (biased(MODE)) S.slope = p.slopes[g * n + hh] * kLog2e;
             for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || it < N); ++qt, ++it) {
                 const int q0 = qt * kTile + part * 32;
                 const float* row = srow + (it % kQStages) * 2 * kTile + part * 32;
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint8_t* box = sk + part * kBoxBytes;  // (staged where the keys and values were)
         if (!SHARED) {
             if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes) {
-                stage_row(box, r128, acc, key ? p.scale : 1.f, N > 0);
+                stage_row(box, r128, acc, key ? gradient_scale<MODE>(p) : 1.f, N > 0);
                 store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
             }
         } else {
@@ -457,7 +463,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             cluster_sync();
             if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes && owner == rank) {
-                const float f = key ? p.scale : 1.f;
+                const float f = key ? gradient_scale<MODE>(p) : 1.f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {  // 16 dims: this CTA's and the others', in their order
                     float s[16];
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             next = dq_item(p, r + 1);
             next_row = row_of(next);
             if (!it.valid) continue;
-            if (MODE != ATTN_PLAIN && p.slopes) S.slope = p.slopes[it.h] * kLog2e;
+            if (biased(MODE)) S.slope = p.slopes[it.h] * kLog2e;
             auto tile = [&](uint32_t tsw, float dist, uint32_t bits, auto hides) {
                 constexpr bool HIDDEN = decltype(hides)::value;
                 float x[32], y[32];
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         float2 bend = two(1.f);
                         const float2 v = exponents<MODE, -1>(S, make_float2(x[e], x[e + 1]), dist - (float)e, two(R.nlse), bend);
                         float2 P = make_float2(ex2(v.x), ex2(v.y));
-                        if (MODE == ATTN_CAP) P = __fmul2_rn(P, bend);
+                        if (capped(MODE)) P = __fmul2_rn(P, bend);
                         x[e] = P.x;
                         x[e + 1] = P.y;
                     }
@@ -806,7 +812,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             // each warpgroup a quarter of the dims, a thread one row of them
             const int i = it.q0 + row;
-            store_dims<DP / 4>(p.out + ((int64_t)i * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d, p.scale, it.N > 0, i < p.T);
+            store_dims<DP / 4>(p.out + ((int64_t)i * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d, gradient_scale<MODE>(p),
+                               it.N > 0, i < p.T);
             tc_fence_before();  // (the next item's products may overwrite dQ once dz says so)
         }
         if (!ok && lane == 0) {
@@ -873,6 +880,16 @@ cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaS
     return launch_dq<DP, MODE>(p, maps, sms, st);
 }
 
+template <int DP>
+cudaError_t launch_mode(int mode, const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
+    switch (mode) {
+        case ATTN_PLAIN: return launch_both<DP, ATTN_PLAIN>(p, maps, sms, st);
+        case ATTN_BIAS: return launch_both<DP, ATTN_BIAS>(p, maps, sms, st);
+        case ATTN_CAP: return launch_both<DP, ATTN_CAP>(p, maps, sms, st);
+        default: return launch_both<DP, ATTN_CAP_BIAS>(p, maps, sms, st);
+    }
+}
+
 lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
     BwdMaps maps;
     const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs}, dO{p.dO.p, p.dO.ts, p.dO.hs};
@@ -883,16 +900,8 @@ lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st) {
     if (s == LM_OK) s = encode_heads(&maps.dK, lm_heads{p.dK, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.dV, lm_heads{p.dV, (int64_t)p.hk * p.d, p.d}, p.T, p.hk, p.d, kTile);
     if (s != LM_OK) return s;
-    const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes ? ATTN_BIAS : ATTN_PLAIN;
-    cudaError_t e;
-    if (p.d <= 64)
-        e = mode == ATTN_CAP    ? launch_both<64, ATTN_CAP>(p, maps, sms, st)
-            : mode == ATTN_BIAS ? launch_both<64, ATTN_BIAS>(p, maps, sms, st)
-                                : launch_both<64, ATTN_PLAIN>(p, maps, sms, st);
-    else
-        e = mode == ATTN_CAP    ? launch_both<128, ATTN_CAP>(p, maps, sms, st)
-            : mode == ATTN_BIAS ? launch_both<128, ATTN_BIAS>(p, maps, sms, st)
-                                : launch_both<128, ATTN_PLAIN>(p, maps, sms, st);
+    const int mode = (p.slopes ? ATTN_BIAS : 0) | (p.cap > 0.f ? ATTN_CAP : 0);
+    const cudaError_t e = p.d <= 64 ? launch_mode<64>(mode, p, maps, sms, st) : launch_mode<128>(mode, p, maps, sms, st);
     return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn backward launch: %s", cudaGetErrorString(e));
 }
 

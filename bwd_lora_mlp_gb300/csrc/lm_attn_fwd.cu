@@ -17,11 +17,11 @@
 // Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
 // memory: S_0, S_1, O_0, O_1 of 128 columns each, all of it.
 // Measured: 8192 causal tokens, 32 heads of 128 dims, 384 us, 1.43 PFLOP/s, 0.75 of the burst rate of
-// the tensor cores; 4096 tokens with capped scores 212 us (three exponential-unit results a score instead
-// of one).  What bounds it is the way scores -> maximum -> weights -> product: with one score tile a query
+// the tensor cores; 4096 tokens with capped scores 185 us (three exponential-unit results a score instead
+// of one; 212 with tanh formed by itself and the slopes' arithmetic in it).  What bounds it is the way scores -> maximum -> weights -> product: with one score tile a query
 // tile the tensor cores wait for it, and a load or store of tensor memory takes 300 cycles while they
 // multiply from shared memory, 90 while the left operand is in tensor memory.  Eight warps with a whole
-// row a thread instead of sixteen: 384 us too, but capped 234, packed documents 182 against 159, prefixes
+// row a thread instead of sixteen: 384 us too, but capped 234 against 212, packed documents 182 against 159, prefixes
 // 97 against 80.  One CTA an item instead of CTAs that stay: capped 240.
 #include "lm_attn.cuh"
 
@@ -281,10 +281,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int row0 = quarter * 32 + sub * 16 + (lane >> 2), c0 = 2 * (lane & 3);  // rows row0, row0 + 8
         const uint32_t half_lanes = (uint32_t)(quarter * 32 + sub * 16) << 16, all_lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + half_lanes + w * kTile, to = tmem + half_lanes + 2 * kTile + w * DP;
-        // scores in units of log 2: x = s c + bias (plain), or cap tanh(s scale / cap) log2 e + bias
-        const float c = MODE == ATTN_CAP ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
-        const float cap = p.cap * kLog2e;
-        const float cx = MODE == ATTN_PLAIN ? c : 1.f;
+        // scores in units of log 2: x cx, x the product or (capped) n; with slopes x is the score itself.  Capped
+        // ones are short of the constant cap, which lse gets back
+        const float c = capped(MODE) ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e;
+        const float cs = capped(MODE) ? 2.f * p.cap * kLog2e : c;
+        const float cx = biased(MODE) ? 1.f : cs;
         uint32_t nt = 0, nq = 0;
         bool ok = true;
         Item next = item_of(p, 0);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     lo[r] = t.lo - c0;  // (in terms of this lane's first column)
                     hi[r] = t.hi - c0;
                 }
-            const float slope = MODE != ATTN_PLAIN && p.slopes ? p.slopes[it.h] * kLog2e : 0.f;
+            const float slope = biased(MODE) && p.slopes ? p.slopes[it.h] * kLog2e : 0.f;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // running maxima, this lane's sums of weights
             // one key tile; tiles with hidden keys have code of their own.  x[4 g + 2 r + e]: row r, key
             // 8 g + c0 + e of the tile
@@ -314,14 +315,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 tmem_ld_frag32<32>(ts + 64, x);
                 tmem_ld_wait_f32<0>(x);
                 tmem_ld_wait_f32<32>(x);
-                if (MODE != ATTN_PLAIN) {
+                if (capped(MODE)) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const float2 n = cap_n(__fmul2_rn(make_float2(x[e], x[e + 1]), two(c)));
+                        x[e] = n.x;
+                        x[e + 1] = n.y;
+                    }
+                }
+                if (biased(MODE)) {
                     const float dist = (float)(i0 - k0 - c0);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        float v = x[e] * c;
-                        if (MODE == ATTN_CAP) v = cap * tanh_from_2log2e(v);
-                        x[e] = fmaf(-slope, fabsf(dist + (float)((e & 2) * 4 - (e >> 2) * 8 - (e & 1))), v);
-                    }
+                    for (int e = 0; e < 64; ++e)
+                        x[e] = fmaf(-slope, fabsf(dist + (float)((e & 2) * 4 - (e >> 2) * 8 - (e & 1))), x[e] * cs);
                 }
                 if (HIDDEN) {
 #pragma unroll
@@ -422,7 +428,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if ((lane & 3) == 0) {
                     s_inv[w * kTile + row0 + 8 * r] = l[r] > 0.f ? 1.f / l[r] : 0.f;
                     if (i0 + 8 * r < p.T)
-                        p.lse[(int64_t)it.h * p.T + i0 + 8 * r] = l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+                        p.lse[(int64_t)it.h * p.T + i0 + 8 * r] =
+                            l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 + (capped(MODE) ? p.cap : 0.f) : -INFINITY;
                 }
             }
             __syncwarp();
@@ -506,6 +513,16 @@ cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, int sms, cudaSt
     return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
 
+template <int DP>
+cudaError_t launch_mode(int mode, const AttnParams& p, const FwdMaps& maps, int sms, cudaStream_t st) {
+    switch (mode) {
+        case ATTN_PLAIN: return launch_fwd<DP, ATTN_PLAIN>(p, maps, sms, st);
+        case ATTN_BIAS: return launch_fwd<DP, ATTN_BIAS>(p, maps, sms, st);
+        case ATTN_CAP: return launch_fwd<DP, ATTN_CAP>(p, maps, sms, st);
+        default: return launch_fwd<DP, ATTN_CAP_BIAS>(p, maps, sms, st);
+    }
+}
+
 lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
     FwdMaps maps;
     const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs};
@@ -513,17 +530,10 @@ lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.v, v, p.T, p.hk, p.d, kTile);
     if (s != LM_OK) return s;
-    // the plain form folds the scale into the exponent and needs it positive (the maximum of s c is c max s)
-    const int mode = p.cap > 0.f ? ATTN_CAP : p.slopes || !(p.scale > 0.f) ? ATTN_BIAS : ATTN_PLAIN;
-    cudaError_t e;
-    if (p.d <= 64)
-        e = mode == ATTN_CAP    ? launch_fwd<64, ATTN_CAP>(p, maps, sms, st)
-            : mode == ATTN_BIAS ? launch_fwd<64, ATTN_BIAS>(p, maps, sms, st)
-                                : launch_fwd<64, ATTN_PLAIN>(p, maps, sms, st);
-    else
-        e = mode == ATTN_CAP    ? launch_fwd<128, ATTN_CAP>(p, maps, sms, st)
-            : mode == ATTN_BIAS ? launch_fwd<128, ATTN_BIAS>(p, maps, sms, st)
-                                : launch_fwd<128, ATTN_PLAIN>(p, maps, sms, st);
+    // without slopes the factor of the scores goes into the exponent and has to be positive (the maximum of s c
+    // is c max s); the cap's is
+    const int mode = (p.slopes || !(p.scale > 0.f || p.cap > 0.f) ? ATTN_BIAS : 0) | (p.cap > 0.f ? ATTN_CAP : 0);
+    const cudaError_t e = p.d <= 64 ? launch_mode<64>(mode, p, maps, sms, st) : launch_mode<128>(mode, p, maps, sms, st);
     return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "attn forward launch: %s", cudaGetErrorString(e));
 }
 
