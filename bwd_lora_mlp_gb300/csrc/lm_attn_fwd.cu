@@ -18,11 +18,12 @@
 // memory: S_0, S_1, O_0, O_1 of 128 columns each, all of it.
 // Measured: 8192 causal tokens, 32 heads of 128 dims, 384 us, 1.43 PFLOP/s, 0.75 of the burst rate of
 // the tensor cores; 4096 tokens with capped scores 185 us (three exponential-unit results a score instead
-// of one; 212 with tanh formed by itself and the slopes' arithmetic in it).  What bounds it is the way scores -> maximum -> weights -> product: with one score tile a query
-// tile the tensor cores wait for it, and a load or store of tensor memory takes 300 cycles while they
-// multiply from shared memory, 90 while the left operand is in tensor memory.  Eight warps with a whole
-// row a thread instead of sixteen: 384 us too, but capped 234 against 212, packed documents 182 against 159, prefixes
-// 97 against 80.  One CTA an item instead of CTAs that stay: capped 240.
+// of one; 212 with tanh formed by itself and the slopes' arithmetic in it).  What bounds it is the way
+// scores -> maximum -> weights -> product: with one score tile a query tile the tensor cores wait for it,
+// and a load or store of tensor memory takes 300 cycles while they multiply from shared memory, 90 while
+// the left operand is in tensor memory.  Eight warps with a whole row a thread instead of sixteen: 384 us
+// too, but capped 234 against 212, packed documents 182 against 159, prefixes 97 against 80.  One CTA an
+// item instead of CTAs that stay: capped 240 against 212.
 #include "lm_attn.cuh"
 
 namespace lm {
@@ -37,7 +38,7 @@ template <int DP>
 struct FwdCfg {
     static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
     static constexpr int kSlots = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 3072 + (2 + kSlots) * kTileBytes;
+    static constexpr int kSmem = 3 * 1024 + (2 + kSlots) * kTileBytes;
 };
 
 struct FwdMaps {
