@@ -78,7 +78,9 @@ lm_status check_attn_shape(int64_t T, int32_t hq, int32_t hk, int32_t d) {
 lm_status check_attn(const lm_attn* a) {
     if (!a) return report_error(LM_ERR_NULL, "a is NULL");
     if (!std::isfinite(a->scale)) return report_error(LM_ERR_SHAPE, "scale is not finite");
-    if (!std::isfinite(a->cap) || a->cap < 0.f) return report_error(LM_ERR_SHAPE, "cap = %g must be 0 or positive", a->cap);
+    // (a capped score's absolute error is up to 2^-21 cap, and scale / cap has to be a number)
+    if (!(a->cap == 0.f || (a->cap >= 0x1p-14f && a->cap <= 0x1p12f)) || !std::isfinite(3.f * a->scale / (a->cap == 0.f ? 1.f : a->cap)))
+        return report_error(LM_ERR_SHAPE, "cap = %g must be 0 or in [2^-14, 2^12], and 3 scale / cap finite", a->cap);
     if (a->window < 0) return report_error(LM_ERR_SHAPE, "window = %d must be 0 or positive", a->window);
     LL_TRY(want(a->slopes, 4, "slopes"));
     if (a->cu_docs) {

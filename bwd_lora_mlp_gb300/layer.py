@@ -10,7 +10,6 @@ are allocated on the stream that its kernels run on.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 from dataclasses import dataclass
@@ -112,7 +111,7 @@ def _shaped(t: Optional[torch.Tensor], shape, dtype, name: str) -> int:
     """Device address of a contiguous tensor of this shape and type (None: a null pointer)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         _refuse(t, shape, dtype, name)
     return t.data_ptr() or L._empty_ptr(t.device)
 
@@ -125,19 +124,23 @@ def _stream() -> int:
     return _raw_stream(_device())
 
 
-def _on_stream(op):
-    """The operator with a ``stream`` argument: that stream is the current one for the whole call, so that
-    what it allocates and zeroes is ordered before its kernels."""
-    @functools.wraps(op)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return op(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            raw = L._stream(stream)
-            stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
-            return op(*args, **kw)
-    return call
+def _on(stream):
+    """The stream made the current one, so that what a call allocates and zeroes is ordered before its kernels."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = L._stream(stream)
+        stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _new(shape, dtype, dev):
+    """A tensor of the call's own and its address (no checks: a small call takes as long as its checks)."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, t.data_ptr() or L._empty_ptr(dev)
+
+
+def _out(t, shape, dtype, dev, name):
+    """The caller's tensor, or a new one, and its address."""
+    return _new(shape, dtype, dev) if t is None else (t, _shaped(t, shape, dtype, name))
 
 
 # ---------------------------------------------------------------------------------------------
@@ -147,7 +150,7 @@ def _on_stream(op):
 @dataclass
 class Attn:
     """What one attention call computes (lm_attn): scores scale * q.k, capped by cap * tanh(. / cap)
-    when cap > 0, less slopes[head] * |i - j| when slopes is given; token i sees the tokens j <= i of
+    when cap > 0 (2^-14 to 2^12), less slopes[head] * |i - j| when slopes is given; token i sees the tokens j <= i of
     its document (all of it when not causal, and always the document's first prefix tokens) nearer
     than window (0: no limit).  cu_docs: int32 document offsets (n + 1; None: one document), prefix:
     int32 (n), slopes: float32 (query heads)."""
@@ -194,37 +197,40 @@ def attn_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
     return _size("attn_workspace_size", T, hq, hk, d)
 
 
-@_on_stream
-def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None) -> dict:
+def attn_fwd(q, k, v, a: Attn, train: bool = True, O=None, lse=None, O_lo=None, ws=None, stream=None) -> dict:
     """q (T, hq, d), k and v (T, hk, d) -> O (T, hq, d), lse (hq, T) and, with ``train``, O_lo (int8: more
     bits of O, for the backward)."""
+    if stream is not None:
+        with _on(stream):
+            return attn_fwd(q, k, v, a, train, O, lse, O_lo, ws)
     (T, hq, d), hk = q.shape, k.shape[1]
     dev = q.device
-    O = torch.empty((T, hq, d), dtype=torch.bfloat16, device=dev) if O is None else O
-    lse = torch.empty((hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-    if train and O_lo is None:
-        O_lo = torch.empty((T, hq, _d16(d)), dtype=torch.int8, device=dev)
+    hs = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v")
+    O, pO = _out(O, (T, hq, d), torch.bfloat16, dev, "O")
+    lse, pl = _out(lse, (hq, T), torch.float32, dev, "lse")
+    plo = 0
+    if train or O_lo is not None:
+        O_lo, plo = _out(O_lo, (T, hq, _d16(d)), torch.int8, dev, "O_lo")
     ws = workspace(attn_workspace_size(T, hq, hk, d), dev) if ws is None else ws
-    _call("attn_fwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
-          a.c_struct(hq), _shaped(O, (T, hq, d), torch.bfloat16, "O"), _shaped(O_lo, (T, hq, _d16(d)), torch.int8, "O_lo"),
-          _shaped(lse, (hq, T), torch.float32, "lse"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    _call("attn_fwd", T, hq, hk, d, *hs, a.c_struct(hq), pO, plo, pl, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
 
 
-@_on_stream
-def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None) -> dict:
+def attn_bwd(q, k, v, dO, fwd: dict, a: Attn, dQ=None, dK=None, dV=None, ws=None, stream=None) -> dict:
     """The gradients of q, k and v from dO (T, hq, d) and the forward's result."""
+    if stream is not None:
+        with _on(stream):
+            return attn_bwd(q, k, v, dO, fwd, a, dQ, dK, dV, ws)
     (T, hq, d), hk = q.shape, k.shape[1]
     dev, bf = q.device, torch.bfloat16
-    dQ = torch.empty((T, hq, d), dtype=bf, device=dev) if dQ is None else dQ
-    dK = torch.empty((T, hk, d), dtype=bf, device=dev) if dK is None else dK
-    dV = torch.empty((T, hk, d), dtype=bf, device=dev) if dV is None else dV
+    hs = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"), _heads(dO, T, hq, d, "dO")
+    dQ, pq = _out(dQ, (T, hq, d), bf, dev, "dQ")
+    dK, pk = _out(dK, (T, hk, d), bf, dev, "dK")
+    dV, pv = _out(dV, (T, hk, d), bf, dev, "dV")
     ws = fwd["ws"] if ws is None else ws
-    _call("attn_bwd", T, hq, hk, d, _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k"), _heads(v, T, hk, d, "v"),
-          _heads(dO, T, hq, d, "dO"), _shaped(fwd["O"], (T, hq, d), bf, "O"),
+    _call("attn_bwd", T, hq, hk, d, *hs, _shaped(fwd["O"], (T, hq, d), bf, "O"),
           _shaped(fwd["O_lo"], (T, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, T), torch.float32, "lse"),
-          a.c_struct(hq), _shaped(dQ, (T, hq, d), bf, "dQ"), _shaped(dK, (T, hk, d), bf, "dK"),
-          _shaped(dV, (T, hk, d), bf, "dV"), L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+          a.c_struct(hq), pq, pk, pv, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"dQ": dQ, "dK": dK, "dV": dV}
 
 
@@ -259,45 +265,53 @@ def addnorm_workspace_size(T: int, d: int) -> int:
     return _size("addnorm_workspace_size", T, d)
 
 
-@_on_stream
-def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None) -> dict:
+def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
     """h (T, d) bf16 or float32, y (T, d) bf16 or None -> h (the sum; h itself without y), x (None
     without w_in), rstd_y, rstd_h."""
+    if stream is not None:
+        with _on(stream):
+            return addnorm_fwd(h, y, n, h_out, x)
     T, d = h.shape
-    dev, f32, bf = h.device, torch.float32, torch.bfloat16
+    dev, ht, f32, bf = h.device, h.dtype, torch.float32, torch.bfloat16
     td = (T, d)
-    if y is not None and h_out is None:
-        h_out = torch.empty(td, dtype=h.dtype, device=dev)
-    if n.w_in is not None and x is None:
-        x = torch.empty(td, dtype=bf, device=dev)
-    rstd_y = torch.empty(T, dtype=f32, device=dev) if n.w_post is not None else None
-    rstd_h = torch.empty(T, dtype=f32, device=dev) if n.w_in is not None else None
-    _call("addnorm_fwd", T, d, _shaped(h, td, h.dtype, "h"), _shaped(y, td, bf, "y"), n.c_struct(d, h.dtype),
-          _shaped(h_out, td, h.dtype, "h_out"), _shaped(x, td, bf, "x"), _shaped(rstd_y, (T,), f32, "rstd_y"),
-          _shaped(rstd_h, (T,), f32, "rstd_h"), _stream())
+    ph, py, c = _shaped(h, td, ht, "h"), _shaped(y, td, bf, "y"), n.c_struct(d, ht)
+    rstd_y = rstd_h = None
+    po = px = pry = prh = 0
+    if y is not None or h_out is not None:
+        h_out, po = _out(h_out, td, ht, dev, "h_out")
+    if n.w_in is not None:
+        rstd_h, prh = _new((T,), f32, dev)
+    if n.w_in is not None or x is not None:
+        x, px = _out(x, td, bf, dev, "x")
+    if n.w_post is not None:
+        rstd_y, pry = _new((T,), f32, dev)
+    _call("addnorm_fwd", T, d, ph, py, c, po, px, pry, prh, _stream())
     return {"h": h if y is None else h_out, "x": x, "rstd_y": rstd_y, "rstd_h": rstd_h}
 
 
-@_on_stream
-def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None) -> dict:
+def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None,
+                stream=None) -> dict:
     """Gradients from those of the sum (dh_out, None: zero) and of x (dx), with the forward's inputs h and
     y: dh, dy, and with ``weights`` the float32 gradients of the vectors that are there."""
+    if stream is not None:
+        with _on(stream):
+            return addnorm_bwd(h, y, dh_out, dx, fwd, n, weights, dh, dy, ws)
     T, d = h.shape
-    dev, f32, bf = h.device, torch.float32, torch.bfloat16
-    dh = torch.empty((T, d), dtype=h.dtype, device=dev) if dh is None else dh
-    dy = torch.empty((T, d), dtype=bf, device=dev) if dy is None and y is not None else dy
+    dev, ht, f32, bf = h.device, h.dtype, torch.float32, torch.bfloat16
+    td = (T, d)
+    ins = (_shaped(h, td, ht, "h"), _shaped(y, td, bf, "y"), _shaped(dh_out, td, ht, "dh_out"), _shaped(dx, td, bf, "dx"),
+           _shaped(fwd["rstd_y"], (T,), f32, "rstd_y"), _shaped(fwd["rstd_h"], (T,), f32, "rstd_h"), n.c_struct(d, ht))
+    dh, ph = _out(dh, td, ht, dev, "dh")
+    py = 0
+    if y is not None or dy is not None:
+        dy, py = _out(dy, td, bf, dev, "dy")
 
     def grad(w):
-        return torch.empty(d, dtype=f32, device=dev) if weights and w is not None else None
+        return _new((d,), f32, dev) if weights and w is not None else (None, 0)
 
-    dw_in, dw_post, dgate = grad(n.w_in), grad(n.w_post), grad(n.gate)
+    (dw_in, pi), (dw_post, pp), (dgate, pg) = grad(n.w_in), grad(n.w_post), grad(n.gate)
     ws = workspace(addnorm_workspace_size(T, d), dev) if ws is None else ws
-    _call("addnorm_bwd", T, d, _shaped(h, (T, d), h.dtype, "h"), _shaped(y, (T, d), bf, "y"),
-          _shaped(dh_out, (T, d), h.dtype, "dh_out"), _shaped(dx, (T, d), bf, "dx"),
-          _shaped(fwd["rstd_y"], (T,), f32, "rstd_y"), _shaped(fwd["rstd_h"], (T,), f32, "rstd_h"),
-          n.c_struct(d, h.dtype), _shaped(dh, (T, d), h.dtype, "dh"), _shaped(dy, (T, d), bf, "dy"),
-          _shaped(dw_in, (d,), f32, "dw_in"), _shaped(dw_post, (d,), f32, "dw_post"), _shaped(dgate, (d,), f32, "dgate"),
-          L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    _call("addnorm_bwd", T, d, *ins, ph, py, pi, pp, pg, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
     return {"dh": dh, "dy": dy, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
 
 
@@ -325,35 +339,44 @@ def _targets(t: torch.Tensor, T: int):
     return _shaped(t, (T,), t.dtype, "targets"), _INDEX[t.dtype]
 
 
-@_on_stream
-def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0) -> dict:
+def logprob_fwd(logits, targets, k: int = 0, scale: float = 1.0, stream=None) -> dict:
     """logits (T, V) bf16 or float32 (rows may be strided), targets (T) -> logp, entropy, lse (T) float32 and,
     for k > 0, top_ids (T, k) int32 and top_logp (T, k) float32."""
-    T, V = logits.shape
+    if stream is not None:
+        with _on(stream):
+            return logprob_fwd(logits, targets, k, scale)
     p, ld, dt = _rows2d(logits, "logits")
+    T, V = logits.shape
     tp, ti = _targets(targets, T)
     dev, f32 = logits.device, torch.float32
-    logp, entropy, lse = (torch.empty(T, dtype=f32, device=dev) for _ in range(3))
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev) if k > 0 else None
-    top = torch.empty((T, k), dtype=f32, device=dev) if k > 0 else None
-    _call("logprob_fwd", T, V, ld, p, dt, tp, ti, scale, k, L._ptr(logp), L._ptr(entropy), L._ptr(lse), L._ptr(ids),
-          L._ptr(top), _stream())
+    logp, pl = _new((T,), f32, dev)
+    entropy, pe = _new((T,), f32, dev)
+    lse, ps = _new((T,), f32, dev)
+    ids = top = None
+    pi = pt = 0
+    if k > 0:
+        ids, pi = _new((T, k), torch.int32, dev)
+        top, pt = _new((T, k), f32, dev)
+    _call("logprob_fwd", T, V, ld, p, dt, tp, ti, scale, k, pl, pe, ps, pi, pt, _stream())
     return {"logp": logp, "entropy": entropy, "lse": lse, "top_ids": ids, "top_logp": top}
 
 
-@_on_stream
-def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: float = 1.0, dlogits=None) -> dict:
+def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: float = 1.0, dlogits=None,
+                stream=None) -> dict:
     """dlogits (T, V), in the logits' type, from the gradients of logp and entropy (T float32; None: zero).
     ``dlogits`` may be ``logits`` itself."""
-    T, V = logits.shape
+    if stream is not None:
+        with _on(stream):
+            return logprob_bwd(logits, targets, fwd, dlogp, dentropy, scale, dlogits)
     p, ld, dt = _rows2d(logits, "logits")
+    T, V = logits.shape
     tp, ti = _targets(targets, T)
     f32 = torch.float32
     if dlogits is None:
         dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
-    if dlogits.shape != (T, V) or dlogits.dtype != logits.dtype:
+    po, ldo, dto = _rows2d(dlogits, "dlogits")
+    if dlogits.shape != (T, V) or dto != dt:
         raise ValueError("dlogits must have the logits' shape and type")
-    po, ldo, _ = _rows2d(dlogits, "dlogits")
     _call("logprob_bwd", T, V, ld, p, dt, tp, ti, scale, _shaped(fwd["lse"], (T,), f32, "lse"),
           _shaped(fwd["entropy"], (T,), f32, "entropy"), _shaped(dlogp, (T,), f32, "dlogp"),
           _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, _stream())

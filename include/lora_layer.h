@@ -63,7 +63,7 @@ typedef struct lm_heads {
 
 typedef struct lm_attn {
     float scale;            /* finite */
-    float cap;              /* 0, or positive */
+    float cap;              /* 0, or in [2^-14, 2^12]: a capped score's absolute error is up to 2^-21 cap */
     const float* slopes;    /* hq floats (4-byte aligned), or NULL */
     int32_t causal;
     int32_t window;         /* 0, or positive */

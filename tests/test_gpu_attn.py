@@ -244,3 +244,19 @@ def test_key_tiles_of_one_two_and_four_ctas(T, hq, hk, d, docs):
     got, again = _run(*args, a), _run(*args, a)
     _compare(got, ref)
     assert all(torch.equal(got[n], again[n]) for n in got)
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -14, 0.3, 1000.0])
+def test_caps_far_from_the_scores(cap):
+    """Scores all but cut off, and all but left alone.  1 / (1 + e) near 1/2 is off by 2^-24.5 (the exponential,
+    2 ulp, of which a quarter counts), 2^-25 (the sum's rounding) and 2^-24 (the reciprocal, 1 ulp), times 2 cap;
+    the maximum and lse are rounded at the size of the cap, 2^-24 each: together below 2^-21.5 cap."""
+    args, a, ref = _case(200, 2, 1, 64, cap, seed=31)
+    got = _run(*args, a)
+    lse, want = host64(got["lse"]), ref["lse"]
+    assert np.abs(lse - want).max() <= LSE_ABS + cap * 2.0 ** -21.5
+    for n in ("O", "dV", "dQ", "dK"):
+        if cap < 1e-3 and n in ("dQ", "dK"):  # (du/dz underflows nearly everywhere)
+            assert np.isfinite(host64(got[n])).all()
+        else:
+            check(n, host64(got[n]), ref[n], REL)

@@ -159,6 +159,38 @@ def test_a_stream_given_by_argument():
     torch.cuda.synchronize()
 
 
+def test_a_captured_step_replays_the_same_bits():
+    q, k, v, dO, a = _attn_case()
+    h, dx = (torch.randn(300, 256, device="cuda").bfloat16() for _ in range(2))
+    n = M.AddNorm(w_in=torch.ones(256, device="cuda"))
+    t = torch.randint(256, (300,), device="cuda")
+    ws, wn = L.workspace(M.attn_workspace_size(300, 4, 2, 64)), L.workspace(M.addnorm_workspace_size(300, 256))
+
+    def step():
+        fw = M.attn_fwd(q, k, v, a, ws=ws)
+        out = [fw["O"], fw["lse"], *M.attn_bwd(q, k, v, dO, fw, a).values()]
+        an = M.addnorm_fwd(h, fw["O"].view(300, 256), n)
+        ab = M.addnorm_bwd(h, fw["O"].view(300, 256), None, dx, an, n, ws=wn)
+        lp = M.logprob_fwd(an["x"], t, k=4)
+        out += [an["x"], ab["dh"], ab["dy"], ab["dw_in"], lp["logp"], lp["top_ids"]]
+        return out + [M.logprob_bwd(an["x"], t, lp, lp["entropy"])["dlogits"]]
+
+    want = [x.clone() for x in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    L.lm_workspace_check(ws)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ------------------------------------------------------------------------------------ bounded waits
 @pytest.mark.parametrize("kernel,family", [(1, 5), (2, 6), (4, 7)])
 def test_starved_attention_reports_timeout_then_recovers(kernel, family):

@@ -120,6 +120,8 @@ def test_attention_refuses(call, outs, ins):
     inf, nan = float("inf"), float("nan")
     for a, st in ((M.lm_attn(nan, 0, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE), (M.lm_attn(inf, 0, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE),
                   (M.lm_attn(1, -1, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE), (M.lm_attn(1, inf, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE),
+                  (M.lm_attn(1, 2.0 ** 13, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE), (M.lm_attn(1, 1e-30, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE),
+                  (M.lm_attn(1e38, 1e-3, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE),
                   (M.lm_attn(1, nan, 0, 1, 0, docs, 0, 3, 0), L.LM_ERR_SHAPE), (M.lm_attn(1, 0, 0, 1, -1, docs, 0, 3, 0), L.LM_ERR_SHAPE),
                   (M.lm_attn(1, 0, 0, 1, 0, docs, 0, 0, 0), L.LM_ERR_SHAPE),       # offsets of no document
                   (M.lm_attn(1, 0, 0, 1, 0, 0, docs, 3, 0), L.LM_ERR_SHAPE),       # a prefix without documents
