@@ -32,6 +32,20 @@ __host__ __device__ inline TokRange range_in(int t, int s, int e, int pre, int T
     r.qhi = e < t + W ? e : t + W;
     return r;
 }
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+__device__ __forceinline__ TokRange range_of(const lm_attn& a, int t, int T) {
+    // the document: the largest m with cu[m] <= t (empty documents before it are skipped)
+    int m = 0, over = a.n_docs;
+    while (m + 1 < over) {
+        const int mid = (m + over) >> 1;
+        if (a.cu_docs[mid] <= t) m = mid;
+        else over = mid;
+    }
+    const int s = clampi(a.cu_docs[m], 0, T), e = clampi(a.cu_docs[m + 1], 0, T);
+    // padding: empty intervals at t, which keeps all four non-decreasing over the tokens
+    if (t < s || t >= e) return TokRange{t, t, t, t};
+    return range_in(t, s, e, a.prefix ? clampi(a.prefix[m], 0, e - s) : 0, T, a.causal, a.window);
+}
 // of token t < T: from the table, or (one document) from the masks themselves
 __device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
     if (p.rng) {

@@ -78,10 +78,16 @@ struct BwdMaps {
 // nothing get zeros, whatever dO holds.  (8192 tokens, 32 heads of 128: 33 us, 5.0 TB/s; a token and head at a
 // time, the results scattered, 37.)
 constexpr int kDeltaHeads = 4;
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, float* ndelta, float* nlse) {
+__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ lm_attn a_,
+                                                         float* ndelta, float* nlse, TokRange* rng) {
     __shared__ float s_delta[kDeltaHeads][16], s_nlse[kDeltaHeads][16];
     griddep_launch_dependents();
     griddep_wait();
+    if ((int)blockIdx.y * kDeltaHeads >= p.hq) {  // one row of CTAs more than the heads need: who sees whom
+        const int t = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+        if (t < p.T) rng[t] = range_of(a_, t, p.T);
+        return;
+    }
     const int sub = threadIdx.x & 15, mine = threadIdx.x >> 4;
     const int t0 = (int)blockIdx.x * 16, t = t0 + mine, h0 = (int)blockIdx.y * kDeltaHeads;
     float lse[kDeltaHeads];
@@ -125,9 +131,10 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
         (which ? nlse : ndelta)[(int64_t)(h0 + r) * p.Tp + t0 + sub] = which ? s_nlse[r][sub] : s_delta[r][sub];
 }
 
-cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st) {
-    const dim3 grid((unsigned)(p.Tp / 16), (unsigned)((p.hq + kDeltaHeads - 1) / kDeltaHeads));  // (Tp: whole 128-token tiles)
-    return launch_pdl(attn_delta_kernel, grid, dim3(256), 0, st, nullptr, 0, p, ndelta, nlse);
+cudaError_t launch_attn_delta(const AttnParams& p, const lm_attn& a, float* ndelta, float* nlse, TokRange* rng, cudaStream_t st) {
+    // (Tp: whole 128-token tiles)
+    const dim3 grid((unsigned)(p.Tp / 16), (unsigned)((p.hq + kDeltaHeads - 1) / kDeltaHeads + (rng ? 1 : 0)));
+    return launch_pdl(attn_delta_kernel, grid, dim3(256), 0, st, nullptr, 0, p, a, ndelta, nlse, rng);
 }
 
 // ------------------------------------------------------------------ dK, dV

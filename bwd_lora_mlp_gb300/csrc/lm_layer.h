@@ -62,7 +62,8 @@ struct AttnParams {
 enum AttnKernel : int { K_ATTN_FWD = 1, K_ATTN_DKV = 2, K_ATTN_DQ = 4 };
 cudaError_t launch_attn_ranges(const lm_attn& a, int64_t T, TokRange* out, cudaStream_t st);
 lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st);
-cudaError_t launch_attn_delta(const AttnParams& p, float* ndelta, float* nlse, cudaStream_t st);
+// rng: the table of who sees whom is written too
+cudaError_t launch_attn_delta(const AttnParams& p, const lm_attn& a, float* ndelta, float* nlse, TokRange* rng, cudaStream_t st);
 lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st);
 
 // ---- addnorm

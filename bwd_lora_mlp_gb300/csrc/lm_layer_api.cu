@@ -242,10 +242,9 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
     float* nlse = reinterpret_cast<float*>(static_cast<char*>(ws) + P.nlse);
     p.ndelta = delta;
     p.nlse = nlse;
-    LL_TRY(attn_ranges(a, p, st));
     {
         LaunchTag tag("attn.delta", st);
-        LL_TRY(launched(launch_attn_delta(p, delta, nlse, st), "attn delta launch"));
+        LL_TRY(launched(launch_attn_delta(p, *a, delta, nlse, const_cast<TokRange*>(p.rng), st), "attn delta launch"));
     }
     return launch_attn_bwd(p, sms, st);
 }
