@@ -46,10 +46,11 @@ __device__ __forceinline__ TokRange range_of(const lm_attn& a, int t, int T) {
     if (t < s || t >= e) return TokRange{t, t, t, t};
     return range_in(t, s, e, a.prefix ? clampi(a.prefix[m], 0, e - s) : 0, T, a.causal, a.window);
 }
-// of token t < T: from the table, or (one document) from the masks themselves
+// of token t < T: from the table, or (one document) from the masks themselves.  (Not by a read-only load: the
+// kernel may have begun before the one that writes the table ended.)
 __device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
     if (p.rng) {
-        const int4 v = __ldg(reinterpret_cast<const int4*>(p.rng) + t);
+        const int4 v = *(reinterpret_cast<const int4*>(p.rng) + t);
         return TokRange{v.x, v.y, v.z, v.w};
     }
     return range_in(t, 0, p.T, 0, p.T, p.causal, p.window);
