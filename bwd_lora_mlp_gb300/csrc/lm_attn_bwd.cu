@@ -12,7 +12,9 @@
 // attn_dkv is bound by the way from one product to the next: S to P to the next S, whose place P takes,
 // and the same for dP and dz; sixteen warps share each step, 32 columns a thread.  8192 causal tokens, 32
 // query heads on 8 of 128 dims: 788 us, 1.40 PFLOP/s, 0.73 of the burst rate.  attn_dq has room for a second
-// score tile and runs its three products at 0.94 of it, 458 us.
+// score tile and runs its three products at 0.94 of it, 458 us.  Both are one launch, dQ's CTAs after the
+// others: they fill what dK and dV's last items leave.  In two launches a whole step of 700 tokens took 76 us
+// against 60, of 5000 in 84 documents 155 against 124, of 8192 causal ones the same.
 // Tried in attn_dkv: eight warps that form P and eight that form dz from its bf16 rounding, a tile apart,
 // 699 us there, but dK's error 2.9e-3 against 2.4e-3, and 133 against 119 for capped prefixes, 62 against 58
 // for a biased window; the same with P in f16 for dz, 748 and 208 against 192 for packed documents; two groups
@@ -150,8 +152,7 @@ struct DkvCfg {
 
 // SHARED: a cluster of `ctas` CTAs shares the key tile.
 template <int DP, int MODE, bool SHARED>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_dkv_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps, int ctas) {
+__device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& maps, int ctas) {
     const int split = SHARED ? ctas : 1;
     using C = DkvCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -526,9 +527,13 @@ struct DqItem {
     int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row
     bool valid;
 };
-__device__ __forceinline__ DqItem dq_item(const AttnParams& p, int k) {
-    const int nqt = (p.T + kTile - 1) / kTile, G = (int)gridDim.x;
-    const int idx = k & 1 ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
+// This CTA's place among those that form dQ.
+struct DqCtas {
+    int at, of;
+};
+__device__ __forceinline__ DqItem dq_item(const AttnParams& p, const DqCtas& who, int k) {
+    const int nqt = (p.T + kTile - 1) / kTile;
+    const int idx = k & 1 ? (k + 1) * who.of - 1 - who.at : k * who.of + who.at;
     DqItem it{idx % p.hq, (nqt - 1 - idx / p.hq) * kTile, 0, 0, 0, 0, idx < nqt * p.hq};
     if (it.valid) {
         const TokRange rf = tok_range(p, it.q0), rl = tok_range(p, min(it.q0 + kTile, p.T) - 1);
@@ -541,8 +546,7 @@ __device__ __forceinline__ DqItem dq_item(const AttnParams& p, int k) {
 }
 
 template <int DP, int MODE>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    attn_dq_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps) {
+__device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps, const DqCtas& who) {
     using C = DqCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t tdp = tmem + 2 * kTile, tdq = tmem + 3 * kTile;
-    const int rounds = ((p.T + kTile - 1) / kTile * p.hq + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int rounds = ((p.T + kTile - 1) / kTile * p.hq + who.of - 1) / who.of;
 
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 bool ok = true;
                 uint32_t nk = 0, nv = 0, nq[2] = {0, 0};  // tiles asked for
                 for (int r = p.starve & K_ATTN_DQ ? rounds : 0; ok && r < rounds; ++r) {
-                    const DqItem it = dq_item(p, r);
+                    const DqItem it = dq_item(p, who, r);
                     auto query = [&](int which) {  // Q, then dO
                         if (!mbar_wait(smem_u32(&qempty[which]), (nq[which] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;
                         const uint32_t bar = smem_u32(&qfull[which]);
@@ -662,10 +666,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             inside_tokens(p, in0, in1);
             bool ok = true;
             uint32_t base = 0, items = 0;  // tiles and items with tiles before this one
-            DqItem next = dq_item(p, 0);
+            DqItem next = dq_item(p, who, 0);
             for (int r = 0; ok && r < rounds; ++r) {
                 const DqItem it = next;
-                next = dq_item(p, r + 1);
+                next = dq_item(p, who, r + 1);
                 if (it.N <= 0) continue;
                 auto scores = [&](int j) {  // S(j) = Q K^T, in buffer t & 1
                     const uint32_t t = base + (uint32_t)j, s = t % C::kKStages;
@@ -743,12 +747,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ScoreMath S = score_math<MODE>(p);
         bool ok = true;
         uint32_t t = 0, items = 0;  // tiles; items with tiles
-        DqItem next = dq_item(p, 0);
+        DqItem next = dq_item(p, who, 0);
         RowOf next_row = row_of(next);
         for (int r = 0; ok && r < rounds; ++r) {
             const DqItem it = next;
             const RowOf R = next_row;
-            next = dq_item(p, r + 1);
+            next = dq_item(p, who, r + 1);
             next_row = row_of(next);
             if (!it.valid) continue;
             if (biased(MODE)) S.slope = p.slopes[it.h] * kLog2e;
@@ -838,19 +842,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ------------------------------------------------------------------ launches
+constexpr int kDqWaves = 4;
+// One launch: the first `dkv` CTAs form dK and dV, the others dQ as SMs come free.
 template <int DP, int MODE, bool SHARED>
-cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int items, int split, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_dkv_kernel<DP, MODE, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               DkvCfg<DP>::kSmem);
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ BwdMaps maps, int ctas, int dkv) {
+    if ((int)blockIdx.x < dkv) attn_dkv<DP, MODE, SHARED>(p, maps, ctas);
+    else attn_dq<DP, MODE>(p, maps, DqCtas{(int)blockIdx.x - dkv, (int)gridDim.x - dkv});
+}
+template <int DP, int MODE, bool SHARED>
+cudaError_t launch_bwd(const AttnParams& p, const BwdMaps& maps, int items, int split, int dq, cudaStream_t st) {
+    constexpr int kSmem = DkvCfg<DP>::kSmem > DqCfg<DP>::kSmem ? DkvCfg<DP>::kSmem : DqCfg<DP>::kSmem;
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_bwd_kernel<DP, MODE, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
     cluster.val.clusterDim = {(unsigned)split, 1, 1};
-    return launch_pdl(attn_dkv_kernel<DP, MODE, SHARED>, dim3((unsigned)(items * split)), dim3(kBwdThreads), DkvCfg<DP>::kSmem, st,
-                      &cluster, SHARED ? 1 : 0, p, maps, split);
+    const unsigned grid = (unsigned)(items * split + (dq + split - 1) / split * split);
+    LaunchTag tag("attn.bwd", st);
+    return launch_pdl(attn_bwd_kernel<DP, MODE, SHARED>, dim3(grid), dim3(kBwdThreads), kSmem, st, &cluster, SHARED ? 1 : 0, p, maps,
+                      split, items * split);
 }
 template <int DP, int MODE>
-cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
+cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
     // A key tile is shared where there are fewer of them than SMs and the (head, query tile) pairs that see one
     // are many: down to 4 a CTA while the SMs take all CTAs at once, from 32 a CTA up to two CTAs an SM.  A join
     // costs about six pairs.  (32 query heads on 8, 128 dims: 512 tokens 35 -> 24 us with four CTAs a tile, 27 with
@@ -864,27 +879,12 @@ cudaError_t launch_dkv(const AttnParams& p, const BwdMaps& maps, int sms, cudaSt
         if (!(after <= sms && pairs >= 8) && !(after <= 2 * sms && pairs >= 32)) break;
         split *= 2;
     }
-    return split > 1 ? launch_dkv<DP, MODE, true>(p, maps, items, split, st) : launch_dkv<DP, MODE, false>(p, maps, items, 1, st);
-}
-template <int DP, int MODE>
-cudaError_t launch_dq(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_dq_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               DqCfg<DP>::kSmem);
-    if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)((p.T + kTile - 1) / kTile) * p.hq;
-    const unsigned grid = (unsigned)(items < sms ? items : sms);
-    return launch_pdl(attn_dq_kernel<DP, MODE>, dim3(grid), dim3(kBwdThreads), DqCfg<DP>::kSmem, st, nullptr, 0, p, maps);
-}
-
-template <int DP, int MODE>
-cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
-    {
-        LaunchTag tag("attn.dkv", st);
-        const cudaError_t e = launch_dkv<DP, MODE>(p, maps, sms, st);
-        if (e != cudaSuccess) return e;
-    }
-    LaunchTag tag("attn.dq", st);
-    return launch_dq<DP, MODE>(p, maps, sms, st);
+    // dQ's CTAs stay and take items, but a few an SM, as those that start late should have less to do (8192 tokens in
+    // 14 documents: 506 us with four, 516 with one or two, 515 with eight)
+    const int64_t dq_items = (int64_t)tiles * p.hq;
+    const int dq = (int)(dq_items < kDqWaves * sms ? dq_items : kDqWaves * sms);
+    return split > 1 ? launch_bwd<DP, MODE, true>(p, maps, items, split, dq, st)
+                     : launch_bwd<DP, MODE, false>(p, maps, items, 1, dq, st);
 }
 
 template <int DP>
