@@ -120,9 +120,9 @@ def test_the_example_learns(example):
 
 
 # ------------------------------------------------------------------------------------ streams
-def _attn_case(T=300):
+def _attn_case(T=300, hq=4, hk=2, d=64):
     g = torch.Generator().manual_seed(1)
-    q, k, v, dO = (torch.randn(T, h, 64, generator=g).bfloat16().cuda() for h in (4, 2, 2, 4))
+    q, k, v, dO = (torch.randn(T, h, d, generator=g).bfloat16().cuda() for h in (hq, hk, hk, hq))
     return q, k, v, dO, M.Attn(scale=0.125, cu_docs=torch.tensor([0, 100, T], dtype=torch.int32, device="cuda"))
 
 
@@ -193,9 +193,10 @@ def test_a_captured_step_replays_the_same_bits():
 
 # ------------------------------------------------------------------------------------ bounded waits
 @pytest.mark.parametrize("kernel,family", [(1, 5), (2, 6), (4, 7)])
-def test_starved_attention_reports_timeout_then_recovers(kernel, family):
-    q, k, v, dO, a = _attn_case()
-    ws = L.workspace(M.attn_workspace_size(q.shape[0], 4, 2, 64))
+@pytest.mark.parametrize("T,hq,hk,d", [(300, 4, 2, 64), (520, 8, 1, 128)])  # (the second: four CTAs a key tile)
+def test_starved_attention_reports_timeout_then_recovers(kernel, family, T, hq, hk, d):
+    q, k, v, dO, a = _attn_case(T, hq, hk, d)
+    ws = L.workspace(M.attn_workspace_size(T, hq, hk, d))
     fw = M.attn_fwd(q, k, v, a, ws=ws)
     want = M.attn_bwd(q, k, v, dO, fw, a)
     L.lm_workspace_check(ws)
