@@ -32,9 +32,9 @@ constexpr float kRescale = 8.f;
 // Rows of fewer keys than this, and all rows with slopes (whose weights are those of their nearest keys),
 // multiply what the rounding of their weights left out.  (dO.O's part of the error of dQ and dK goes with the
 // sum of a row's squared weights: with rows of fewer than 128 keys only, they were 2.5e-3 to 2.7e-3 off in
-// documents of some hundred tokens, in windows and with slopes, now 2.4e-3; a step of 8192 tokens in 14
-// documents takes 516 us instead of 511, a causal one 1660 instead of 1653.)
-constexpr int kFewKeys = 1024;
+// documents of some hundred tokens and with slopes, now 2.4e-3.  A step of 8192 tokens in 14 documents takes
+// 512 us instead of 507; with 1024 here it takes 518, and one of 2048 tokens 166 instead of 161.)
+constexpr int kFewKeys = 512;
 // Sixteen softmax warps and a warpgroup for the loader's and the issuer's: 640 threads start with 96
 // registers each.
 constexpr int kFwdThreads = 640, kFwdMath = 16, kFwdMathRegs = 104, kFwdIssueRegs = 64;
@@ -77,17 +77,17 @@ struct Item {
     bool valid;
 };
 __device__ __forceinline__ Item item_of(const AttnParams& p, int k) {
-    const int nqb = (p.T + 2 * kTile - 1) / (2 * kTile), G = (int)gridDim.x;
+    const int nqb = (p.T + p.rows - 1) / p.rows, G = (int)gridDim.x;
     const int idx = k & 1 ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
     Item it;
     it.valid = idx < nqb * p.hq;
     it.h = idx % p.hq;
-    it.q0 = (nqb - 1 - idx / p.hq) * 2 * kTile;
+    it.q0 = (nqb - 1 - idx / p.hq) * p.rows;
     it.span[0] = it.span[1] = TileSpan{0, 0, 0, 0};
     it.J0 = it.J1 = 0;
     if (it.valid) {
         it.span[0] = key_tiles(p, it.q0);
-        it.span[1] = key_tiles(p, it.q0 + kTile);
+        if (p.rows > kTile) it.span[1] = key_tiles(p, it.q0 + kTile);
         it.J0 = it.span[0].any() ? it.span[0].j0 : it.span[1].j0;
         if (it.span[1].any()) it.J0 = min(it.J0, it.span[1].j0);
         it.J1 = max(it.span[0].j1, it.span[1].j1);
@@ -95,7 +95,7 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int k) {
     return it;
 }
 __device__ __forceinline__ int rounds_of(const AttnParams& p) {
-    const int n = (p.T + 2 * kTile - 1) / (2 * kTile) * p.hq;
+    const int n = (p.T + p.rows - 1) / p.rows * p.hq;
     return (n + (int)gridDim.x - 1) / (int)gridDim.x;
 }
 
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int k = 0; ok && k < rounds; ++k) {
             const Item it = next;
             next = item_of(p, k + 1);
-            if (!it.valid) continue;
+            if (!it.valid || w * kTile >= p.rows) continue;
             const TileSpan sp = w ? it.span[1] : it.span[0];
             const int i0 = it.q0 + w * kTile + row0;
             int lo[2] = {0, 0}, hi[2] = {0, 0};
@@ -520,7 +520,7 @@ cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, int sms, cudaSt
     const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                FwdCfg<DP>::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)((p.T + 2 * kTile - 1) / (2 * kTile)) * p.hq;
+    const int64_t items = (int64_t)((p.T + p.rows - 1) / p.rows) * p.hq;
     const unsigned grid = (unsigned)(items < sms ? items : sms);
     return launch_pdl(attn_fwd_kernel<DP, MODE>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
 }
@@ -535,8 +535,12 @@ cudaError_t launch_mode(int mode, const AttnParams& p, const FwdMaps& maps, int 
     }
 }
 
-lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st) {
+lm_status launch_attn_fwd(const AttnParams& given, int sms, cudaStream_t st) {
     FwdMaps maps;
+    AttnParams p = given;
+    // One query tile an item where the SMs take all of them at once (512 tokens, 32 heads: 19.5 us, 20.8 with two;
+    // 1024 tokens, 16 heads of 64 dims: 24.1 and 26.0)
+    p.rows = (int64_t)((p.T + 2 * kTile - 1) / (2 * kTile)) * p.hq * 2 <= sms ? kTile : 2 * kTile;
     const lm_heads q{p.q.p, p.q.ts, p.q.hs}, k{p.k.p, p.k.ts, p.k.hs}, v{p.v.p, p.v.ts, p.v.hs};
     lm_status s = encode_heads(&maps.q, q, p.T, p.hq, p.d, kTile);
     if (s == LM_OK) s = encode_heads(&maps.k, k, p.T, p.hk, p.d, kTile);

@@ -51,6 +51,7 @@ struct AttnParams {
     const float* lse_in;
     const float *ndelta, *nlse;  // -dO.O and -lse log2 e, rows of Tp
     int32_t Tp;                 // T rounded up to whole tiles
+    int32_t rows;               // forward: queries of an item, 256 or 128
     uint16_t* out;         // O, or dQ
     int8_t* out_lo;
     float* lse;
