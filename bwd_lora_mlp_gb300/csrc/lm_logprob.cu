@@ -265,6 +265,7 @@ template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
     __shared__ LpShared sm;
     griddep_launch_dependents();
+    if (cluster > 1) cluster_arrive();  // (waited for where the CTAs write to the first one's shared memory)
     griddep_wait();
     const int64_t t = blockIdx.x / cluster;
     const int part = cluster > 1 ? (int)cluster_rank() : 0;
@@ -332,12 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(
     s = join<kThreads / 32>(sm.warp[threadIdx.x & (kThreads / 32 - 1)]);
     if (p.k) segment_top(row, j0, j1, p.k, order_key(own) & (j0 < j1 ? ~0u : 0u), sm);
     if (cluster > 1) {
+        __syncwarp();
+        cluster_wait();  // CTA 0 has started
         if (threadIdx.x == 0) {
             st_first(&sm.seg[part][0], s.m);
             st_first(&sm.seg[part][1], s.S);
             st_first(&sm.seg[part][2], s.w);
         }
         if (threadIdx.x < p.k) st_first(&sm.best[part * p.k + threadIdx.x], sm.mine[threadIdx.x]);
+        __syncwarp();
         cluster_sync();
         if (part) return;
         const int i = threadIdx.x & (kMaxCluster - 1);
