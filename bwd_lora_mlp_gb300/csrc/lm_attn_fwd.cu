@@ -437,11 +437,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int r = 0; r < 2; ++r) {
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                // (no weight at all: nothing is seen; a NaN sum is one, of O and of lse)
                 if ((lane & 3) == 0) {
-                    s_inv[w * kTile + row0 + 8 * r] = l[r] > 0.f ? 1.f / l[r] : 0.f;
+                    s_inv[w * kTile + row0 + 8 * r] = l[r] == 0.f ? 0.f : 1.f / l[r];
                     if (i0 + 8 * r < p.T)
                         p.lse[(int64_t)it.h * p.T + i0 + 8 * r] =
-                            l[r] > 0.f ? (m[r] + log2f(l[r])) * kLn2 + (capped(MODE) ? p.cap : 0.f) : -INFINITY;
+                            l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2 + (capped(MODE) ? p.cap : 0.f);
                 }
             }
             __syncwarp();
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     tmem_ld_x16(tmem + all_lanes + 2 * kTile + w * DP + cc, raw);
                     tmem_ld_wait16(raw);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = inv > 0.f ? __uint_as_float(raw[e]) * inv : 0.f;
+                    for (int e = 0; e < 16; ++e) o[e] = inv == 0.f ? 0.f : __uint_as_float(raw[e]) * inv;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0.f;

@@ -34,8 +34,10 @@ typedef enum lm_index { LM_I32 = 0, LM_I64 = 1 } lm_index;
  * sees them, whatever values they hold, NaN included.  A token that sees nothing has O = 0,
  * lse = -inf and adds nothing to any gradient.  cu_docs must not decrease; offsets are clamped to
  * [0, T] and a prefix to its document.  (They are device values: the host cannot check them.  With
- * other contents results are unspecified, and no access leaves its buffer.)  A value that is not
- * finite can reach rows of other documents that share a 128-token tile with it.
+ * other contents results are unspecified, and no access leaves its buffer.)  A NaN score makes its
+ * query's weights, O and lse NaN, as does one of +inf (but capped); what they reach by the formulas is NaN.
+ * A value that is not finite can besides reach tokens that see nothing of it, of its own document and of
+ * documents that have a token in the same 128 (128 n to 128 n + 127): it is a factor of hidden weights too.
  *
  * q (T x hq x d), k and v (T x hk x d) bf16, hk divides hq, d a multiple of 8, at most 128.  Their
  * tokens and heads may be strided (slices of one QKV buffer, head-major layouts): strides in
