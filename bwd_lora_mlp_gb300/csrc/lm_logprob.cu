@@ -94,7 +94,7 @@ __device__ __forceinline__ float logit(const uint32_t (&w)[4], int e) {
     return F32 ? __uint_as_float(w[e % 4]) : e & 1 ? bf16hi(w[e / 2 % 4]) : bf16lo(w[e / 2 % 4]);
 }
 
-// Running softmax sums; max_nan keeps a NaN, and the sums of a row with one are NaN.
+// Running softmax sums; max_nan keeps a NaN: a maximum that is one stays one, and the sums with it.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -131,8 +131,8 @@ __device__ __forceinline__ Sums join(Sums s) {
 #pragma unroll
     for (int o = N / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float d = fmaxf(s.m - m, -1e30f), f = lp_ex2(d * kL2e);  // (where f is 0, any finite d does)
-    // w moves with the maximum: sum e^{x-m} (x-m); an empty part counts nothing
-    const bool any = s.S > 0.f;
+    // w moves with the maximum: sum e^{x-m} (x-m); an empty part counts nothing (a NaN sum is not empty)
+    const bool any = s.S != 0.f;
     s.w = any ? f * fmaf(s.S, d, s.w) : 0.f;
     s.S = any ? s.S * f : 0.f;
 #pragma unroll
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(
         const float d = fmaxf(s.m - big, -1e30f), f = s.m == -INFINITY ? 0.f : lp_ex2(d * kL2e);  // (f 0: no 0 x inf)
         s.w = s.S > 0.f ? f * fmaf(s.S, d, s.w) : 0.f;
         s.S *= f;
-        s.m = big;
+        s.m = max_nan(s.m, big);  // (a NaN comes here every time and stays)
     };
     constexpr int U = 4;
     scan<U>(row, j0, j1, [&](uint32_t (&w)[U][4], int64_t, int) {
