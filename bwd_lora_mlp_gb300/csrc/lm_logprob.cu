@@ -391,6 +391,8 @@ cudaError_t launch_logprob_fwd(const LogprobParams& p, cudaStream_t st) {
 // ------------------------------------------------------------------ backward
 constexpr int kBwdThreads = 256;
 constexpr int kBwdVecs = 8;  // 16-byte vectors of a thread: a CTA takes a stretch of 2048 of them
+// e^x of this and of anything below is 0 in fp32; the factor beside it then stays finite for gradients up to 1e36
+constexpr float kNoWeight = -128.f;
 
 template <bool F32>
 __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_constant__ LogprobParams p, unsigned per_row) {
@@ -405,10 +407,10 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_c
     const float g = p.dlogp && at >= 0 ? p.dlogp[t] : 0.f;
     const bool empty = lse == -INFINITY;
     const float k0 = -p.scale * fmaf(gH, H, g), k1 = -p.scale * gH, at_target = p.scale * g;
-    // scale (-p (g + gH (log p + H))); p = 0 where log p = -inf (0 x any finite number)
+    // scale (-p (g + gH (log p + H))); where p = 0 any finite factor does
     auto soft = [&](float x) {
         const float lp = __fmul_rn(x, p.scale) - lse;
-        return empty ? 0.f : lp_ex2(lp * kL2e) * fmaf(k1, fmaxf(lp, -1e30f), k0);
+        return empty ? 0.f : lp_ex2(lp * kL2e) * fmaf(k1, fmaxf(lp, kNoWeight), k0);
     };
     auto grad = [&](float x, int64_t j) { return soft(x) + (j == at && !empty ? at_target : 0.f); };
     auto put = [&](int64_t j, float d) {
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_c
                         const float2 lp = __fadd2_rn(__fmul2_rn(make_float2(d[e], d[e + 1]), make_float2(p.scale, p.scale)),
                                                      make_float2(-lse, -lse));
                         const float2 q = __fmul2_rn(lp, make_float2(kL2e, kL2e));
-                        const float2 c = __ffma2_rn(make_float2(k1, k1), make_float2(fmaxf(lp.x, -1e30f), fmaxf(lp.y, -1e30f)),
+                        const float2 c = __ffma2_rn(make_float2(k1, k1), make_float2(fmaxf(lp.x, kNoWeight), fmaxf(lp.y, kNoWeight)),
                                                     make_float2(k0, k0));
                         const float2 r = __fmul2_rn(make_float2(lp_ex2(q.x), lp_ex2(q.y)), c);
                         d[e] = r.x;
