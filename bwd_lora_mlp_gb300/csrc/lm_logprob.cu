@@ -19,7 +19,7 @@ namespace lm {
 
 constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr int kCand = 1024;  // alternatives above the bound that fit
+constexpr int kCand = 512;  // alternatives above the bound that fit (to place n of them takes n^2 / kThreads steps a thread)
 constexpr float kL2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -31,14 +31,16 @@ __device__ __forceinline__ int64_t target_of(const LogprobParams& p, int64_t t) 
     const int64_t v = p.i64 ? static_cast<const int64_t*>(p.targets)[t] : static_cast<const int32_t*>(p.targets)[t];
     return v >= 0 && v < p.V ? v : -1;
 }
-// Larger keys for larger logits; +0 and -0 are equal, every NaN is the largest.
+// Larger keys for larger logits; +0 and -0 are equal, every NaN is the largest.  kNothing: that of -inf, the smallest.
+constexpr uint32_t kNothing = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0xFFFFFFFFu;
     const uint32_t b = __float_as_uint(x + 0.f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 // (key, index) as one number: larger logit first, then the lower index; 0 is none
-__device__ __forceinline__ uint64_t rank_of(float x, uint32_t j) { return ((uint64_t)order_key(x) << 32) | (0xFFFFFFFFu - j); }
+__device__ __forceinline__ uint64_t rank_of(uint32_t key, uint32_t j) { return ((uint64_t)key << 32) | (0xFFFFFFFFu - j); }
+__device__ __forceinline__ uint64_t rank_of(float x, uint32_t j) { return rank_of(order_key(x), j); }
 
 template <bool F32>
 struct Row {
@@ -167,51 +169,107 @@ struct LpShared {
     uint64_t red[kThreads / 32];
     int count;
     int ties[kThreads / 32];
+    // what segment_top leaves for segment_top_ties
+    const char* row;
+    int64_t j0, j1;
+    uint32_t own_max[kThreads];
 };
+__shared__ LpShared sm;  // (the functions below that are not inlined address it directly)
 
-// The k best of [j0, j1) (fewer if it is shorter: the rest are 0) to sm.mine, best first.
-template <bool F32>
-__device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, uint32_t own_max, LpShared& sm) {
+// The k-th largest of the threads' maxima, down to bit `to` (the bits below are 0), and how many reach it.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t own_max, int k, int to, int& reach) {
+    uint32_t bound = 0;
+    reach = kThreads;
+#pragma unroll 1
+    for (int bit = 31; bit >= to; --bit) {
+        const uint32_t t = bound | (1u << bit);
+        const int n = __syncthreads_count(own_max >= t);
+        if (n >= k) bound = t, reach = n;
+    }
+    return bound;
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+    return key & 0x80000000u ? __uint_as_float(key & 0x7FFFFFFFu) : __uint_as_float(~key);
+}
+// What is at or above `least` (or NaN), or only what is above it, to the candidates; their number, which may be
+// more than fit.  `look`: this thread's largest is among them.  FEW: they are expected to fit, and whether they do
+// is not looked at on the way (1000 x 50257 with five alternatives: 30 us without, 37 with that).
+template <bool FEW, bool F32>
+__device__ __forceinline__ int collect(const Row<F32>& row, int64_t j0, int64_t j1, float least, bool strict, bool look) {
     constexpr int W = Row<F32>::kVec;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto take = [&](float x, int64_t j) {
+        if (x < least || (strict && x == least)) return;
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kCand) sm.cand[at] = rank_of(x, (uint32_t)j);
+    };
+    if (look) scan<4>(row, j0, j1, [&](const uint32_t (&w)[4][4], int64_t j, int n) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t one[1][4] = {{w[u][0], w[u][1], w[u][2], w[u][3]}};
+            if (u * kThreads < n && !(largest<1, F32>(one) < least) && (FEW || *(volatile int*)&sm.count <= kCand))
+#pragma unroll 1
+                for (int64_t i = j + (int64_t)u * kThreads * W, end = i + W; i < end; ++i) take(row.at(i), i);
+        }
+    }, take);
+    __syncthreads();
+    return sm.count;
+}
+// The candidates' k best to sm.mine: each one's place is the number of better ones (whatever order they came in).
+__device__ __forceinline__ void place_candidates(int n, int k) {
+    for (int c = threadIdx.x; c < n; c += kThreads) {
+        const uint64_t r = sm.cand[c];
+        int place = 0;
+        for (int q = 0; q < n; ++q) place += sm.cand[q] > r;
+        if (place < k) sm.mine[place] = r;
+    }
+}
+
+// The k best of [j0, j1) (fewer if it is shorter: the rest are 0) to sm.mine, best first.  False: more reach the
+// bound than fit, and nothing is done.
+template <bool F32>
+__device__ __noinline__ bool segment_top(const Row<F32>& row, int64_t j0, int64_t j1, int k, uint32_t own_max) {
+    const int tid = threadIdx.x;
     if (tid < kMaxTop) sm.mine[tid] = 0;
     if (tid == 0) sm.count = 0;
-    // the k-th largest of the threads' maxima from the top bit down (16 bits: that of a bf16, but for the
-    // sixteen ones of a negative one's key; for fp32 a little below it, a bound as good)
-    uint32_t bound = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t t = bound | (1u << bit);
-        if (__syncthreads_count(own_max >= t) >= k) bound = t;
+    // 16 bits of the k-th largest of the threads' maxima: a little below it (of a bf16 nothing lies between), a
+    // bound as good where logits differ.  What reaches it is in a thread whose own largest does
+    int reach;
+    const uint32_t bound = kth_largest(own_max, k, 16, reach);
+    // (of logits that differ k threads and a few more reach it)
+    const bool alike = reach > kThreads * 3 / 4 && j1 - j0 > kThreads;
+    const int n = alike ? kCand + 1 : collect<true>(row, j0, j1, logit_of(bound), false, own_max >= bound);
+    if (n > kCand) {
+        if (tid == 0) sm.row = row.p, sm.j0 = j0, sm.j1 = j1;
+        sm.own_max[tid] = own_max;
+        __syncthreads();
+        return false;
     }
-    const float least = bound & 0x80000000u ? __uint_as_float(bound & 0x7FFFFFFFu) : __uint_as_float(~bound);
-    // what is at or above the bound (or NaN), above it only in a second try
-    auto collect = [&](bool strict) {
-        auto take = [&](float x, int64_t j) {
-            if (x < least || (strict && x == least)) return;
-            const int at = atomicAdd(&sm.count, 1);
-            if (at < kCand) sm.cand[at] = rank_of(x, (uint32_t)j);
-        };
-        // (what reaches the bound is in a thread whose own largest does)
-        if (own_max >= bound) scan<4>(row, j0, j1, [&](const uint32_t (&w)[4][4], int64_t j, int n) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t one[1][4] = {{w[u][0], w[u][1], w[u][2], w[u][3]}};
-                if (u * kThreads < n && !(largest<1, F32>(one) < least))
-#pragma unroll 1
-                    for (int64_t i = j + (int64_t)u * kThreads * W, end = i + W; i < end; ++i) take(row.at(i), i);
-            }
-        }, take);
-        __syncthreads();
-        return sm.count;
-    };
-    int n = collect(false);
-    const bool ties = n > kCand;
-    if (ties) {  // many equal to the bound: only what is above it, and then from the lowest index up
-        __syncthreads();
+    place_candidates(n, k);
+    __syncthreads();
+    return true;
+}
+
+// The same where more reach the bound than fit: masked rows, flat ones, fp32 logits that differ in their low bits
+// only.  The bound is made exact, a logit's own key; then what is above it are few, and the rest are equal to
+// it, from the lowest index up.  (Where it works on comes through shared memory: kept in registers for a call that
+// is seldom made, it cost the kernel spills.  20 alternatives, all but ten logits masked: 4 rows of 131072 bf16
+// 15 us, 1000 of 50257 79; 11 and 36 unmasked, 67 and 940 with a search of the segment for each alternative.)
+template <bool F32>
+__device__ __noinline__ void segment_top_ties(int k) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Row<F32> row{sm.row};
+    const int64_t j0 = sm.j0, j1 = sm.j1;
+    const uint32_t own_max = sm.own_max[tid];
+    int reach;
+    const uint32_t bound = kth_largest(own_max, k, 0, reach);
+    int n = kCand + 1;
+    bool ties = false;
+    for (int strict = F32 && bound != kNothing ? 0 : 1; strict < 2 && n > kCand; ++strict) {
         if (tid == 0) sm.count = 0;
         __syncthreads();
-        n = collect(true);
+        n = collect<false>(row, j0, j1, logit_of(bound), strict, strict ? own_max > bound : own_max >= bound);
+        __syncthreads();
+        ties = strict;
     }
     if (n > kCand) {  // a few threads hold most of the largest: k searches of the segment
         uint64_t last = ~0ull;
@@ -233,37 +291,28 @@ __device__ __noinline__ void segment_top(const Row<F32>& row, int64_t j0, int64_
         __syncthreads();
         return;
     }
-    // each candidate's place is the number of better ones (whatever order they came in)
-    for (int c = tid; c < n; c += kThreads) {
-        const uint64_t r = sm.cand[c];
-        int place = 0;
-        for (int q = 0; q < n; ++q) place += sm.cand[q] > r;
-        if (place < k) sm.mine[place] = r;
-    }
-    if (ties) {
-        int have = min(n, k);
-        for (int64_t j = j0; have < k && j < j1; j += kThreads) {
-            const bool tie = j + tid < j1 && row.at(j + tid) == least;
-            const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-            __syncthreads();
-            if (lane == 0) sm.ties[warp] = __popc(votes);
-            __syncthreads();
-            int before = have, total = 0;
-            for (int q = 0; q < kThreads / 32; ++q) {
-                if (q < warp) before += sm.ties[q];
-                total += sm.ties[q];
-            }
-            const int place = before + __popc(votes & ((1u << lane) - 1u));
-            if (tie && place < k) sm.mine[place] = rank_of(least, (uint32_t)(j + tid));
-            have += total;
+    place_candidates(n, k);
+    int have = ties ? min(n, k) : k;
+    for (int64_t j = j0; have < k && j < j1; j += kThreads) {
+        const bool tie = j + tid < j1 && order_key(row.at(j + tid)) == bound;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        __syncthreads();
+        if (lane == 0) sm.ties[warp] = __popc(votes);
+        __syncthreads();
+        int before = have, total = 0;
+        for (int q = 0; q < kThreads / 32; ++q) {
+            if (q < warp) before += sm.ties[q];
+            total += sm.ties[q];
         }
+        const int place = before + __popc(votes & ((1u << lane) - 1u));
+        if (tie && place < k) sm.mine[place] = rank_of(bound, (uint32_t)(j + tid));
+        have += total;
     }
     __syncthreads();
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(const __grid_constant__ LogprobParams p, int cluster) {
-    __shared__ LpShared sm;
     griddep_launch_dependents();
     if (cluster > 1) cluster_arrive();  // (waited for where the CTAs write to the first one's shared memory)
     griddep_wait();
@@ -331,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(
     if ((threadIdx.x & 31) == 0) sm.warp[threadIdx.x >> 5] = s;
     __syncthreads();
     s = join<kThreads / 32>(sm.warp[threadIdx.x & (kThreads / 32 - 1)]);
-    if (p.k) segment_top(row, j0, j1, p.k, order_key(own) & (j0 < j1 ? ~0u : 0u), sm);
+    if (p.k && !segment_top(row, j0, j1, p.k, order_key(own) & (j0 < j1 ? ~0u : 0u))) segment_top_ties<F32>(p.k);
     if (cluster > 1) {
         __syncwarp();
         cluster_wait();  // CTA 0 has started

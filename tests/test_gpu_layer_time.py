@@ -53,3 +53,22 @@ def test_a_last_tile_of_one_token():
     """129 tokens are 256 with less to do: the same tiles, and the tokens past the end come as zeros."""
     part, whole = _us(_attn_step(129, 32, 1, 128)), _us(_attn_step(256, 32, 1, 128))
     assert part <= 1.15 * whole, (part, whole)
+
+
+@pytest.mark.parametrize("T,V,dtype", [(4, 131072, torch.float32), (4, 131072, torch.bfloat16), (700, 32000, torch.bfloat16),
+                                       (700, 32000, torch.float32), (4096, 1000, torch.bfloat16), (4096, 1000, torch.float32)])
+@pytest.mark.parametrize("rows", ["ten left of -inf", "ten left of -1e9", "ten left of the lowest value", "flat"])
+def test_alternatives_of_masked_and_flat_rows(rows, T, V, dtype):
+    """Twenty alternatives where ten logits are not masked, or all are the same negative number, next to rows of
+    which each logit is another: not more than three times as long."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = (torch.randn(T, V, generator=g, device="cuda") * 3).to(dtype)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda")
+    fill = {"ten left of -inf": -float("inf"), "ten left of -1e9": -1e9, "ten left of the lowest value": torch.finfo(dtype).min,
+            "flat": -3.3}[rows]
+    y = torch.full_like(x, fill)
+    if rows != "flat":
+        at = torch.randperm(V, generator=g, device="cuda")[:10]
+        y[:, at] = x[:, at]
+    plain, masked = _us(lambda: M.logprob_fwd(x, t, 20)), _us(lambda: M.logprob_fwd(y, t, 20))
+    assert masked <= 3 * plain, (masked, plain)
