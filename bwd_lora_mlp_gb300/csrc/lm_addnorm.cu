@@ -497,7 +497,7 @@ static cudaError_t bwd_types(const AddNormParams& p, const RowPlan& P, cudaStrea
 cudaError_t launch_addnorm_fwd(const AddNormParams& p, cudaStream_t st) {
     const RowPlan P = plan_rows(p.d, kFwdOne);
     if (P.nv == 2) return P.threads <= 512 ? fwd_types<2, 512>(p, P, st) : fwd_types<2, 1024>(p, P, st);
-    return P.threads <= 512 ? fwd_types<1, 512>(p, P, st) : fwd_types<1, 1024>(p, P, st);
+    return fwd_types<1, 512>(p, P, st);
 }
 cudaError_t launch_addnorm_bwd(const AddNormParams& p, cudaStream_t st) {
     const RowPlan P = plan_rows(p.d, kBwdOne);
