@@ -286,7 +286,8 @@ def addnorm_fwd(h, y, n: AddNorm, h_out=None, x=None, stream=None) -> dict:
     if n.w_post is not None:
         rstd_y, pry = _new((T,), f32, dev)
     _call("addnorm_fwd", T, d, ph, py, c, po, px, pry, prh, _stream())
-    return {"h": h if y is None else h_out, "x": x, "rstd_y": rstd_y, "rstd_h": rstd_h}
+    # (a buffer given for a result that is not there is checked, not written and not returned)
+    return {"h": h if y is None else h_out, "x": x if n.w_in is not None else None, "rstd_y": rstd_y, "rstd_h": rstd_h}
 
 
 def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, dh=None, dy=None, ws=None,
@@ -312,7 +313,7 @@ def addnorm_bwd(h, y, dh_out, dx, fwd: dict, n: AddNorm, weights: bool = True, d
     (dw_in, pi), (dw_post, pp), (dgate, pg) = grad(n.w_in), grad(n.w_post), grad(n.gate)
     ws = workspace(addnorm_workspace_size(T, d), dev) if ws is None else ws
     _call("addnorm_bwd", T, d, *ins, ph, py, pi, pp, pg, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
-    return {"dh": dh, "dy": dy, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
+    return {"dh": dh, "dy": dy if y is not None else None, "dw_in": dw_in, "dw_post": dw_post, "dgate": dgate, "ws": ws}
 
 
 # ---------------------------------------------------------------------------------------------
