@@ -32,8 +32,10 @@ constexpr float kRescale = 8.f;
 // Rows of fewer keys than this, and all rows with slopes (whose weights are those of their nearest keys),
 // multiply what the rounding of their weights left out.  (dO.O's part of the error of dQ and dK goes with the
 // sum of a row's squared weights: with rows of fewer than 128 keys only, they were 2.5e-3 to 2.7e-3 off in
-// documents of some hundred tokens and with slopes, now 2.4e-3.  A step of 8192 tokens in 14 documents takes
-// 512 us instead of 507; with 1024 here it takes 518, and one of 2048 tokens 166 instead of 161.)
+// documents of some hundred tokens and with slopes, now 2.4e-3.  O itself, rounded to bf16, is 1.66e-3 off in rows
+// with the low bits and 2.3e-3 without.  Twice as many keys here would bring rows of 512 to 1023 keys to the former,
+// dQ and dK by less than 3 %: 2.40e-3 and 2.37e-3 to 2.37e-3 and 2.36e-3 at 1024 tokens.  A step of 8192 tokens in 14
+// documents takes 512 us instead of 507; with 1024 here it takes 518, and one of 2048 tokens 166 instead of 161.)
 constexpr int kFewKeys = 512;
 // Sixteen softmax warps and a warpgroup for the loader's and the issuer's: 640 threads start with 96
 // registers each.
