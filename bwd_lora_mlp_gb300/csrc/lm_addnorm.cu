@@ -20,6 +20,8 @@
 
 namespace lm {
 
+// GB300's, not asked of the device: a workspace's size has to be known on a host without one, and the sums over
+// tokens, by CTA, are the same bits everywhere.
 constexpr int kSms = 152;
 
 // A row takes `warps` warps, each thread NV vectors of 8 columns; a CTA holds `rows` of them.

@@ -11,14 +11,16 @@
 // crossing threads.
 // attn_dkv is bound by the way from one product to the next: S to P to the next S, whose place P takes,
 // and the same for dP and dz; sixteen warps share each step, 32 columns a thread.  8192 causal tokens, 32
-// query heads on 8 of 128 dims: 788 us, 1.40 PFLOP/s, 0.73 of the burst rate.  attn_dq has room for a second
-// score tile and runs its three products at 0.94 of it, 458 us.  Both are one launch, dQ's CTAs after the
-// others: they fill what dK and dV's last items leave.  In two launches a whole step of 700 tokens took 76 us
-// against 60, of 5000 in 84 documents 155 against 124, of 8192 causal ones the same.
+// query heads on 8 of 128 dims, by itself: 776 us, 1.42 PFLOP/s, 0.74 of the burst rate.  attn_dq has room for a
+// second score tile and runs its three products at 0.92 of it, 470 us by itself.  Both are one launch, dQ's CTAs
+// after the others: they fill what dK and dV's last items leave, 1222 us.  (14 documents: 196 and 139 by
+// themselves, 302 together.)  In two launches a whole step of 700 tokens took 76 us against 60, of 5000 in 84
+// documents 155 against 124.  These are times of single launches; step after step the 8192 tokens draw all of the
+// board's power, and the lower clock takes the forward, delta and this launch from 1649 us together to 1763.
 // Tried in attn_dkv: eight warps that form P and eight that form dz from its bf16 rounding, a tile apart,
 // 699 us there, but dK's error 2.9e-3 against 2.4e-3, and 133 against 119 for capped prefixes, 62 against 58
-// for a biased window; the same with P in f16 for dz, 748 and 208 against 192 for packed documents; two groups
-// of eight that take every other tile, 771 and 223; P and dz handed over in two halves, 897 (a store to tensor
+// for a biased window; the same with P in f16 for dz, 748 and 208 against 192 for packed documents (788 for the kept
+// form then); two groups of eight that take every other tile, 771 and 223; P and dz handed over in two halves, 897 (a store to tensor
 // memory and its wait take 300 cycles while the tensor cores multiply from shared memory).  In attn_dq: one
 // CTA an item instead of CTAs that stay, 479; K and V asked for in another order than they are used, 623.
 #include "lm_attn.cuh"

@@ -16,12 +16,14 @@
 // and the backward takes differences against their O.
 // Shared memory (d = 128): 64 KB of queries and a ring of five 32 KB key and value tiles; tensor
 // memory: S_0, S_1, O_0, O_1 of 128 columns each, all of it.
-// Measured: 8192 causal tokens, 32 heads of 128 dims, 384 us, 1.43 PFLOP/s, 0.75 of the burst rate of
-// the tensor cores; 4096 tokens with capped scores 185 us (three exponential-unit results a score instead
-// of one; 212 with tanh formed by itself and the slopes' arithmetic in it).  What bounds it is the way
-// scores -> maximum -> weights -> product: with one score tile a query tile the tensor cores wait for it,
-// and a load or store of tensor memory takes 300 cycles while they multiply from shared memory, 90 while
-// the left operand is in tensor memory.  Eight warps with a whole row a thread instead of sixteen: 384 us
+// Measured: 8192 causal tokens, 32 heads of 128 dims, 384 to 391 us (box to box), 1.43 to 1.41 PFLOP/s, 0.75 to
+// 0.73 of the burst rate of the tensor cores; 4096 tokens with capped scores 185 us (three exponential-unit
+// results a score instead of one; 212 with tanh formed by itself and the slopes' arithmetic in it).  What bounds
+// it is the way scores -> maximum -> weights -> product: with one score tile a query tile the tensor cores wait
+// for it, and a load or store of tensor memory takes 300 cycles while they multiply from shared memory, 90 while
+// the left operand is in tensor memory.  With capped scores that way is longer, and no unit is full: the
+// exponential unit is 49 % busy, the tensor cores 33 %, the warps wait for tensor memory first and for the
+// exponential unit's queue next.  Eight warps with a whole row a thread instead of sixteen: 384 us
 // too, but capped 234 against 212, packed documents 182 against 159, prefixes 97 against 80.  One CTA an
 // item instead of CTAs that stay: capped 240 against 212.
 #include "lm_attn.cuh"

@@ -4,11 +4,14 @@
 // one CTA's, or a cluster's of up to eight where there are fewer rows than the device holds CTAs, each
 // taking a segment, joined through distributed shared memory.  The k alternatives: the k-th largest of
 // the threads' own maxima bounds the k-th largest logit from below, so a second look (from L2) by the
-// threads whose own maximum reaches the bound finds k of them among a few dozen.  Bound by memory:
-// 4096 x 131072 bf16 172 us, 6.2 TB/s (0.92 of the copy rate); at 1000 x 50257 with five alternatives 42 us,
-// 2.4 TB/s: three rows a CTA place, whose joins and second looks are as long as their passes.  (CTAs of 512
+// threads whose own maximum reaches the bound finds k of them among a few dozen; rows of equal logits
+// (masked, flat) take another look or two.  Bound by memory:
+// 4096 x 131072 bf16 171 us, 6.2 TB/s (0.92 of the copy rate); at 1000 x 50257 with five alternatives 42 us,
+// 2.4 TB/s: 1000 rows on 608 CTA places, whose joins and second looks are as long as their passes.  (CTAs of 512
 // threads: 176 and 51 us.)
-// Backward: one pass, dx = scale (g 1[target] - p (g + gH (log p + H))): 4096 x 131072 372 us, 5.8 TB/s (0.85).
+// Backward: one pass, dx = scale (g 1[target] - p (g + gH (log p + H))): 4096 x 131072 372 us, 5.8 TB/s (0.85), as long
+// as the two tensors' rows lie alike on 16 bytes; where they do not, elements go one by one: 1000 x 50257 read with
+// a row stride of 50304 and written without gaps 304 us, with the same stride 45.
 #include <algorithm>
 #include <type_traits>
 
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_fwd_kernel(
 
 template <bool F32>
 static cudaError_t fwd_launch(const LogprobParams& p, cudaStream_t st) {
-    // A CTA per row fills the device from about four rows an SM on; with fewer, a row is shared, as long as
+    // A CTA per row fills the 152 SMs from about four rows an SM on; with fewer, a row is shared, as long as
     // a CTA's segment keeps every thread a few vectors.  (4 rows of 131072 fp32, 20 alternatives: 8 CTAs a row
     // 15 us, 16 a row 21.)
     int c = 1;
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprob_bwd_kernel(const __grid_c
                 for (int64_t i = j; i < s1; ++i) put(i, grad(row.at(i), i));
             }
         }
-    } else {  // the rows of the two tensors lie differently: element by element
+    } else {  // the rows of the two tensors lie differently: element by element, at a seventh of the rate
         for (int64_t j = s0 + threadIdx.x; j < s1; j += kBwdThreads) put(j, grad(row.at(j), j));
     }
 }

@@ -132,7 +132,9 @@ LM_API lm_status addnorm_bwd(int64_t T, int64_t d, const void* h, const uint16_t
  * The backward: dlogits_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + entropy)),
  * in the logits' type (T x V, row stride ld_out >= V), from the forward's lse and entropy; dlogp and
  * dentropy T fp32, each may be NULL (zero; entropy is needed with dentropy).  dlogits may be the
- * logits themselves (ld_out == ld). */
+ * logits themselves (ld_out == ld).  Rows that lie alike in both, modulo 16 bytes (the same stride does), are read
+ * and written in vectors, others element by element, about seven times as long: a slice of a padded buffer's
+ * rows wants its gradient in place, or in a buffer padded alike. */
 LM_API lm_status logprob_fwd(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const void* targets,
                              int32_t index, float scale, int32_t k, float* logp, float* entropy, float* lse,
                              int32_t* top_ids, float* top_logp, lm_stream stream);
