@@ -105,4 +105,31 @@ constexpr int kMaxTop = 32;
 cudaError_t launch_logprob_fwd(const LogprobParams& p, cudaStream_t st);
 cudaError_t launch_logprob_bwd(const LogprobParams& p, cudaStream_t st);
 
+// ---- qkrope
+// The query heads, or the key heads: what is read (x, and backward dy) and written (y: the result, or dx).
+struct RopeSide {
+    const uint16_t *x, *dy;
+    uint16_t* y;
+    int64_t x_ts, x_hs, dy_ts, dy_hs, y_ts, y_hs;
+    const void* w;
+    float* dw;
+    int32_t heads;
+    int32_t parts, per_part;  // (from here on: the launcher's) warps of a token, heads of a warp
+    int32_t blocks;           // CTAs
+};
+struct QkRopeParams {
+    int64_t T;
+    int32_t d, rot, axes;
+    const float* inv_freq;
+    const void* pos;
+    const int32_t* axis;
+    bool pos_i64, w_f32, norm, interleaved;
+    float factor, eps, w_offset;
+    RopeSide q, k;
+    float* part;
+    int32_t vec, lanes;  // the launcher's: dims of a vector, lanes of a head
+};
+size_t qkrope_part_bytes(int d);
+cudaError_t launch_qkrope(QkRopeParams p, bool backward, cudaStream_t st);
+
 }  // namespace lm

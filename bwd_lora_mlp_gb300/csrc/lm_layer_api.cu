@@ -479,3 +479,249 @@ extern "C" lm_status logprob_bwd(int64_t T, int64_t V, int64_t ld, const void* l
     LaunchTag tag("logprob.bwd", st);
     return launched(launch_logprob_bwd(p, st), "logprob backward launch");
 }
+
+// ------------------------------------------------------------------ qkrope
+namespace {
+// Whether two strided tensors share no element.  Rows of the one may lie between rows of the other: with equal
+// token strides, or equal head strides, it is enough that their places modulo that stride are apart.
+struct Strided {
+    const lm_heads* t;
+    int64_t T;
+    int heads, d;
+    const char* name;
+};
+bool apart(const Strided& a, const Strided& b) {
+    if (!overlap(heads_span(a.t, a.T, a.heads, a.d, a.name), heads_span(b.t, b.T, b.heads, b.d, b.name))) return true;
+    auto between = [](const Strided& x, const Strided& y, int64_t period, int64_t ex, int64_t ey) {
+        if (ex > period || ey > period) return false;
+        const int64_t off = (reinterpret_cast<intptr_t>(y.t->p) - reinterpret_cast<intptr_t>(x.t->p)) / 2;
+        const int64_t at = ((off % period) + period) % period;
+        return at >= ex && at + ey <= period;
+    };
+    auto row = [](const Strided& x) { return (x.heads - 1) * x.t->head_stride + x.d; };
+    auto column = [](const Strided& x) { return (x.T - 1) * x.t->token_stride + x.d; };
+    return (a.t->token_stride == b.t->token_stride && between(a, b, a.t->token_stride, row(a), row(b))) ||
+           (a.t->head_stride == b.t->head_stride && between(a, b, a.t->head_stride, column(a), column(b)));
+}
+// an output's own tokens and heads must not share elements
+lm_status check_own(const Strided& a) {
+    if ((a.heads - 1) * a.t->head_stride + a.d <= a.t->token_stride || (a.T - 1) * a.t->token_stride + a.d <= a.t->head_stride)
+        return LM_OK;
+    return report_error(LM_ERR_ALIAS, "%s: its tokens and heads overlap", a.name);
+}
+bool same_place(const lm_heads* a, const lm_heads* b) {
+    return a->p == b->p && a->token_stride == b->token_stride && a->head_stride == b->head_stride;
+}
+
+lm_status check_qkrope_shape(int64_t T, int32_t hq, int32_t hk, int32_t d) {
+    LL_TRY(check_tokens(T, (int64_t(1) << 31) - 1));
+    if (hq < 1 || hk < 0 || hq > 1024 || hk > 1024)
+        return report_error(LM_ERR_SHAPE, "hq = %d must be in [1, 1024], hk = %d in [0, 1024]", hq, hk);
+    if (d < 8 || d > 256 || d % 8 != 0) return report_error(LM_ERR_SHAPE, "d = %d must be a multiple of 8 in [8, 256]", d);
+    return LM_OK;
+}
+
+lm_status check_qkrope(const lm_qkrope* r, int32_t hk, int32_t d) {
+    if (!r) return report_error(LM_ERR_NULL, "r is NULL");
+    if (r->rot < 0 || r->rot > d || r->rot % 8 != 0)
+        return report_error(LM_ERR_SHAPE, "rot = %d must be a multiple of 8 in [0, d]", r->rot);
+    if (!r->rot && !r->norm) return report_error(LM_ERR_SHAPE, "neither a norm nor a rotation: nothing to do");
+    if (r->pos_index != LM_I32 && r->pos_index != LM_I64) return report_error(LM_ERR_DTYPE, "pos_index = %d is not known", r->pos_index);
+    if (r->w_dtype != LM_BF16 && r->w_dtype != LM_F32) return report_error(LM_ERR_DTYPE, "w_dtype = %d is not known", r->w_dtype);
+    if (r->rot) {
+        if (r->axes < 1) return report_error(LM_ERR_SHAPE, "axes = %d must be positive", r->axes);
+        LL_TRY(need(r->inv_freq, 4, "inv_freq"));
+        LL_TRY(want(r->pos, r->pos_index == LM_I64 ? 8 : 4, "pos"));
+        LL_TRY(want(r->axis, 4, "axis"));
+        if (r->axes > 1) {
+            LL_TRY(need(r->pos, 4, "pos"));
+            LL_TRY(need(r->axis, 4, "axis"));
+        }
+        if (!std::isfinite(r->factor)) return report_error(LM_ERR_SHAPE, "factor is not finite");
+    } else {
+        LL_TRY(must_be_null(r->inv_freq, "inv_freq", "with rot = 0"));
+        LL_TRY(must_be_null(r->pos, "pos", "with rot = 0"));
+        LL_TRY(must_be_null(r->axis, "axis", "with rot = 0"));
+    }
+    if (r->norm) {
+        if (!(r->eps > 0.f) || !std::isfinite(r->eps)) return report_error(LM_ERR_SHAPE, "eps = %g must be positive", r->eps);
+        if (!std::isfinite(r->w_offset)) return report_error(LM_ERR_SHAPE, "w_offset is not finite");
+        LL_TRY(want(r->w_q, r->w_dtype == LM_F32 ? 4 : 2, "w_q"));
+        LL_TRY(want(r->w_k, r->w_dtype == LM_F32 ? 4 : 2, "w_k"));
+        if (!hk) LL_TRY(must_be_null(r->w_k, "w_k", "without keys"));
+    } else {
+        LL_TRY(must_be_null(r->w_q, "w_q", "without a norm"));
+        LL_TRY(must_be_null(r->w_k, "w_k", "without a norm"));
+    }
+    return LM_OK;
+}
+
+// outputs against each other and against what is read; an output may be the input at the same index of `over`
+lm_status check_rope_places(std::initializer_list<Strided> outs, std::initializer_list<Strided> over,
+                            std::initializer_list<Strided> ins, std::initializer_list<Span> flat_outs,
+                            std::initializer_list<Span> flat) {
+    for (const Strided* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->t) continue;
+        LL_TRY(check_own(*o));
+        for (const Strided* q = o + 1; q != outs.end(); ++q)
+            if (q->t && !apart(*o, *q)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, q->name);
+        for (const Strided* q = over.begin(); q != over.end(); ++q)
+            if (q->t && !(q - over.begin() == o - outs.begin() && same_place(o->t, q->t)) && !apart(*o, *q))
+                return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, q->name);
+        for (const Strided& q : ins)
+            if (q.t && !apart(*o, q)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, q.name);
+        const Span s = heads_span(o->t, o->T, o->heads, o->d, o->name);
+        for (const Span& f : flat)
+            if (overlap(s, f)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, f.name);
+        for (const Span& f : flat_outs)
+            if (overlap(s, f)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, f.name);
+    }
+    for (const Span* o = flat_outs.begin(); o != flat_outs.end(); ++o) {
+        for (const std::initializer_list<Strided>* l : {&over, &ins})
+            for (const Strided& q : *l)
+                if (q.t && overlap(*o, heads_span(q.t, q.T, q.heads, q.d, q.name)))
+                    return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, q.name);
+        for (const Span& f : flat)
+            if (overlap(*o, f)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, f.name);
+        for (const Span* q = o + 1; q != flat_outs.end(); ++q)
+            if (overlap(*o, *q)) return report_error(LM_ERR_ALIAS, "%s overlaps %s", o->name, q->name);
+    }
+    return LM_OK;
+}
+
+struct RopeFlat {
+    Span inv_freq, pos, axis, w_q, w_k;
+};
+RopeFlat rope_flat(int64_t T, int32_t d, const lm_qkrope* r) {
+    const size_t half = (size_t)r->rot / 2 * 4, wb = (size_t)d * (r->w_dtype == LM_F32 ? 4 : 2);
+    return RopeFlat{{r->inv_freq, half, "inv_freq"},
+                    {r->pos, (size_t)T * (r->rot ? r->axes : 0) * (r->pos_index == LM_I64 ? 8 : 4), "pos"},
+                    {r->axis, half, "axis"},
+                    {r->w_q, wb, "w_q"},
+                    {r->w_k, wb, "w_k"}};
+}
+
+QkRopeParams qkrope_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_qkrope* r) {
+    QkRopeParams p{};
+    p.T = T;
+    p.d = d;
+    p.rot = r->rot;
+    p.axes = r->rot ? r->axes : 1;
+    p.inv_freq = r->inv_freq;
+    p.pos = r->pos;
+    p.axis = p.axes > 1 ? r->axis : nullptr;  // (one axis: all pairs are its)
+    p.pos_i64 = r->pos_index == LM_I64;
+    p.w_f32 = r->w_dtype == LM_F32;
+    p.norm = r->norm != 0;
+    p.interleaved = r->interleaved != 0;
+    p.factor = r->factor;
+    p.eps = r->eps;
+    p.w_offset = r->w_offset;
+    p.q.heads = hq;
+    p.k.heads = hk;
+    p.q.w = r->w_q;
+    p.k.w = r->w_k;
+    return p;
+}
+void side_in(RopeSide& S, const lm_heads* t) { S.x = t->p, S.x_ts = t->token_stride, S.x_hs = t->head_stride; }
+void side_grad(RopeSide& S, const lm_heads* t) { S.dy = t->p, S.dy_ts = t->token_stride, S.dy_hs = t->head_stride; }
+void side_out(RopeSide& S, const lm_heads* t) {
+    S.y = const_cast<uint16_t*>(t->p), S.y_ts = t->token_stride, S.y_hs = t->head_stride;
+}
+}  // namespace
+
+extern "C" lm_status qkrope_workspace_size(int64_t T, int32_t hq, int32_t hk, int32_t d, size_t* bytes) {
+    LL_TRY(check_qkrope_shape(T, hq, hk, d));
+    if (!bytes) return report_error(LM_ERR_NULL, "bytes is NULL");
+    *bytes = 256 + qkrope_part_bytes(d);
+    return LM_OK;
+}
+
+extern "C" lm_status qkrope_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                                const lm_qkrope* r, const lm_heads* q_out, const lm_heads* k_out, lm_stream stream) {
+    LL_TRY(check_qkrope_shape(T, hq, hk, d));
+    LL_TRY(check_qkrope(r, hk, d));
+    LL_TRY(check_heads(q, T, hq, d, "q"));
+    LL_TRY(check_heads(q_out, T, hq, d, "q_out"));
+    if (hk) {
+        LL_TRY(check_heads(k, T, hk, d, "k"));
+        LL_TRY(check_heads(k_out, T, hk, d, "k_out"));
+    } else {
+        LL_TRY(must_be_null(k, "k", "with hk = 0"));
+        LL_TRY(must_be_null(k_out, "k_out", "with hk = 0"));
+    }
+    if (T == 0) return LM_OK;
+    const RopeFlat f = rope_flat(T, d, r);
+    LL_TRY(check_rope_places({{q_out, T, hq, d, "q_out"}, {k_out, T, hk, d, "k_out"}}, {{q, T, hq, d, "q"}, {k, T, hk, d, "k"}}, {}, {},
+                             {f.inv_freq, f.pos, f.axis, f.w_q, f.w_k}));
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    QkRopeParams p = qkrope_params(T, hq, hk, d, r);
+    side_in(p.q, q);
+    side_out(p.q, q_out);
+    if (hk) {
+        side_in(p.k, k);
+        side_out(p.k, k_out);
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    LaunchTag tag("qkrope.fwd", st);
+    return launched(launch_qkrope(p, false, st), "qkrope forward launch");
+}
+
+extern "C" lm_status qkrope_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                                const lm_heads* dq, const lm_heads* dk, const lm_qkrope* r, const lm_heads* dq_in,
+                                const lm_heads* dk_in, float* dw_q, float* dw_k, void* ws, size_t ws_bytes, lm_stream stream) {
+    LL_TRY(check_qkrope_shape(T, hq, hk, d));
+    LL_TRY(check_qkrope(r, hk, d));
+    const bool norm = r->norm != 0;
+    if (norm) LL_TRY(check_heads(q, T, hq, d, "q"));
+    LL_TRY(check_heads(dq, T, hq, d, "dq"));
+    LL_TRY(check_heads(dq_in, T, hq, d, "dq_in"));
+    if (hk) {
+        if (norm) LL_TRY(check_heads(k, T, hk, d, "k"));
+        LL_TRY(check_heads(dk, T, hk, d, "dk"));
+        LL_TRY(check_heads(dk_in, T, hk, d, "dk_in"));
+    } else {
+        LL_TRY(must_be_null(k, "k", "with hk = 0"));
+        LL_TRY(must_be_null(dk, "dk", "with hk = 0"));
+        LL_TRY(must_be_null(dk_in, "dk_in", "with hk = 0"));
+        LL_TRY(must_be_null(dw_k, "dw_k", "with hk = 0"));
+    }
+    LL_TRY(want(dw_q, 4, "dw_q"));
+    LL_TRY(want(dw_k, 4, "dw_k"));
+    const size_t total = 256 + qkrope_part_bytes(d), gb = (size_t)d * 4;
+    if (norm) {
+        LL_TRY(need(ws, 32, "ws"));
+        if (ws_bytes < total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, total);
+    } else {
+        LL_TRY(must_be_null(dw_q, "dw_q", "without a norm"));
+        LL_TRY(must_be_null(dw_k, "dw_k", "without a norm"));
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    if (T == 0) {  // sums over no tokens
+        for (float* g : {dw_q, dw_k})
+            if (g) LL_TRY(launched(cudaMemsetAsync(g, 0, gb, st), "cudaMemsetAsync"));
+        return LM_OK;
+    }
+    const RopeFlat f = rope_flat(T, d, r);
+    LL_TRY(check_rope_places({{dq_in, T, hq, d, "dq_in"}, {dk_in, T, hk, d, "dk_in"}}, {{dq, T, hq, d, "dq"}, {dk, T, hk, d, "dk"}},
+                             {{norm ? q : nullptr, T, hq, d, "q"}, {norm ? k : nullptr, T, hk, d, "k"}},
+                             {{dw_q, gb, "dw_q"}, {dw_k, gb, "dw_k"}, {norm ? ws : nullptr, total, "ws"}},
+                             {f.inv_freq, f.pos, f.axis, f.w_q, f.w_k}));
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    QkRopeParams p = qkrope_params(T, hq, hk, d, r);
+    if (norm) side_in(p.q, q);
+    side_grad(p.q, dq);
+    side_out(p.q, dq_in);
+    p.q.dw = dw_q;
+    if (hk) {
+        if (norm) side_in(p.k, k);
+        side_grad(p.k, dk);
+        side_out(p.k, dk_in);
+        p.k.dw = dw_k;
+    }
+    p.part = norm ? reinterpret_cast<float*>(static_cast<char*>(ws) + 256) : nullptr;
+    LaunchTag tag("qkrope.bwd", st);
+    return launched(launch_qkrope(p, true, st), "qkrope backward launch");
+}

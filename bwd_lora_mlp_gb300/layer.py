@@ -1,6 +1,6 @@
 """ctypes binding of the layer operators of liblora_mlp.so (include/lora_layer.h): attention over
-packed documents, the residual add with the norms before and after a block, and log probabilities
-of given tokens, forward and backward.
+packed documents, the residual add with the norms before and after a block, log probabilities
+of given tokens, and norms of query and key heads with the rotation by position, forward and backward.
 
 Argument marshalling only, as in lib.py: types and layouts are checked here, sizes and pointers by
 the C entry point of the same name, and every non-zero status raises ``LmError``.  Every operator
@@ -44,9 +44,16 @@ class lm_addnorm(ctypes.Structure):
                 ("h_dtype", _I32), ("w_dtype", _I32), ("reserved", _I32)]
 
 
+class lm_qkrope(ctypes.Structure):
+    _fields_ = [("inv_freq", _P), ("pos", _P), ("axis", _P), ("w_q", _P), ("w_k", _P), ("factor", _F), ("eps", _F),
+                ("w_offset", _F), ("rot", _I32), ("axes", _I32), ("interleaved", _I32), ("norm", _I32), ("pos_index", _I32),
+                ("w_dtype", _I32), ("reserved", _I32)]
+
+
 _HP = ctypes.POINTER(lm_heads)
 _AP = ctypes.POINTER(lm_attn)
 _NP = ctypes.POINTER(lm_addnorm)
+_RP = ctypes.POINTER(lm_qkrope)
 
 _SIGS = {
     "attn_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
@@ -58,6 +65,9 @@ _SIGS = {
     "addnorm_bwd": ([_I64, _I64, _P, _P, _P, _P, _P, _P, _NP, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
     "logprob_fwd": ([_I64, _I64, _I64, _P, _I32, _P, _I32, _F, _I32, _P, _P, _P, _P, _P, _P], _I32),
     "logprob_bwd": ([_I64, _I64, _I64, _P, _I32, _P, _I32, _F, _P, _P, _P, _P, _P, _I64, _P], _I32),
+    "qkrope_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
+    "qkrope_fwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _RP, _HP, _HP, _P], _I32),
+    "qkrope_bwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _RP, _HP, _HP, _P, _P, _P, _SZ, _P], _I32),
 }
 
 _fns = {}
@@ -383,3 +393,124 @@ def logprob_bwd(logits, targets, fwd: dict, dlogp=None, dentropy=None, scale: fl
           _shaped(fwd["entropy"], (T,), f32, "entropy"), _shaped(dlogp, (T,), f32, "dlogp"),
           _shaped(dentropy, (T,), f32, "dentropy"), po, ldo, _stream())
     return {"dlogits": dlogits}
+
+
+# ---------------------------------------------------------------------------------------------
+# norms of query and key heads, rotation by position
+
+
+def _here(*tensors) -> None:
+    """Every tensor on the current device, whose stream a call is made on."""
+    at = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError("a call's tensors must lie on the current device (cuda:%d), got one on %s" % (at, t.device))
+
+
+@dataclass
+class QkRope:
+    """Norm of each query and key head (``norm``; root mean square, weights w_q and w_k + w_offset of d values, all
+    bf16 or all float32, None: 1), then the rotation of its first 2 len(inv_freq) dims by position (inv_freq
+    None: no rotation): pair p turns by pos[axis[p]][token] * inv_freq[p], and the rotated dims are multiplied
+    by ``factor``.  Pairs are dims (p, p + len) or, ``interleaved``, (2p, 2p + 1).  inv_freq: float32; pos: int32 or
+    int64, (T), or (axes, T) with axis (int32, an axis for each pair; numbers outside are clamped); None: the
+    token's index."""
+    inv_freq: Optional[torch.Tensor] = None
+    pos: Optional[torch.Tensor] = None
+    axis: Optional[torch.Tensor] = None
+    interleaved: bool = False
+    factor: float = 1.0
+    norm: bool = False
+    w_q: Optional[torch.Tensor] = None
+    w_k: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    w_offset: float = 0.0
+
+    def c_struct(self, T: int, d: int) -> lm_qkrope:
+        f, pos, axis = self.inv_freq, self.pos, self.axis
+        if f is None and (pos is not None or axis is not None):
+            raise ValueError("pos and axis need inv_freq")
+        _here(f, pos, axis, self.w_q, self.w_k)
+        pairs = 0 if f is None else f.numel()
+        axes, pi = 1, LM_I32
+        if pos is not None:
+            if pos.dtype not in _INDEX:
+                raise TypeError("pos must be int32 or int64, got %s" % pos.dtype)
+            pi = _INDEX[pos.dtype]
+            axes = pos.shape[0] if pos.dim() == 2 else 1
+        w = self.w_q if self.w_q is not None else self.w_k
+        wt = torch.bfloat16 if w is None else w.dtype
+        if wt not in _DTYPES:
+            raise TypeError("w_q and w_k must be bfloat16 or float32, got %s" % wt)
+        return lm_qkrope(_shaped(f, (pairs,), torch.float32, "inv_freq"),
+                         0 if pos is None else _shaped(pos, (axes, T) if pos.dim() == 2 else (T,), pos.dtype, "pos"),
+                         _shaped(axis, (pairs,), torch.int32, "axis"), _shaped(self.w_q, (d,), wt, "w_q"),
+                         _shaped(self.w_k, (d,), wt, "w_k"), self.factor, self.eps, self.w_offset, 2 * pairs, axes,
+                         bool(self.interleaved), bool(self.norm), pi, _DTYPES[wt], 0)
+
+
+def _heads_out(t, like, T, h, d, name):
+    """The caller's strided tensor, or a new contiguous one."""
+    if t is None:
+        t = torch.empty((T, h, d), dtype=torch.bfloat16, device=like.device)
+    else:
+        _here(t)
+    return t, _heads(t, T, h, d, name)
+
+
+def qkrope_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
+    return _size("qkrope_workspace_size", T, hq, hk, d)
+
+
+def qkrope_fwd(q, k, r: QkRope, q_out=None, k_out=None, stream=None) -> dict:
+    """q (T, hq, d) and k (T, hk, d; or None) bf16, strided like attn_fwd's -> q and k, normed and rotated.  q_out and
+    k_out may be q and k themselves, or other slices of one buffer."""
+    if stream is not None:
+        with _on(stream):
+            return qkrope_fwd(q, k, r, q_out, k_out)
+    T, hq, d = q.shape
+    hk = 0 if k is None else k.shape[1]
+    _here(q, k)
+    sq, sk = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k") if hk else None
+    c = r.c_struct(T, d)
+    q_out, oq = _heads_out(q_out, q, T, hq, d, "q_out")
+    ok = None
+    if hk:
+        k_out, ok = _heads_out(k_out, q, T, hk, d, "k_out")
+    _call("qkrope_fwd", T, hq, hk, d, sq, sk, c, oq, ok, _stream())
+    return {"q": q_out, "k": k_out if hk else None}
+
+
+def qkrope_bwd(q, k, dq, dk, r: QkRope, weights: bool = True, dq_in=None, dk_in=None, ws=None, stream=None) -> dict:
+    """The gradients of the forward's inputs q and k from those of its results, and with ``weights`` the float32
+    gradients dw_q and dw_k of the weights that are there.  Without a norm q and k are not read and may be None.
+    dq_in may be dq, dk_in may be dk."""
+    if stream is not None:
+        with _on(stream):
+            return qkrope_bwd(q, k, dq, dk, r, weights, dq_in, dk_in, ws)
+    T, hq, d = dq.shape
+    hk = 0 if dk is None else dk.shape[1]
+    dev = dq.device
+    _here(dq, dk)
+    sq = sk = None
+    if r.norm:
+        _here(q, k)
+        sq, sk = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k") if hk else None
+    gq, gk = _heads(dq, T, hq, d, "dq"), _heads(dk, T, hk, d, "dk") if hk else None
+    c = r.c_struct(T, d)
+    dq_in, oq = _heads_out(dq_in, dq, T, hq, d, "dq_in")
+    ok = None
+    if hk:
+        dk_in, ok = _heads_out(dk_in, dq, T, hk, d, "dk_in")
+
+    def grad(w):
+        return _new((d,), torch.float32, dev) if weights and w is not None else (None, 0)
+
+    (dw_q, pq), (dw_k, pk) = grad(r.w_q), grad(r.w_k)
+    pw = n = 0
+    if r.norm:
+        ws = torch.empty(qkrope_workspace_size(T, hq, hk, d), dtype=torch.uint8, device=dev) if ws is None else ws
+        _here(ws)
+        pw, n = L._ptr(ws, torch.uint8, "ws"), ws.numel()
+    _call("qkrope_bwd", T, hq, hk, d, sq, sk, gq, gk, c, oq, ok, pq, pk, pw, n, _stream())
+    return {"dq": dq_in, "dk": dk_in if hk else None, "dw_q": dw_q, "dw_k": dw_k, "ws": ws}

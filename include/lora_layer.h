@@ -142,6 +142,51 @@ LM_API lm_status logprob_bwd(int64_t T, int64_t V, int64_t ld, const void* logit
                              int32_t index, float scale, const float* lse, const float* entropy, const float* dlogp,
                              const float* dentropy, void* dlogits, int64_t ld_out, lm_stream stream);
 
+/* ---- norms of query and key heads with the rotation by position ------------------------------
+ * For every head a (d values) of queries and of keys, each with its own weight:
+ *   n = a * rsqrt(mean(a^2) + eps) * (w + w_offset)      (norm != 0; w == NULL: 1)      n = a (norm == 0)
+ *   (y_i, y_j) = factor * (n_i cos t - n_j sin t, n_j cos t + n_i sin t),  t = pos[axis[p]][token] * inv_freq[p]
+ * over the pairs p of the first rot dims: (i, j) = (p, p + rot / 2), or (2p, 2p + 1) with interleaved != 0.
+ * Dims from rot on are n.  rot == 0: no rotation (the norm alone; inv_freq, pos and axis must be NULL).
+ * inv_freq: rot / 2 finite floats.  pos: axes x T whole numbers (contiguous; NULL with axes == 1: the token's
+ * index), any from -2^31 to 2^31; axis: rot / 2 numbers that say which axis turns a pair (clamped to
+ * [0, axes); NULL with axes == 1: all the same).  Angles are exact to 2^-30 of a turn however far the position.
+ *
+ * q (T x hq x d) and k (T x hk x d; NULL with hk == 0) bf16 and the results likewise, each with strides of its
+ * own as in attn_fwd: elements, multiples of 8, at least d, base 16-byte aligned.  d and rot are multiples of 8,
+ * d at most 256, rot at most d.  (Multiples of 16 of both, and rot / 2 with them, are read 16 bytes at a time,
+ * others 8.)  A result may be its input (the same address and strides) and may lie beside other inputs and
+ * results in one buffer (slices of a fused QKV buffer), else nothing may overlap.
+ * The backward takes the gradients of the results and, for the norm, the forward's inputs (norm == 0: q and k are
+ * not read and may be NULL), and writes the inputs' gradients (dq_in may be dq, dk_in may be dk) and, where wanted
+ * (not NULL; norm != 0), the fp32 sums over tokens and heads dw_q and dw_k (d each).  Every sum, angle and
+ * mean is fp32; what is rounded to bf16 is the result. */
+typedef struct lm_qkrope {
+    const float* inv_freq;
+    const void* pos;
+    const int32_t* axis;
+    const void* w_q;
+    const void* w_k;
+    float factor;
+    float eps; /* > 0 */
+    float w_offset;
+    int32_t rot;
+    int32_t axes;
+    int32_t interleaved;
+    int32_t norm;
+    int32_t pos_index; /* lm_index */
+    int32_t w_dtype;   /* lm_dtype */
+    int32_t reserved;
+} lm_qkrope;
+
+LM_API lm_status qkrope_workspace_size(int64_t T, int32_t hq, int32_t hk, int32_t d, size_t* bytes);
+LM_API lm_status qkrope_fwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                            const lm_qkrope* r, const lm_heads* q_out, const lm_heads* k_out, lm_stream stream);
+LM_API lm_status qkrope_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                            const lm_heads* dq, const lm_heads* dk, const lm_qkrope* r, const lm_heads* dq_in,
+                            const lm_heads* dk_in, float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
+                            lm_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

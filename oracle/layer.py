@@ -150,3 +150,51 @@ def logprob_backward(logits, targets, dlogp=None, dentropy=None, scale=1.0) -> n
             d = d - np.where(p > 0, dentropy[:, None] * p * (lp + f["entropy"][:, None]), 0.0)
     d[np.arange(T)[has], targets[has]] += g[has]
     return scale * d
+
+
+# ---------------------------------------------------------------------------------------------
+# norms of query and key heads, rotation by position
+
+
+def qkrope_angles(T, inv_freq, pos=None, axis=None) -> np.ndarray:
+    """(T, pairs) angles in radians; pos (T,) or (axes, T), axis the row that turns each pair."""
+    f = np.asarray(inv_freq, dtype=np.float64)
+    p = np.arange(T)[None] if pos is None else np.atleast_2d(np.asarray(pos))
+    which = np.zeros(f.size, dtype=int) if axis is None else np.clip(axis, 0, p.shape[0] - 1)
+    return p[which].T.astype(np.float64) * f
+
+
+def _pair_dims(pairs, interleaved):
+    p = np.arange(pairs)
+    return (2 * p, 2 * p + 1) if interleaved else (p, p + pairs)
+
+
+def qkrope_forward(x, angles=None, interleaved=False, factor=1.0, norm=False, w=None, eps=1e-6, w_offset=0.0) -> np.ndarray:
+    """One side (queries or keys): x (T, h, d) -> the same."""
+    y = np.array(x, dtype=np.float64)
+    if norm:
+        y = y / np.sqrt((y * y).mean(axis=-1, keepdims=True) + eps) * (1.0 if w is None else w + w_offset)
+    if angles is None:
+        return y
+    i, j = _pair_dims(angles.shape[1], interleaved)
+    c, s = factor * np.cos(angles)[:, None], factor * np.sin(angles)[:, None]
+    out = y.copy()
+    out[..., i], out[..., j] = y[..., i] * c - y[..., j] * s, y[..., j] * c + y[..., i] * s
+    return out
+
+
+def qkrope_backward(x, dy, angles=None, interleaved=False, factor=1.0, norm=False, w=None, eps=1e-6, w_offset=0.0):
+    """(dx, dw) of one side; dw None without a weight."""
+    g = np.array(dy, dtype=np.float64)
+    if angles is not None:
+        i, j = _pair_dims(angles.shape[1], interleaved)
+        c, s = factor * np.cos(angles)[:, None], factor * np.sin(angles)[:, None]
+        g[..., i], g[..., j] = dy[..., i] * c + dy[..., j] * s, dy[..., j] * c - dy[..., i] * s
+    if not norm:
+        return g, None
+    T, h, d = g.shape
+    flat = np.asarray(x, dtype=np.float64).reshape(T * h, d)
+    wv = np.ones(d) if w is None else w + w_offset
+    r = 1.0 / np.sqrt((flat * flat).mean(axis=1, keepdims=True) + eps)
+    dx, dw = _norm_back(g.reshape(T * h, d), flat, r, wv)
+    return dx.reshape(T, h, d), None if w is None else dw
