@@ -1,0 +1,443 @@
+// Distillation from a teacher's top logits, with the log probabilities of given tokens (include/lora_layer.h).
+//   x = scale z,  lse = log sum e^x,  q = e^{x - lse};  p the teacher's K entries, S their tokens
+//   without rest  kl = sum_k p_k (log p_k - log q_k)                        dx_j = q_j - p_j
+//   with rest     the same + p_r (log p_r - log q_r),  p_r = 1 - sum p,     dx_j = W q_j - p_j in S,
+//                 q_r = sum of q outside S,  W = sum p + p_r                dx_j = q_j (W - p_r / q_r) elsewhere
+// Forward: one pass over the logits.  With rest, the running maximum and sum leave the tokens of S out, so that q_r
+// comes from its own terms and not from what 1 - sum q leaves: each vector has a byte in shared memory that says
+// which of its logits are in S.  The K entries' own terms are summed before the pass, while its first loads
+// are under way; at the end one thread joins scalars.  The sum at scale 1 for the tokens' own log probabilities
+// takes a second exponential only where scale is not 1.
+// Backward: one pass; outside S, dx_j = (W q_r - p_r) e^{x_j} / sum of e^x outside S, a share of at most 1, which no size
+// of logits overflows.  The entries in a CTA's stretch are read before it is written and written after it.
+#include <algorithm>
+
+#include "lm_rows.cuh"
+
+namespace lm {
+
+constexpr int kMarks = 16384;     // vectors of a row (a CTA's segment) with a byte of their own
+constexpr int kEntryWarps = kMaxEntries / 32;
+// One row of `saved`: what the backward takes from the forward.
+// Logarithms are of sums relative to a logit that is written beside them: with masks of the type's lowest
+// value a sum's logarithm is nothing beside the maximum.
+struct Saved {
+    float top, l2, l1;  // the row's largest logit; log2 of sum e^{(z - top) scale}, of sum e^{z - top}
+    float m, ml2;       // the same over the logits that are not entries (with rest), at scale
+    float coef, W, tl;  // others: coef 2^{(z - m) c - ml2}; entries: W q - p,  p = e^{y - tl}
+};
+
+template <bool REST>
+__device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t t, int k) {
+    const int64_t i = t * p.K + k;
+    const float y = p.v_f32 ? static_cast<const float*>(p.values)[i]
+                            : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.values)[i] << 16);
+    return REST ? y : y * p.scale;  // (log probabilities are what they are)
+}
+__device__ __forceinline__ int id_at(const DistillParams& p, int64_t t, int k) {
+    const int64_t i = t * p.K + k;
+    const int64_t v = p.i64 ? static_cast<const int64_t*>(p.ids)[i] : static_cast<const int32_t*>(p.ids)[i];
+    return v >= 0 && v < p.V ? (int)v : -1;
+}
+__device__ __forceinline__ int64_t hard_target(const DistillParams& p, int64_t t) {
+    if (!p.targets) return -1;
+    const int64_t v = p.t64 ? static_cast<const int64_t*>(p.targets)[t] : static_cast<const int32_t*>(p.targets)[t];
+    return v >= 0 && v < p.V ? v : -1;
+}
+
+// A running maximum and the sums of e^{(z - m) scale} and e^{z - m}.
+struct Part {
+    float m, S, S1;
+};
+// 2^{(a - m) c}, 0 for a = -inf also where m is
+__device__ __forceinline__ float brought(float a, float m, float c) {
+    return a == -INFINITY ? 0.f : lp_ex2(fmaxf(a - m, -1e30f) * c);
+}
+template <int N, bool TWO>
+__device__ __forceinline__ Part join_parts(Part s, float c) {
+    float m = s.m;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    s.S *= brought(s.m, m, c);
+    if (TWO) s.S1 *= brought(s.m, m, kL2e);
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+        s.S += __shfl_xor_sync(0xffffffffu, s.S, o);
+        if (TWO) s.S1 += __shfl_xor_sync(0xffffffffu, s.S1, o);
+    }
+    if (m != m) s.S = s.S1 = m;
+    s.m = m;
+    return s;
+}
+
+struct DistillShared {
+    int ids[kMaxEntries];
+    float red[kEntryWarps][2], sums[kEntryWarps][4];
+    Part warp[kThreads / 32], seg[kMaxCluster];
+};
+
+template <bool F32, bool REST, bool TWO>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(const __grid_constant__ DistillParams p, int cluster) {
+    __shared__ DistillShared sm;
+    __shared__ uint4 marks4[REST ? kMarks / 16 : 1];
+    uint8_t* marks = reinterpret_cast<uint8_t*>(marks4);
+    griddep_launch_dependents();
+    if (cluster > 1) cluster_arrive();  // (waited for where the CTAs write to the first one's shared memory)
+    griddep_wait();
+    constexpr int W = Row<F32>::kVec;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t = blockIdx.x / cluster;
+    const int part = cluster > 1 ? (int)cluster_rank() : 0;
+    const Row<F32> row{static_cast<const char*>(p.logits) + t * p.ld * (F32 ? 4 : 2)};
+    const int64_t len = ((p.V + cluster - 1) / cluster + 63) / 64 * 64;  // segments of whole 64-element stretches
+    const int64_t j0 = min(p.V, part * len), j1 = min(p.V, j0 + len);
+    const int64_t a = min(j1, j0 + row.head(j0)), nv = (j1 - a) / W;
+    const float c = p.scale * kL2e;
+
+    // ---- the entries
+    int id = -1;
+    float y = -INFINITY, x = -INFINITY;
+    if (tid < p.K) {
+        id = id_at(p, t, tid);
+        if (id >= 0 && part == 0) {
+            y = teacher_at<REST>(p, t, tid);
+            x = row.at(id);
+        }
+    }
+    if (tid < kMaxEntries) sm.ids[tid] = id;
+    const int64_t target = tid == 0 && part == 0 ? hard_target(p, t) : -1;
+    const float zt = target >= 0 ? row.at(target) : 0.f;
+    if (REST)
+        for (int i = tid; i < min((int64_t)kMarks, nv + 15) / 16; i += kThreads) marks4[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (REST && id >= a && id < a + nv * W) {
+        const int64_t v = (id - a) / W;
+        const int i = (int)(v & (kMarks - 1));
+        atomicOr(reinterpret_cast<uint32_t*>(marks4) + i / 4, 1u << (i % 4 * 8 + (int)(id - a - v * W)));
+    }
+    bool any = false;
+    float ytop = -INFINITY, xtop = -INFINITY;
+    if (part == 0) {
+        if (warp < kEntryWarps) {
+            float yt = y, xt = x;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                yt = max_nan(yt, __shfl_xor_sync(0xffffffffu, yt, o));
+                xt = max_nan(xt, __shfl_xor_sync(0xffffffffu, xt, o));
+            }
+            if (lane == 0) sm.red[warp][0] = yt, sm.red[warp][1] = xt;
+        }
+        any = __syncthreads_or(id >= 0);
+#pragma unroll
+        for (int w = 0; w < kEntryWarps; ++w) {
+            ytop = max_nan(ytop, sm.red[w][0]);
+            xtop = max_nan(xtop, sm.red[w][1]);
+        }
+        if (warp < kEntryWarps) {
+            // (weights of at most e^-5 < 1 / K: their sum with logits of the lowest value does not overflow)
+            const float yref = REST || ytop == -INFINITY ? 0.f : ytop + 5.f, xref = xtop == -INFINITY ? 0.f : xtop;
+            const float e = id >= 0 ? expf(y - yref) : 0.f, dx = (x - xref) * p.scale;
+            // sum e, sum e (log p - log q) up to what is the same for all, and (each token once) the entries' e^x
+            float v[4] = {e, e == 0.f ? 0.f : e * (y - yref - dx), 0.f, 0.f};
+            if (REST) {
+                bool first = id >= 0;
+                for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
+                if (first) {
+                    v[2] = brought(x, xref, c);
+                    v[3] = brought(x, xref, kL2e);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < (REST ? TWO ? 4 : 3 : 2); ++i) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+                if (lane == 0) sm.sums[warp][i] = v[i];
+            }
+        }
+    } else if (REST) {
+        __syncthreads();
+    }
+
+    // ---- the pass
+    Part s{-INFINITY, 0.f, 0.f};
+    auto rise = [&](float big) {  // the running maximum follows, and the sums with it (a NaN comes here every time and stays)
+        s.S *= brought(s.m, big, c);
+        if (TWO) s.S1 *= brought(s.m, big, kL2e);
+        s.m = max_nan(s.m, big);
+    };
+    auto entry_bits = [&](int64_t j) {  // where vectors share a byte: which of the W logits from j on are entries
+        uint32_t b = 0;
+        for (int k = 0; k < p.K; ++k) {
+            const int64_t at = sm.ids[k] - j;
+            if (sm.ids[k] >= 0 && (uint64_t)at < (uint64_t)W) b |= 1u << at;
+        }
+        return b;
+    };
+    constexpr int U = 4;
+    scan<U>(row, j0, j1, [&](uint32_t (&w)[U][4], int64_t j, int) {
+        if (REST) {
+            const int v = (int)((j - a) / W);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t b = marks[(v + u * kThreads) & (kMarks - 1)];
+                if (b) {
+                    if (nv > kMarks) b = entry_bits(j + (int64_t)u * kThreads * W);
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        if (b >> e & 1u) {
+                            if (F32) w[u][e % 4] = 0xFF800000u;
+                            else w[u][e / 2 % 4] = e & 1 ? (w[u][e / 2 % 4] & 0xFFFFu) | 0xFF800000u : (w[u][e / 2 % 4] & 0xFFFF0000u) | 0xFF80u;
+                        }
+                }
+            }
+        }
+        const float big = largest<U, F32>(w);
+        if (!(big <= s.m)) rise(big);
+        if (s.m == -INFINITY) return;
+        float2 S2[2] = {make_float2(s.S, 0.f), make_float2(0.f, 0.f)}, T2[2] = {make_float2(s.S1, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < W; e += 2) {
+                const float2 d = __fadd2_rn(make_float2(logit<F32>(w[u], e), logit<F32>(w[u], e + 1)), make_float2(-s.m, -s.m));
+                const float2 q = __fmul2_rn(d, make_float2(c, c));
+                S2[u & 1] = __fadd2_rn(S2[u & 1], make_float2(lp_ex2(q.x), lp_ex2(q.y)));
+                if (TWO) {
+                    const float2 r = __fmul2_rn(d, make_float2(kL2e, kL2e));
+                    T2[u & 1] = __fadd2_rn(T2[u & 1], make_float2(lp_ex2(r.x), lp_ex2(r.y)));
+                }
+            }
+        s.S = (S2[0].x + S2[0].y) + (S2[1].x + S2[1].y);
+        s.S1 = (T2[0].x + T2[0].y) + (T2[1].x + T2[1].y);
+    }, [&](float z, int64_t j) {
+        if (REST && (entry_bits(j) & 1u)) return;
+        if (!(z <= s.m)) rise(z);
+        if (z == -INFINITY) return;
+        s.S += lp_ex2((z - s.m) * c);
+        if (TWO) s.S1 += lp_ex2((z - s.m) * kL2e);
+    });
+    if (s.m != s.m) s.S = s.S1 = s.m;
+    s = join_parts<32, TWO>(s, c);
+    if (lane == 0) sm.warp[warp] = s;
+    __syncthreads();
+    s = join_parts<kThreads / 32, TWO>(sm.warp[tid & (kThreads / 32 - 1)], c);
+    if (cluster > 1) {
+        __syncwarp();
+        cluster_wait();  // CTA 0 has started
+        if (tid == 0) {
+            st_first(&sm.seg[part].m, s.m);
+            st_first(&sm.seg[part].S, s.S);
+            st_first(&sm.seg[part].S1, s.S1);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (part) return;
+        const int i = tid & (kMaxCluster - 1);
+        s = join_parts<kMaxCluster, TWO>(i < cluster ? sm.seg[i] : Part{-INFINITY, 0.f, 0.f}, c);
+    }
+    if (tid) return;
+
+    // ---- the row's scalars
+    float E = 0.f, Bs = 0.f, Es = 0.f, Es1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kEntryWarps; ++w) {
+        E += sm.sums[w][0];
+        Bs += sm.sums[w][1];
+        if (REST) Es += sm.sums[w][2];
+        if (REST && TWO) Es1 += sm.sums[w][3];
+    }
+    const float xref = xtop == -INFINITY ? 0.f : xtop;
+    const float top = REST && any ? max_nan(s.m, xtop) : s.m;  // the row's largest logit
+    const bool empty = top == -INFINITY;
+    const float fr = brought(s.m, top, c), fs = REST ? brought(xtop, top, c) : 0.f;
+    const float rest = s.S * fr, total = REST ? rest + Es * fs : rest;
+    const float log_total = logf(total), lse = empty ? -INFINITY : fmaf(top, p.scale, log_total);
+    float log_total1 = p.scale == 1.f ? log_total : NAN;  // (not wanted, and not formed, at another scale)
+    if (TWO) {
+        const float r1 = s.S1 * brought(s.m, top, kL2e);
+        log_total1 = logf(REST ? r1 + Es1 * brought(xtop, top, kL2e) : r1);
+    }
+    Saved o{top, log_total * kL2e, log_total1 * kL2e, top, log_total * kL2e, 1.f, 1.f, 0.f};
+    float kl = 0.f;
+    const float dl = (top - xref) * p.scale + log_total;  // lse - xref scale
+    if (REST) {
+        const bool others = s.m != -INFINITY;  // some logit outside the entries weighs something
+        const float pr = E != E ? E : others ? fmaxf(1.f - E, 0.f) : 0.f, lr = logf(s.S);
+        const float lqr = others ? (s.m - top) * p.scale + (lr - log_total) : -INFINITY;
+        if (any) kl = Bs + E * dl + (pr > 0.f ? pr * (logf(pr) - lqr) : pr);
+        o.W = E + pr;
+        o.m = others ? s.m : 0.f;
+        o.ml2 = others ? lr * kL2e : INFINITY;
+        o.coef = any && others ? fmaf(o.W, rest / total, -pr) : 0.f;
+    } else {
+        const float lE = logf(E);
+        if (any && E != 0.f) kl = Bs / E - lE + dl;
+        o.tl = any && E != 0.f ? ytop + 5.f + lE : INFINITY;
+        if (!any || E == 0.f) o.coef = o.W = 0.f;
+    }
+    if (empty) kl = any && E > 0.f ? INFINITY : 0.f;  // no distribution: what the teacher expects is infinitely far
+    p.kl[t] = kl;
+    p.lse[t] = lse;
+    if (p.logp) p.logp[t] = target < 0 ? 0.f : empty ? -INFINITY : zt - top - log_total1;
+    float4* out = reinterpret_cast<float4*>(p.saved + t * 8);
+    out[0] = make_float4(o.top, o.l2, o.l1, o.m);
+    out[1] = make_float4(o.ml2, o.coef, o.W, o.tl);
+}
+
+template <bool F32, bool REST, bool TWO>
+static cudaError_t fwd_launch(const DistillParams& p, cudaStream_t st) {
+    // as for the log probabilities: a row is shared by a cluster where there are fewer rows than places for CTAs
+    int c = 1;
+    while (c < kMaxCluster && p.T * c * 2 <= 152 * 1024 / kThreads && p.V / (c * 2) >= kThreads * 8) c *= 2;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim = {(unsigned)c, 1, 1};
+    return launch_pdl(distill_fwd_kernel<F32, REST, TWO>, dim3((unsigned)(p.T * c)), dim3(kThreads), 0, st, &a, 1, p, c);
+}
+template <bool F32>
+static cudaError_t fwd_forms(const DistillParams& p, cudaStream_t st) {
+    const bool two = p.scale != 1.f && p.targets;
+    if (p.rest) return two ? fwd_launch<F32, true, true>(p, st) : fwd_launch<F32, true, false>(p, st);
+    return two ? fwd_launch<F32, false, true>(p, st) : fwd_launch<F32, false, false>(p, st);
+}
+cudaError_t launch_distill_fwd(const DistillParams& p, cudaStream_t st) {
+    return p.f32 ? fwd_forms<true>(p, st) : fwd_forms<false>(p, st);
+}
+
+// ------------------------------------------------------------------ backward
+constexpr int kDbThreads = 256;
+constexpr int kDbVecs = 8;  // 16-byte vectors of a thread: a CTA takes a stretch of 2048 of them
+
+template <bool F32, bool REST, bool TWO>
+__global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_constant__ DistillParams p, unsigned per_row) {
+    __shared__ int ids[kMaxEntries];
+    __shared__ float ps[kMaxEntries];
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int W = Row<F32>::kVec;
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x / per_row;
+    const Row<F32> row{static_cast<const char*>(p.logits) + t * p.ld * (F32 ? 4 : 2)};
+    char* out = static_cast<char*>(p.dlogits) + t * p.ld_out * (F32 ? 4 : 2);
+    // stretches begin at the row's first 16-byte boundary; the first CTA also takes what is before it
+    const int64_t a = min(p.V, row.head(0)), n = (int64_t)kDbThreads * kDbVecs * W;
+    const int64_t s0 = a + (blockIdx.x - t * per_row) * n, s1 = min(p.V, s0 + n), from = s0 == a ? 0 : s0;
+    const bool alike = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15) == 0;
+    const int64_t at = hard_target(p, t);
+    const float gk = p.dkl ? p.dkl[t] * p.scale : 0.f, gh = p.dlogp && at >= 0 ? p.dlogp[t] : 0.f;
+    auto put = [&](int64_t j, float d) {
+        if (F32) reinterpret_cast<float*>(out)[j] = d;
+        else reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
+    };
+    const float4 s_a = reinterpret_cast<const float4*>(p.saved + t * 8)[0], s_b = reinterpret_cast<const float4*>(p.saved + t * 8)[1];
+    const Saved s{s_a.x, s_a.y, s_a.z, s_a.w, s_b.x, s_b.y, s_b.z, s_b.w};
+    const float c = p.scale * kL2e;
+    const bool none = (gk == 0.f && gh == 0.f) || s.top == -INFINITY;  // the row's gradient is 0, whatever it holds
+    uint4 raw[kDbVecs];
+    if (alike && !none)
+#pragma unroll
+        for (int u = 0; u < kDbVecs; ++u) {
+            const int64_t j = s0 + (u * kDbThreads + tid) * W;
+            if (j + W <= s1) raw[u] = *reinterpret_cast<const uint4*>(row.p + j * (F32 ? 4 : 2));
+        }
+    // the entries of this stretch: their logits are read before anything is written over them
+    int id = -1;
+    float x = 0.f;
+    if (!none) {
+        float pk = 0.f;
+        if (tid < p.K && gk != 0.f) {
+            id = id_at(p, t, tid);
+            if (id < from || id >= s1) id = -1;
+            if (id >= 0) {
+                x = row.at(id);
+                pk = expf(teacher_at<REST>(p, t, tid) - s.tl);
+            }
+        }
+        if (tid < kMaxEntries) ids[tid] = id, ps[tid] = pk;
+        __syncthreads();
+    }
+    // with one scale, a token's own softmax outside the entries is their share of it times e^{(z - m)} / sum
+    const float qr = !REST ? 1.f : s.ml2 == INFINITY ? 0.f : lp_ex2(fmaf(s.m - s.top, c, s.ml2 - s.l2));
+    const float k0 = TWO ? gk * s.coef : fmaf(gk, s.coef, -gh * qr), k1 = -gh;
+    auto soft = [&](float z) {
+        float d = k0 * lp_ex2(fmaf(z - s.m, c, -s.ml2));
+        if (TWO) d = fmaf(k1, lp_ex2(fmaf(z - s.top, kL2e, -s.l1)), d);
+        return d;
+    };
+    auto grad = [&](int64_t j) { return none ? 0.f : soft(row.at(j)) + (j == at ? gh : 0.f); };
+    if (s0 == a && tid < a) put(tid, grad(tid));
+    if (alike) {
+#pragma unroll
+        for (int u = 0; u < kDbVecs; ++u) {
+            const int64_t j = s0 + (u * kDbThreads + tid) * W;
+            if (j + W <= s1) {
+                float d[W];
+                if (none) {
+#pragma unroll
+                    for (int e = 0; e < W; ++e) d[e] = 0.f;
+                } else {
+                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                    for (int e = 0; e < W; e += 2) {
+                        const float2 z = make_float2(logit<F32>(w, e), logit<F32>(w, e + 1));
+                        const float2 q = __ffma2_rn(__fadd2_rn(z, make_float2(-s.m, -s.m)), make_float2(c, c), make_float2(-s.ml2, -s.ml2));
+                        float2 r = __fmul2_rn(make_float2(lp_ex2(q.x), lp_ex2(q.y)), make_float2(k0, k0));
+                        if (TWO) {
+                            const float2 l1 = __ffma2_rn(__fadd2_rn(z, make_float2(-s.top, -s.top)), make_float2(kL2e, kL2e),
+                                                         make_float2(-s.l1, -s.l1));
+                            r = __ffma2_rn(make_float2(k1, k1), make_float2(lp_ex2(l1.x), lp_ex2(l1.y)), r);
+                        }
+                        d[e] = r.x;
+                        d[e + 1] = r.y;
+                    }
+                    if ((uint64_t)(at - j) < (uint64_t)W) {  // the target is one of these
+#pragma unroll
+                        for (int e = 0; e < W; ++e) d[e] += at - j == e ? gh : 0.f;
+                    }
+                }
+                uint4 v;
+                if (F32) v = make_uint4(__float_as_uint(d[0]), __float_as_uint(d[1]), __float_as_uint(d[2]), __float_as_uint(d[3]));
+                else v = make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[W - 4], d[W - 3]),
+                                    pack_bf16x2(d[W - 2], d[W - 1]));
+                *reinterpret_cast<uint4*>(out + j * (F32 ? 4 : 2)) = v;
+            } else {
+                for (int64_t i = j; i < s1; ++i) put(i, grad(i));
+            }
+        }
+    } else {  // the rows of the two tensors lie differently: element by element
+        for (int64_t j = s0 + tid; j < s1; j += kDbThreads) put(j, grad(j));
+    }
+    if (none) return;
+    __syncthreads();
+    if (id < 0) return;
+    float pk = 0.f;
+    for (int k = 0; k < p.K; ++k)
+        if (ids[k] == id) {
+            if (k < tid) return;  // (a token given twice is its first entry's)
+            pk += ps[k];
+        }
+    const float q = lp_ex2(fmaf(x - s.top, c, -s.l2));
+    float d = gk * fmaf(s.W, q, -pk) + (id == at ? gh : 0.f);
+    if (gh != 0.f) d = fmaf(-gh, TWO ? lp_ex2(fmaf(x - s.top, kL2e, -s.l1)) : q, d);
+    put(id, d);
+}
+
+template <bool F32, bool REST, bool TWO>
+static cudaError_t bwd_launch(const DistillParams& p, cudaStream_t st) {
+    const int64_t n = (int64_t)kDbThreads * kDbVecs * Row<F32>::kVec;
+    const int64_t per_row = (p.V + n - 1) / n;
+    if (p.T * per_row > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return launch_pdl(distill_bwd_kernel<F32, REST, TWO>, dim3((unsigned)(p.T * per_row)), dim3(kDbThreads), 0, st, nullptr, 0, p,
+                      (unsigned)per_row);
+}
+template <bool F32>
+static cudaError_t bwd_forms(const DistillParams& p, cudaStream_t st) {
+    const bool two = p.scale != 1.f && p.dlogp;
+    if (p.rest) return two ? bwd_launch<F32, true, true>(p, st) : bwd_launch<F32, true, false>(p, st);
+    return two ? bwd_launch<F32, false, true>(p, st) : bwd_launch<F32, false, false>(p, st);
+}
+cudaError_t launch_distill_bwd(const DistillParams& p, cudaStream_t st) {
+    return p.f32 ? bwd_forms<true>(p, st) : bwd_forms<false>(p, st);
+}
+
+}  // namespace lm

@@ -132,4 +132,21 @@ struct QkRopeParams {
 size_t qkrope_part_bytes(int d);
 cudaError_t launch_qkrope(QkRopeParams p, bool backward, cudaStream_t st);
 
+// ---- distill
+struct DistillParams {
+    int64_t T, V, ld, ld_out;
+    const void* logits;
+    bool f32, i64, t64, v_f32, rest;
+    int32_t K;
+    const void *ids, *values, *targets;
+    float scale;
+    float *kl, *logp, *lse;
+    float* saved;  // T x 8
+    const float *dkl, *dlogp;
+    void* dlogits;
+};
+constexpr int kMaxEntries = 128;
+cudaError_t launch_distill_fwd(const DistillParams& p, cudaStream_t st);
+cudaError_t launch_distill_bwd(const DistillParams& p, cudaStream_t st);
+
 }  // namespace lm

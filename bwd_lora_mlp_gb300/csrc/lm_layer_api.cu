@@ -725,3 +725,112 @@ extern "C" lm_status qkrope_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, co
     LaunchTag tag("qkrope.bwd", st);
     return launched(launch_qkrope(p, true, st), "qkrope backward launch");
 }
+
+// ------------------------------------------------------------------ distill
+namespace {
+lm_status check_distill(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                        const void* targets, int32_t index, float scale) {
+    LL_TRY(check_tokens(T, (int64_t(1) << 31) - 1));
+    if (V < 1 || V > (int64_t(1) << 30)) return report_error(LM_ERR_SHAPE, "V = %lld is not in [1, 2^30]", (long long)V);
+    if (ld < V || ld > (int64_t(1) << 40)) return report_error(LM_ERR_SHAPE, "ld = %lld is smaller than V = %lld", (long long)ld, (long long)V);
+    if (dtype != LM_BF16 && dtype != LM_F32) return report_error(LM_ERR_DTYPE, "dtype = %d is not known", dtype);
+    if (!(scale > 0.f) || !std::isfinite(scale)) return report_error(LM_ERR_SHAPE, "scale = %g must be positive", scale);
+    LL_TRY(need(logits, dtype == LM_F32 ? 4 : 2, "logits"));
+    if (!t) return report_error(LM_ERR_NULL, "t is NULL");
+    if (t->K < 1 || t->K > kMaxEntries) return report_error(LM_ERR_SHAPE, "K = %d is not in [1, %d]", t->K, kMaxEntries);
+    if (t->index != LM_I32 && t->index != LM_I64) return report_error(LM_ERR_DTYPE, "index = %d of ids is not known", t->index);
+    if (t->dtype != LM_BF16 && t->dtype != LM_F32) return report_error(LM_ERR_DTYPE, "dtype = %d of values is not known", t->dtype);
+    LL_TRY(need(t->ids, t->index == LM_I64 ? 8 : 4, "ids"));
+    LL_TRY(need(t->values, t->dtype == LM_F32 ? 4 : 2, "values"));
+    if (!targets) return LM_OK;
+    if (index != LM_I32 && index != LM_I64) return report_error(LM_ERR_DTYPE, "index = %d is not known", index);
+    return need(targets, index == LM_I64 ? 8 : 4, "targets");
+}
+
+struct DistillIn {
+    Span ids, values, targets;
+};
+DistillIn distill_in(int64_t T, const lm_teacher* t, const void* targets, int32_t index) {
+    const size_t n = (size_t)T * t->K;
+    return DistillIn{{t->ids, n * (t->index == LM_I64 ? 8 : 4), "ids"},
+                     {t->values, n * (t->dtype == LM_F32 ? 4 : 2), "values"},
+                     {targets, (size_t)T * (index == LM_I64 ? 8 : 4), "targets"}};
+}
+
+DistillParams distill_params(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                             const void* targets, int32_t index, float scale) {
+    DistillParams p{};
+    p.T = T;
+    p.V = V;
+    p.ld = ld;
+    p.logits = logits;
+    p.f32 = dtype == LM_F32;
+    p.i64 = t->index == LM_I64;
+    p.t64 = index == LM_I64;
+    p.v_f32 = t->dtype == LM_F32;
+    p.rest = t->rest != 0;
+    p.K = t->K;
+    p.ids = t->ids;
+    p.values = t->values;
+    p.targets = targets;
+    p.scale = scale;
+    return p;
+}
+}  // namespace
+
+extern "C" lm_status distill_fwd(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                                 const void* targets, int32_t index, float scale, float* kl, float* logp, float* lse,
+                                 float* saved, lm_stream stream) {
+    LL_TRY(check_distill(T, V, ld, logits, dtype, t, targets, index, scale));
+    LL_TRY(need(kl, 4, "kl"));
+    LL_TRY(need(lse, 4, "lse"));
+    LL_TRY(need(saved, 32, "saved"));
+    if (targets) LL_TRY(need(logp, 4, "logp"));
+    else LL_TRY(must_be_null(logp, "logp", "without targets"));
+    const size_t rb = (size_t)T * 4;
+    const DistillIn in = distill_in(T, t, targets, index);
+    LL_TRY(check_alias({{kl, rb, "kl"}, {logp, rb, "logp"}, {lse, rb, "lse"}, {saved, rb * 8, "saved"}},
+                       {{logits, logit_bytes(T, V, ld, dtype), "logits"}, in.ids, in.values, in.targets}));
+    if (T == 0) return LM_OK;
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    DistillParams p = distill_params(T, V, ld, logits, dtype, t, targets, index, scale);
+    p.kl = kl;
+    p.logp = logp;
+    p.lse = lse;
+    p.saved = saved;
+    cudaStream_t st = (cudaStream_t)stream;
+    LaunchTag tag("distill.fwd", st);
+    return launched(launch_distill_fwd(p, st), "distill forward launch");
+}
+
+extern "C" lm_status distill_bwd(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                                 const void* targets, int32_t index, float scale, const float* saved, const float* dkl,
+                                 const float* dlogp, void* dlogits, int64_t ld_out, lm_stream stream) {
+    LL_TRY(check_distill(T, V, ld, logits, dtype, t, targets, index, scale));
+    if (ld_out < V || ld_out > (int64_t(1) << 40))
+        return report_error(LM_ERR_SHAPE, "ld_out = %lld is smaller than V = %lld", (long long)ld_out, (long long)V);
+    LL_TRY(need(saved, 32, "saved"));
+    LL_TRY(want(dkl, 4, "dkl"));
+    LL_TRY(want(dlogp, 4, "dlogp"));
+    if (!targets) LL_TRY(must_be_null(dlogp, "dlogp", "without targets"));
+    LL_TRY(need(dlogits, dtype == LM_F32 ? 4 : 2, "dlogits"));
+    const size_t rb = (size_t)T * 4;
+    const bool in_place = dlogits == logits && ld_out == ld;
+    const DistillIn in = distill_in(T, t, targets, index);
+    LL_TRY(check_alias({{dlogits, logit_bytes(T, V, ld_out, dtype), "dlogits"}},
+                       {{in_place ? nullptr : logits, logit_bytes(T, V, ld, dtype), "logits"}, in.ids, in.values, in.targets,
+                        {saved, rb * 8, "saved"}, {dkl, rb, "dkl"}, {dlogp, rb, "dlogp"}}));
+    if (T == 0) return LM_OK;
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    DistillParams p = distill_params(T, V, ld, logits, dtype, t, targets, index, scale);
+    p.saved = const_cast<float*>(saved);
+    p.dkl = dkl;
+    p.dlogp = dlogp;
+    p.dlogits = dlogits;
+    p.ld_out = ld_out;
+    cudaStream_t st = (cudaStream_t)stream;
+    LaunchTag tag("distill.bwd", st);
+    return launched(launch_distill_bwd(p, st), "distill backward launch");
+}

@@ -1,6 +1,7 @@
 """ctypes binding of the layer operators of liblora_mlp.so (include/lora_layer.h): attention over
 packed documents, the residual add with the norms before and after a block, log probabilities
-of given tokens, and norms of query and key heads with the rotation by position, forward and backward.
+of given tokens, norms of query and key heads with the rotation by position, and distillation from a
+teacher's top logits, forward and backward.
 
 Argument marshalling only, as in lib.py: types and layouts are checked here, sizes and pointers by
 the C entry point of the same name, and every non-zero status raises ``LmError``.  Every operator
@@ -50,10 +51,15 @@ class lm_qkrope(ctypes.Structure):
                 ("w_dtype", _I32), ("reserved", _I32)]
 
 
+class lm_teacher(ctypes.Structure):
+    _fields_ = [("ids", _P), ("values", _P), ("K", _I32), ("index", _I32), ("dtype", _I32), ("rest", _I32)]
+
+
 _HP = ctypes.POINTER(lm_heads)
 _AP = ctypes.POINTER(lm_attn)
 _NP = ctypes.POINTER(lm_addnorm)
 _RP = ctypes.POINTER(lm_qkrope)
+_TP = ctypes.POINTER(lm_teacher)
 
 _SIGS = {
     "attn_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
@@ -68,6 +74,8 @@ _SIGS = {
     "qkrope_workspace_size": ([_I64, _I32, _I32, _I32, _SZP], _I32),
     "qkrope_fwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _RP, _HP, _HP, _P], _I32),
     "qkrope_bwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _RP, _HP, _HP, _P, _P, _P, _SZ, _P], _I32),
+    "distill_fwd": ([_I64, _I64, _I64, _P, _I32, _TP, _P, _I32, _F, _P, _P, _P, _P, _P], _I32),
+    "distill_bwd": ([_I64, _I64, _I64, _P, _I32, _TP, _P, _I32, _F, _P, _P, _P, _P, _I64, _P], _I32),
 }
 
 _fns = {}
@@ -514,3 +522,82 @@ def qkrope_bwd(q, k, dq, dk, r: QkRope, weights: bool = True, dq_in=None, dk_in=
         pw, n = L._ptr(ws, torch.uint8, "ws"), ws.numel()
     _call("qkrope_bwd", T, hq, hk, d, sq, sk, gq, gk, c, oq, ok, pq, pk, pw, n, _stream())
     return {"dq": dq_in, "dk": dk_in if hk else None, "dw_q": dw_q, "dw_k": dw_k, "ws": ws}
+
+
+# ---------------------------------------------------------------------------------------------
+# distillation from a teacher's top logits
+
+
+@dataclass
+class Teacher:
+    """What a teacher says of each row: ``ids`` (T, K; int32 or int64, outside [0, V): no entry) and ``values``
+    (T, K; bfloat16 or float32), K at most 128.  ``rest`` False: logits, a softmax of scale * values over the
+    row's entries is the teacher; True: log probabilities, and what they leave is one more outcome."""
+    ids: torch.Tensor
+    values: torch.Tensor
+    rest: bool = False
+
+    def c_struct(self, T: int) -> lm_teacher:
+        ids, values = self.ids, self.values
+        if not isinstance(ids, torch.Tensor) or ids.dtype not in _INDEX or ids.dim() != 2:
+            raise TypeError("ids must be a 2D int32 or int64 tensor")
+        if not isinstance(values, torch.Tensor) or values.dtype not in _DTYPES:
+            raise TypeError("values must be a bfloat16 or float32 tensor")
+        shape = (T, ids.shape[1])
+        return lm_teacher(_shaped(ids, shape, ids.dtype, "ids"), _shaped(values, shape, values.dtype, "values"), shape[1],
+                          _INDEX[ids.dtype], _DTYPES[values.dtype], bool(self.rest))
+
+
+def _alike(t):
+    """A new tensor whose rows lie as t's do, modulo 16 bytes (t: 2D with contiguous rows)."""
+    T, V = t.shape
+    ld, es = t.stride(0) if T > 1 else V, t.element_size()
+    off = t.data_ptr() % 16 // es
+    if ld > 2 * V + 16 // es:  # (not the gaps of a much wider buffer: the nearest stride that lies alike)
+        ld = V + (ld - V) % (16 // es)
+    buf = torch.empty(off + T * ld, dtype=t.dtype, device=t.device)
+    return buf.as_strided((T, V), (ld, 1), off)
+
+
+def distill_fwd(logits, teacher: Teacher, targets=None, scale: float = 1.0, stream=None) -> dict:
+    """logits (T, V) bf16 or float32 (rows may be strided) -> kl (T), the divergence from the teacher at scale * logits,
+    lse (T) and, with targets (T; int32 or int64), logp (T), their log probabilities at scale 1, all float32;
+    ``saved`` is for the backward."""
+    if stream is not None:
+        with _on(stream):
+            return distill_fwd(logits, teacher, targets, scale)
+    p, ld, dt = _rows2d(logits, "logits")
+    T, V = logits.shape
+    _here(logits, teacher.ids, teacher.values, targets)
+    tp, ti = (0, LM_I32) if targets is None else _targets(targets, T)
+    dev, f32 = logits.device, torch.float32
+    kl, pk = _new((T,), f32, dev)
+    lse, pl = _new((T,), f32, dev)
+    saved, ps = _new((T, 8), f32, dev)
+    logp, pp = (None, 0) if targets is None else _new((T,), f32, dev)
+    _call("distill_fwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, pk, pp, pl, ps, _stream())
+    return {"kl": kl, "logp": logp, "lse": lse, "saved": saved}
+
+
+def distill_bwd(logits, teacher: Teacher, fwd: dict, dkl=None, targets=None, dlogp=None, scale: float = 1.0, dlogits=None,
+                stream=None) -> dict:
+    """dlogits (T, V), in the logits' type, from the gradients of kl and logp (T float32; None: zero), with the
+    forward's arguments.  ``dlogits`` may be ``logits`` itself; a new one has rows that lie as the logits' do."""
+    if stream is not None:
+        with _on(stream):
+            return distill_bwd(logits, teacher, fwd, dkl, targets, dlogp, scale, dlogits)
+    if dlogp is not None and fwd["logp"] is None:
+        raise ValueError("dlogp needs a forward with targets")
+    p, ld, dt = _rows2d(logits, "logits")
+    T, V = logits.shape
+    _here(logits, teacher.ids, teacher.values, targets, dkl, dlogp, dlogits)
+    tp, ti = (0, LM_I32) if targets is None else _targets(targets, T)
+    f32 = torch.float32
+    if dlogits is None:
+        dlogits = _alike(logits)
+    po, ldo, dto = _rows2d(dlogits, "dlogits")
+    if dlogits.shape != (T, V) or dto != dt:
+        raise ValueError("dlogits must have the logits' shape and type")
+    _call("distill_bwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, _shaped(fwd["saved"], (T, 8), f32, "saved"),
+          _shaped(dkl, (T,), f32, "dkl"), _shaped(dlogp, (T,), f32, "dlogp"), po, ldo, _stream())
+    return {"dlogits": dlogits}

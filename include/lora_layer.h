@@ -187,6 +187,44 @@ LM_API lm_status qkrope_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const 
                             const lm_heads* dk_in, float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
                             lm_stream stream);
 
+/* ---- distillation from a teacher's top logits ------------------------------------------------
+ *   x = scale * logits   lse = log sum_j exp(x_j)   q = exp(x - lse)
+ * and for the row's teacher entries k (token ids[k], p_k):
+ *   rest == 0: values are the teacher's logits, p = softmax of scale * values over the row's entries,
+ *              kl = sum_k p_k (log p_k - log q_ids[k])
+ *   rest != 0: values are the teacher's log probabilities (of its own whole vocabulary), p_k = exp(values[k]), and what
+ *              they leave is one more outcome, p_r = max(0, 1 - sum_k p_k), q_r = the sum of q over all other tokens (p_r = 0
+ *              where no other token has a logit above -inf):
+ *              kl = sum_k p_k (log p_k - log q_ids[k]) + p_r (log p_r - log q_r)
+ * logits as in logprob_fwd; ids (T x K int32 or int64) and values (T x K bf16 or fp32), contiguous, 1 <= K <= 128.  An
+ * id outside [0, V) is no entry, whatever its value; a value of -inf has p = 0 (with rest its token still is not among
+ * the others); a token given twice counts with both values.  A row without entries has kl = 0.  Entries with weight on logits
+ * of -inf make kl infinite.  scale > 0.
+ * targets (T int32 or int64, or NULL): the log probabilities of given tokens at scale 1, in the same pass:
+ *   logp = logits_target - log sum_j exp(logits_j)      (0 for a target outside [0, V); a NULL logp with NULL targets)
+ * kl, lse and logp T fp32; saved (T x 8 fp32, 32-byte aligned) is for the backward.
+ * The backward: dlogits_j = dkl dkl/dlogits_j + dlogp (1[j = target] - softmax(logits)_j), in the logits' type, row
+ * stride ld_out >= V, from the forward's saved (other arguments as there; dkl and dlogp T fp32, each may be NULL: zero).
+ * With rest, a token among the others has dkl/dx = W q_j - p_r q_j / q_r, W = sum p + p_r; an entry's has W q_j - p_k.
+ * A row whose dkl is 0 and whose dlogp is 0 or has no target has gradient 0, whatever it holds.  dlogits may be the logits
+ * themselves (ld_out == ld); rows that lie alike in both modulo 16 bytes are read and written in vectors, others element
+ * by element.  A NaN logit makes its row's results NaN; a row of nothing but -inf has lse = logp = -inf and gradient 0. */
+typedef struct lm_teacher {
+    const void* ids;
+    const void* values;
+    int32_t K;
+    int32_t index; /* lm_index of ids */
+    int32_t dtype; /* lm_dtype of values */
+    int32_t rest;
+} lm_teacher;
+
+LM_API lm_status distill_fwd(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                             const void* targets, int32_t index, float scale, float* kl, float* logp, float* lse,
+                             float* saved, lm_stream stream);
+LM_API lm_status distill_bwd(int64_t T, int64_t V, int64_t ld, const void* logits, int32_t dtype, const lm_teacher* t,
+                             const void* targets, int32_t index, float scale, const float* saved, const float* dkl,
+                             const float* dlogp, void* dlogits, int64_t ld_out, lm_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

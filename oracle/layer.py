@@ -198,3 +198,80 @@ def qkrope_backward(x, dy, angles=None, interleaved=False, factor=1.0, norm=Fals
     r = 1.0 / np.sqrt((flat * flat).mean(axis=1, keepdims=True) + eps)
     dx, dw = _norm_back(g.reshape(T * h, d), flat, r, wv)
     return dx.reshape(T, h, d), None if w is None else dw
+
+
+# ---------------------------------------------------------------------------------------------
+# distillation from a teacher's top logits
+
+
+def _log_softmax_row(x):
+    """(log softmax, log sum); a row of nothing but -inf has log sum -inf and no distribution (NaN)."""
+    m = x.max(initial=-np.inf)
+    if np.isneginf(m):
+        return np.full(x.shape, np.nan), -np.inf
+    l = np.log(np.exp(x - m).sum())
+    return (x - m) - l, m + l  # (beside the lowest numbers of a type l is nothing)
+
+
+def distill_forward(logits, ids, values, targets=None, scale=1.0, rest=False) -> dict:
+    T, V = logits.shape
+    out = {"kl": np.zeros(T), "lse": np.zeros(T), "logp": None if targets is None else np.zeros(T)}
+    for t in range(T):
+        lq, out["lse"][t] = _log_softmax_row(scale * logits[t])
+        lq = np.where(np.isnan(lq) & ~np.isnan(logits[t]), -np.inf, lq)
+        out["kl"][t] = sum(p * (lp - l) for p, lp, l in _outcomes(lq, ids[t], values[t], scale, rest) if p > 0)
+        if targets is not None and 0 <= targets[t] < V:
+            l1, s1 = _log_softmax_row(logits[t])
+            out["logp"][t] = -np.inf if np.isneginf(s1) else l1[targets[t]]
+    return out
+
+
+def _entries(ids, values, V, scale, rest):
+    """The row's entries as (id, log p)."""
+    has = [(int(i), float(v)) for i, v in zip(ids, values) if 0 <= i < V]
+    if rest or not has:
+        return has
+    lp, s = _log_softmax_row(scale * np.array([v for _, v in has]))
+    return [] if np.isneginf(s) else [(i, l) for (i, _), l in zip(has, lp)]
+
+
+def _outcomes(lq, ids, values, scale, rest):
+    """(p, log p, log q) of every outcome."""
+    e = _entries(ids, values, lq.size, scale, rest)
+    res = [(np.exp(l), l, lq[i]) for i, l in e]
+    if rest and e:
+        left = max(0.0, 1.0 - sum(p for p, _, _ in res))
+        others = _log_softmax_row(np.delete(lq, sorted({i for i, _ in e})))[1]
+        if left > 0 and not np.isneginf(others):  # (no other token: no such outcome)
+            res.append((left, np.log(left), others))
+    return res
+
+
+def distill_backward(logits, ids, values, dkl=None, targets=None, dlogp=None, scale=1.0, rest=False) -> np.ndarray:
+    T, V = logits.shape
+    d = np.zeros((T, V))
+    for t in range(T):
+        lq, s = _log_softmax_row(scale * logits[t])
+        if np.isneginf(s):
+            continue
+        if dkl is not None and dkl[t] != 0:
+            q, e = np.exp(lq), _entries(ids[t], values[t], V, scale, rest)
+            p = np.zeros(V)
+            for i, l in e:
+                p[i] += np.exp(l)
+            if rest and e:
+                left, mine = max(0.0, 1.0 - p.sum()), np.zeros(V, dtype=bool)
+                mine[[i for i, _ in e]] = True
+                lo, so = _log_softmax_row(np.where(mine, -np.inf, scale * logits[t]))
+                if np.isneginf(so):
+                    left = 0.0
+                else:  # (q / q_r where both may be tiny)
+                    p = np.where(mine, p, left * np.exp(np.where(mine, 0.0, lo)))
+                d[t] = scale * dkl[t] * (q * (p[mine].sum() + left) - p)
+            elif e:
+                d[t] = scale * dkl[t] * (q * p.sum() - p)
+        if dlogp is not None and 0 <= targets[t] < V and dlogp[t] != 0:
+            l1, _ = _log_softmax_row(logits[t])
+            d[t] -= dlogp[t] * np.exp(l1)
+            d[t, targets[t]] += dlogp[t]
+    return d
