@@ -1109,10 +1109,10 @@ lm_status report_error(lm_status s, const char* fmt, ...) {
 // What the layer operators' translation units share with this one (lm_layer.h).
 lm_status device_ready(int* sms) { return ready(sms); }
 
-lm_status encode_heads(CUtensorMap* m, const lm_heads& t, int64_t T, int heads, int d, int rows) {
+lm_status encode_heads(CUtensorMap* m, const lm_heads& t, int64_t T, int heads, int d, int rows, int box_heads) {
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
     cuuint64_t strides[2] = {(cuuint64_t)t.head_stride * 2, (cuuint64_t)t.token_stride * 2};
-    cuuint32_t box[3] = {64u, 1u, (cuuint32_t)rows};
+    cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)rows};
     cuuint32_t es[3] = {1u, 1u, 1u};
     const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(t.p), dims, strides, box, es,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -56,6 +56,25 @@ __device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
     return range_in(t, 0, p.T, 0, p.T, p.causal, p.window);
 }
 
+// Whose keys: the queries' own tokens (SELF), or those of another tensor of another length (CROSS; FEW: few queries, the
+// heads of a group packed into one tile and the keys split).  The keys [lo, hi) that query t sees, and
+// the queries [qlo, qhi) that see key t: the ends do not decrease over the tokens in either form.
+enum AttnForm : int { ATTN_SELF = 0, ATTN_CROSS = 1, ATTN_FEW = 2 };
+template <int FORM>
+__device__ __forceinline__ TokRange query_range(const AttnParams& p, int t) {
+    if constexpr (FORM == ATTN_SELF) return tok_range(p, t);
+    if (!p.qrange) return TokRange{0, p.Tk, 0, 0};
+    const int2 v = *(p.qrange + t);
+    return TokRange{v.x, v.y, 0, 0};
+}
+template <int FORM>
+__device__ __forceinline__ TokRange key_range(const AttnParams& p, int t) {
+    if constexpr (FORM == ATTN_SELF) return tok_range(p, t);
+    if (!p.krange) return TokRange{0, 0, 0, p.T};
+    const int2 v = *(p.krange + t);
+    return TokRange{0, 0, v.x, v.y};
+}
+
 // ---------------------------------------------------------------- errors
 __device__ __forceinline__ void attn_error(const AttnParams& p, int family, int where) {
     if (p.err) {
@@ -228,6 +247,20 @@ __device__ __forceinline__ void clear_padding(uint8_t* tile, int boxes, int t0, 
             for (int b = 0; b < boxes; ++b)
                 for (int c = 0; c < 8; ++c)
                     *reinterpret_cast<uint4*>(tile + b * kBoxBytes + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+}
+// The same by rows: bit r of `seen` says that row r is somebody's (rows past the last token come as zeros, and count).
+__device__ __forceinline__ void clear_unseen(uint8_t* tile, int boxes, const uint4& seen) {
+    if ((seen.x & seen.y & seen.z & seen.w) == ~0u) return;
+    const uint32_t w[4] = {seen.x, seen.y, seen.z, seen.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        for (uint32_t left = ~w[q]; left; left &= left - 1) {
+            const int r = q * 32 + __ffs(left) - 1;
+            for (int b = 0; b < boxes; ++b)
+                for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(tile + b * kBoxBytes + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+        }
     fence_proxy_async_smem();
 }
 // Rows past the last token come as zeros, so the tokens that need no clearing end with the last tile.  (4097 causal

@@ -14,8 +14,8 @@ namespace lm {
 lm_status report_error(lm_status s, const char* fmt, ...);
 // LM_OK on a device of compute capability 10.3; its SM count.  Fetches the tensor-map encoder.
 lm_status device_ready(int* sms);
-// 3D bf16 tensor map over (d, heads, tokens): box 64 x 1 x rows, 128-byte swizzle; reads outside give 0
-lm_status encode_heads(CUtensorMap* m, const lm_heads& t, int64_t T, int heads, int d, int rows);
+// 3D bf16 tensor map over (d, heads, tokens): box 64 x box_heads x rows, 128-byte swizzle; reads outside give 0
+lm_status encode_heads(CUtensorMap* m, const lm_heads& t, int64_t T, int heads, int d, int rows, int box_heads = 1);
 // An event pair around the kernel launched inside its lifetime, when tracing is on.
 class LaunchTag {
   public:
@@ -39,6 +39,7 @@ struct HeadsIn {
 };
 struct AttnParams {
     int32_t T, hq, hk, d, d16;  // d16: d rounded up to 16
+    int32_t Tk;                 // keys (T, but for cross attention)
     float scale, cap;
     const float* slopes;
     const TokRange* rng;   // T entries, or null: one document
@@ -51,7 +52,13 @@ struct AttnParams {
     const float* lse_in;
     const float *ndelta, *nlse;  // -dO.O and -lse log2 e, rows of Tp
     int32_t Tp;                 // T rounded up to whole tiles
-    int32_t rows;               // forward: queries of an item, 256 or 128
+    int32_t rows;               // forward: queries of an item, 256 or 128 (few queries: tokens of a tile)
+    // cross attention; null: every query sees every key.  By token, and by tile the rows that see or are seen at all
+    const int2 *qrange, *krange;
+    const uint4 *qseen, *kseen;
+    int32_t splits;             // few queries: parts of the keys; their sums, T x hq rows each
+    float* part_o;
+    float2* part_ml;
     uint16_t* out;         // O, or dQ
     int8_t* out_lo;
     float* lse;
@@ -66,6 +73,18 @@ lm_status launch_attn_fwd(const AttnParams& p, int sms, cudaStream_t st);
 // rng: the table of who sees whom is written too
 cudaError_t launch_attn_delta(const AttnParams& p, const lm_attn& a, float* ndelta, float* nlse, TokRange* rng, cudaStream_t st);
 lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st);
+
+// ---- cross attention
+struct CrossTables {
+    int2 *qrange, *krange;
+    uint4 *qseen, *kseen;
+};
+cudaError_t launch_cross_ranges(const lm_cross& a, int64_t Tq, int64_t Tk, const CrossTables& t, cudaStream_t st);
+// parts of the keys, and tokens of a query tile, of the form for few queries; splits 0: the other form
+void plan_few(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t* splits, int32_t* tokens);
+cudaError_t launch_fill(float* out, int64_t n, float v, cudaStream_t st);
+lm_status launch_cross_fwd(const AttnParams& p, int sms, cudaStream_t st);
+lm_status launch_cross_bwd(const AttnParams& p, int sms, cudaStream_t st);
 
 // ---- addnorm
 struct AddNormParams {

@@ -126,7 +126,7 @@ AttnPlan plan_attn(int64_t T, int32_t hq) {
 AttnParams attn_params(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
                        const lm_heads* v, const lm_attn* a, void* ws) {
     AttnParams p{};
-    p.T = (int32_t)T;
+    p.T = p.Tk = (int32_t)T;
     p.Tp = (int32_t)whole_tiles(T);
     p.hq = hq;
     p.hk = hk;
@@ -247,6 +247,180 @@ extern "C" lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, cons
         LL_TRY(launched(launch_attn_delta(p, *a, delta, nlse, const_cast<TokRange*>(p.rng), st), "attn delta launch"));
     }
     return launch_attn_bwd(p, sms, st);
+}
+
+// ------------------------------------------------------------------ cross attention
+namespace {
+lm_status check_cross_shape(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d) {
+    LL_TRY(check_attn_shape(Tq, hq, hk, d));
+    if (Tk < 0 || Tk > kMaxTokens) return report_error(LM_ERR_SHAPE, "Tk = %lld is not in [0, %lld]", (long long)Tk, (long long)kMaxTokens);
+    return LM_OK;
+}
+
+lm_status check_cross(const lm_cross* a) {
+    if (!a) return report_error(LM_ERR_NULL, "a is NULL");
+    if (!(a->scale > 0.f)) return report_error(LM_ERR_SHAPE, "scale = %g must be positive", a->scale);
+    lm_attn like{};
+    like.scale = a->scale;
+    like.cap = a->cap;
+    LL_TRY(check_attn(&like));
+    if (!a->cu_q) {
+        LL_TRY(must_be_null(a->cu_k, "cu_k", "without cu_q"));
+        return must_be_null(a->k_len, "k_len", "without cu_q");
+    }
+    LL_TRY(need(a->cu_q, 4, "cu_q"));
+    LL_TRY(need(a->cu_k, 4, "cu_k"));
+    LL_TRY(want(a->k_len, 4, "k_len"));
+    if (a->n_docs < 1) return report_error(LM_ERR_SHAPE, "n_docs = %d must be positive", a->n_docs);
+    return LM_OK;
+}
+
+struct CrossPlan {
+    int32_t splits, tokens;
+    size_t qrange, krange, qseen, kseen, delta, nlse, part_ml, part_o, total;
+};
+
+CrossPlan plan_cross(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d) {
+    CrossPlan P;
+    plan_few(Tq, Tk, hq, hk, &P.splits, &P.tokens);
+    size_t at = 256;  // after the error word
+    auto take = [&at](size_t bytes) {
+        const size_t here = at;
+        at = (at + bytes + 255) & ~size_t(255);
+        return here;
+    };
+    const size_t rows = (size_t)Tq * hq * (P.splits > 1 ? P.splits : 0);
+    P.qrange = take((size_t)Tq * sizeof(int2));
+    P.krange = take((size_t)Tk * sizeof(int2));
+    P.qseen = take((size_t)whole_tiles(Tq) / 8);
+    P.kseen = take((size_t)whole_tiles(Tk) / 8);
+    P.delta = take((size_t)whole_tiles(Tq) * hq * 4);
+    P.nlse = take((size_t)whole_tiles(Tq) * hq * 4);
+    P.part_ml = take(rows * sizeof(float2));
+    P.part_o = take(rows * d * sizeof(float));
+    P.total = at;
+    return P;
+}
+
+// the parameters of both directions, and who sees whom (a launch with documents)
+lm_status cross_begin(AttnParams* p, const CrossPlan& P, int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d,
+                      const lm_heads* q, const lm_heads* k, const lm_heads* v, const lm_cross* a, void* ws, cudaStream_t st) {
+    lm_attn like{};
+    like.scale = a->scale;
+    like.cap = a->cap;
+    *p = attn_params(Tq, hq, hk, d, q, k, v, &like, ws);
+    p->Tk = (int32_t)Tk;
+    if (!a->cu_q) return LM_OK;
+    char* base = static_cast<char*>(ws);
+    const CrossTables t{reinterpret_cast<int2*>(base + P.qrange), reinterpret_cast<int2*>(base + P.krange),
+                        reinterpret_cast<uint4*>(base + P.qseen), reinterpret_cast<uint4*>(base + P.kseen)};
+    p->qrange = t.qrange;
+    p->krange = t.krange;
+    p->qseen = t.qseen;
+    p->kseen = t.kseen;
+    LaunchTag tag("cross.ranges", st);
+    return launched(launch_cross_ranges(*a, Tq, Tk, t, st), "cross ranges launch");
+}
+}  // namespace
+
+extern "C" lm_status cross_workspace_size(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, size_t* bytes) {
+    LL_TRY(check_cross_shape(Tq, Tk, hq, hk, d));
+    if (!bytes) return report_error(LM_ERR_NULL, "bytes is NULL");
+    *bytes = plan_cross(Tq, Tk, hq, hk, d).total;
+    return LM_OK;
+}
+
+extern "C" lm_status cross_fwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                               const lm_heads* v, const lm_cross* a, uint16_t* O, int8_t* O_lo, float* lse, void* ws,
+                               size_t ws_bytes, lm_stream stream) {
+    LL_TRY(check_cross_shape(Tq, Tk, hq, hk, d));
+    LL_TRY(check_cross(a));
+    LL_TRY(check_heads(q, Tq, hq, d, "q"));
+    LL_TRY(check_heads(k, Tk, hk, d, "k"));
+    LL_TRY(check_heads(v, Tk, hk, d, "v"));
+    LL_TRY(need(O, 32, "O"));
+    LL_TRY(want(O_lo, 32, "O_lo"));
+    LL_TRY(need(lse, 32, "lse"));
+    LL_TRY(need(ws, 32, "ws"));
+    const CrossPlan P = plan_cross(Tq, Tk, hq, hk, d);
+    if (ws_bytes < P.total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, P.total);
+    const size_t ob = (size_t)Tq * hq * d * 2, lob = (size_t)Tq * hq * ((d + 15) / 16 * 16), lb = (size_t)Tq * hq * 4;
+    LL_TRY(check_alias({{O, ob, "O"}, {O_lo, lob, "O_lo"}, {lse, lb, "lse"}, {ws, P.total, "ws"}},
+                       {heads_span(q, Tq, hq, d, "q"), heads_span(k, Tk, hk, d, "k"), heads_span(v, Tk, hk, d, "v")}));
+    if (Tq == 0) return LM_OK;
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (Tk == 0) {  // nothing is seen
+        LL_TRY(launched(cudaMemsetAsync(O, 0, ob, st), "cudaMemsetAsync"));
+        if (O_lo) LL_TRY(launched(cudaMemsetAsync(O_lo, 0, lob, st), "cudaMemsetAsync"));
+        return launched(launch_fill(lse, (int64_t)Tq * hq, -INFINITY, st), "fill launch");
+    }
+    AttnParams p;
+    LL_TRY(cross_begin(&p, P, Tq, Tk, hq, hk, d, q, k, v, a, ws, st));
+    p.out = O;
+    p.out_lo = O_lo;
+    p.lse = lse;
+    p.splits = P.splits;
+    p.rows = P.tokens;
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + P.part_ml);
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + P.part_o);
+    LaunchTag tag("cross.fwd", st);
+    return launch_cross_fwd(p, sms, st);
+}
+
+extern "C" lm_status cross_bwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, const lm_heads* q, const lm_heads* k,
+                               const lm_heads* v, const lm_heads* dO, const uint16_t* O, const int8_t* O_lo, const float* lse,
+                               const lm_cross* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws, size_t ws_bytes,
+                               lm_stream stream) {
+    LL_TRY(check_cross_shape(Tq, Tk, hq, hk, d));
+    LL_TRY(check_cross(a));
+    LL_TRY(check_heads(q, Tq, hq, d, "q"));
+    LL_TRY(check_heads(k, Tk, hk, d, "k"));
+    LL_TRY(check_heads(v, Tk, hk, d, "v"));
+    LL_TRY(check_heads(dO, Tq, hq, d, "dO"));
+    LL_TRY(need(O, 32, "O"));
+    LL_TRY(want(O_lo, 32, "O_lo"));
+    LL_TRY(need(lse, 32, "lse"));
+    LL_TRY(need(dQ, 32, "dQ"));
+    LL_TRY(need(dK, 32, "dK"));
+    LL_TRY(need(dV, 32, "dV"));
+    LL_TRY(need(ws, 32, "ws"));
+    const CrossPlan P = plan_cross(Tq, Tk, hq, hk, d);
+    if (ws_bytes < P.total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, P.total);
+    const size_t bq = (size_t)Tq * hq * d * 2, bk = (size_t)Tk * hk * d * 2;
+    LL_TRY(check_alias({{dQ, bq, "dQ"}, {dK, bk, "dK"}, {dV, bk, "dV"}, {ws, P.total, "ws"}},
+                       {heads_span(q, Tq, hq, d, "q"), heads_span(k, Tk, hk, d, "k"), heads_span(v, Tk, hk, d, "v"),
+                        heads_span(dO, Tq, hq, d, "dO"), {O, bq, "O"}, {O_lo, (size_t)Tq * hq * ((d + 15) / 16 * 16), "O_lo"},
+                        {lse, (size_t)Tq * hq * 4, "lse"}}));
+    if (Tq == 0 && Tk == 0) return LM_OK;
+    int sms = 0;
+    LL_TRY(device_ready(&sms));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (Tq == 0 || Tk == 0) {  // nothing is seen
+        if (bq) LL_TRY(launched(cudaMemsetAsync(dQ, 0, bq, st), "cudaMemsetAsync"));
+        if (bk) LL_TRY(launched(cudaMemsetAsync(dK, 0, bk, st), "cudaMemsetAsync"));
+        if (bk) LL_TRY(launched(cudaMemsetAsync(dV, 0, bk, st), "cudaMemsetAsync"));
+        return LM_OK;
+    }
+    AttnParams p;
+    LL_TRY(cross_begin(&p, P, Tq, Tk, hq, hk, d, q, k, v, a, ws, st));
+    p.dO = {dO->p, dO->token_stride, dO->head_stride};
+    p.O = O;
+    p.O_lo = O_lo;
+    p.lse_in = lse;
+    p.out = dQ;
+    p.dK = dK;
+    p.dV = dV;
+    float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + P.delta);
+    float* nlse = reinterpret_cast<float*>(static_cast<char*>(ws) + P.nlse);
+    p.ndelta = delta;
+    p.nlse = nlse;
+    {
+        LaunchTag tag("cross.delta", st);
+        LL_TRY(launched(launch_attn_delta(p, lm_attn{}, delta, nlse, nullptr, st), "cross delta launch"));
+    }
+    return launch_cross_bwd(p, sms, st);
 }
 
 // ------------------------------------------------------------------ addnorm

@@ -1,5 +1,5 @@
 """ctypes binding of the layer operators of liblora_mlp.so (include/lora_layer.h): attention over
-packed documents, the residual add with the norms before and after a block, log probabilities
+packed documents and to the states of another length, the residual add with the norms before and after a block, log probabilities
 of given tokens, norms of query and key heads with the rotation by position, and distillation from a
 teacher's top logits, forward and backward.
 
@@ -40,6 +40,10 @@ class lm_attn(ctypes.Structure):
                 ("prefix", _P), ("n_docs", _I32), ("reserved", _I32)]
 
 
+class lm_cross(ctypes.Structure):
+    _fields_ = [("scale", _F), ("cap", _F), ("cu_q", _P), ("cu_k", _P), ("k_len", _P), ("n_docs", _I32), ("reserved", _I32)]
+
+
 class lm_addnorm(ctypes.Structure):
     _fields_ = [("w_in", _P), ("w_post", _P), ("gate", _P), ("alpha", _F), ("eps", _F), ("w_offset", _F),
                 ("h_dtype", _I32), ("w_dtype", _I32), ("reserved", _I32)]
@@ -57,6 +61,7 @@ class lm_teacher(ctypes.Structure):
 
 _HP = ctypes.POINTER(lm_heads)
 _AP = ctypes.POINTER(lm_attn)
+_CP = ctypes.POINTER(lm_cross)
 _NP = ctypes.POINTER(lm_addnorm)
 _RP = ctypes.POINTER(lm_qkrope)
 _TP = ctypes.POINTER(lm_teacher)
@@ -66,6 +71,9 @@ _SIGS = {
     "attn_debug_inject": ([_I32, ctypes.c_uint64], _I32),
     "attn_fwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
     "attn_bwd": ([_I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _P, _P, _P, _AP, _P, _P, _P, _P, _SZ, _P], _I32),
+    "cross_workspace_size": ([_I64, _I64, _I32, _I32, _I32, _SZP], _I32),
+    "cross_fwd": ([_I64, _I64, _I32, _I32, _I32, _HP, _HP, _HP, _CP, _P, _P, _P, _P, _SZ, _P], _I32),
+    "cross_bwd": ([_I64, _I64, _I32, _I32, _I32, _HP, _HP, _HP, _HP, _P, _P, _P, _CP, _P, _P, _P, _P, _SZ, _P], _I32),
     "addnorm_workspace_size": ([_I64, _I64, _SZP], _I32),
     "addnorm_fwd": ([_I64, _I64, _P, _P, _NP, _P, _P, _P, _P, _P], _I32),
     "addnorm_bwd": ([_I64, _I64, _P, _P, _P, _P, _P, _P, _NP, _P, _P, _P, _P, _P, _P, _SZ, _P], _I32),
@@ -601,3 +609,73 @@ def distill_bwd(logits, teacher: Teacher, fwd: dict, dkl=None, targets=None, dlo
     _call("distill_bwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, _shaped(fwd["saved"], (T, 8), f32, "saved"),
           _shaped(dkl, (T,), f32, "dkl"), _shaped(dlogp, (T,), f32, "dlogp"), po, ldo, _stream())
     return {"dlogits": dlogits}
+
+
+# ---------------------------------------------------------------------------------------------
+# attention to the states of another length
+
+
+@dataclass
+class Cross:
+    """What one cross-attention call computes (lm_cross): scores scale * q.k, capped by cap * tanh(. / cap) when cap > 0.
+    Without cu_q every query sees every key; with it document m's queries [cu_q[m], cu_q[m + 1]) see the first
+    k_len[m] (None: all) of its keys [cu_k[m], cu_k[m + 1]) (int32: n + 1 offsets each, n lengths)."""
+    scale: float
+    cap: float = 0.0
+    cu_q: Optional[torch.Tensor] = None
+    cu_k: Optional[torch.Tensor] = None
+    k_len: Optional[torch.Tensor] = None
+
+    def c_struct(self) -> lm_cross:
+        if self.cu_q is None and self.cu_k is None and self.k_len is None:
+            return lm_cross(self.scale, self.cap, 0, 0, 0, 0, 0)
+        if self.cu_q is None or self.cu_k is None:
+            raise ValueError("cu_q and cu_k belong together, and k_len to them")
+        _here(self.cu_q, self.cu_k, self.k_len)
+        n = self.cu_q.numel() - 1
+        return lm_cross(self.scale, self.cap, _shaped(self.cu_q, (n + 1,), torch.int32, "cu_q"),
+                        _shaped(self.cu_k, (n + 1,), torch.int32, "cu_k"), _shaped(self.k_len, (n,), torch.int32, "k_len"), n, 0)
+
+
+def cross_workspace_size(Tq: int, Tk: int, hq: int, hk: int, d: int) -> int:
+    return _size("cross_workspace_size", Tq, Tk, hq, hk, d)
+
+
+def cross_fwd(q, k, v, a: Cross, train: bool = True, O=None, lse=None, O_lo=None, ws=None, stream=None) -> dict:
+    """q (Tq, hq, d), k and v (Tk, hk, d) -> O (Tq, hq, d), lse (hq, Tq) and, with ``train``, O_lo (as attn_fwd's)."""
+    if stream is not None:
+        with _on(stream):
+            return cross_fwd(q, k, v, a, train, O, lse, O_lo, ws)
+    (Tq, hq, d), (Tk, hk) = q.shape, k.shape[:2]
+    dev = q.device
+    _here(q, k, v, ws)
+    hs = _heads(q, Tq, hq, d, "q"), _heads(k, Tk, hk, d, "k"), _heads(v, Tk, hk, d, "v")
+    O, pO = _out(O, (Tq, hq, d), torch.bfloat16, dev, "O")
+    lse, pl = _out(lse, (hq, Tq), torch.float32, dev, "lse")
+    plo = 0
+    if train or O_lo is not None:
+        O_lo, plo = _out(O_lo, (Tq, hq, _d16(d)), torch.int8, dev, "O_lo")
+    if ws is None:
+        ws = torch.empty(cross_workspace_size(Tq, Tk, hq, hk, d), dtype=torch.uint8, device=dev)
+        ws[:256].zero_()  # (the error word; the parts' sums may be megabytes)
+    _call("cross_fwd", Tq, Tk, hq, hk, d, *hs, a.c_struct(), pO, plo, pl, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
+
+
+def cross_bwd(q, k, v, dO, fwd: dict, a: Cross, dQ=None, dK=None, dV=None, ws=None, stream=None) -> dict:
+    """The gradients of q, k and v from dO (Tq, hq, d) and the forward's result."""
+    if stream is not None:
+        with _on(stream):
+            return cross_bwd(q, k, v, dO, fwd, a, dQ, dK, dV, ws)
+    (Tq, hq, d), (Tk, hk) = q.shape, k.shape[:2]
+    dev, bf = q.device, torch.bfloat16
+    ws = fwd["ws"] if ws is None else ws
+    _here(q, k, v, dO, ws)
+    hs = _heads(q, Tq, hq, d, "q"), _heads(k, Tk, hk, d, "k"), _heads(v, Tk, hk, d, "v"), _heads(dO, Tq, hq, d, "dO")
+    dQ, pq = _out(dQ, (Tq, hq, d), bf, dev, "dQ")
+    dK, pk = _out(dK, (Tk, hk, d), bf, dev, "dK")
+    dV, pv = _out(dV, (Tk, hk, d), bf, dev, "dV")
+    _call("cross_bwd", Tq, Tk, hq, hk, d, *hs, _shaped(fwd["O"], (Tq, hq, d), bf, "O"),
+          _shaped(fwd["O_lo"], (Tq, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, Tq), torch.float32, "lse"),
+          a.c_struct(), pq, pk, pv, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    return {"dQ": dQ, "dK": dK, "dV": dV}

@@ -85,6 +85,40 @@ LM_API lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm
                           const float* lse, const lm_attn* a, uint16_t* dQ, uint16_t* dK, uint16_t* dV, void* ws,
                           size_t ws_bytes, lm_stream stream);
 
+/* ---- attention to the states of another length (an encoder's) ---------------------------------
+ * attn_fwd's formulas without slopes, q of Tq tokens and k, v of Tk:
+ *   u_ij = scale q_i . k_j, or cap tanh(scale q_i . k_j / cap)   O_i = sum_j P_ij v_j   P = softmax of u over what i sees
+ * cu_q == NULL: every query sees all Tk keys.  Else document m holds the queries [cu_q[m], cu_q[m + 1]) and the places of
+ * keys [cu_k[m], cu_k[m + 1]) (n_docs + 1 offsets each), of which the first k_len[m] are there (NULL: all; n_docs
+ * lengths; held to the document's places): its queries see those.  Other queries see nothing; other keys are
+ * seen by nothing.  As in attn_fwd a query that sees nothing has O = 0, lse = -inf and no part in any gradient, a key
+ * that nothing sees has gradient 0, and both may hold anything, NaN included; offsets must not decrease and are
+ * device values; with others results are unspecified, and no access leaves its buffer.  A value that is
+ * not finite among those that are seen can besides reach queries and keys of documents that share its 128 tokens.
+ * scale > 0.  Tq, Tk <= 2^20; q (Tq x hq x d), k and v (Tk x hk x d), strided as in attn_fwd, O, O_lo and lse as there.
+ * The backward writes dQ (Tq x hq x d), dK and dV (Tk x hk x d) bf16, contiguous.  Rounding as in attn_fwd and
+ * attn_bwd.  Few queries (one new token of each sequence) split the keys among CTAs, whose sums are joined in fp32.
+ * The workspace begins with the error word; one serves both calls, and calls that may overlap need one each.
+ * Kernel families in its reports, and attn_debug_inject, as for attn_fwd and attn_bwd. */
+typedef struct lm_cross {
+    float scale;
+    float cap;              /* as in lm_attn */
+    const int32_t* cu_q;    /* n_docs + 1 offsets (4-byte aligned), or NULL */
+    const int32_t* cu_k;    /* n_docs + 1 offsets; given with cu_q and only then */
+    const int32_t* k_len;   /* n_docs lengths, or NULL; needs cu_q */
+    int32_t n_docs;
+    int32_t reserved;
+} lm_cross;
+
+LM_API lm_status cross_workspace_size(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, size_t* bytes);
+LM_API lm_status cross_fwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, const lm_heads* q,
+                           const lm_heads* k, const lm_heads* v, const lm_cross* a, uint16_t* O, int8_t* O_lo,
+                           float* lse, void* ws, size_t ws_bytes, lm_stream stream);
+LM_API lm_status cross_bwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, const lm_heads* q,
+                           const lm_heads* k, const lm_heads* v, const lm_heads* dO, const uint16_t* O,
+                           const int8_t* O_lo, const float* lse, const lm_cross* a, uint16_t* dQ, uint16_t* dK,
+                           uint16_t* dV, void* ws, size_t ws_bytes, lm_stream stream);
+
 /* ---- residual add with the norms before and after a block ----------------------------------
  *   N(a; w) = a * rsqrt(mean(a^2) + eps) * (w + w_offset)     (over a row's d values)
  *   h_out = h + alpha * gate * N(y; w_post)      x = N(h_out; w_in)

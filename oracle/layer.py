@@ -21,12 +21,24 @@ def visible(T, causal=True, window=0, cu_docs=None, prefix=None) -> np.ndarray:
     return see
 
 
+def cross_visible(Tq, Tk, cu_q=None, cu_k=None, k_len=None) -> np.ndarray:
+    """(Tq, Tk) truth values for attn_forward and attn_backward with keys of another tensor."""
+    if cu_q is None:
+        return np.ones((Tq, Tk), dtype=bool)
+    see = np.zeros((Tq, Tk), dtype=bool)
+    for m in range(len(cu_q) - 1):
+        n = cu_k[m + 1] - cu_k[m] if k_len is None else min(k_len[m], cu_k[m + 1] - cu_k[m])
+        see[cu_q[m]:cu_q[m + 1], cu_k[m]:cu_k[m] + n] = True
+    return see
+
+
 def _scores(q, k, see, scale, cap, slope):
     z = scale * (q @ k.T)
     t = np.tanh(z / cap) if cap else None
     s = cap * t if cap else z
-    n = np.arange(q.shape[0], dtype=np.float64)
-    s = s - slope * np.abs(n[:, None] - n[None, :])
+    if slope:  # (of a token from another of the same tensor)
+        n = np.arange(q.shape[0], dtype=np.float64)
+        s = s - slope * np.abs(n[:, None] - n[None, :])
     bend = 1.0 - t * t if cap else np.ones_like(z)
     s = np.where(see, s, -np.inf)
     m = s.max(axis=1, keepdims=True, initial=-np.inf)
