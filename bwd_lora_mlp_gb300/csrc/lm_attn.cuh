@@ -263,6 +263,21 @@ __device__ __forceinline__ void clear_unseen(uint8_t* tile, int boxes, const uin
         }
     fence_proxy_async_smem();
 }
+// By a whole warp, a row a lane.
+__device__ __forceinline__ void clear_unseen_warp(uint8_t* tile, int boxes, const uint4& seen) {
+    if ((seen.x & seen.y & seen.z & seen.w) == ~0u) return;
+    const uint32_t w[4] = {seen.x, seen.y, seen.z, seen.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (!(w[q] >> (threadIdx.x & 31) & 1u)) {
+            uint8_t* row = tile + (q * 32 + (threadIdx.x & 31)) * 128;
+            for (int b = 0; b < boxes; ++b)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)  // (lanes apart in the banks)
+                    *reinterpret_cast<uint4*>(row + b * kBoxBytes + ((c ^ (threadIdx.x & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+        }
+    fence_proxy_async_smem();
+}
 // Rows past the last token come as zeros, so the tokens that need no clearing end with the last tile.  (4097 causal
 // tokens, 32 heads on 8 of 128 dims, a step: 502 us; 607 with those rows cleared too.)
 __device__ __forceinline__ void inside_tokens(const AttnParams& p, int& in0, int& in1) {

@@ -46,11 +46,14 @@ constexpr int kFewKeys = 512;
 constexpr int kFwdThreads = 640, kFwdMath = 16, kFwdMathRegs = 104, kFwdIssueRegs = 64;
 static_assert(4 * kFwdMathRegs + kFwdIssueRegs <= 5 * 96, "a register split above the launch's total waits forever");
 
-template <int DP>
+// (few queries: one query tile, and the list of the key tiles that a CTA takes)
+constexpr int kFewTiles = 4096 + 64;
+template <int DP, int FORM>
 struct FwdCfg {
     static constexpr uint32_t kTileBytes = (DP / 64) * kBoxBytes;
-    static constexpr int kSlots = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 3 * 1024 + (2 + kSlots) * kTileBytes;
+    static constexpr int kSlots = DP == 128 ? 5 : 8, kQTiles = FORM == ATTN_FEW ? 1 : 2;
+    static constexpr int kHead = FORM == ATTN_FEW ? (2048 + kFewTiles * 2 + 1023) / 1024 * 1024 : 2048;
+    static constexpr int kSmem = 1024 + kHead + (kQTiles + kSlots) * kTileBytes;
 };
 
 struct FwdMaps {
@@ -77,8 +80,8 @@ __device__ __forceinline__ TileSpan key_tiles(const AttnParams& p, int q0, int t
 }
 // Item k of this CTA: the heavier items first (under a causal mask the last queries see the most keys),
 // dealt out forwards and backwards in turn, so that every CTA gets about the same work.
-// In the form for few queries an item is one tile of queries of all heads of a group, and one of `splits` parts
-// of the keys that it sees; h is its key/value head.
+// In the form for few queries an item is one tile of queries of all heads of a group, and one of `splits` shares
+// of the key tiles that it sees; h is its key/value head.
 struct Item {
     int h, q0, part;
     TileSpan span[2];
@@ -91,22 +94,14 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int k) {
     const int idx = k & 1 ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
     Item it;
     it.part = 0;
-    if constexpr (FORM == ATTN_FEW) {
-        it.valid = idx < nqb * p.hk * p.splits;
-        it.h = idx % p.hk;
-        it.part = idx / p.hk % p.splits;
-        it.q0 = idx / p.hk / p.splits * p.rows;
-        it.span[0] = it.span[1] = TileSpan{0, 0, 0, 0};
-        it.J0 = it.J1 = 0;
-        if (it.valid) {
-            TileSpan& sp = it.span[0];
-            sp = key_tiles<FORM>(p, it.q0, p.rows);
-            const int n = sp.j1 - sp.j0;  // (at most 2^13 tiles, 152 parts)
-            sp.j1 = sp.j0 + n * (it.part + 1) / p.splits;
-            sp.j0 += n * it.part / p.splits;
-            it.J0 = sp.j0;
-            it.J1 = sp.j1;
-        }
+    if constexpr (FORM == ATTN_FEW) {  // (one a CTA)
+        it.valid = k == 0;
+        it.h = (int)blockIdx.x % p.hk;
+        it.part = (int)blockIdx.x / p.hk % p.splits;
+        it.q0 = (int)blockIdx.x / p.hk / p.splits * p.rows;
+        it.span[0] = it.span[1] = it.valid ? key_tiles<FORM>(p, it.q0, p.rows) : TileSpan{0, 0, 0, 0};
+        it.J0 = it.span[0].j0;
+        it.J1 = it.span[0].j1;
         return it;
     }
     it.valid = idx < nqb * p.hq;
@@ -125,14 +120,63 @@ __device__ __forceinline__ Item item_of(const AttnParams& p, int k) {
 }
 template <int FORM>
 __device__ __forceinline__ int rounds_of(const AttnParams& p) {
-    const int n = (p.T + p.rows - 1) / p.rows * (FORM == ATTN_FEW ? p.hk * p.splits : p.hq);
+    if (FORM == ATTN_FEW) return 1;
+    const int n = (p.T + p.rows - 1) / p.rows * p.hq;
     return (n + (int)gridDim.x - 1) / (int)gridDim.x;
+}
+
+// The CTA's share of the key tiles that its queries see, as a list: tiles that nobody sees are left out of it (padded
+// states), and the shares are of those that are left.  All threads come here; red: 64 ints of shared memory.
+__device__ __forceinline__ void few_setup(const AttnParams& p, uint16_t* list, int* red, int& tiles, bool& few_rows) {
+    constexpr int kWarps = kFwdThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = p.hq / p.hk;
+    const Item it = item_of<ATTN_FEW>(p, 0);
+    bool few = false;
+    if ((int)threadIdx.x < p.rows && it.q0 + (int)threadIdx.x < p.T) {
+        const TokRange r = query_range<ATTN_FEW>(p, it.q0 + (int)threadIdx.x);
+        few = r.hi > r.lo && r.hi - r.lo < kFewKeys;
+    }
+    few_rows = __syncthreads_or(few);
+    const int n = max(it.J1 - it.J0, 0);
+    auto share = [&](int total, int part) { return (int)((int64_t)total * part / p.splits); };
+    if (!p.kseen) {
+        const int a = share(n, it.part);
+        tiles = share(n, it.part + 1) - a;
+        for (int i = threadIdx.x; i < tiles; i += kFwdThreads) list[i] = (uint16_t)(it.J0 + a + i);
+        __syncthreads();
+        return;
+    }
+    const int len = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, j0 = min(n, warp * len), j1 = min(n, j0 + len);
+    auto seen = [&](int i) {
+        if (i >= j1) return false;
+        const uint4 b = p.kseen[it.J0 + i];
+        return (b.x | b.y | b.z | b.w) != 0u;
+    };
+    int mine = 0;
+    for (int i = j0; i < j1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, seen(i + lane)));
+    if (lane == 0) red[warp] = mine;
+    __syncthreads();
+    int total = 0, at = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) at += red[w];
+        total += red[w];
+    }
+    const int a = share(total, it.part), z = share(total, it.part + 1);
+    for (int i = j0; i < j1; i += 32) {
+        const bool on = seen(i + lane);
+        const uint32_t votes = __ballot_sync(0xffffffffu, on);
+        const int r = at + __popc(votes & ((1u << lane) - 1u));
+        if (on && r >= a && r < z) list[r - a] = (uint16_t)(it.J0 + i + lane);
+        at += __popc(votes);
+    }
+    tiles = z - a;
+    __syncthreads();
 }
 
 template <int DP, int MODE, int FORM>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwdMaps maps) {
-    using C = FwdCfg<DP>;
+    using C = FwdCfg<DP, FORM>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
@@ -147,9 +191,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint4* s_seen = reinterpret_cast<uint4*>(smem + 768);   // [slot] the tile's keys that somebody sees (not SELF)
+    uint64_t* clean = reinterpret_cast<uint64_t*>(smem + 896);  // [slot] and the others have been cleared
+    uint16_t* s_tiles = reinterpret_cast<uint16_t*>(smem + 2048);  // (few queries) this CTA's key tiles
     float* s_inv = reinterpret_cast<float*>(smem + 1024);  // [2][128] 1 / l
-    uint8_t* sq = smem + 2048;
-    uint8_t* ring = sq + 2 * C::kTileBytes;
+    uint8_t* sq = smem + C::kHead;
+    uint8_t* ring = sq + C::kQTiles * C::kTileBytes;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     griddep_launch_dependents();
@@ -157,6 +203,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
+            if (FORM != ATTN_SELF) mbar_init(smem_u32(&clean[s]), 1);
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(smem_u32(&qfull[w]), 1);
@@ -185,6 +232,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const int rounds = rounds_of<FORM>(p), group = p.hq / p.hk;
+    // few queries: this CTA's key tiles, of those that the query tile sees its share, and whether a row sees few keys
+    int tiles = 0;
+    bool few_rows = false;
+    if constexpr (FORM == ATTN_FEW) few_setup(p, s_tiles, reinterpret_cast<int*>(s_inv), tiles, few_rows);
 
     if (warp >= kFwdMath) {
         regs_down<kFwdIssueRegs>();
@@ -192,10 +243,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) {
                 bool ok = true;
                 uint32_t n = 0, nq[2] = {0, 0};  // tiles and queries asked for
+                auto pair_of = [&](const Item& it, int j, auto between) {  // K_j, then V_j
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
+                        if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) return false;
+                        if (FORM != ATTN_SELF && kv && p.kseen) s_seen[s] = p.kseen[j];
+                        mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
+                                        smem_u32(&full[s]), b * 64, FORM == ATTN_FEW ? it.h : it.h / group, j * kTile);
+                        ++n;
+                        if (kv == 0 && !between()) return false;
+                    }
+                    return true;
+                };
                 for (int k = p.starve & K_ATTN_FWD ? rounds : 0; ok && k < rounds; ++k) {
                     const Item it = item_of<FORM>(p, k);
                     auto query = [&](int w) {
-                        if (!it.span[w].any()) return true;
+                        if (FORM == ATTN_FEW ? tiles == 0 : !it.span[w].any()) return true;
                         if (!mbar_wait(smem_u32(&qempty[w]), (nq[w] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;
                         const uint32_t bar = smem_u32(&qfull[w]);
                         // (few queries: a box of all heads of the group, rows of a token next to each other)
@@ -207,24 +272,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         return true;
                     };
                     ok = query(0);  // then K, then the other queries: the first scores wait for what they need
-                    for (int j = it.J0; ok && j < it.J1; ++j)
-                        for (int kv = 0; kv < 2; ++kv) {
-                            const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
-                            if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) {
-                                ok = false;
-                                break;
-                            }
-                            if (FORM != ATTN_SELF && kv && p.kseen) s_seen[s] = p.kseen[j];
-                            mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
-                            for (int b = 0; b < DP / 64; ++b)
-                                tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
-                                            smem_u32(&full[s]), b * 64, FORM == ATTN_FEW ? it.h : it.h / group, j * kTile);
-                            ++n;
-                            if (j == it.J0 && kv == 0 && !query(1)) {
-                                ok = false;
-                                break;
-                            }
-                        }
+                    if constexpr (FORM == ATTN_FEW) {
+                        for (int i = 0; ok && i < tiles; ++i) ok = pair_of(it, s_tiles[i], [] { return true; });
+                    } else {
+                        for (int j = it.J0; ok && j < it.J1; ++j)
+                            ok = pair_of(it, j, [&] { return j != it.J0 || query(1); });
+                    }
                 }
                 if (!ok) {
                     attn_error(p, 5, 1);
@@ -245,8 +298,55 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (FORM == ATTN_SELF) inside_tokens(p, in0, in1);
             bool ok = true;
             uint32_t n = 0, nt[2] = {0, 0}, nq[2] = {0, 0};  // ring position of K_{J0}; tiles, items of each query tile
+            // V's rows that nobody sees are zeros
+            auto values = [&](uint32_t nv) {
+                uint64_t* bar = FORM != ATTN_SELF && p.kseen ? clean : full;
+                return mbar_wait(smem_u32(&bar[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+            };
+            if constexpr (FORM == ATTN_FEW) {
+                // O_w (+)= P_w V, V at ring position nv; last: of this accumulator
+                auto weighted = [&](int w, uint32_t nv, uint32_t parity, bool first, bool both, bool last) {
+                    const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
+                    const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!mbar_wait(smem_u32(&pfull[2 * w + half]), parity, s_abort, p.wait_ns)) return false;
+                        tc_fence_after();
+                        const uint32_t a = ts + half * 32;
+                        const uint32_t b = desc_cols(sv) + half * 512;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, first && !half && !kk ? 0u : 1u);
+                        if (both) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
+                        }
+                        if (half && last) umma_commit(smem_u32(&odone[w]));
+                    }
+                    return true;
+                };
+                // tile i is accumulator i & 1's: the next tile's scores are formed while this one's weights are
+                auto scores = [&](int i) {
+                    const uint32_t nk = 2 * (uint32_t)i, sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
+                    if (!mbar_wait(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns)) return false;
+                    tc_fence_after();
+                    mma_rows<DP>(tmem + (i & 1) * kTile, desc_rows(smem_u32(sq)), desc_rows(sk), ksteps, ids);
+                    umma_commit(smem_u32(&sfull[i & 1]));
+                    umma_commit(smem_u32(&empty[nk % C::kSlots]));
+                    return true;
+                };
+                if (tiles > 0) ok = mbar_wait(smem_u32(&qfull[0]), 0, s_abort, p.wait_ns) && scores(0);
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const uint32_t nv = 2 * (uint32_t)i + 1;
+                    ok = (i + 1 >= tiles || scores(i + 1)) && values(nv);
+                    if (!ok) break;
+                    tc_fence_after();
+                    ok = weighted(i & 1, nv, (uint32_t)(i >> 1) & 1u, i < 2, few_rows, i + 2 >= tiles);
+                    if (ok) umma_commit(smem_u32(&empty[nv % C::kSlots]));
+                }
+            }
             Item next = item_of<FORM>(p, 0);
-            for (int k = 0; ok && k < rounds; ++k) {
+            for (int k = 0; FORM != ATTN_FEW && ok && k < rounds; ++k) {
                 const Item it = next;
                 next = item_of<FORM>(p, k + 1);
                 if (it.J1 <= it.J0) continue;
@@ -255,12 +355,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const uint32_t sk = smem_u32(ring + (nk % C::kSlots) * C::kTileBytes);
                     const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
                     if (j > it.J0) {
-                        ok = mbar_wait(smem_u32(&full[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
+                        ok = values(nv);
                         if (!ok) break;
                         if (FORM == ATTN_SELF)
                             clear_padding(ring + (nv % C::kSlots) * C::kTileBytes, DP / 64, (j - 1) * kTile, in0, in1);
-                        else if (p.kseen)
-                            clear_unseen(ring + (nv % C::kSlots) * C::kTileBytes, DP / 64, s_seen[nv % C::kSlots]);
                     }
                     if (j < it.J1) {
                         ok = mbar_wait(smem_u32(&full[nk % C::kSlots]), (nk / C::kSlots) & 1u, s_abort, p.wait_ns);
@@ -319,6 +417,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
         }
+        if (FORM != ATTN_SELF && warp == kFwdMath + 2 && p.kseen) {  // ---------------- clears values that nobody sees
+            bool ok = true;
+            uint32_t n = 0;
+            auto pair_of = [&] {
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const uint32_t s = n % C::kSlots;
+                    if (!mbar_wait_warp(smem_u32(&full[s]), (n / C::kSlots) & 1u, s_abort, p.wait_ns)) return false;
+                    if (kv) clear_unseen_warp(ring + s * C::kTileBytes, DP / 64, s_seen[s]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&clean[s]));
+                }
+                return true;
+            };
+            if constexpr (FORM == ATTN_FEW) {
+                for (int i = 0; ok && i < tiles; ++i) ok = pair_of();
+            } else {
+                for (int k = 0; ok && k < rounds; ++k) {
+                    const Item it = item_of<FORM>(p, k);
+                    for (int j = it.J0; ok && j < it.J1; ++j) ok = pair_of();
+                }
+            }
+            if (!ok && lane == 0) {
+                attn_error(p, 5, 4);
+                *s_abort = 1;
+            }
+        }
     } else {  // ---------------- softmax: 16 query rows a warp, two of them (and a quarter of each) a thread
         regs_up<kFwdMathRegs>();
         const int w = warp >> 3, quarter = warp & 3, sub = (warp >> 2) & 1;
@@ -336,11 +460,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int k = 0; ok && k < rounds; ++k) {
             const Item it = next;
             next = item_of<FORM>(p, k + 1);
-            if (!it.valid || (FORM == ATTN_FEW ? w : w * kTile >= p.rows)) continue;
+            if (!it.valid || (FORM != ATTN_FEW && w * kTile >= p.rows)) continue;
             const TileSpan sp = w ? it.span[1] : it.span[0];
             // token and head of a row of the tile (T for rows of no token)
             auto token_of = [&](int row) {
-                if (FORM != ATTN_FEW) return it.q0 + w * kTile + row;
+                if (FORM != ATTN_FEW) return it.q0 + w * kTile + row;  // (few: both accumulators are of the same queries)
                 return row < p.rows * group ? it.q0 + row / group : p.T;
             };
             auto head_of = [&](int row) { return FORM != ATTN_FEW ? it.h : it.h * group + row % group; };
@@ -357,9 +481,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // running maxima, this lane's sums of weights
             // one key tile; tiles with hidden keys have code of their own.  x[4 g + 2 r + e]: row r, key
             // 8 g + c0 + e of the tile
-            auto tile = [&](int j, auto hides, auto few) {
+            auto tile = [&](int j, bool begun, auto hides, auto few) {
                 constexpr bool HIDDEN = decltype(hides)::value, REST = decltype(few)::value;
                 const int k0 = j * kTile;
+                if (FORM == ATTN_FEW && HIDDEN) {  // none of the warp's rows sees any of these keys
+                    const int a = k0 - c0, z = a + kTile;
+                    if (!__any_sync(0xffffffffu, (lo[0] < z && hi[0] > a && lo[0] < hi[0]) || (lo[1] < z && hi[1] > a && lo[1] < hi[1]))) {
+                        const uint32_t none[16] = {};
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            tmem_st_pairs16(ts + half * 32, none);
+                            if (REST) tmem_st_pairs16(ts + 64 + half * 32, none);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&pfull[2 * w]));
+                            mbar_arrive(smem_u32(&pfull[2 * w + 1]));
+                        }
+                        return;
+                    }
+                }
                 float x[64];
                 tmem_ld_frag32<0>(ts, x);
                 tmem_ld_frag32<32>(ts + 64, x);
@@ -422,7 +565,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     }
                     // the earlier tiles are in O since these scores are there: products end in the order they
                     // are issued
-                    if (j > sp.j0) {
+                    if (begun) {
 #pragma unroll 1
                         for (int cc = 0; cc < DP; cc += 32) {
                             float o[16];
@@ -461,18 +604,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 l[0] += s2[0].x + s2[0].y;
                 l[1] += s2[1].x + s2[1].y;
             };
-            for (int j = sp.j0; j < sp.j1; ++j, ++nt) {
-                ok = mbar_wait_warp(smem_u32(&sfull[w]), nt & 1u, s_abort, p.wait_ns);
-                if (!ok) break;
+            auto step = [&](int j, bool begun, bool few) {
+                if (!mbar_wait_warp(smem_u32(&sfull[w]), nt & 1u, s_abort, p.wait_ns)) return false;
                 tc_fence_after();
-                if (sp.few_keys<MODE>()) {
-                    if (sp.hides(j)) tile(j, std::true_type{}, std::true_type{});
-                    else tile(j, std::false_type{}, std::true_type{});
+                if (few) {
+                    if (sp.hides(j)) tile(j, begun, std::true_type{}, std::true_type{});
+                    else tile(j, begun, std::false_type{}, std::true_type{});
                 } else if constexpr (!biased(MODE)) {
-                    if (sp.hides(j)) tile(j, std::true_type{}, std::false_type{});
-                    else tile(j, std::false_type{}, std::false_type{});
+                    if (sp.hides(j)) tile(j, begun, std::true_type{}, std::false_type{});
+                    else tile(j, begun, std::false_type{}, std::false_type{});
                 }
+                return true;
+            };
+            if constexpr (FORM == ATTN_FEW) {
+                for (int i = w; ok && i < tiles; i += 2, ++nt) ok = step(s_tiles[i], i >= 2, few_rows);
+            } else {
+                for (int j = sp.j0; ok && j < sp.j1; ++j, ++nt) ok = step(j, j > sp.j0, sp.few_keys<MODE>());
             }
+            const bool any = FORM == ATTN_FEW ? w < tiles : sp.any();  // (uniform over the query tile's warps)
             if (!ok) break;
             // ---- the item's rows: sums over a row's four lanes, then 1 / l to the quarter's two warps
 #pragma unroll
@@ -484,9 +633,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int i = token_of(row0 + 8 * r), h = head_of(row0 + 8 * r);
                     s_inv[w * kTile + row0 + 8 * r] = l[r] == 0.f ? 0.f : 1.f / l[r];
                     if (i < p.T) {
-                        if (FORM == ATTN_FEW && p.splits > 1)
-                            p.part_ml[(int64_t)it.part * p.T * p.hq + (int64_t)i * p.hq + h] = make_float2(m[r], l[r]);
-                        else
+                        if (FORM == ATTN_FEW && p.parts > 1)
+                            p.part_ml[(int64_t)(2 * it.part + w) * p.T * p.hq + (int64_t)i * p.hq + h] = make_float2(m[r], l[r]);
+                        else if (FORM != ATTN_FEW || w == 0)
                             p.lse[(int64_t)h * p.T + i] =
                                 l[r] == 0.f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2 + (capped(MODE) ? p.cap : 0.f);
                     }
@@ -501,7 +650,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float inv = s_inv[w * kTile + row];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&lready[4 * w + quarter]));
-            if (sp.any()) {
+            if (any) {
                 ok = mbar_wait_warp(smem_u32(&odone[w]), nq & 1u, s_abort, p.wait_ns);
                 if (!ok) break;
                 ++nq;
@@ -511,24 +660,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int64_t at = (int64_t)i * p.hq + h;
             uint16_t* out = p.out + at * p.d;
             int8_t* out_lo = p.out_lo ? p.out_lo + at * p.d16 : nullptr;
-            const bool partial = FORM == ATTN_FEW && p.splits > 1;
-            if (partial) {  // unnormalised, in fp32; a part that saw nothing has l = 0 and no row
-                float* dst = p.part_o + ((int64_t)it.part * p.T * p.hq + at) * p.d;
+            const bool partial = FORM == ATTN_FEW && (p.parts > 1 || w);
+            if (FORM == ATTN_FEW && p.parts > 1 && any) {  // unnormalised, in fp32; rows that saw nothing have l = 0 and are not read
+                float* dst = p.part_o + ((int64_t)(2 * it.part + w) * p.T * p.hq + at) * p.d;
+                const bool mine = i < p.T && inv != 0.f;
+                if (__any_sync(0xffffffffu, mine))
 #pragma unroll 1
-                for (int cc = sub * (DP / 2); cc < (sub + 1) * (DP / 2) && sp.any(); cc += 16) {
-                    uint32_t raw[16];
-                    tmem_ld_x16(tmem + all_lanes + 2 * kTile + w * DP + cc, raw);
-                    tmem_ld_wait16(raw);
+                    for (int cc = sub * (DP / 2); cc < (sub + 1) * (DP / 2); cc += 16) {
+                        uint32_t raw[16];
+                        tmem_ld_x16(tmem + all_lanes + 2 * kTile + w * DP + cc, raw);
+                        tmem_ld_wait16(raw);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        if (i < p.T && cc + e < p.d)
-                            *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
-                }
+                        for (int e = 0; e < 16; e += 4)
+                            if (mine && cc + e < p.d)
+                                *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+                    }
             }
 #pragma unroll 1
             for (int cc = sub * (DP / 2); cc < (sub + 1) * (DP / 2) && !partial; cc += 16) {
                 float o[16];
-                if (sp.any()) {  // (uniform over the query tile's warps)
+                if (any) {
                     uint32_t raw[16];
                     tmem_ld_x16(tmem + all_lanes + 2 * kTile + w * DP + cc, raw);
                     tmem_ld_wait16(raw);
@@ -580,11 +731,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <int DP, int MODE, int FORM>
 cudaError_t launch_fwd(const AttnParams& p, const FwdMaps& maps, int sms, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<DP, MODE, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               FwdCfg<DP>::kSmem);
+                                               FwdCfg<DP, FORM>::kSmem);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)((p.T + p.rows - 1) / p.rows) * (FORM == ATTN_FEW ? p.hk * p.splits : p.hq);
-    const unsigned grid = (unsigned)(items < sms ? items : sms);
-    return launch_pdl(attn_fwd_kernel<DP, MODE, FORM>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP>::kSmem, st, nullptr, 0, p, maps);
+    const unsigned grid = (unsigned)(items < sms || FORM == ATTN_FEW ? items : sms);
+    return launch_pdl(attn_fwd_kernel<DP, MODE, FORM>, dim3(grid), dim3(kFwdThreads), FwdCfg<DP, FORM>::kSmem, st, nullptr, 0, p, maps);
 }
 
 }  // namespace lm

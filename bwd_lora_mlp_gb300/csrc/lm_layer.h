@@ -56,7 +56,7 @@ struct AttnParams {
     // cross attention; null: every query sees every key.  By token, and by tile the rows that see or are seen at all
     const int2 *qrange, *krange;
     const uint4 *qseen, *kseen;
-    int32_t splits;             // few queries: parts of the keys; their sums, T x hq rows each
+    int32_t splits, parts;      // few queries: CTAs that share the keys; parts that are joined, T x hq rows each
     float* part_o;
     float2* part_ml;
     uint16_t* out;         // O, or dQ
@@ -80,8 +80,12 @@ struct CrossTables {
     uint4 *qseen, *kseen;
 };
 cudaError_t launch_cross_ranges(const lm_cross& a, int64_t Tq, int64_t Tk, const CrossTables& t, cudaStream_t st);
-// parts of the keys, and tokens of a query tile, of the form for few queries; splits 0: the other form
-void plan_few(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t* splits, int32_t* tokens);
+// the form for few queries: CTAs that share the keys of a query tile, the parts that they leave (1: the result itself)
+// and the tile's tokens; splits 0: the other form
+struct FewPlan {
+    int32_t splits, parts, tokens;
+};
+FewPlan plan_few(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk);
 cudaError_t launch_fill(float* out, int64_t n, float v, cudaStream_t st);
 lm_status launch_cross_fwd(const AttnParams& p, int sms, cudaStream_t st);
 lm_status launch_cross_bwd(const AttnParams& p, int sms, cudaStream_t st);

@@ -276,20 +276,20 @@ lm_status check_cross(const lm_cross* a) {
 }
 
 struct CrossPlan {
-    int32_t splits, tokens;
+    FewPlan few;
     size_t qrange, krange, qseen, kseen, delta, nlse, part_ml, part_o, total;
 };
 
 CrossPlan plan_cross(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d) {
     CrossPlan P;
-    plan_few(Tq, Tk, hq, hk, &P.splits, &P.tokens);
+    P.few = plan_few(Tq, Tk, hq, hk);
     size_t at = 256;  // after the error word
     auto take = [&at](size_t bytes) {
         const size_t here = at;
         at = (at + bytes + 255) & ~size_t(255);
         return here;
     };
-    const size_t rows = (size_t)Tq * hq * (P.splits > 1 ? P.splits : 0);
+    const size_t rows = (size_t)Tq * hq * (P.few.parts > 1 ? P.few.parts : 0);
     P.qrange = take((size_t)Tq * sizeof(int2));
     P.krange = take((size_t)Tk * sizeof(int2));
     P.qseen = take((size_t)whole_tiles(Tq) / 8);
@@ -361,8 +361,9 @@ extern "C" lm_status cross_fwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, i
     p.out = O;
     p.out_lo = O_lo;
     p.lse = lse;
-    p.splits = P.splits;
-    p.rows = P.tokens;
+    p.splits = P.few.splits;
+    p.parts = P.few.parts;
+    p.rows = P.few.tokens;
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + P.part_ml);
     p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + P.part_o);
     LaunchTag tag("cross.fwd", st);
