@@ -5,11 +5,16 @@
 //                 q_r = sum of q outside S,  W = sum p + p_r                dx_j = q_j (W - p_r / q_r) elsewhere
 // Forward: one pass over the logits.  With rest, the running maximum and sum leave the tokens of S out, so that q_r
 // comes from its own terms and not from what 1 - sum q leaves: each vector has a byte in shared memory that says
-// which of its logits are in S.  The K entries' own terms are summed before the pass, while its first loads
-// are under way; at the end one thread joins scalars.  The sum at scale 1 for the tokens' own log probabilities
-// takes a second exponential only where scale is not 1.
+// which of its logits are in S.  What the K entries add is asked for before the pass and summed after it; one
+// thread joins the scalars.  The sum at scale 1 for the tokens' own log probabilities takes a second exponential
+// only where scale is not 1.  Bound by memory in long rows: 4096 x 131072 with rest and tokens 181 us, 5.9 TB/s (0.87 of the
+// copy rate); 8192 x 32000 with two exponentials 97 us, 5.4 TB/s; 1000 x 50257 with rest 27 us: six or seven rows an SM, whose
+// beginnings and ends show.  (The second exponential by arithmetic, a polynomial of degree 5, instead of the exponential
+// unit: 8192 x 32000 167 us instead of 123, for a quarter of the elements 131; rows asked for further ahead in L2: 185 to
+// 192 us at 4096 x 131072.)
 // Backward: one pass; outside S, dx_j = (W q_r - p_r) e^{x_j} / sum of e^x outside S, a share of at most 1, which no size
 // of logits overflows.  The entries in a CTA's stretch are read before it is written and written after it.
+// 4096 x 131072 387 us, 5.5 TB/s; 8192 x 32000 198 us, 5.3; 1000 x 50257 33 us, 6.1.
 #include <algorithm>
 
 #include "lm_rows.cuh"
@@ -76,8 +81,8 @@ struct DistillShared {
     Part warp[kThreads / 32], seg[kMaxCluster];
 };
 
-template <bool F32, bool REST, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(const __grid_constant__ DistillParams p, int cluster) {
+template <bool F32, bool REST, bool TWO, int N>
+__global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_constant__ DistillParams p, int cluster) {
     __shared__ DistillShared sm;
     __shared__ uint4 marks4[REST ? kMarks / 16 : 1];
     uint8_t* marks = reinterpret_cast<uint8_t*>(marks4);
@@ -91,10 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(
     const Row<F32> row{static_cast<const char*>(p.logits) + t * p.ld * (F32 ? 4 : 2)};
     const int64_t len = ((p.V + cluster - 1) / cluster + 63) / 64 * 64;  // segments of whole 64-element stretches
     const int64_t j0 = min(p.V, part * len), j1 = min(p.V, j0 + len);
-    const int64_t a = min(j1, j0 + row.head(j0)), nv = (j1 - a) / W;
     const float c = p.scale * kL2e;
+    constexpr int U = 4;
+    Scan<U, F32, N> pass(row, j0, j1);  // (its first loads are under way)
+    const int64_t a = pass.a;
+    const int nv = pass.nv;
 
-    // ---- the entries
+    // ---- the entries: asked for here, and (but for their marks) looked at after the pass
     int id = -1;
     float y = -INFINITY, x = -INFINITY;
     if (tid < p.K) {
@@ -104,57 +112,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(
             x = row.at(id);
         }
     }
-    if (tid < kMaxEntries) sm.ids[tid] = id;
     const int64_t target = tid == 0 && part == 0 ? hard_target(p, t) : -1;
     const float zt = target >= 0 ? row.at(target) : 0.f;
-    if (REST)
-        for (int i = tid; i < min((int64_t)kMarks, nv + 15) / 16; i += kThreads) marks4[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (REST && id >= a && id < a + nv * W) {
-        const int64_t v = (id - a) / W;
-        const int i = (int)(v & (kMarks - 1));
-        atomicOr(reinterpret_cast<uint32_t*>(marks4) + i / 4, 1u << (i % 4 * 8 + (int)(id - a - v * W)));
-    }
-    bool any = false;
-    float ytop = -INFINITY, xtop = -INFINITY;
-    if (part == 0) {
-        if (warp < kEntryWarps) {
-            float yt = y, xt = x;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                yt = max_nan(yt, __shfl_xor_sync(0xffffffffu, yt, o));
-                xt = max_nan(xt, __shfl_xor_sync(0xffffffffu, xt, o));
-            }
-            if (lane == 0) sm.red[warp][0] = yt, sm.red[warp][1] = xt;
+    if (REST) {
+        if (tid < kMaxEntries) sm.ids[tid] = id;
+        for (int i = tid; i < min(kMarks, nv + 15) / 16; i += N) marks4[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        if (id >= a && id < a + (int64_t)nv * W) {
+            const int64_t v = (id - a) / W;
+            const int i = (int)(v & (kMarks - 1));
+            atomicOr(reinterpret_cast<uint32_t*>(marks4) + i / 4, 1u << (i % 4 * 8 + (int)(id - a - v * W)));
         }
-        any = __syncthreads_or(id >= 0);
-#pragma unroll
-        for (int w = 0; w < kEntryWarps; ++w) {
-            ytop = max_nan(ytop, sm.red[w][0]);
-            xtop = max_nan(xtop, sm.red[w][1]);
-        }
-        if (warp < kEntryWarps) {
-            // (weights of at most e^-5 < 1 / K: their sum with logits of the lowest value does not overflow)
-            const float yref = REST || ytop == -INFINITY ? 0.f : ytop + 5.f, xref = xtop == -INFINITY ? 0.f : xtop;
-            const float e = id >= 0 ? expf(y - yref) : 0.f, dx = (x - xref) * p.scale;
-            // sum e, sum e (log p - log q) up to what is the same for all, and (each token once) the entries' e^x
-            float v[4] = {e, e == 0.f ? 0.f : e * (y - yref - dx), 0.f, 0.f};
-            if (REST) {
-                bool first = id >= 0;
-                for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
-                if (first) {
-                    v[2] = brought(x, xref, c);
-                    v[3] = brought(x, xref, kL2e);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < (REST ? TWO ? 4 : 3 : 2); ++i) {
-#pragma unroll
-                for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-                if (lane == 0) sm.sums[warp][i] = v[i];
-            }
-        }
-    } else if (REST) {
         __syncthreads();
     }
 
@@ -173,15 +141,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(
         }
         return b;
     };
-    constexpr int U = 4;
-    scan<U>(row, j0, j1, [&](uint32_t (&w)[U][4], int64_t j, int) {
+    pass.run([&](uint32_t (&w)[U][4], int64_t j, int) {
         if (REST) {
             const int v = (int)((j - a) / W);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                uint32_t b = marks[(v + u * kThreads) & (kMarks - 1)];
+                uint32_t b = marks[(v + u * N) & (kMarks - 1)];
                 if (b) {
-                    if (nv > kMarks) b = entry_bits(j + (int64_t)u * kThreads * W);
+                    if (nv > kMarks) b = entry_bits(j + (int64_t)u * N * W);
 #pragma unroll
                     for (int e = 0; e < W; ++e)
                         if (b >> e & 1u) {
@@ -219,8 +186,45 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(
     if (s.m != s.m) s.S = s.S1 = s.m;
     s = join_parts<32, TWO>(s, c);
     if (lane == 0) sm.warp[warp] = s;
+    if (warp < kEntryWarps) {
+        float yt = y, xt = x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            yt = max_nan(yt, __shfl_xor_sync(0xffffffffu, yt, o));
+            xt = max_nan(xt, __shfl_xor_sync(0xffffffffu, xt, o));
+        }
+        if (lane == 0) sm.red[warp][0] = yt, sm.red[warp][1] = xt;
+    }
+    const bool any = __syncthreads_or(id >= 0);
+    s = join_parts<N / 32, TWO>(sm.warp[tid & (N / 32 - 1)], c);
+    float ytop = -INFINITY, xtop = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kEntryWarps; ++w) {
+        ytop = max_nan(ytop, sm.red[w][0]);
+        xtop = max_nan(xtop, sm.red[w][1]);
+    }
+    if (part == 0 && warp < kEntryWarps) {
+        // (weights of at most e^-5 < 1 / K: their sum with logits of the lowest value does not overflow)
+        const float yref = REST || ytop == -INFINITY ? 0.f : ytop + 5.f, xref = xtop == -INFINITY ? 0.f : xtop;
+        const float e = id >= 0 ? expf(y - yref) : 0.f, dx = (x - xref) * p.scale;
+        // sum e, sum e (log p - log q) up to what is the same for all, and (each token once) the entries' e^x
+        float v[4] = {e, e == 0.f ? 0.f : e * (y - yref - dx), 0.f, 0.f};
+        if (REST) {
+            bool first = id >= 0;
+            for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
+            if (first) {
+                v[2] = brought(x, xref, c);
+                v[3] = brought(x, xref, kL2e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < (REST ? TWO ? 4 : 3 : 2); ++i) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            if (lane == 0) sm.sums[warp][i] = v[i];
+        }
+    }
     __syncthreads();
-    s = join_parts<kThreads / 32, TWO>(sm.warp[tid & (kThreads / 32 - 1)], c);
     if (cluster > 1) {
         __syncwarp();
         cluster_wait();  // CTA 0 has started
@@ -284,15 +288,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) distill_fwd_kernel(
     out[1] = make_float4(o.ml2, o.coef, o.W, o.tl);
 }
 
-template <bool F32, bool REST, bool TWO>
-static cudaError_t fwd_launch(const DistillParams& p, cudaStream_t st) {
-    // as for the log probabilities: a row is shared by a cluster where there are fewer rows than places for CTAs
-    int c = 1;
-    while (c < kMaxCluster && p.T * c * 2 <= 152 * 1024 / kThreads && p.V / (c * 2) >= kThreads * 8) c *= 2;
+template <bool F32, bool REST, bool TWO, int N>
+static cudaError_t fwd_rows(const DistillParams& p, int c, cudaStream_t st) {
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeClusterDimension;
     a.val.clusterDim = {(unsigned)c, 1, 1};
-    return launch_pdl(distill_fwd_kernel<F32, REST, TWO>, dim3((unsigned)(p.T * c)), dim3(kThreads), 0, st, &a, 1, p, c);
+    return launch_pdl(distill_fwd_kernel<F32, REST, TWO, N>, dim3((unsigned)(p.T * c)), dim3(N), 0, st, &a, 1, p, c);
+}
+template <bool F32, bool REST, bool TWO>
+static cudaError_t fwd_launch(const DistillParams& p, cudaStream_t st) {
+    // As for the log probabilities: a row is shared by a cluster where there are fewer rows than places for CTAs.
+    int c = 1;
+    while (c < kMaxCluster && p.T * c * 2 <= 152 * 1024 / kThreads && p.V / (c * 2) >= kThreads * 8) c *= 2;
+    // A row of its own has half the threads: eight rows an SM instead of four, so that the beginning and end of a row, in
+    // which it reads little, are a smaller part of its time.  (8192 x 32000 97 us instead of 109, 1000 x 50257 27 instead of
+    // 31, 4096 x 131072 the same; a row of eight CTAs 5.2 us instead of 4.7.)
+    return c == 1 ? fwd_rows<F32, REST, TWO, kThreads / 2>(p, c, st) : fwd_rows<F32, REST, TWO, kThreads>(p, c, st);
 }
 template <bool F32>
 static cudaError_t fwd_forms(const DistillParams& p, cudaStream_t st) {

@@ -24,6 +24,8 @@ constexpr int kRopeSms = 152;  // GB300's: a workspace's size has to be known on
 // registers for one), steps on their way, CTAs an SM.  (Three or more steps, or three CTAs of fewer registers, are no
 // faster: 16384 tokens 154 us a step against 146.)
 constexpr int kFwdHeads = 2, kFwdStages = 2, kBwdStages = 2, kFwdCtas = 2, kBwdCtas = 2;
+static_assert(2 * kFwdHeads * kFwdStages * kRopeThreads * 16 + kRopeWarps * 1024 <= 48 * 1024 &&
+              4 * kBwdStages * kRopeThreads * 16 + kRopeWarps * 1024 <= 48 * 1024, "more shared memory has to be asked for");
 // Items a warp has at least, where tokens have parts enough (4097 tokens of 24 heads of 80: 28 us; with 16, 31).
 constexpr int kTurns = 4;
 
@@ -511,9 +513,8 @@ static void plan(QkRopeParams& p, int ctas, int heads_at_once) {
 
 template <typename K>
 static cudaError_t launch_pieces(K kernel, int pieces, const QkRopeParams& p, cudaStream_t st) {
-    const size_t smem = (size_t)pieces * kRopeThreads * p.vec * 2;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    return e == cudaSuccess ? launch_pdl(kernel, dim3((unsigned)(p.q.blocks + p.k.blocks)), dim3(kRopeThreads), smem, st, nullptr, 0, p) : e;
+    const size_t smem = (size_t)pieces * kRopeThreads * p.vec * 2;  // (at most 40 KB with the angles' 8: no attribute is needed)
+    return launch_pdl(kernel, dim3((unsigned)(p.q.blocks + p.k.blocks)), dim3(kRopeThreads), smem, st, nullptr, 0, p);
 }
 template <int VEC, bool NORM, bool INTER>
 static cudaError_t launch(const QkRopeParams& p, bool backward, cudaStream_t st) {

@@ -64,6 +64,47 @@ __device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1
     const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
     if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
 }
+// The same pass by a CTA of N threads, in two steps: the first batch's loads are under way from the beginning, run(f, one)
+// does the rest.
+template <int U, bool F32, int N>
+struct Scan {
+    static constexpr int W = Row<F32>::kVec;
+    const Row<F32>& row;
+    int64_t j0, j1, a;  // a: the first boundary
+    int nv;
+    const char* base;
+    uint4 next[U];
+    __device__ __forceinline__ Scan(const Row<F32>& row_, int64_t j0_, int64_t j1_) : row(row_), j0(j0_), j1(j1_) {
+        a = min(j1, j0 + row.head(j0));
+        nv = (int)((j1 - a) / W);
+        base = row.p + a * (F32 ? 4 : 2);
+        load(threadIdx.x);
+    }
+    __device__ __forceinline__ void load(int v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * N < nv) next[u] = *reinterpret_cast<const uint4*>(base + (int64_t)(v + u * N) * 16);
+    }
+    template <typename F, typename G>
+    __device__ __forceinline__ void run(F f, G one) {
+        for (int v = threadIdx.x; v < nv; v += U * N) {
+            uint32_t w[U][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u][0] = next[u].x, w[u][1] = next[u].y, w[u][2] = next[u].z, w[u][3] = next[u].w;
+            if (v + (U - 1) * N >= nv)  // (the last batch of some threads: what is not there counts nothing)
+#pragma unroll
+                for (int u = 1; u < U; ++u)
+                    if (v + u * N >= nv)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[u][e] = F32 ? 0xFF800000u : 0xFF80FF80u;
+            load(v + U * N);
+            f(w, a + (int64_t)v * W, nv - v);
+        }
+        const int64_t b = a + (int64_t)nv * W;
+        const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
+        if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
+    }
+};
 // logit e of a vector
 template <bool F32>
 __device__ __forceinline__ float logit(const uint32_t (&w)[4], int e) {
