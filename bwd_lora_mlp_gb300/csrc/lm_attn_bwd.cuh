@@ -172,6 +172,9 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
                     tma_load_3d(smem_u32(sv + b * kBoxBytes), &maps.v, smem_u32(kvfull), b * 64, g, k0);
                 }
                 uint32_t it = 0, no = 0;  // query and dO tiles asked for
+                // (which queries see something is asked for a tile ahead, as which keys are seen below)
+                uint4 seen = make_uint4(0, 0, 0, 0);
+                if (FORM != ATTN_SELF && p.qseen) seen = p.qseen[qt0 + qi0];
                 for (int hh = hh0; ok && (SHARED ? no < (uint32_t)N : hh < n); ++hh)
                     for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || no < (uint32_t)N); ++qt) {
                         const int h = g * n + hh;
@@ -181,7 +184,10 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
                             ok = false;
                             break;
                         }
-                        if (FORM != ATTN_SELF && p.qseen) s_seen[s] = p.qseen[qt];
+                        if (FORM != ATTN_SELF && p.qseen) {
+                            s_seen[s] = seen;
+                            seen = p.qseen[qt + 1 < qt0 + nt ? qt + 1 : qt0];
+                        }
                         mbar_expect_tx(bq, C::kTileBytes + 2 * C::kRowBytes);
                         for (int b = 0; b < DP / 64; ++b)
                             tma_load_3d(smem_u32(sq + s * C::kTileBytes + b * kBoxBytes), &maps.q, bq, b * 64, h, qt * kTile);
@@ -511,6 +517,7 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint4* s_seen = reinterpret_cast<uint4*>(smem + 768);  // [key stage] the tile's keys that somebody sees (not SELF)
+    uint64_t* clean = reinterpret_cast<uint64_t*>(smem + 896);  // [key stage] and the others have been cleared
     uint8_t* sq = smem + 1024;
     uint8_t* so = sq + C::kTileBytes;
     uint8_t* sk = so + C::kTileBytes;
@@ -522,6 +529,7 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
         for (int s = 0; s < C::kKStages; ++s) {
             mbar_init(smem_u32(&kfull[s]), 1);
             mbar_init(smem_u32(&kempty[s]), 1);
+            if (FORM != ATTN_SELF) mbar_init(smem_u32(&clean[s]), 1);
         }
         for (int s = 0; s < C::kVStages; ++s) {
             mbar_init(smem_u32(&vfull[s]), 1);
@@ -562,8 +570,10 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
             if (lane == 0) {
                 bool ok = true;
                 uint32_t nk = 0, nv = 0, nq[2] = {0, 0};  // tiles asked for
+                uint4 seen = make_uint4(0, 0, 0, 0);
                 for (int r = p.starve & K_ATTN_DQ ? rounds : 0; ok && r < rounds; ++r) {
                     const DqItem it = dq_item<FORM>(p, who, r);
+                    if (FORM != ATTN_SELF && p.kseen && it.N > 0) seen = p.kseen[it.kt0];
                     auto query = [&](int which) {  // Q, then dO
                         if (!mbar_wait(smem_u32(&qempty[which]), (nq[which] & 1u) ^ 1u, s_abort, p.wait_ns)) return false;
                         const uint32_t bar = smem_u32(&qfull[which]);
@@ -588,7 +598,10 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
                                 ok = false;
                                 break;
                             }
-                            if (FORM != ATTN_SELF && !kv && p.kseen) s_seen[st] = p.kseen[it.kt0 + j];
+                            if (FORM != ATTN_SELF && !kv && p.kseen) {
+                                s_seen[st] = seen;
+                                seen = p.kseen[it.kt0 + min(j + 1, it.N - 1)];
+                            }
                             mbar_expect_tx(bar, C::kTileBytes);
                             for (int b = 0; b < DP / 64; ++b)
                                 tma_load_3d(smem_u32((kv ? sv : sk) + st * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k, bar,
@@ -622,9 +635,9 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
                 if (it.N <= 0) continue;
                 auto scores = [&](int j) {  // S(j) = Q K^T, in buffer t & 1
                     const uint32_t t = base + (uint32_t)j, s = t % C::kKStages;
-                    if (!mbar_wait(smem_u32(&kfull[s]), (t / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
+                    uint64_t* there = FORM != ATTN_SELF && p.kseen ? clean : kfull;
+                    if (!mbar_wait(smem_u32(&there[s]), (t / C::kKStages) & 1u, s_abort, p.wait_ns)) return false;
                     if (FORM == ATTN_SELF) clear_padding(sk + s * C::kTileBytes, DP / 64, (it.kt0 + j) * kTile, in0, in1);
-                    else if (p.kseen) clear_unseen(sk + s * C::kTileBytes, DP / 64, s_seen[s]);
                     tc_fence_after();
                     mma_rows<DP>(tmem + (t & 1u) * kTile, desc_rows(smem_u32(sq)), desc_rows(smem_u32(sk + s * C::kTileBytes)), ksteps,
                                  ids);
@@ -673,6 +686,25 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
             umma_commit(smem_u32(drain));
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
+        }
+        if (FORM != ATTN_SELF && warp == kBwdMath + 2 && p.kseen) {  // ---------------- clears keys that nobody sees
+            bool ok = true;
+            uint32_t t = 0;
+            for (int r = 0; ok && r < rounds; ++r) {
+                const DqItem it = dq_item<FORM>(p, who, r);
+                for (int j = 0; ok && j < it.N; ++j, ++t) {
+                    const uint32_t s = t % C::kKStages;
+                    ok = mbar_wait_warp(smem_u32(&kfull[s]), (t / C::kKStages) & 1u, s_abort, p.wait_ns);
+                    if (!ok) break;
+                    clear_unseen_warp(sk + s * C::kTileBytes, DP / 64, s_seen[s]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&clean[s]));
+                }
+            }
+            if (!ok && lane == 0) {
+                attn_error(p, 7, 4);
+                *s_abort = 1;
+            }
         }
     } else {  // ---------------- arithmetic: one query row, 32 key columns per thread
         regs_up<kBwdMathRegs>();

@@ -243,11 +243,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) {
                 bool ok = true;
                 uint32_t n = 0, nq[2] = {0, 0};  // tiles and queries asked for
-                auto pair_of = [&](const Item& it, int j, auto between) {  // K_j, then V_j
+                // (which keys are seen is asked for a tile ahead: a wait for memory here is a wait of every tile's)
+                uint4 seen = make_uint4(0, 0, 0, 0);
+                auto look = [&](int j) {
+                    if (FORM != ATTN_SELF && p.kseen) seen = p.kseen[j];
+                };
+                auto pair_of = [&](const Item& it, int j, int then, auto between) {  // K_j, then V_j
                     for (int kv = 0; kv < 2; ++kv) {
                         const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
                         if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) return false;
-                        if (FORM != ATTN_SELF && kv && p.kseen) s_seen[s] = p.kseen[j];
+                        if (FORM != ATTN_SELF && kv && p.kseen) {
+                            s_seen[s] = seen;
+                            look(then);
+                        }
                         mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
                         for (int b = 0; b < DP / 64; ++b)
                             tma_load_3d(smem_u32(ring + s * C::kTileBytes + b * kBoxBytes), kv ? &maps.v : &maps.k,
@@ -273,10 +281,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     };
                     ok = query(0);  // then K, then the other queries: the first scores wait for what they need
                     if constexpr (FORM == ATTN_FEW) {
-                        for (int i = 0; ok && i < tiles; ++i) ok = pair_of(it, s_tiles[i], [] { return true; });
+                        if (tiles > 0) look(s_tiles[0]);
+                        for (int i = 0; ok && i < tiles; ++i)
+                            ok = pair_of(it, s_tiles[i], s_tiles[min(i + 1, tiles - 1)], [] { return true; });
                     } else {
+                        if (it.J0 < it.J1) look(it.J0);
                         for (int j = it.J0; ok && j < it.J1; ++j)
-                            ok = pair_of(it, j, [&] { return j != it.J0 || query(1); });
+                            ok = pair_of(it, j, min(j + 1, it.J1 - 1), [&] { return j != it.J0 || query(1); });
                     }
                 }
                 if (!ok) {
