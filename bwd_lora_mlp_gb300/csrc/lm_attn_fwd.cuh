@@ -125,26 +125,29 @@ __device__ __forceinline__ int rounds_of(const AttnParams& p) {
     return (n + (int)gridDim.x - 1) / (int)gridDim.x;
 }
 
-// The CTA's share of the key tiles that its queries see, as a list: tiles that nobody sees are left out of it (padded
+// The key tiles that a CTA takes, in order.
+struct FewTiles {
+    int n, first;          // first of them, or < 0: they are listed
+    const uint16_t* list;
+    bool few_rows;         // some row sees few keys
+    __device__ __forceinline__ int operator[](int i) const { return first < 0 ? list[i] : first + i; }
+};
+// The CTA's share of the key tiles that its queries see.  With documents, tiles that nobody sees are left out (padded
 // states), and the shares are of those that are left.  All threads come here; red: 64 ints of shared memory.
-__device__ __forceinline__ void few_setup(const AttnParams& p, uint16_t* list, int* red, int& tiles, bool& few_rows) {
+__device__ __forceinline__ FewTiles few_setup(const AttnParams& p, uint16_t* list, int* red) {
     constexpr int kWarps = kFwdThreads / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = p.hq / p.hk;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Item it = item_of<ATTN_FEW>(p, 0);
+    const int n = max(it.J1 - it.J0, 0);
+    auto share = [&](int total, int part) { return total * part / p.splits; };  // (at most 2^13 tiles, 152 parts)
+    if (!p.kseen) {
+        const int a = share(n, it.part);
+        return FewTiles{share(n, it.part + 1) - a, it.J0 + a, list, p.Tk < kFewKeys};
+    }
     bool few = false;
     if ((int)threadIdx.x < p.rows && it.q0 + (int)threadIdx.x < p.T) {
         const TokRange r = query_range<ATTN_FEW>(p, it.q0 + (int)threadIdx.x);
         few = r.hi > r.lo && r.hi - r.lo < kFewKeys;
-    }
-    few_rows = __syncthreads_or(few);
-    const int n = max(it.J1 - it.J0, 0);
-    auto share = [&](int total, int part) { return (int)((int64_t)total * part / p.splits); };
-    if (!p.kseen) {
-        const int a = share(n, it.part);
-        tiles = share(n, it.part + 1) - a;
-        for (int i = threadIdx.x; i < tiles; i += kFwdThreads) list[i] = (uint16_t)(it.J0 + a + i);
-        __syncthreads();
-        return;
     }
     const int len = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, j0 = min(n, warp * len), j1 = min(n, j0 + len);
     auto seen = [&](int i) {
@@ -153,9 +156,13 @@ __device__ __forceinline__ void few_setup(const AttnParams& p, uint16_t* list, i
         return (b.x | b.y | b.z | b.w) != 0u;
     };
     int mine = 0;
-    for (int i = j0; i < j1; i += 32) mine += __popc(__ballot_sync(0xffffffffu, seen(i + lane)));
+    uint32_t last = 0;
+    for (int i = j0; i < j1; i += 32) {
+        last = __ballot_sync(0xffffffffu, seen(i + lane));
+        mine += __popc(last);
+    }
     if (lane == 0) red[warp] = mine;
-    __syncthreads();
+    const bool few_rows = __syncthreads_or(few);
     int total = 0, at = 0;
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) at += red[w];
@@ -163,14 +170,15 @@ __device__ __forceinline__ void few_setup(const AttnParams& p, uint16_t* list, i
     }
     const int a = share(total, it.part), z = share(total, it.part + 1);
     for (int i = j0; i < j1; i += 32) {
-        const bool on = seen(i + lane);
-        const uint32_t votes = __ballot_sync(0xffffffffu, on);
+        // (up to 640 tiles a warp has 32 of them, and knows)
+        const uint32_t votes = len == 32 ? last : __ballot_sync(0xffffffffu, seen(i + lane));
+        const bool on = votes >> lane & 1u;
         const int r = at + __popc(votes & ((1u << lane) - 1u));
         if (on && r >= a && r < z) list[r - a] = (uint16_t)(it.J0 + i + lane);
         at += __popc(votes);
     }
-    tiles = z - a;
     __syncthreads();
+    return FewTiles{z - a, -1, list, few_rows};
 }
 
 template <int DP, int MODE, int FORM>
@@ -233,9 +241,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const int rounds = rounds_of<FORM>(p), group = p.hq / p.hk;
     // few queries: this CTA's key tiles, of those that the query tile sees its share, and whether a row sees few keys
-    int tiles = 0;
-    bool few_rows = false;
-    if constexpr (FORM == ATTN_FEW) few_setup(p, s_tiles, reinterpret_cast<int*>(s_inv), tiles, few_rows);
+    FewTiles mine{0, 0, nullptr, false};
+    if constexpr (FORM == ATTN_FEW) mine = few_setup(p, s_tiles, reinterpret_cast<int*>(s_inv));
+    const int tiles = mine.n;
 
     if (warp >= kFwdMath) {
         regs_down<kFwdIssueRegs>();
@@ -281,9 +289,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     };
                     ok = query(0);  // then K, then the other queries: the first scores wait for what they need
                     if constexpr (FORM == ATTN_FEW) {
-                        if (tiles > 0) look(s_tiles[0]);
+                        if (tiles > 0) look(mine[0]);
                         for (int i = 0; ok && i < tiles; ++i)
-                            ok = pair_of(it, s_tiles[i], s_tiles[min(i + 1, tiles - 1)], [] { return true; });
+                            ok = pair_of(it, mine[i], mine[min(i + 1, tiles - 1)], [] { return true; });
                     } else {
                         if (it.J0 < it.J1) look(it.J0);
                         for (int j = it.J0; ok && j < it.J1; ++j)
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ok = (i + 1 >= tiles || scores(i + 1)) && values(nv);
                     if (!ok) break;
                     tc_fence_after();
-                    ok = weighted(i & 1, nv, (uint32_t)(i >> 1) & 1u, i < 2, few_rows, i + 2 >= tiles);
+                    ok = weighted(i & 1, nv, (uint32_t)(i >> 1) & 1u, i < 2, mine.few_rows, i + 2 >= tiles);
                     if (ok) umma_commit(smem_u32(&empty[nv % C::kSlots]));
                 }
             }
@@ -628,7 +636,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 return true;
             };
             if constexpr (FORM == ATTN_FEW) {
-                for (int i = w; ok && i < tiles; i += 2, ++nt) ok = step(s_tiles[i], i >= 2, few_rows);
+                for (int i = w; ok && i < tiles; i += 2, ++nt) ok = step(mine[i], i >= 2, mine.few_rows);
             } else {
                 for (int j = sp.j0; ok && j < sp.j1; ++j, ++nt) ok = step(j, j > sp.j0, sp.few_keys<MODE>());
             }

@@ -293,7 +293,7 @@ static cudaError_t fwd_rows(const DistillParams& p, int c, cudaStream_t st) {
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeClusterDimension;
     a.val.clusterDim = {(unsigned)c, 1, 1};
-    return launch_pdl(distill_fwd_kernel<F32, REST, TWO, N>, dim3((unsigned)(p.T * c)), dim3(N), 0, st, &a, 1, p, c);
+    return launch_pdl(distill_fwd_kernel<F32, REST, TWO, N>, dim3((unsigned)(p.T * c)), dim3(N), 0, st, &a, c > 1 ? 1 : 0, p, c);
 }
 template <bool F32, bool REST, bool TWO>
 static cudaError_t fwd_launch(const DistillParams& p, cudaStream_t st) {

@@ -426,6 +426,29 @@ def _here(*tensors) -> None:
             raise ValueError("a call's tensors must lie on the current device (cuda:%d), got one on %s" % (at, t.device))
 
 
+# The usual tensor of a call in as few questions as say that it is one (get_device is -1 on the host); others take the
+# long way, which says what is wrong with them.
+def _flat(t, shape, dtype, dev: int, name: str) -> int:
+    """Device address of a contiguous tensor on the current device (None: a null pointer)."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+            return t.data_ptr() or L._empty_ptr(t.device)
+        _here(t)
+    return _shaped(t, shape, dtype, name)
+
+
+def _heads_at(t, T: int, h: int, d: int, dev: int, name: str) -> lm_heads:
+    if isinstance(t, torch.Tensor):
+        if T > 1 and h > 1 and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (T, h, d):
+            ts, hs, one = t.stride()
+            if one == 1:
+                return lm_heads(t.data_ptr(), ts, hs)
+        _here(t)
+    return _heads(t, T, h, d, name)
+
+
 @dataclass
 class QkRope:
     """Norm of each query and key head (``norm``; root mean square, weights w_q and w_k + w_offset of d values, all
@@ -446,35 +469,39 @@ class QkRope:
     w_offset: float = 0.0
 
     def c_struct(self, T: int, d: int) -> lm_qkrope:
-        f, pos, axis = self.inv_freq, self.pos, self.axis
-        if f is None and (pos is not None or axis is not None):
+        f, pos, axis, wq, wk = self.inv_freq, self.pos, self.axis, self.w_q, self.w_k
+        half, pairs, pp, axes, pi = (), 0, 0, 1, LM_I32
+        if f is not None:
+            pairs = f.numel()
+            half = (pairs,)
+        elif pos is not None or axis is not None:
             raise ValueError("pos and axis need inv_freq")
-        _here(f, pos, axis, self.w_q, self.w_k)
-        pairs = 0 if f is None else f.numel()
-        axes, pi = 1, LM_I32
+        dev = _device()
         if pos is not None:
-            if pos.dtype not in _INDEX:
-                raise TypeError("pos must be int32 or int64, got %s" % pos.dtype)
-            pi = _INDEX[pos.dtype]
-            axes = pos.shape[0] if pos.dim() == 2 else 1
-        w = self.w_q if self.w_q is not None else self.w_k
-        wt = torch.bfloat16 if w is None else w.dtype
-        if wt not in _DTYPES:
+            dt, shape = pos.dtype, (T,)
+            if dt not in _INDEX:
+                raise TypeError("pos must be int32 or int64, got %s" % dt)
+            pi = _INDEX[dt]
+            if pos.dim() == 2:
+                axes = pos.shape[0]
+                shape = (axes, T)
+            pp = _flat(pos, shape, dt, dev, "pos")
+        wt = wq.dtype if wq is not None else wk.dtype if wk is not None else torch.bfloat16
+        wc = _DTYPES.get(wt)
+        if wc is None:
             raise TypeError("w_q and w_k must be bfloat16 or float32, got %s" % wt)
-        return lm_qkrope(_shaped(f, (pairs,), torch.float32, "inv_freq"),
-                         0 if pos is None else _shaped(pos, (axes, T) if pos.dim() == 2 else (T,), pos.dtype, "pos"),
-                         _shaped(axis, (pairs,), torch.int32, "axis"), _shaped(self.w_q, (d,), wt, "w_q"),
-                         _shaped(self.w_k, (d,), wt, "w_k"), self.factor, self.eps, self.w_offset, 2 * pairs, axes,
-                         bool(self.interleaved), bool(self.norm), pi, _DTYPES[wt], 0)
+        one = (d,)
+        return lm_qkrope(_flat(f, half, torch.float32, dev, "inv_freq"), pp, _flat(axis, half, torch.int32, dev, "axis"),
+                         _flat(wq, one, wt, dev, "w_q"), _flat(wk, one, wt, dev, "w_k"), self.factor, self.eps, self.w_offset,
+                         2 * pairs, axes, bool(self.interleaved), bool(self.norm), pi, wc, 0)
 
 
-def _heads_out(t, like, T, h, d, name):
+def _heads_out(t, T, h, d, dev, at: int, name):
     """The caller's strided tensor, or a new contiguous one."""
     if t is None:
-        t, p = _new((T, h, d), torch.bfloat16, like.device)
+        t, p = _new((T, h, d), torch.bfloat16, dev)
         return t, lm_heads(p, h * d, d)
-    _here(t)
-    return t, _heads(t, T, h, d, name)
+    return t, _heads_at(t, T, h, d, at, name)
 
 
 def qkrope_workspace_size(T: int, hq: int, hk: int, d: int) -> int:
@@ -487,16 +514,15 @@ def qkrope_fwd(q, k, r: QkRope, q_out=None, k_out=None, stream=None) -> dict:
     if stream is not None:
         with _on(stream):
             return qkrope_fwd(q, k, r, q_out, k_out)
-    T, hq, d = q.shape
+    (T, hq, d), dev, at = q.shape, q.device, _device()
     hk = 0 if k is None else k.shape[1]
-    _here(q, k)
-    sq, sk = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k") if hk else None
-    c = r.c_struct(T, d)
-    q_out, oq = _heads_out(q_out, q, T, hq, d, "q_out")
-    ok = None
+    sq, c = _heads_at(q, T, hq, d, at, "q"), r.c_struct(T, d)
+    q_out, oq = _heads_out(q_out, T, hq, d, dev, at, "q_out")
+    sk = ok = None
     if hk:
-        k_out, ok = _heads_out(k_out, q, T, hk, d, "k_out")
-    _call("qkrope_fwd", T, hq, hk, d, sq, sk, c, oq, ok, _stream())
+        sk = _heads_at(k, T, hk, d, at, "k")
+        k_out, ok = _heads_out(k_out, T, hk, d, dev, at, "k_out")
+    _call("qkrope_fwd", T, hq, hk, d, sq, sk, c, oq, ok, _raw_stream(at))
     return {"q": q_out, "k": k_out if hk else None}
 
 
@@ -507,31 +533,26 @@ def qkrope_bwd(q, k, dq, dk, r: QkRope, weights: bool = True, dq_in=None, dk_in=
     if stream is not None:
         with _on(stream):
             return qkrope_bwd(q, k, dq, dk, r, weights, dq_in, dk_in, ws)
-    T, hq, d = dq.shape
+    (T, hq, d), dev, at = dq.shape, dq.device, _device()
     hk = 0 if dk is None else dk.shape[1]
-    dev = dq.device
-    _here(dq, dk)
-    sq = sk = None
-    if r.norm:
-        _here(q, k)
-        sq, sk = _heads(q, T, hq, d, "q"), _heads(k, T, hk, d, "k") if hk else None
-    gq, gk = _heads(dq, T, hq, d, "dq"), _heads(dk, T, hk, d, "dk") if hk else None
-    c = r.c_struct(T, d)
-    dq_in, oq = _heads_out(dq_in, dq, T, hq, d, "dq_in")
-    ok = None
+    gq, c = _heads_at(dq, T, hq, d, at, "dq"), r.c_struct(T, d)
+    dq_in, oq = _heads_out(dq_in, T, hq, d, dev, at, "dq_in")
+    sq = sk = gk = ok = dw_q = dw_k = None
+    pq = pk = pw = n = 0
     if hk:
-        dk_in, ok = _heads_out(dk_in, dq, T, hk, d, "dk_in")
-
-    def grad(w):
-        return _new((d,), torch.float32, dev) if weights and w is not None else (None, 0)
-
-    (dw_q, pq), (dw_k, pk) = grad(r.w_q), grad(r.w_k)
-    pw = n = 0
+        gk = _heads_at(dk, T, hk, d, at, "dk")
+        dk_in, ok = _heads_out(dk_in, T, hk, d, dev, at, "dk_in")
     if r.norm:
-        ws = torch.empty(qkrope_workspace_size(T, hq, hk, d), dtype=torch.uint8, device=dev) if ws is None else ws
-        _here(ws)
-        pw, n = L._ptr(ws, torch.uint8, "ws"), ws.numel()
-    _call("qkrope_bwd", T, hq, hk, d, sq, sk, gq, gk, c, oq, ok, pq, pk, pw, n, _stream())
+        sq, sk = _heads_at(q, T, hq, d, at, "q"), _heads_at(k, T, hk, d, at, "k") if hk else None
+        if weights and r.w_q is not None:
+            dw_q, pq = _new((d,), torch.float32, dev)
+        if weights and r.w_k is not None:
+            dw_k, pk = _new((d,), torch.float32, dev)
+        if ws is None:
+            ws = torch.empty(qkrope_workspace_size(T, hq, hk, d), dtype=torch.uint8, device=dev)
+        n = ws.numel()
+        pw = _flat(ws, (n,), torch.uint8, at, "ws")
+    _call("qkrope_bwd", T, hq, hk, d, sq, sk, gq, gk, c, oq, ok, pq, pk, pw, n, _raw_stream(at))
     return {"dq": dq_in, "dk": dk_in if hk else None, "dw_q": dw_q, "dw_k": dw_k, "ws": ws}
 
 
@@ -554,9 +575,9 @@ class Teacher:
             raise TypeError("ids must be a 2D int32 or int64 tensor")
         if not isinstance(values, torch.Tensor) or values.dtype not in _DTYPES:
             raise TypeError("values must be a bfloat16 or float32 tensor")
-        shape = (T, ids.shape[1])
-        return lm_teacher(_shaped(ids, shape, ids.dtype, "ids"), _shaped(values, shape, values.dtype, "values"), shape[1],
-                          _INDEX[ids.dtype], _DTYPES[values.dtype], bool(self.rest))
+        it, vt, K, dev = ids.dtype, values.dtype, ids.shape[1], _device()
+        return lm_teacher(_flat(ids, (T, K), it, dev, "ids"), _flat(values, (T, K), vt, dev, "values"), K, _INDEX[it], _DTYPES[vt],
+                          bool(self.rest))
 
 
 def _alike(t):
@@ -579,14 +600,13 @@ def distill_fwd(logits, teacher: Teacher, targets=None, scale: float = 1.0, stre
             return distill_fwd(logits, teacher, targets, scale)
     p, ld, dt = _rows2d(logits, "logits")
     T, V = logits.shape
-    _here(logits, teacher.ids, teacher.values, targets)
+    _here(logits, targets)
     tp, ti = (0, LM_I32) if targets is None else _targets(targets, T)
     dev, f32 = logits.device, torch.float32
+    kl, pk = _new((T,), f32, dev)
+    lse, pl = _new((T,), f32, dev)
     saved, ps = _new((T, 8), f32, dev)
-    rows, pk = _new((2 if targets is None else 3, T), f32, dev)  # (one allocation)
-    kl, lse, *logp = rows.unbind(0)
-    logp = logp[0] if logp else None
-    pl, pp = pk + 4 * T, 0 if logp is None else pk + 8 * T
+    logp, pp = (None, 0) if targets is None else _new((T,), f32, dev)
     _call("distill_fwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, pk, pp, pl, ps, _stream())
     return {"kl": kl, "logp": logp, "lse": lse, "saved": saved}
 
@@ -602,16 +622,16 @@ def distill_bwd(logits, teacher: Teacher, fwd: dict, dkl=None, targets=None, dlo
         raise ValueError("dlogp needs a forward with targets")
     p, ld, dt = _rows2d(logits, "logits")
     T, V = logits.shape
-    _here(logits, teacher.ids, teacher.values, targets, dkl, dlogp, dlogits)
+    _here(logits, targets, dlogits)
     tp, ti = (0, LM_I32) if targets is None else _targets(targets, T)
-    f32 = torch.float32
+    f32, at, t1 = torch.float32, _device(), (T,)
     if dlogits is None:
         dlogits = _alike(logits)
     po, ldo, dto = _rows2d(dlogits, "dlogits")
     if dlogits.shape != (T, V) or dto != dt:
         raise ValueError("dlogits must have the logits' shape and type")
-    _call("distill_bwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, _shaped(fwd["saved"], (T, 8), f32, "saved"),
-          _shaped(dkl, (T,), f32, "dkl"), _shaped(dlogp, (T,), f32, "dlogp"), po, ldo, _stream())
+    _call("distill_bwd", T, V, ld, p, dt, teacher.c_struct(T), tp, ti, scale, _flat(fwd["saved"], (T, 8), f32, at, "saved"),
+          _flat(dkl, t1, f32, at, "dkl"), _flat(dlogp, t1, f32, at, "dlogp"), po, ldo, _raw_stream(at))
     return {"dlogits": dlogits}
 
 
@@ -650,19 +670,21 @@ def cross_fwd(q, k, v, a: Cross, train: bool = True, O=None, lse=None, O_lo=None
     if stream is not None:
         with _on(stream):
             return cross_fwd(q, k, v, a, train, O, lse, O_lo, ws)
-    (Tq, hq, d), (Tk, hk) = q.shape, k.shape[:2]
-    dev = q.device
-    _here(q, k, v, ws)
-    hs = _heads(q, Tq, hq, d, "q"), _heads(k, Tk, hk, d, "k"), _heads(v, Tk, hk, d, "v")
-    O, pO = _out(O, (Tq, hq, d), torch.bfloat16, dev, "O")
-    lse, pl = _out(lse, (hq, Tq), torch.float32, dev, "lse")
+    (Tq, hq, d), (Tk, hk, _) = q.shape, k.shape
+    dev, at = q.device, _device()
+    hs = _heads_at(q, Tq, hq, d, at, "q"), _heads_at(k, Tk, hk, d, at, "k"), _heads_at(v, Tk, hk, d, at, "v")
+    O, pO = _new((Tq, hq, d), torch.bfloat16, dev) if O is None else (O, _flat(O, (Tq, hq, d), torch.bfloat16, at, "O"))
+    lse, pl = _new((hq, Tq), torch.float32, dev) if lse is None else (lse, _flat(lse, (hq, Tq), torch.float32, at, "lse"))
     plo = 0
     if train or O_lo is not None:
-        O_lo, plo = _out(O_lo, (Tq, hq, _d16(d)), torch.int8, dev, "O_lo")
+        shape = (Tq, hq, _d16(d))
+        O_lo, plo = _new(shape, torch.int8, dev) if O_lo is None else (O_lo, _flat(O_lo, shape, torch.int8, at, "O_lo"))
     if ws is None:
         ws = torch.empty(cross_workspace_size(Tq, Tk, hq, hk, d), dtype=torch.uint8, device=dev)
         ws[:256].zero_()  # (the error word; the parts' sums may be megabytes)
-    _call("cross_fwd", Tq, Tk, hq, hk, d, *hs, a.c_struct(), pO, plo, pl, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    n = ws.numel()
+    _call("cross_fwd", Tq, Tk, hq, hk, d, *hs, a.c_struct(), pO, plo, pl, _flat(ws, (n,), torch.uint8, at, "ws"), n,
+          _raw_stream(at))
     return {"O": O, "lse": lse, "O_lo": O_lo, "ws": ws}
 
 
@@ -671,15 +693,17 @@ def cross_bwd(q, k, v, dO, fwd: dict, a: Cross, dQ=None, dK=None, dV=None, ws=No
     if stream is not None:
         with _on(stream):
             return cross_bwd(q, k, v, dO, fwd, a, dQ, dK, dV, ws)
-    (Tq, hq, d), (Tk, hk) = q.shape, k.shape[:2]
-    dev, bf = q.device, torch.bfloat16
+    (Tq, hq, d), (Tk, hk, _) = q.shape, k.shape
+    dev, at, bf = q.device, _device(), torch.bfloat16
+    sq, sk = (Tq, hq, d), (Tk, hk, d)
     ws = fwd["ws"] if ws is None else ws
-    _here(q, k, v, dO, ws)
-    hs = _heads(q, Tq, hq, d, "q"), _heads(k, Tk, hk, d, "k"), _heads(v, Tk, hk, d, "v"), _heads(dO, Tq, hq, d, "dO")
-    dQ, pq = _out(dQ, (Tq, hq, d), bf, dev, "dQ")
-    dK, pk = _out(dK, (Tk, hk, d), bf, dev, "dK")
-    dV, pv = _out(dV, (Tk, hk, d), bf, dev, "dV")
-    _call("cross_bwd", Tq, Tk, hq, hk, d, *hs, _shaped(fwd["O"], (Tq, hq, d), bf, "O"),
-          _shaped(fwd["O_lo"], (Tq, hq, _d16(d)), torch.int8, "O_lo"), _shaped(fwd["lse"], (hq, Tq), torch.float32, "lse"),
-          a.c_struct(), pq, pk, pv, L._ptr(ws, torch.uint8, "ws"), ws.numel(), _stream())
+    hs = (_heads_at(q, Tq, hq, d, at, "q"), _heads_at(k, Tk, hk, d, at, "k"), _heads_at(v, Tk, hk, d, at, "v"),
+          _heads_at(dO, Tq, hq, d, at, "dO"))
+    dQ, pq = _new(sq, bf, dev) if dQ is None else (dQ, _flat(dQ, sq, bf, at, "dQ"))
+    dK, pk = _new(sk, bf, dev) if dK is None else (dK, _flat(dK, sk, bf, at, "dK"))
+    dV, pv = _new(sk, bf, dev) if dV is None else (dV, _flat(dV, sk, bf, at, "dV"))
+    n = ws.numel()
+    _call("cross_bwd", Tq, Tk, hq, hk, d, *hs, _flat(fwd["O"], sq, bf, at, "O"),
+          _flat(fwd["O_lo"], (Tq, hq, _d16(d)), torch.int8, at, "O_lo"), _flat(fwd["lse"], (hq, Tq), torch.float32, at, "lse"),
+          a.c_struct(), pq, pk, pv, _flat(ws, (n,), torch.uint8, at, "ws"), n, _raw_stream(at))
     return {"dQ": dQ, "dK": dK, "dV": dV}
