@@ -197,34 +197,6 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     }
     const bool any = __syncthreads_or(id >= 0);
     s = join_parts<N / 32, TWO>(sm.warp[tid & (N / 32 - 1)], c);
-    float ytop = -INFINITY, xtop = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kEntryWarps; ++w) {
-        ytop = max_nan(ytop, sm.red[w][0]);
-        xtop = max_nan(xtop, sm.red[w][1]);
-    }
-    if (part == 0 && warp < kEntryWarps) {
-        // (weights of at most e^-5 < 1 / K: their sum with logits of the lowest value does not overflow)
-        const float yref = REST || ytop == -INFINITY ? 0.f : ytop + 5.f, xref = xtop == -INFINITY ? 0.f : xtop;
-        const float e = id >= 0 ? expf(y - yref) : 0.f, dx = (x - xref) * p.scale;
-        // sum e, sum e (log p - log q) up to what is the same for all, and (each token once) the entries' e^x
-        float v[4] = {e, e == 0.f ? 0.f : e * (y - yref - dx), 0.f, 0.f};
-        if (REST) {
-            bool first = id >= 0;
-            for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
-            if (first) {
-                v[2] = brought(x, xref, c);
-                v[3] = brought(x, xref, kL2e);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < (REST ? TWO ? 4 : 3 : 2); ++i) {
-#pragma unroll
-            for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-            if (lane == 0) sm.sums[warp][i] = v[i];
-        }
-    }
-    __syncthreads();
     if (cluster > 1) {
         __syncwarp();
         cluster_wait();  // CTA 0 has started
@@ -239,44 +211,67 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         const int i = tid & (kMaxCluster - 1);
         s = join_parts<kMaxCluster, TWO>(i < cluster ? sm.seg[i] : Part{-INFINITY, 0.f, 0.f}, c);
     }
+    float ytop = -INFINITY, xtop = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kEntryWarps; ++w) {
+        ytop = max_nan(ytop, sm.red[w][0]);
+        xtop = max_nan(xtop, sm.red[w][1]);
+    }
+    const float top = REST && any ? max_nan(s.m, xtop) : s.m;  // the row's largest logit
+    const bool empty = top == -INFINITY;
+    // the teacher's weights, and (each token once) the entries' e^x; a sum over the entries, the same in all threads
+    auto over_entries = [&](float v, int which) {
+        if (warp < kEntryWarps) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) sm.sums[warp][which] = v;
+        }
+    };
+    auto total_of = [&](int which) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEntryWarps; ++w) v += sm.sums[w][which];
+        return v;
+    };
+    const float yref = REST || ytop == -INFINITY ? 0.f : ytop;
+    const float e = id >= 0 ? expf(y - yref) : 0.f;
+    over_entries(e, 0);
+    if (REST) {
+        bool first = id >= 0 && warp < kEntryWarps;
+        for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
+        over_entries(first ? brought(x, top, c) : 0.f, 1);
+        if (TWO) over_entries(first ? brought(x, top, kL2e) : 0.f, 2);
+    }
+    __syncthreads();
+    const float E = total_of(0), rest = s.S * brought(s.m, top, c), total = REST ? rest + total_of(1) : rest, log_total = logf(total);
+    // sum p (log p - log q); each log p - log q is formed before it is weighed: their sum is far smaller than its parts
+    const float tl = REST ? 0.f : ytop + logf(E), p_k = e == 0.f ? 0.f : REST ? e : e / E;
+    over_entries(p_k == 0.f ? 0.f : p_k * ((y - tl) - ((x - top) * p.scale - log_total)), 3);
+    __syncthreads();
     if (tid) return;
 
     // ---- the row's scalars
-    float E = 0.f, Bs = 0.f, Es = 0.f, Es1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kEntryWarps; ++w) {
-        E += sm.sums[w][0];
-        Bs += sm.sums[w][1];
-        if (REST) Es += sm.sums[w][2];
-        if (REST && TWO) Es1 += sm.sums[w][3];
-    }
-    const float xref = xtop == -INFINITY ? 0.f : xtop;
-    const float top = REST && any ? max_nan(s.m, xtop) : s.m;  // the row's largest logit
-    const bool empty = top == -INFINITY;
-    const float fr = brought(s.m, top, c), fs = REST ? brought(xtop, top, c) : 0.f;
-    const float rest = s.S * fr, total = REST ? rest + Es * fs : rest;
-    const float log_total = logf(total), lse = empty ? -INFINITY : fmaf(top, p.scale, log_total);
+    const float lse = empty ? -INFINITY : fmaf(top, p.scale, log_total);
     float log_total1 = p.scale == 1.f ? log_total : NAN;  // (not wanted, and not formed, at another scale)
     if (TWO) {
         const float r1 = s.S1 * brought(s.m, top, kL2e);
-        log_total1 = logf(REST ? r1 + Es1 * brought(xtop, top, kL2e) : r1);
+        log_total1 = logf(REST ? r1 + total_of(2) : r1);
     }
     Saved o{top, log_total * kL2e, log_total1 * kL2e, top, log_total * kL2e, 1.f, 1.f, 0.f};
-    float kl = 0.f;
-    const float dl = (top - xref) * p.scale + log_total;  // lse - xref scale
+    float kl = any ? total_of(3) : 0.f;
     if (REST) {
         const bool others = s.m != -INFINITY;  // some logit outside the entries weighs something
         const float pr = E != E ? E : others ? fmaxf(1.f - E, 0.f) : 0.f, lr = logf(s.S);
-        const float lqr = others ? (s.m - top) * p.scale + (lr - log_total) : -INFINITY;
-        if (any) kl = Bs + E * dl + (pr > 0.f ? pr * (logf(pr) - lqr) : pr);
+        // log (p_r / q_r): of the quotient, whose logarithm is small, where q_r is a number of ordinary size
+        const float qr = rest / total;
+        const float far = qr >= 1e-30f || !(qr == qr) ? logf(pr / qr) : logf(pr) - ((s.m - top) * p.scale + (lr - log_total));
+        if (any) kl += pr > 0.f ? pr * far : pr;
         o.W = E + pr;
         o.m = others ? s.m : 0.f;
         o.ml2 = others ? lr * kL2e : INFINITY;
-        o.coef = any && others ? fmaf(o.W, rest / total, -pr) : 0.f;
+        o.coef = any && others ? fmaf(o.W, qr, -pr) : 0.f;
     } else {
-        const float lE = logf(E);
-        if (any && E != 0.f) kl = Bs / E - lE + dl;
-        o.tl = any && E != 0.f ? ytop + 5.f + lE : INFINITY;
+        o.tl = any && E != 0.f ? tl : INFINITY;
         if (!any || E == 0.f) o.coef = o.W = 0.f;
     }
     if (empty) kl = any && E > 0.f ? INFINITY : 0.f;  // no distribution: what the teacher expects is infinitely far
