@@ -40,6 +40,8 @@ constexpr float kRescale = 8.f;
 // with the low bits and 2.3e-3 without.  Twice as many keys here would bring rows of 512 to 1023 keys to the former,
 // dQ and dK by less than 3 %: 2.40e-3 and 2.37e-3 to 2.37e-3 and 2.36e-3 at 1024 tokens.  A step of 8192 tokens in 14
 // documents takes 512 us instead of 507; with 1024 here it takes 518, and one of 2048 tokens 166 instead of 161.)
+// (The form for few queries always does: it waits for memory, and takes 15.4 us with them where it took 14.4, 48.9 for
+// 48.0; O is then 1.66e-3 off instead of 1.96e-3 and 2.15e-3.)
 constexpr int kFewKeys = 512;
 // Sixteen softmax warps and a warpgroup for the loader's and the issuer's: 640 threads start with 96
 // registers each.
@@ -129,7 +131,6 @@ __device__ __forceinline__ int rounds_of(const AttnParams& p) {
 struct FewTiles {
     int n, first;          // first of them, or < 0: they are listed
     const uint16_t* list;
-    bool few_rows;         // some row sees few keys
     __device__ __forceinline__ int operator[](int i) const { return first < 0 ? list[i] : first + i; }
 };
 // The CTA's share of the key tiles that its queries see.  With documents, tiles that nobody sees are left out (padded
@@ -142,12 +143,7 @@ __device__ __forceinline__ FewTiles few_setup(const AttnParams& p, uint16_t* lis
     auto share = [&](int total, int part) { return total * part / p.splits; };  // (at most 2^13 tiles, 152 parts)
     if (!p.kseen) {
         const int a = share(n, it.part);
-        return FewTiles{share(n, it.part + 1) - a, it.J0 + a, list, p.Tk < kFewKeys};
-    }
-    bool few = false;
-    if ((int)threadIdx.x < p.rows && it.q0 + (int)threadIdx.x < p.T) {
-        const TokRange r = query_range<ATTN_FEW>(p, it.q0 + (int)threadIdx.x);
-        few = r.hi > r.lo && r.hi - r.lo < kFewKeys;
+        return FewTiles{share(n, it.part + 1) - a, it.J0 + a, list};
     }
     const int len = ((n + kWarps - 1) / kWarps + 31) / 32 * 32, j0 = min(n, warp * len), j1 = min(n, j0 + len);
     auto seen = [&](int i) {
@@ -162,7 +158,7 @@ __device__ __forceinline__ FewTiles few_setup(const AttnParams& p, uint16_t* lis
         mine += __popc(last);
     }
     if (lane == 0) red[warp] = mine;
-    const bool few_rows = __syncthreads_or(few);
+    __syncthreads();
     int total = 0, at = 0;
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) at += red[w];
@@ -178,7 +174,7 @@ __device__ __forceinline__ FewTiles few_setup(const AttnParams& p, uint16_t* lis
         at += __popc(votes);
     }
     __syncthreads();
-    return FewTiles{z - a, -1, list, few_rows};
+    return FewTiles{z - a, -1, list};
 }
 
 template <int DP, int MODE, int FORM>
@@ -240,8 +236,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const int rounds = rounds_of<FORM>(p), group = p.hq / p.hk;
-    // few queries: this CTA's key tiles, of those that the query tile sees its share, and whether a row sees few keys
-    FewTiles mine{0, 0, nullptr, false};
+    // few queries: this CTA's key tiles, of those that the query tile sees its share
+    FewTiles mine{0, 0, nullptr};
     if constexpr (FORM == ATTN_FEW) mine = few_setup(p, s_tiles, reinterpret_cast<int*>(s_inv));
     const int tiles = mine.n;
 
@@ -323,8 +319,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 return mbar_wait(smem_u32(&bar[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
             };
             if constexpr (FORM == ATTN_FEW) {
-                // O_w (+)= P_w V, V at ring position nv; last: of this accumulator
-                auto weighted = [&](int w, uint32_t nv, uint32_t parity, bool first, bool both, bool last) {
+                // O_w (+)= P_w V, and what the rounding of P left out; V at ring position nv; last: of this accumulator
+                auto weighted = [&](int w, uint32_t nv, uint32_t parity, bool first, bool last) {
                     const uint32_t ts = tmem + w * kTile, to = tmem + 2 * kTile + w * DP;
                     const uint32_t sv = smem_u32(ring + (nv % C::kSlots) * C::kTileBytes);
 #pragma unroll
@@ -336,10 +332,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_bf16_ts(to, a + kk * 8, desc(b + kk * 128), ido, first && !half && !kk ? 0u : 1u);
-                        if (both) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk) umma_bf16_ts(to, a + 64 + kk * 8, desc(b + kk * 128), ido, 1u);
                         if (half && last) umma_commit(smem_u32(&odone[w]));
                     }
                     return true;
@@ -360,7 +354,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ok = (i + 1 >= tiles || scores(i + 1)) && values(nv);
                     if (!ok) break;
                     tc_fence_after();
-                    ok = weighted(i & 1, nv, (uint32_t)(i >> 1) & 1u, i < 2, mine.few_rows, i + 2 >= tiles);
+                    ok = weighted(i & 1, nv, (uint32_t)(i >> 1) & 1u, i < 2, i + 2 >= tiles);
                     if (ok) umma_commit(smem_u32(&empty[nv % C::kSlots]));
                 }
             }
@@ -629,14 +623,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 if (few) {
                     if (sp.hides(j)) tile(j, begun, std::true_type{}, std::true_type{});
                     else tile(j, begun, std::false_type{}, std::true_type{});
-                } else if constexpr (!biased(MODE)) {
+                } else if constexpr (!biased(MODE) && FORM != ATTN_FEW) {
                     if (sp.hides(j)) tile(j, begun, std::true_type{}, std::false_type{});
                     else tile(j, begun, std::false_type{}, std::false_type{});
                 }
                 return true;
             };
             if constexpr (FORM == ATTN_FEW) {
-                for (int i = w; ok && i < tiles; i += 2, ++nt) ok = step(mine[i], i >= 2, mine.few_rows);
+                for (int i = w; ok && i < tiles; i += 2, ++nt) ok = step(mine[i], i >= 2, true);
             } else {
                 for (int j = sp.j0; ok && j < sp.j1; ++j, ++nt) ok = step(j, j > sp.j0, sp.few_keys<MODE>());
             }
