@@ -8,8 +8,8 @@
 // turn, and position times that, modulo 2^64, is the angle's place in its turn to 2^-33 of one for positions
 // up to 2^31.  Queries and keys have CTAs of their own, so the backward's weights and sums over tokens are one
 // set of registers; a second kernel joins the CTAs' sums in order.
-// Bound by memory as far as its arithmetic lets it: 8192 tokens, 32 + 8 heads of 128 read from a fused buffer, 82 us a
-// step in a graph, forward 32 (5.3 TB/s, 0.78 of the copy rate) and backward 49 (5.1); 16384 tokens 146 us, 5.8 TB/s.
+// Bound by memory as far as its arithmetic lets it: 8192 tokens, 32 + 8 heads of 128 read from a fused buffer, 80 us a
+// step in a graph, forward 30 (5.6 TB/s, 0.83 of the copy rate) and backward 49 (5.1); 16384 tokens 143 us, 5.9 TB/s.
 // (Heads loaded to registers four at a time by the lane and the angles formed by every lane for itself: 116 and 205.)
 #include <algorithm>
 
@@ -22,12 +22,13 @@ constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeSms = 152;  // GB300's: a workspace's size has to be known on a host without one
 // Heads of a lane at a step (two forward: two chains of shuffles and reciprocal roots at a time; the backward has
 // registers for one), steps on their way, CTAs an SM.  (Three or more steps, or three CTAs of fewer registers, are no
-// faster: 16384 tokens 154 us a step against 146.)
+// faster: 16384 tokens 154 us a step against 146 before positions came ahead, too.)
 constexpr int kFwdHeads = 2, kFwdStages = 2, kBwdStages = 2, kFwdCtas = 2, kBwdCtas = 2;
-static_assert(2 * kFwdHeads * kFwdStages * kRopeThreads * 16 + kRopeWarps * 1024 <= 48 * 1024 &&
-              4 * kBwdStages * kRopeThreads * 16 + kRopeWarps * 1024 <= 48 * 1024, "more shared memory has to be asked for");
-// Items a warp has at least, where tokens have parts enough (4097 tokens of 24 heads of 80: 28 us; with 16, 31).
+static_assert(2 * kFwdHeads * kFwdStages * kRopeThreads * 16 + kRopeWarps * 2048 <= 48 * 1024 &&
+              4 * kBwdStages * kRopeThreads * 16 + kRopeWarps * 2048 <= 48 * 1024, "more shared memory has to be asked for");
+// Items a warp has at least, where tokens have parts enough (4097 tokens of 24 heads of 80: 24.5 us; with 16, 26.6).
 constexpr int kTurns = 4;
+static_assert(kFwdStages < 4 && kBwdStages < 4, "a place of positions would be written while it is read");
 
 // f / (2 pi) as a fraction of a turn in units of 2^-64, whole turns left out.  f = m 2^e with a 24-bit m; 1 / (2 pi)
 // to 128 bits.
@@ -113,8 +114,10 @@ struct Place {
 struct Walk {
     uint32_t item, t;
     int h, h1;  // the step's first head, and the part's end
+    uint32_t n; // items begun before this one
     __device__ __forceinline__ Walk(const RopeSide& S, int first_block) {
         item = __shfl_sync(0xffffffffu, (blockIdx.x - first_block) * kRopeWarps + (threadIdx.x >> 5), 0);
+        n = 0;
         begin(S);
     }
     __device__ __forceinline__ bool more(const QkRopeParams& p, const RopeSide& S) const { return item < (uint32_t)p.T * (uint32_t)S.parts; }
@@ -133,10 +136,39 @@ struct Walk {
         h += heads;
         if (h < h1) return false;
         item += (uint32_t)S.blocks * kRopeWarps;
+        ++n;
         begin(S);
         return true;
     }
     __device__ __forceinline__ int64_t at(int64_t ts, int64_t hs) const { return (int64_t)t * ts + (int64_t)h * hs; }
+};
+
+// The positions of a warp's coming items: copied ahead with their first heads, an axis a lane.  (Read where they are
+// needed, they were waited for at every item: 16384 tokens 146 us a step, 143 so; 4097 with three axes 28, 24.5 so.)  Four items are on their way at most.
+constexpr int kPosAxes = 32, kPosItems = 4;
+struct Positions {
+    char* slots;  // the warp's
+    __device__ __forceinline__ explicit Positions(char* mine) : slots(mine) {}
+    __device__ __forceinline__ static bool ahead(const QkRopeParams& p) { return p.pos && p.axes <= kPosAxes; }
+    __device__ __forceinline__ void ask(const QkRopeParams& p, const Walk& A) const {
+        const int a = threadIdx.x & 31;
+        if (!ahead(p) || a >= p.axes) return;
+        const uint32_t dst = smem_u32(slots + ((A.n % kPosItems) * kPosAxes + a) * 8);
+        const int64_t i = (int64_t)a * p.T + A.t;
+        if (p.pos_i64)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(static_cast<const int64_t*>(p.pos) + i) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(static_cast<const int32_t*>(p.pos) + i) : "memory");
+    }
+    __device__ __forceinline__ int64_t at(const QkRopeParams& p, const Walk& W, int axis) const {
+        if (!p.pos) return W.t;
+        if (!ahead(p)) {
+            const int64_t i = (int64_t)axis * p.T + W.t;
+            return p.pos_i64 ? static_cast<const int64_t*>(p.pos)[i] : static_cast<const int32_t*>(p.pos)[i];
+        }
+        const char* q = slots + ((W.n % kPosItems) * kPosAxes + axis) * 8;
+        return p.pos_i64 ? *reinterpret_cast<const int64_t*>(q) : *reinterpret_cast<const int32_t*>(q);
+    }
 };
 
 // The angles of a token, once for the warp: each lane forms up to four pairs' cosines and sines (times the factor)
@@ -154,18 +186,13 @@ struct Angles {
             axis[i] = on && p.axis ? min(max(p.axis[e], 0), p.axes - 1) : 0;
         }
     }
-    __device__ __forceinline__ void at_token(const QkRopeParams& p, int64_t t) {
-        __syncwarp();  // (the last token's have been read)
+    __device__ __forceinline__ void at_token(const QkRopeParams& p, const Positions& pos, const Walk& W) {
+        __syncwarp();  // (the last token's have been read; this one's positions are there)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = (threadIdx.x & 31) + 32 * i;
             if (32 * i >= p.rot / 2) break;
-            int64_t pos = t;
-            if (p.pos) {
-                const int64_t at = axis[i] * p.T + t;
-                pos = p.pos_i64 ? static_cast<const int64_t*>(p.pos)[at] : static_cast<const int32_t*>(p.pos)[at];
-            }
-            const uint64_t turn = (uint64_t)pos * f[i];
+            const uint64_t turn = (uint64_t)pos.at(p, W, axis[i]) * f[i];
             // within half a turn of zero, where the fast sine's absolute error is below 2^-21
             float sn, cs;
             __sincosf((float)(int32_t)(turn >> 32) * 1.4629180792671596e-9f, &sn, &cs);
@@ -257,12 +284,14 @@ template <int VEC, bool NORM, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) qkrope_fwd_kernel(const __grid_constant__ QkRopeParams p) {
     extern __shared__ uint4 smem[];
     __shared__ __align__(16) float angles[kRopeWarps][256];
+    __shared__ __align__(8) char coming[kRopeWarps][kPosItems * kPosAxes * 8];
     griddep_launch_dependents();
     griddep_wait();
     const bool keys = (int)blockIdx.x >= p.q.blocks;
     const RopeSide& S = keys ? p.k : p.q;
     const Place<VEC, INTER> at(p);
     const Pieces<VEC> pieces(smem);
+    const Positions pos(coming[threadIdx.x >> 5]);
     Walk W(S, keys ? p.q.blocks : 0);
     if (!W.more(p, S)) return;
     Walk A = W;  // asks kFwdStages steps ahead
@@ -270,6 +299,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) qkrope_fwd_kernel(cons
     const uint16_t* x = S.x + at.sub * S.x_hs + at.at[0];
     uint16_t* y = S.y + at.sub * S.y_hs + at.at[0];
     const int64_t x_step = at.hpw * S.x_hs, y_step = at.hpw * S.y_hs;
+    bool fresh_ask = true;
     auto ask = [&](int stage) {
         if (A.more(p, S)) {
             const uint16_t* src = x + A.at(S.x_ts, S.x_hs);
@@ -279,7 +309,8 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) qkrope_fwd_kernel(cons
                     pieces.ask((stage * kFwdHeads + i) * 2, src + i * x_step);
                     pieces.ask((stage * kFwdHeads + i) * 2 + 1, src + i * x_step + gap);
                 }
-            A.next(S, heads);
+            if (fresh_ask) pos.ask(p, A);
+            fresh_ask = A.next(S, heads);
         }
         commit();  // (a group a turn, empty ones too: the wait below counts them)
     };
@@ -292,11 +323,11 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas) qkrope_fwd_kernel(cons
     const float inv_d = 1.f / (float)p.d;
     bool fresh = true;
     for (int stage = 0; W.more(p, S); stage = stage + 1 == kFwdStages ? 0 : stage + 1) {
+        wait_for<kFwdStages - 1>();
         if (fresh) {
-            angle.at_token(p, W.t);
+            angle.at_token(p, pos, W);
             angle.take(at, c, s, ns);
         }
-        wait_for<kFwdStages - 1>();
         uint32_t u[kFwdHeads][VEC];
 #pragma unroll
         for (int i = 0; i < kFwdHeads; ++i) pieces.take((stage * kFwdHeads + i) * 2, u[i]);
@@ -346,18 +377,21 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
     constexpr int kTensors = NORM ? 4 : 2;  // vectors of a head: dy, and for the norm x
     extern __shared__ uint4 smem[];
     __shared__ __align__(16) float angles[kRopeWarps][256];  // (in the end the warps' sums)
+    __shared__ __align__(8) char coming[kRopeWarps][kPosItems * kPosAxes * 8];
     griddep_launch_dependents();
     griddep_wait();
     const bool keys = (int)blockIdx.x >= p.q.blocks;
     const RopeSide& S = keys ? p.k : p.q;
     const Place<VEC, INTER> at(p);
     const Pieces<VEC> pieces(smem);
+    const Positions pos(coming[threadIdx.x >> 5]);
     Walk W(S, keys ? p.q.blocks : 0);
     Walk A = W;
     const int gap = at.at[1] - at.at[0];
     const uint16_t* dy = S.dy + at.sub * S.dy_hs + at.at[0];
     const uint16_t* x = NORM ? S.x + at.sub * S.x_hs + at.at[0] : nullptr;
     uint16_t* dx = S.y + at.sub * S.y_hs + at.at[0];
+    bool fresh_ask = true;
     auto ask = [&](int stage) {
         if (A.more(p, S)) {
             if (at.on && A.h + at.sub < A.h1) {
@@ -370,7 +404,8 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
                     pieces.ask(kTensors * stage + 3, src + gap);
                 }
             }
-            A.next(S, at.hpw);
+            if (fresh_ask) pos.ask(p, A);
+            fresh_ask = A.next(S, at.hpw);
         }
         commit();
     };
@@ -385,11 +420,11 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
     const float inv_d = 1.f / (float)p.d;
     bool fresh = true;
     for (int stage = 0; W.more(p, S); stage = stage + 1 == kBwdStages ? 0 : stage + 1) {
+        wait_for<kBwdStages - 1>();
         if (fresh) {
-            angle.at_token(p, W.t);
+            angle.at_token(p, pos, W);
             angle.take(at, c, s, ns);
         }
-        wait_for<kBwdStages - 1>();
         const bool mine = at.on && W.h + at.sub < W.h1;
         uint32_t u[VEC];
         Dims<VEC> g, n;
@@ -513,7 +548,7 @@ static void plan(QkRopeParams& p, int ctas, int heads_at_once) {
 
 template <typename K>
 static cudaError_t launch_pieces(K kernel, int pieces, const QkRopeParams& p, cudaStream_t st) {
-    const size_t smem = (size_t)pieces * kRopeThreads * p.vec * 2;  // (at most 40 KB with the angles' 8: no attribute is needed)
+    const size_t smem = (size_t)pieces * kRopeThreads * p.vec * 2;  // (48 KB at most with the angles and positions: no attribute is needed)
     return launch_pdl(kernel, dim3((unsigned)(p.q.blocks + p.k.blocks)), dim3(kRopeThreads), smem, st, nullptr, 0, p);
 }
 template <int VEC, bool NORM, bool INTER>
