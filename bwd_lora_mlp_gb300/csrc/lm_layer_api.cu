@@ -271,7 +271,7 @@ lm_status check_cross(const lm_cross* a) {
     LL_TRY(need(a->cu_q, 4, "cu_q"));
     LL_TRY(need(a->cu_k, 4, "cu_k"));
     LL_TRY(want(a->k_len, 4, "k_len"));
-    if (a->n_docs < 1) return report_error(LM_ERR_SHAPE, "n_docs = %d must be positive", a->n_docs);
+    if (a->n_docs < 1 || a->n_docs > 1 << 30) return report_error(LM_ERR_SHAPE, "n_docs = %d is not in [1, 2^30]", a->n_docs);
     return LM_OK;
 }
 

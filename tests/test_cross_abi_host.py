@@ -91,7 +91,7 @@ def test_refusals(call, outs, ins):
     for k, v in (("Tq", -1), ("Tk", -1), ("Tk", 2 ** 20 + 1), ("hk", 3), ("d", 60), ("d", 136)):
         assert call(dict(base, **{k: v})) == L.LM_ERR_SHAPE, (k, v)
     for kw in (dict(scale=0.0), dict(scale=-0.125), dict(scale=float("nan")), dict(scale=float("inf")), dict(cap=-1.0),
-               dict(cap=2.0 ** -15), dict(cap=2.0 ** 13), dict(cap=float("nan")), dict(n_docs=0), dict(n_docs=-1), dict(cu_q=None)):
+               dict(cap=2.0 ** -15), dict(cap=2.0 ** 13), dict(cap=float("nan")), dict(n_docs=0), dict(n_docs=-1), dict(n_docs=2 ** 30 + 1), dict(cu_q=None)):
         assert call(with_a(**kw)) == L.LM_ERR_SHAPE, kw
     assert call(with_a(cu_k=None)) == L.LM_ERR_NULL
     for n in ("cu_q", "cu_k", "k_len"):
