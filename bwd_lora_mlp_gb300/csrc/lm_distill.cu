@@ -14,7 +14,8 @@
 // 192 us at 4096 x 131072.)
 // Backward: one pass; outside S, dx_j = (W q_r - p_r) e^{x_j} / sum of e^x outside S, a share of at most 1, which no size
 // of logits overflows.  The entries in a CTA's stretch are read before it is written and written after it.
-// 4096 x 131072 387 us, 5.5 TB/s; 8192 x 32000 198 us, 5.3; 1000 x 50257 33 us, 6.1.
+// 4096 x 131072 348 us, 6.2 TB/s (0.91 of the copy rate); 8192 x 32000 183 us, 5.7; 1000 x 50257 29 us, 6.9 (its logits
+// are in part still in L2).
 #include <algorithm>
 
 #include "lm_rows.cuh"
@@ -311,8 +312,12 @@ cudaError_t launch_distill_fwd(const DistillParams& p, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kDbThreads = 256;
-constexpr int kDbVecs = 8;  // 16-byte vectors of a thread: a CTA takes a stretch of 2048 of them
+// 16-byte vectors of a thread: a CTA takes a stretch of 1024 of them.  Small CTAs, many of them: each waits for its entries
+// and their logits between its loads and its stores, and once more before the entries' own gradients.  (4096 x 131072 and
+// 8192 x 32000: 128 threads of 8 vectors 348 and 183 us, of 10 345 and 178, of 6 369 and 194, of 12 350 and 192; 256 of 8 382
+// and 195, of 4 396 and 234; 512 of 8 413 and 220.)
+constexpr int kDbThreads = 128, kDbVecs = 8;
+static_assert(kDbThreads >= kMaxEntries, "a thread an entry");
 
 template <bool F32, bool REST, bool TWO>
 __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_constant__ DistillParams p, unsigned per_row) {
