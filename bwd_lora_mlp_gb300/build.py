@@ -30,7 +30,7 @@ DIGEST = LIB + ".digest"
 
 SOURCES = ["lm_api.cu", "lm_aux.cu", "lm_gemm_fwd.cu", "lm_gemm_bwd.cu", "lm_gemm2.cu", "lm_gemm2_nf4.cu", "lm_static_ws.cu",
            "lm_dual.cu", "lm_layer_api.cu", "lm_attn.cu", "lm_attn_fwd.cu", "lm_attn_bwd.cu", "lm_addnorm.cu", "lm_logprob.cu", "lm_qkrope.cu",
-           "lm_distill.cu", "lm_cross.cu"]
+           "lm_distill.cu", "lm_cross.cu", "lm_cross_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

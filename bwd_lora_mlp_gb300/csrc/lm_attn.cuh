@@ -57,9 +57,9 @@ __device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
 }
 
 // Whose keys: the queries' own tokens (SELF), or those of another tensor of another length (CROSS; FEW: few queries, the
-// heads of a group packed into one tile and the keys split).  The keys [lo, hi) that query t sees, and
+// heads of a group packed into one tile and the keys split; PARTS: CROSS, the backward's sums in parts).  The keys [lo, hi) that query t sees, and
 // the queries [qlo, qhi) that see key t: the ends do not decrease over the tokens in either form.
-enum AttnForm : int { ATTN_SELF = 0, ATTN_CROSS = 1, ATTN_FEW = 2 };
+enum AttnForm : int { ATTN_SELF = 0, ATTN_CROSS = 1, ATTN_FEW = 2, ATTN_PARTS = 3 };
 template <int FORM>
 __device__ __forceinline__ TokRange query_range(const AttnParams& p, int t) {
     if constexpr (FORM == ATTN_SELF) return tok_range(p, t);
@@ -373,6 +373,26 @@ __device__ __forceinline__ void store_dims(uint16_t* dst, uint32_t t, int c0, in
         } else {  // (d = 8 modulo 16: rows lie on 16 bytes, and the last chunk is half there)
             *reinterpret_cast<uint4*>(q) = make_uint4(v[0], v[1], v[2], v[3]);
             if (c0 + c + 8 < d) *reinterpret_cast<uint4*>(q + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+// The same in fp32 (a part of a sum that another kernel joins).
+template <int N>
+__device__ __forceinline__ void store_dims_f32(float* dst, uint32_t t, int c0, int d, float f, bool any, bool mine) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t o[16];
+        if (any) {
+            tmem_ld_x16(t + c0 + c, o);
+            tmem_ld_wait16(o);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (any)
+                v = make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
+                                __uint_as_float(o[e + 3]) * f);
+            if (mine && c0 + c + e < d) *reinterpret_cast<float4*>(dst + c0 + c + e) = v;
         }
     }
 }

@@ -118,7 +118,10 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (under a causal mask the first keys, seen by most, come first)
-    const int item = (int)blockIdx.x / split, rank = (int)blockIdx.x % split;
+    // PARTS: `kparts` CTAs that are no cluster share a key tile; their sums are joined by another kernel
+    constexpr bool kShares = SHARED || FORM == ATTN_PARTS;
+    const int shares = SHARED ? split : FORM == ATTN_PARTS ? p.kparts : 1;
+    const int item = (int)blockIdx.x / shares, rank = (int)blockIdx.x % shares;
     const int g = item % p.hk, n = p.hq / p.hk;
 
     griddep_launch_dependents();
@@ -157,9 +160,9 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
     const TokRange rf = key_range<FORM>(p, k0), rl = key_range<FORM>(p, min(k0 + kTile, p.Tk) - 1);
     const int qt0 = uni(rf.qlo / kTile), nt = uni(rl.qhi > rf.qlo ? (rl.qhi + kTile - 1) / kTile - qt0 : 0);
     // (head of the group, query tile) pairs, heads outermost: this CTA's are [first, first + N)
-    auto begin = [&](int r) { return (int)((int64_t)nt * n * r / split); };
-    const int first = SHARED ? begin(rank) : 0, N = SHARED ? begin(rank + 1) - first : nt * n;
-    const int hh0 = SHARED && nt ? first / nt : 0, qi0 = SHARED && nt ? first % nt : 0;
+    auto begin = [&](int r) { return (int)((int64_t)nt * n * r / shares); };
+    const int first = kShares ? begin(rank) : 0, N = kShares ? begin(rank + 1) - first : nt * n;
+    const int hh0 = kShares && nt ? first / nt : 0, qi0 = kShares && nt ? first % nt : 0;
 
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
@@ -175,8 +178,8 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
                 // (which queries see something is asked for a tile ahead, as which keys are seen below)
                 uint4 seen = make_uint4(0, 0, 0, 0);
                 if (FORM != ATTN_SELF && p.qseen) seen = p.qseen[qt0 + qi0];
-                for (int hh = hh0; ok && (SHARED ? no < (uint32_t)N : hh < n); ++hh)
-                    for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || no < (uint32_t)N); ++qt) {
+                for (int hh = hh0; ok && (kShares ? no < (uint32_t)N : hh < n); ++hh)
+                    for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!kShares || no < (uint32_t)N); ++qt) {
                         const int h = g * n + hh;
                         const uint32_t s = no % kQStages, ph = (no / kQStages) & 1u;
                         const uint32_t bq = smem_u32(&qfull[s]), bo = smem_u32(&ofull[s]);
@@ -361,9 +364,9 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
             return true;
         };
         int it = 0;
-        for (int hh = hh0; ok && (SHARED ? it < N : hh < n); ++hh) {
+        for (int hh = hh0; ok && (kShares ? it < N : hh < n); ++hh) {
             if (biased(MODE)) S.slope = p.slopes[g * n + hh] * kLog2e;
-            for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!SHARED || it < N); ++qt, ++it) {
+            for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!kShares || it < N); ++qt, ++it) {
                 const int q0 = qt * kTile + part * 32;
                 const float* row = srow + (it % kQStages) * 2 * kTile + part * 32;
                 // every query of the tile sees every key of this one, or some pair is hidden
@@ -392,11 +395,15 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
         }
         // (b's box, of 64 dims of dV or dK, is the (b % split)-th CTA's to write)
         constexpr int kBoxes = DP / 64;
-        const int r128 = (warp & 3) * 32 + lane, b = part % kBoxes, owner = part % split;
+        const int r128 = (warp & 3) * 32 + lane, b = part % kBoxes, owner = SHARED ? part % split : 0;
         const bool key = part >= kBoxes;
         const uint32_t acc = (key ? tdk : tdv) + lanes + b * 64;
         uint8_t* box = sk + part * kBoxBytes;  // (staged where the keys and values were)
-        if (!SHARED) {
+        if (FORM == ATTN_PARTS && p.kparts > 1) {  // this share's sums, in fp32
+            if (ok && part < 2 * kBoxes)
+                store_dims_f32<64>(p.part_dkv + ((((int64_t)rank * 2 + (key ? 1 : 0)) * p.Tk + k) * p.hk + g) * p.d,
+                                   (key ? tdk : tdv) + lanes, b * 64, p.d, key ? gradient_scale<MODE>(p) : 1.f, N > 0, k < p.Tk);
+        } else if (!SHARED) {
             if (group_ok(ok, s_bad + part, 1 + part) && part < 2 * kBoxes) {
                 stage_row(box, r128, acc, key ? gradient_scale<MODE>(p) : 1.f, N > 0);
                 store_box(key ? &maps.dK : &maps.dV, box, b * 64, g, k0, 1 + part, r128 == 0);
@@ -475,7 +482,8 @@ struct DqCfg {
 // forwards and backwards in turn).  CTAs stay: the next item's operands load and its first scores are
 // formed while this one's rows are written (10 thousand cycles an item otherwise, as much as five tiles).
 struct DqItem {
-    int h, q0, kt0, N;    // key tiles [kt0, kt0 + N)
+    int h, q0, kt0, N;    // key tiles [kt0, kt0 + N) (PARTS: one of `qparts` parts of them)
+    int part;
     int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row
     bool valid;
 };
@@ -485,13 +493,22 @@ struct DqCtas {
 };
 template <int FORM>
 __device__ __forceinline__ DqItem dq_item(const AttnParams& p, const DqCtas& who, int k) {
-    const int nqt = (p.T + kTile - 1) / kTile;
-    const int idx = k & 1 ? (k + 1) * who.of - 1 - who.at : k * who.of + who.at;
-    DqItem it{idx % p.hq, (nqt - 1 - idx / p.hq) * kTile, 0, 0, 0, 0, idx < nqt * p.hq};
+    const int nqt = (p.T + kTile - 1) / kTile, parts = FORM == ATTN_PARTS ? p.qparts : 1;
+    int idx = k & 1 ? (k + 1) * who.of - 1 - who.at : k * who.of + who.at, part = 0;
+    if (FORM == ATTN_PARTS) {
+        part = idx % parts;
+        idx /= parts;
+    }
+    DqItem it{idx % p.hq, (nqt - 1 - idx / p.hq) * kTile, 0, 0, part, 0, 0, idx < nqt * p.hq};
     if (it.valid) {
         const TokRange rf = query_range<FORM>(p, it.q0), rl = query_range<FORM>(p, min(it.q0 + kTile, p.T) - 1);
         it.kt0 = rf.lo / kTile;
         it.N = rl.hi > rf.lo ? (rl.hi + kTile - 1) / kTile - it.kt0 : 0;
+        if (FORM == ATTN_PARTS) {  // (at most 2^13 tiles and a few hundred parts)
+            const int from = it.N * part / parts, to = it.N * (part + 1) / parts;
+            it.kt0 += from;
+            it.N = to - from;
+        }
         it.lo_max = rl.lo;
         it.hi_min = rf.hi;
     }
@@ -562,7 +579,7 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
     griddep_wait();
     const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
     const uint32_t tdp = tmem + 2 * kTile, tdq = tmem + 3 * kTile;
-    const int rounds = ((p.T + kTile - 1) / kTile * p.hq + who.of - 1) / who.of;
+    const int rounds = ((p.T + kTile - 1) / kTile * p.hq * (FORM == ATTN_PARTS ? p.qparts : 1) + who.of - 1) / who.of;
 
     if (warp >= kBwdMath) {
         regs_down<kBwdIssueRegs>();
@@ -805,7 +822,10 @@ __device__ __forceinline__ void attn_dq(const AttnParams& p, const BwdMaps& maps
             }
             // each warpgroup a quarter of the dims, a thread one row of them
             const int i = it.q0 + row;
-            store_dims<DP / 4>(p.out + ((int64_t)i * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d, gradient_scale<MODE>(p),
+            if (FORM == ATTN_PARTS && p.qparts > 1)
+                store_dims_f32<DP / 4>(p.part_dq + (((int64_t)it.part * p.T + i) * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d,
+                                       gradient_scale<MODE>(p), it.N > 0, i < p.T);
+            else store_dims<DP / 4>(p.out + ((int64_t)i * p.hq + it.h) * p.d, tdq + lanes, part * (DP / 4), p.d, gradient_scale<MODE>(p),
                                it.N > 0, i < p.T);
             tc_fence_before();  // (the next item's products may overwrite dQ once dz says so)
         }
@@ -856,17 +876,19 @@ cudaError_t launch_both(const AttnParams& p, const BwdMaps& maps, int sms, cudaS
     const int tiles = (p.T + kTile - 1) / kTile, items = (p.Tk + kTile - 1) / kTile * p.hk;  // (of queries; of keys)
     const int reach = p.window > 0 && p.window / kTile + 2 < tiles ? p.window / kTile + 2 : tiles;
     int split = 1;
-    while (split < DkvCfg<DP>::kMaxSplit) {
+    while (FORM != ATTN_PARTS && split < DkvCfg<DP>::kMaxSplit) {
         const int pairs = p.hq / p.hk * reach / split, after = items * split * 2;
         if (!(after <= sms && pairs >= 8) && !(after <= 2 * sms && pairs >= 32)) break;
         split *= 2;
     }
     // dQ's CTAs stay and take items, but a few an SM, as those that start late should have less to do (8192 tokens in
     // 14 documents: 506 us with four, 516 with one or two, 515 with eight)
-    const int64_t dq_items = (int64_t)tiles * p.hq;
+    const int64_t dq_items = (int64_t)tiles * p.hq * (FORM == ATTN_PARTS ? p.qparts : 1);
     const int dq = (int)(dq_items < kDqWaves * sms ? dq_items : kDqWaves * sms);
-    return split > 1 ? launch_bwd<DP, MODE, true, FORM>(p, maps, items, split, dq, st)
-                     : launch_bwd<DP, MODE, false, FORM>(p, maps, items, 1, dq, st);
+    if constexpr (FORM != ATTN_PARTS) {
+        if (split > 1) return launch_bwd<DP, MODE, true, FORM>(p, maps, items, split, dq, st);
+    }
+    return launch_bwd<DP, MODE, false, FORM>(p, maps, items * (FORM == ATTN_PARTS ? p.kparts : 1), 1, dq, st);
 }
 
 inline lm_status encode_bwd(const AttnParams& p, BwdMaps* maps) {

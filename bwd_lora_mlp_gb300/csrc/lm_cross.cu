@@ -1,11 +1,11 @@
-// Cross attention (include/lora_layer.h): queries of T tokens, keys and values of another tensor of Tk.
+// Cross attention forward (include/lora_layer.h): queries of T tokens, keys and values of another tensor of Tk.  The
+// backward is in lm_cross_bwd.cu.
 // The kernels are attention's own (lm_attn_fwd.cuh, lm_attn_bwd.cuh); what a query sees is an interval of keys whose
 // ends do not decrease here too, read from tables of its own.  Few queries have another form of the forward: the rows
 // of a tile are the heads of a group, token by token, so a key tile is read once for all of them, and the keys
 // are dealt out in parts, one CTA each; a second kernel joins the parts' sums in order.
 #include <algorithm>
 
-#include "lm_attn_bwd.cuh"
 #include "lm_attn_fwd.cuh"
 
 namespace lm {
@@ -68,8 +68,6 @@ cudaError_t launch_fill(float* out, int64_t n, float v, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ few queries
-// GB300's SMs: the workspace's size has to be known on a host without one.
-constexpr int kCrossSms = 152;
 FewPlan plan_few(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk) {
     const int group = hq / hk;
     FewPlan P{0, 0, 0};
@@ -191,18 +189,6 @@ lm_status launch_cross_fwd(const AttnParams& given, int sms, cudaStream_t st) {
         e = rows <= kCrossSms ? join<8>(p, rows, st) : join<4>(p, rows, st);
     }
     return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "cross attention forward launch: %s", cudaGetErrorString(e));
-}
-
-template <int DP>
-static cudaError_t bwd_modes(const AttnParams& p, const BwdMaps& maps, int sms, cudaStream_t st) {
-    return p.cap > 0.f ? launch_both<DP, ATTN_CAP, ATTN_CROSS>(p, maps, sms, st) : launch_both<DP, ATTN_PLAIN, ATTN_CROSS>(p, maps, sms, st);
-}
-lm_status launch_cross_bwd(const AttnParams& p, int sms, cudaStream_t st) {
-    BwdMaps maps;
-    const lm_status s = encode_bwd(p, &maps);
-    if (s != LM_OK) return s;
-    const cudaError_t e = p.d <= 64 ? bwd_modes<64>(p, maps, sms, st) : bwd_modes<128>(p, maps, sms, st);
-    return e == cudaSuccess ? LM_OK : report_error(LM_ERR_CUDA, "cross attention backward launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace lm

@@ -59,6 +59,8 @@ struct AttnParams {
     int32_t splits, parts;      // few queries: CTAs that share the keys; parts that are joined, T x hq rows each
     float* part_o;
     float2* part_ml;
+    int32_t kparts, qparts;     // cross attention backward: CTAs that share a key tile, parts of a query tile's keys
+    float *part_dkv, *part_dq;  // their sums: [part][dV, dK][Tk][hk][d], [part][T][hq][d]
     uint16_t* out;         // O, or dQ
     int8_t* out_lo;
     float* lse;
@@ -75,6 +77,9 @@ cudaError_t launch_attn_delta(const AttnParams& p, const lm_attn& a, float* ndel
 lm_status launch_attn_bwd(const AttnParams& p, int sms, cudaStream_t st);
 
 // ---- cross attention
+// GB300's SMs, not asked of the device: a workspace's size has to be known on a host without one, and parts, whose sums
+// are joined in order, are the same everywhere.
+constexpr int kCrossSms = 152;
 struct CrossTables {
     int2 *qrange, *krange;
     uint4 *qseen, *kseen;
@@ -86,6 +91,12 @@ struct FewPlan {
     int32_t splits, parts, tokens;
 };
 FewPlan plan_few(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk);
+// the backward's parts (1: none), of a call with `docs` documents (1: without), and the most that any such call has
+struct BwdParts {
+    int32_t k, q;
+};
+BwdParts plan_parts(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d, int32_t docs);
+BwdParts most_parts(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk);
 cudaError_t launch_fill(float* out, int64_t n, float v, cudaStream_t st);
 lm_status launch_cross_fwd(const AttnParams& p, int sms, cudaStream_t st);
 lm_status launch_cross_bwd(const AttnParams& p, int sms, cudaStream_t st);

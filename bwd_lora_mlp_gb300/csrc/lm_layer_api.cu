@@ -277,7 +277,7 @@ lm_status check_cross(const lm_cross* a) {
 
 struct CrossPlan {
     FewPlan few;
-    size_t qrange, krange, qseen, kseen, delta, nlse, part_ml, part_o, total;
+    size_t qrange, krange, qseen, kseen, delta, nlse, part_ml, part_o, part_dkv, part_dq, total;
 };
 
 CrossPlan plan_cross(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d) {
@@ -298,7 +298,12 @@ CrossPlan plan_cross(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, int32_t d) 
     P.nlse = take((size_t)whole_tiles(Tq) * hq * 4);
     P.part_ml = take(rows * sizeof(float2));
     P.part_o = take(rows * d * sizeof(float));
-    P.total = at;
+    const size_t forward = at;  // (the backward's parts lie where the forward's were)
+    at = P.part_ml;
+    const BwdParts most = most_parts(Tq, Tk, hq, hk);
+    P.part_dkv = take(most.k > 1 ? (size_t)most.k * 2 * Tk * hk * d * sizeof(float) : 0);
+    P.part_dq = take(most.q > 1 ? (size_t)most.q * Tq * hq * d * sizeof(float) : 0);
+    P.total = at > forward ? at : forward;
     return P;
 }
 
@@ -417,6 +422,11 @@ extern "C" lm_status cross_bwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, i
     float* nlse = reinterpret_cast<float*>(static_cast<char*>(ws) + P.nlse);
     p.ndelta = delta;
     p.nlse = nlse;
+    const BwdParts parts = plan_parts(Tq, Tk, hq, hk, d, a->cu_q ? a->n_docs : 1);
+    p.kparts = parts.k;
+    p.qparts = parts.q;
+    p.part_dkv = reinterpret_cast<float*>(static_cast<char*>(ws) + P.part_dkv);
+    p.part_dq = reinterpret_cast<float*>(static_cast<char*>(ws) + P.part_dq);
     {
         LaunchTag tag("cross.delta", st);
         LL_TRY(launched(launch_attn_delta(p, lm_attn{}, delta, nlse, nullptr, st), "cross delta launch"));

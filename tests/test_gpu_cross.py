@@ -84,7 +84,9 @@ def _check(*shape, **kw):
 SHAPES = [(1, 1, 1, 1, 64), (1, 2, 2, 1, 128), (1, 129, 4, 2, 128), (2, 700, 32, 8, 128), (5, 127, 5, 1, 64), (31, 300, 6, 2, 80),
           (33, 128, 20, 4, 80), (64, 1000, 8, 8, 64), (127, 65, 2, 2, 64), (129, 257, 4, 4, 96), (257, 128, 8, 2, 64),
           (300, 1, 2, 1, 8), (1, 300, 1, 1, 8), (385, 515, 6, 2, 72), (130, 1300, 16, 1, 128), (700, 90, 32, 8, 128),
-          (3, 40, 300, 1, 16), (7, 1500, 1, 1, 128), (1200, 260, 7, 1, 64)]
+          (3, 40, 300, 1, 16), (7, 1500, 1, 1, 128), (1200, 260, 7, 1, 64),
+          # a key tile of many CTAs; a query tile's keys in parts; both
+          (3000, 78, 4, 1, 64), (2000, 155, 4, 2, 96), (160, 4200, 20, 4, 32), (100, 2000, 4, 1, 128), (1400, 1100, 3, 1, 64)]
 
 
 @pytest.mark.parametrize("Tq,Tk,hq,hk,d", SHAPES)
@@ -103,6 +105,9 @@ SEGMENTS = [  # Tq, Tk, cu_q, cu_k, k_len
     (3, 900, [0, 1, 2, 3], [0, 300, 600, 900], [300, 7, 250]),
     (500, 130, [0, 100, 200, 300, 400, 500], [0, 0, 30, 60, 100, 130], [0, 30, 1, 40, 30]),
     (140, 260, [140, 140], [0, 260], None),                                  # nobody sees anything
+    (2600, 200, [0, 900, 901, 2600], [0, 70, 140, 200], [70, 3, 50]),        # (parts of the backward, as above)
+    (2600, 150, [50, 2500], [10, 150], [100]),
+    (60, 9000, [0, 20, 58], [0, 4500, 8990], [4400, 1]),
 ]
 
 
