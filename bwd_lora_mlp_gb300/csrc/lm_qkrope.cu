@@ -8,8 +8,8 @@
 // turn, and position times that, modulo 2^64, is the angle's place in its turn to 2^-33 of one for positions
 // up to 2^31.  Queries and keys have CTAs of their own, so the backward's weights and sums over tokens are one
 // set of registers; a second kernel joins the CTAs' sums in order.
-// Bound by memory as far as its arithmetic lets it: 8192 tokens, 32 + 8 heads of 128 read from a fused buffer, 80 us a
-// step in a graph, forward 30 (5.6 TB/s, 0.83 of the copy rate) and backward 49 (5.1); 16384 tokens 143 us, 5.9 TB/s.
+// Bound by memory as far as its arithmetic lets it: 8192 tokens, 32 + 8 heads of 128 read from a fused buffer, 78 us a
+// step in a graph, forward 30 (5.6 TB/s, 0.83 of the copy rate) and backward 49 (5.1); 16384 tokens 140 us, 5.9 TB/s.
 // (Heads loaded to registers four at a time by the lane and the angles formed by every lane for itself: 116 and 205.)
 #include <algorithm>
 
@@ -26,7 +26,7 @@ constexpr int kRopeSms = 152;  // GB300's: a workspace's size has to be known on
 constexpr int kFwdHeads = 2, kFwdStages = 2, kBwdStages = 2, kFwdCtas = 2, kBwdCtas = 2;
 static_assert(2 * kFwdHeads * kFwdStages * kRopeThreads * 16 + kRopeWarps * 2048 <= 48 * 1024 &&
               4 * kBwdStages * kRopeThreads * 16 + kRopeWarps * 2048 <= 48 * 1024, "more shared memory has to be asked for");
-// Items a warp has at least, where tokens have parts enough (4097 tokens of 24 heads of 80: 24.5 us; with 16, 26.6).
+// Items a warp has at least, where tokens have parts enough (4097 tokens of 24 heads of 80, CTAs by heads: 24.5 us; with 16, 26.6).
 constexpr int kTurns = 4;
 static_assert(kFwdStages < 4 && kBwdStages < 4, "a place of positions would be written while it is read");
 
@@ -527,9 +527,12 @@ static void plan(QkRopeParams& p, int ctas, int heads_at_once) {
     p.vec = p.d % 16 == 0 && p.rot % 16 == 0 ? 8 : 4;
     p.lanes = 1;
     while (p.lanes * 2 * p.vec < p.d) p.lanes *= 2;
-    const int at_once = 32 / p.lanes * heads_at_once, all = ctas * kRopeSms, heads = p.q.heads + p.k.heads;
-    // CTAs by heads, at least one each
-    const int of_q = p.k.heads ? std::max(1, std::min(all - 1, (all * p.q.heads + heads / 2) / heads)) : all;
+    const int at_once = 32 / p.lanes * heads_at_once, all = ctas * kRopeSms;
+    // CTAs by what a token takes, its steps and half of one for its angles; at least one each.  (8192 tokens of 32 + 1
+    // heads, a step: 68 us, by heads alone 79, a whole step for the angles 73; 64 + 8: 129, 137, 133.)
+    auto cost = [&](const RopeSide& S) { return (S.heads + at_once - 1) / at_once * 2 + 1; };
+    const int both = cost(p.q) + cost(p.k);
+    const int of_q = p.k.heads ? std::max(1, std::min(all - 1, (all * cost(p.q) + both / 2) / both)) : all;
     for (RopeSide* S : {&p.q, &p.k}) {
         S->parts = S->per_part = 1;
         S->blocks = 0;
