@@ -14,7 +14,7 @@
 // 192 us at 4096 x 131072.)
 // Backward: one pass; outside S, dx_j = (W q_r - p_r) e^{x_j} / sum of e^x outside S, a share of at most 1, which no size
 // of logits overflows.  The entries in a CTA's stretch are read before it is written and written after it.
-// 4096 x 131072 348 us, 6.2 TB/s (0.91 of the copy rate); 8192 x 32000 183 us, 5.7; 1000 x 50257 29 us, 6.9 (its logits
+// 4096 x 131072 322 us, 6.7 TB/s (0.98 of the copy rate); 8192 x 32000 173 us, 6.1; 1000 x 50257 28 us, 7.2 (its logits
 // are in part still in L2).
 #include <algorithm>
 
@@ -76,8 +76,15 @@ __device__ __forceinline__ Part join_parts(Part s, float c) {
     return s;
 }
 
+// Which of entries k to k + 3 are of token id, and the first of those that are (beyond all entries: none)
+__device__ __forceinline__ uint32_t same_of(const int* ids, int k, int id) {
+    const int4 v = *reinterpret_cast<const int4*>(ids + k);
+    return (v.x == id ? 1u : 0u) | (v.y == id ? 2u : 0u) | (v.z == id ? 4u : 0u) | (v.w == id ? 8u : 0u);
+}
+__device__ __forceinline__ int before(uint32_t same) { return same ? __ffs((int)same) - 1 : kMaxEntries; }
+
 struct DistillShared {
-    int ids[kMaxEntries];
+    alignas(16) int ids[kMaxEntries];
     float red[kEntryWarps][2], sums[kEntryWarps][4];
     Part warp[kThreads / 32], seg[kMaxCluster];
 };
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     over_entries(e, 0);
     if (REST) {
         bool first = id >= 0 && warp < kEntryWarps;
-        for (int k = 0; k < tid && first; ++k) first = sm.ids[k] != id;
+        for (int k = 0; k < tid && first; k += 4) first = k + before(same_of(sm.ids, k, id)) >= tid;
         over_entries(first ? brought(x, top, c) : 0.f, 1);
         if (TWO) over_entries(first ? brought(x, top, kL2e) : 0.f, 2);
     }
@@ -314,14 +321,15 @@ cudaError_t launch_distill_fwd(const DistillParams& p, cudaStream_t st) {
 // ------------------------------------------------------------------ backward
 // 16-byte vectors of a thread: a CTA takes a stretch of 1024 of them.  Small CTAs, many of them: each waits for its entries
 // and their logits between its loads and its stores, and once more before the entries' own gradients.  (4096 x 131072 and
-// 8192 x 32000: 128 threads of 8 vectors 348 and 183 us, of 10 345 and 178, of 6 369 and 194, of 12 350 and 192; 256 of 8 382
-// and 195, of 4 396 and 234; 512 of 8 413 and 220.)
+// 8192 x 32000: 128 threads of 8 vectors 322 and 173 us, of 10 320 and 172 but 2048 x 32000 44 instead of 42, of 6 337 and 185.
+// With a slower search for tokens given twice, one entry a step, 8 vectors took 345 and 182, 256 threads of them 378 and 191,
+// of 4 392 and 230, 512 of 8 409 and 216.)
 constexpr int kDbThreads = 128, kDbVecs = 8;
 static_assert(kDbThreads >= kMaxEntries, "a thread an entry");
 
 template <bool F32, bool REST, bool TWO>
 __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_constant__ DistillParams p, unsigned per_row) {
-    __shared__ int ids[kMaxEntries];
+    __shared__ __align__(16) int ids[kMaxEntries];
     __shared__ float ps[kMaxEntries];
     griddep_launch_dependents();
     griddep_wait();
@@ -422,11 +430,11 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
     __syncthreads();
     if (id < 0) return;
     float pk = 0.f;
-    for (int k = 0; k < p.K; ++k)
-        if (ids[k] == id) {
-            if (k < tid) return;  // (a token given twice is its first entry's)
-            pk += ps[k];
-        }
+    for (int k = 0; k < p.K; k += 4) {
+        uint32_t same = same_of(ids, k, id);
+        if (same && k + before(same) < tid) return;  // (a token given twice is its first entry's)
+        for (; same; same &= same - 1) pk += ps[k + before(same)];
+    }
     const float q = lp_ex2(fmaf(x - s.top, c, -s.l2));
     float d = gk * fmaf(s.W, q, -pk) + (id == at ? gh : 0.f);
     if (gh != 0.f) d = fmaf(-gh, TWO ? lp_ex2(fmaf(x - s.top, kL2e, -s.l1)) : q, d);
