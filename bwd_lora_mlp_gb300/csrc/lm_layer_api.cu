@@ -275,6 +275,8 @@ lm_status check_cross(const lm_cross* a) {
     return LM_OK;
 }
 
+Span docs_span(const int32_t* p, int64_t n, const char* name) { return Span{p, (size_t)n * 4, name}; }
+
 struct CrossPlan {
     FewPlan few;
     size_t qrange, krange, qseen, kseen, delta, nlse, part_ml, part_o, part_dkv, part_dq, total;
@@ -351,7 +353,9 @@ extern "C" lm_status cross_fwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, i
     if (ws_bytes < P.total) return report_error(LM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, P.total);
     const size_t ob = (size_t)Tq * hq * d * 2, lob = (size_t)Tq * hq * ((d + 15) / 16 * 16), lb = (size_t)Tq * hq * 4;
     LL_TRY(check_alias({{O, ob, "O"}, {O_lo, lob, "O_lo"}, {lse, lb, "lse"}, {ws, P.total, "ws"}},
-                       {heads_span(q, Tq, hq, d, "q"), heads_span(k, Tk, hk, d, "k"), heads_span(v, Tk, hk, d, "v")}));
+                       {heads_span(q, Tq, hq, d, "q"), heads_span(k, Tk, hk, d, "k"), heads_span(v, Tk, hk, d, "v"),
+                        docs_span(a->cu_q, int64_t{a->n_docs} + 1, "cu_q"), docs_span(a->cu_k, int64_t{a->n_docs} + 1, "cu_k"),
+                        docs_span(a->k_len, a->n_docs, "k_len")}));
     if (Tq == 0) return LM_OK;
     int sms = 0;
     LL_TRY(device_ready(&sms));
@@ -398,7 +402,8 @@ extern "C" lm_status cross_bwd(int64_t Tq, int64_t Tk, int32_t hq, int32_t hk, i
     LL_TRY(check_alias({{dQ, bq, "dQ"}, {dK, bk, "dK"}, {dV, bk, "dV"}, {ws, P.total, "ws"}},
                        {heads_span(q, Tq, hq, d, "q"), heads_span(k, Tk, hk, d, "k"), heads_span(v, Tk, hk, d, "v"),
                         heads_span(dO, Tq, hq, d, "dO"), {O, bq, "O"}, {O_lo, (size_t)Tq * hq * ((d + 15) / 16 * 16), "O_lo"},
-                        {lse, (size_t)Tq * hq * 4, "lse"}}));
+                        {lse, (size_t)Tq * hq * 4, "lse"}, docs_span(a->cu_q, int64_t{a->n_docs} + 1, "cu_q"),
+                        docs_span(a->cu_k, int64_t{a->n_docs} + 1, "cu_k"), docs_span(a->k_len, a->n_docs, "k_len")}));
     if (Tq == 0 && Tk == 0) return LM_OK;
     int sms = 0;
     LL_TRY(device_ready(&sms));

@@ -103,6 +103,8 @@ def test_refusals(call, outs, ins):
             if other != out:
                 at = base[other].p if other in heads else base[other]
                 assert call(dict(base, **{out: at})) == L.LM_ERR_ALIAS, (out, other)
+        for n in ("cu_q", "cu_k", "k_len"):
+            assert call(dict(base, **{out: base["a"][n] // 32 * 32})) == L.LM_ERR_ALIAS, (out, n)
     none = dict(_args(Tq=0, Tk=0))
     assert call(none) == L.LM_OK
 
