@@ -84,10 +84,11 @@ struct Place {
     bool turns[2];    // pairs [0, VEC / 2) and the others are rotated, by the angles from pair[0] and from pair[1] on
     int pair[2];
     __device__ __forceinline__ explicit Place(const QkRopeParams& p) {
-        const int lane = threadIdx.x & 31, j = lane & (p.lanes - 1);
+        const int lane = threadIdx.x & 31;
         sub = lane / p.lanes;
         hpw = 32 / p.lanes;
-        on = j * 2 * VEC < p.d;
+        const int j = lane - sub * p.lanes;
+        on = j * 2 * VEC < p.d && sub < hpw;
         if (INTER) {
             at[0] = j * VEC;
             at[1] = p.d / 2 + j * VEC;
@@ -527,6 +528,12 @@ static void plan(QkRopeParams& p, int ctas, int heads_at_once) {
     p.vec = p.d % 16 == 0 && p.rot % 16 == 0 ? 8 : 4;
     p.lanes = 1;
     while (p.lanes * 2 * p.vec < p.d) p.lanes *= 2;
+    // Without a norm lanes have nothing to exchange, and need be no power of two: as many as have dims, where a warp then takes
+    // more heads.  (8192 tokens of 16 + 16 heads of 72: 42 us a step instead of 49; 4097 of 20 + 4 of 80 with three axes 20.5
+    // instead of 21.1.  With the norm, whose sums then take thirds and fifths of a head in turn, 32 + 8 heads of 96 took 90 us
+    // instead of 75, of 80 the same.)
+    const int dims = (p.d + 2 * p.vec - 1) / (2 * p.vec);
+    if (!p.norm && 32 / dims > 32 / p.lanes) p.lanes = dims;
     const int at_once = 32 / p.lanes * heads_at_once, all = ctas * kRopeSms;
     // CTAs by what a token takes, its steps and half of one for its angles; at least one each.  (8192 tokens of 32 + 1
     // heads, a step: 68 us, by heads alone 79, a whole step for the angles 73; 64 + 8: 129, 137, 133.)

@@ -86,6 +86,13 @@ def test_against_the_definition(T, hq, hk, d, rot, inter):
     _check(T, hq, hk, d, rot, inter=inter)
 
 
+@pytest.mark.parametrize("T,hq,hk,d,rot", SHAPES + [(11, 21, 4, 48, 48), (40, 9, 3, 160, 80), (3, 33, 2, 88, 88), (70, 13, 13, 72, 72)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_a_rotation_alone(T, hq, hk, d, rot, inter):
+    """Lanes of a head are then no power of two (5 for 80 dims, 9 for 72, 3 for 24 or 48)."""
+    _check(T, hq, hk, d, rot, inter=inter, norm=False)
+
+
 @pytest.mark.parametrize("kw", [dict(norm=False), dict(norm=False, inter=True, axes=3), dict(axes=3), dict(axes=2, wide=True),
                                 dict(far=1 << 24), dict(far=(1 << 31) - 5001), dict(far=-(1 << 31), wide=True), dict(factor=1.3),
                                 dict(wt=torch.float32, offset=1.0), dict(norm=False, factor=0.5, far=123456)])
