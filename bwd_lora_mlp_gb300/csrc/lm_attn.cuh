@@ -57,8 +57,8 @@ __device__ __forceinline__ TokRange tok_range(const AttnParams& p, int t) {
 }
 
 // Whose keys: the queries' own tokens (SELF), or those of another tensor of another length (CROSS; FEW: few queries, the
-// heads of a group packed into one tile and the keys split; PARTS: CROSS, the backward's sums in parts).  The keys [lo, hi) that query t sees, and
-// the queries [qlo, qhi) that see key t: the ends do not decrease over the tokens in either form.
+// heads of a group packed into one tile and the keys split; PARTS: CROSS, the backward's sums in parts).  The keys
+// [lo, hi) that query t sees, and the queries [qlo, qhi) that see key t: the ends do not decrease over the tokens in any form.
 enum AttnForm : int { ATTN_SELF = 0, ATTN_CROSS = 1, ATTN_FEW = 2, ATTN_PARTS = 3 };
 template <int FORM>
 __device__ __forceinline__ TokRange query_range(const AttnParams& p, int t) {

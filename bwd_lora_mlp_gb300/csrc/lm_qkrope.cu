@@ -4,10 +4,10 @@
 // A head is taken by up to 32 lanes, each two vectors of 8 (or 4) dims that hold whole pairs, so the rotation
 // needs no other lane and a mean a few shuffles.  A warp takes one token at a time: its angles, formed by a lane each
 // and exchanged in shared memory, serve all of the token's heads.  The next heads are on their way to shared memory
-// meanwhile (each thread copies its own pieces: no barrier).  The angle's whole turns have to go before it is rounded: a frequency becomes a 64-bit fraction of a
-// turn, and position times that, modulo 2^64, is the angle's place in its turn to 2^-33 of one for positions
-// up to 2^31.  Queries and keys have CTAs of their own, so the backward's weights and sums over tokens are one
-// set of registers; a second kernel joins the CTAs' sums in order.
+// meanwhile (each thread copies its own pieces: no barrier).  The angle's whole turns have to go before it is rounded: a
+// frequency becomes a 64-bit fraction of a turn, and position times that, modulo 2^64, is the angle's place in its turn
+// to 2^-33 of one for positions up to 2^31.  Queries and keys have CTAs of their own, so the backward's weights and
+// sums over tokens are one set of registers; a second kernel joins the CTAs' sums in order.
 // Bound by memory as far as its arithmetic lets it: 8192 tokens, 32 + 8 heads of 128 read from a fused buffer, 78 us a
 // step in a graph, forward 30 (5.6 TB/s, 0.83 of the copy rate) and backward 49 (5.1); 16384 tokens 140 us, 5.9 TB/s.
 // (Heads loaded to registers four at a time by the lane and the angles formed by every lane for itself: 116 and 205.)
@@ -145,7 +145,8 @@ struct Walk {
 };
 
 // The positions of a warp's coming items: copied ahead with their first heads, an axis a lane.  (Read where they are
-// needed, they were waited for at every item: 16384 tokens 146 us a step, 143 so; 4097 with three axes 28, 24.5 so.)  Four items are on their way at most.
+// needed, they were waited for at every item: 16384 tokens 146 us a step, 143 so; 4097 with three axes 28, 24.5 so.)  Four
+// items are on their way at most.
 constexpr int kPosAxes = 32, kPosItems = 4;
 struct Positions {
     char* slots;  // the warp's
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
     }
 }
 
-// dw of queries (CTA 0) and keys (CTA 1): the sums of the CTAs' partial rows, eight interleaved and then joined.
+// dw of queries (y = 0) and keys (y = 1): the sums of the CTAs' partial rows, 32 of them interleaved and then joined in order.
 __global__ void __launch_bounds__(1024) qkrope_join_kernel(const __grid_constant__ QkRopeParams p) {
     __shared__ float sm[1024];
     griddep_launch_dependents();
