@@ -359,17 +359,19 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
             const int64_t j = s0 + (u * kDbThreads + tid) * W;
             if (j + W <= s1) raw[u] = *reinterpret_cast<const uint4*>(row.p + j * (F32 ? 4 : 2));
         }
-    // the entries of this stretch: their logits are read before anything is written over them
+    // the entries of this stretch: their logits are read before anything is written over them.  (With rest the others'
+    // share of e^x says nothing of them, so a row whose own log probability alone has a gradient asks for them too; what
+    // the teacher thinks of them has no part in it then.)
     int id = -1;
     float x = 0.f;
     if (!none) {
         float pk = 0.f;
-        if (tid < p.K && gk != 0.f) {
+        if (tid < p.K && (REST || gk != 0.f)) {
             id = id_at(p, t, tid);
             if (id < from || id >= s1) id = -1;
             if (id >= 0) {
                 x = row.at(id);
-                pk = expf(teacher_at<REST>(p, t, tid) - s.tl);
+                if (gk != 0.f) pk = expf(teacher_at<REST>(p, t, tid) - s.tl);
             }
         }
         if (tid < kMaxEntries) ids[tid] = id, ps[tid] = pk;
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
     }
     // with one scale, a token's own softmax outside the entries is their share of it times e^{(z - m)} / sum
     const float qr = !REST ? 1.f : s.ml2 == INFINITY ? 0.f : lp_ex2(fmaf(s.m - s.top, c, s.ml2 - s.l2));
-    const float k0 = TWO ? gk * s.coef : fmaf(gk, s.coef, -gh * qr), k1 = -gh;
+    const float coef = gk == 0.f ? 0.f : s.coef, k0 = TWO ? gk * coef : fmaf(gk, coef, -gh * qr), k1 = -gh;
     auto soft = [&](float z) {
         float d = k0 * lp_ex2(fmaf(z - s.m, c, -s.ml2));
         if (TWO) d = fmaf(k1, lp_ex2(fmaf(z - s.top, kL2e, -s.l1)), d);
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
         for (; same; same &= same - 1) pk += ps[k + before(same)];
     }
     const float q = lp_ex2(fmaf(x - s.top, c, -s.l2));
-    float d = gk * fmaf(s.W, q, -pk) + (id == at ? gh : 0.f);
+    float d = (gk == 0.f ? 0.f : gk * fmaf(s.W, q, -pk)) + (id == at ? gh : 0.f);
     if (gh != 0.f) d = fmaf(-gh, TWO ? lp_ex2(fmaf(x - s.top, kL2e, -s.l1)) : q, d);
     put(id, d);
 }
