@@ -29,16 +29,21 @@ constexpr int kEntryWarps = kMaxEntries / 32;
 // value a sum's logarithm is nothing beside the maximum.
 struct Saved {
     float top, l2, l1;  // the row's largest logit; log2 of sum e^{(z - top) scale}, of sum e^{z - top}
-    float m, ml2;       // the same over the logits that are not entries (with rest), at scale
-    float coef, W, tl;  // others: coef 2^{(z - m) c - ml2}; entries: W q - p,  p = e^{y - tl}
+    float m, ml2;       // with rest: the same over the logits that are not entries, at scale; else the teacher's largest value
+                        // and log sum e^{(y - m) scale} over the row's entries
+    float coef, W;      // others: coef times their share of e^x; entries: W q - p
 };
 
-template <bool REST>
 __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t t, int k) {
     const int64_t i = t * p.K + k;
-    const float y = p.v_f32 ? static_cast<const float*>(p.values)[i]
-                            : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.values)[i] << 16);
-    return REST ? y : y * p.scale;  // (log probabilities are what they are)
+    return p.v_f32 ? static_cast<const float*>(p.values)[i]
+                   : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.values)[i] << 16);
+}
+// log p of a value, but for a sum's logarithm: log probabilities are what they are, logits are taken relative to the
+// row's largest before they are scaled, so that nothing is lost of their differences however far from 0 they lie
+template <bool REST>
+__device__ __forceinline__ float teacher_log(float y, float top, float scale) {
+    return REST ? y : (y - top) * scale;
 }
 __device__ __forceinline__ int id_at(const DistillParams& p, int64_t t, int k) {
     const int64_t i = t * p.K + k;
@@ -116,7 +121,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     if (tid < p.K) {
         id = id_at(p, t, tid);
         if (id >= 0 && part == 0) {
-            y = teacher_at<REST>(p, t, tid);
+            y = teacher_at(p, t, tid);
             x = row.at(id);
         }
     }
@@ -241,8 +246,8 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         for (int w = 0; w < kEntryWarps; ++w) v += sm.sums[w][which];
         return v;
     };
-    const float yref = REST || ytop == -INFINITY ? 0.f : ytop;
-    const float e = id >= 0 ? expf(y - yref) : 0.f;
+    const float yref = ytop == -INFINITY ? 0.f : ytop, ly = teacher_log<REST>(y, yref, p.scale);
+    const float e = id >= 0 ? expf(ly) : 0.f;
     over_entries(e, 0);
     if (REST) {
         bool first = id >= 0 && warp < kEntryWarps;
@@ -253,8 +258,8 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     __syncthreads();
     const float E = total_of(0), rest = s.S * brought(s.m, top, c), total = REST ? rest + total_of(1) : rest, log_total = logf(total);
     // sum p (log p - log q); each log p - log q is formed before it is weighed: their sum is far smaller than its parts
-    const float tl = REST ? 0.f : ytop + logf(E), p_k = e == 0.f ? 0.f : REST ? e : e / E;
-    over_entries(p_k == 0.f ? 0.f : p_k * ((y - tl) - ((x - top) * p.scale - log_total)), 3);
+    const float log_E = REST ? 0.f : logf(E), p_k = e == 0.f ? 0.f : REST ? e : e / E;
+    over_entries(p_k == 0.f ? 0.f : p_k * ((ly - log_E) - ((x - top) * p.scale - log_total)), 3);
     __syncthreads();
     if (tid) return;
 
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         const float r1 = s.S1 * brought(s.m, top, kL2e);
         log_total1 = logf(REST ? r1 + total_of(2) : r1);
     }
-    Saved o{top, log_total * kL2e, log_total1 * kL2e, top, log_total * kL2e, 1.f, 1.f, 0.f};
+    Saved o{top, log_total * kL2e, log_total1 * kL2e, 0.f, 0.f, 1.f, 1.f};
     float kl = any ? total_of(3) : 0.f;
     if (REST) {
         const bool others = s.m != -INFINITY;  // some logit outside the entries weighs something
@@ -279,7 +284,8 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         o.ml2 = others ? lr * kL2e : INFINITY;
         o.coef = any && others ? fmaf(o.W, qr, -pr) : 0.f;
     } else {
-        o.tl = any && E != 0.f ? tl : INFINITY;
+        o.m = yref;
+        o.ml2 = any && E != 0.f ? log_E : INFINITY;
         if (!any || E == 0.f) o.coef = o.W = 0.f;
     }
     if (empty) kl = any && E > 0.f ? INFINITY : 0.f;  // no distribution: what the teacher expects is infinitely far
@@ -288,7 +294,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     if (p.logp) p.logp[t] = target < 0 ? 0.f : empty ? -INFINITY : zt - top - log_total1;
     float4* out = reinterpret_cast<float4*>(p.saved + t * 8);
     out[0] = make_float4(o.top, o.l2, o.l1, o.m);
-    out[1] = make_float4(o.ml2, o.coef, o.W, o.tl);
+    out[1] = make_float4(o.ml2, o.coef, o.W, 0.f);
 }
 
 template <bool F32, bool REST, bool TWO, int N>
@@ -349,7 +355,8 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
         else reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
     };
     const float4 s_a = reinterpret_cast<const float4*>(p.saved + t * 8)[0], s_b = reinterpret_cast<const float4*>(p.saved + t * 8)[1];
-    const Saved s{s_a.x, s_a.y, s_a.z, s_a.w, s_b.x, s_b.y, s_b.z, s_b.w};
+    const Saved s{s_a.x, s_a.y, s_a.z, s_a.w, s_b.x, s_b.y, s_b.z};
+    const float m = REST ? s.m : s.top, ml2 = REST ? s.ml2 : s.l2;  // of the logits that coef is a factor of
     const float c = p.scale * kL2e;
     const bool none = (gk == 0.f && gh == 0.f) || s.top == -INFINITY;  // the row's gradient is 0, whatever it holds
     uint4 raw[kDbVecs];
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
             if (id < from || id >= s1) id = -1;
             if (id >= 0) {
                 x = row.at(id);
-                if (gk != 0.f) pk = expf(teacher_at<REST>(p, t, tid) - s.tl);
+                if (gk != 0.f) pk = expf(teacher_log<REST>(teacher_at(p, t, tid), s.m, p.scale) - (REST ? 0.f : s.ml2));
             }
         }
         if (tid < kMaxEntries) ids[tid] = id, ps[tid] = pk;
@@ -381,7 +388,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
     const float qr = !REST ? 1.f : s.ml2 == INFINITY ? 0.f : lp_ex2(fmaf(s.m - s.top, c, s.ml2 - s.l2));
     const float coef = gk == 0.f ? 0.f : s.coef, k0 = TWO ? gk * coef : fmaf(gk, coef, -gh * qr), k1 = -gh;
     auto soft = [&](float z) {
-        float d = k0 * lp_ex2(fmaf(z - s.m, c, -s.ml2));
+        float d = k0 * lp_ex2(fmaf(z - m, c, -ml2));
         if (TWO) d = fmaf(k1, lp_ex2(fmaf(z - s.top, kL2e, -s.l1)), d);
         return d;
     };
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
 #pragma unroll
                     for (int e = 0; e < W; e += 2) {
                         const float2 z = make_float2(logit<F32>(w, e), logit<F32>(w, e + 1));
-                        const float2 q = __ffma2_rn(__fadd2_rn(z, make_float2(-s.m, -s.m)), make_float2(c, c), make_float2(-s.ml2, -s.ml2));
+                        const float2 q = __ffma2_rn(__fadd2_rn(z, make_float2(-m, -m)), make_float2(c, c), make_float2(-ml2, -ml2));
                         float2 r = __fmul2_rn(make_float2(lp_ex2(q.x), lp_ex2(q.y)), make_float2(k0, k0));
                         if (TWO) {
                             const float2 l1 = __ffma2_rn(__fadd2_rn(z, make_float2(-s.top, -s.top)), make_float2(kL2e, kL2e),
