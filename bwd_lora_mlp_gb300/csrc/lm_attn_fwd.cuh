@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), 1);
+            // (a slot is free when its products are done, and when the clearing warp has been there: it looks at every fill of
+            // every slot, and would miss one that the next had replaced)
+            mbar_init(smem_u32(&empty[s]), FORM != ATTN_SELF && p.kseen ? 2 : 1);
             if (FORM != ATTN_SELF) mbar_init(smem_u32(&clean[s]), 1);
         }
         for (int w = 0; w < 2; ++w) {
@@ -439,7 +441,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     if (!mbar_wait_warp(smem_u32(&full[s]), (n / C::kSlots) & 1u, s_abort, p.wait_ns)) return false;
                     if (kv) clear_unseen_warp(ring + s * C::kTileBytes, DP / 64, s_seen[s]);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&clean[s]));
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&clean[s]));
+                        mbar_arrive(smem_u32(&empty[s]));
+                    }
                 }
                 return true;
             };
