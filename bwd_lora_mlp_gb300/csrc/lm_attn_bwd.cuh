@@ -177,7 +177,7 @@ __device__ __forceinline__ void attn_dkv(const AttnParams& p, const BwdMaps& map
                 uint32_t it = 0, no = 0;  // query and dO tiles asked for
                 // (which queries see something is asked for a tile ahead, as which keys are seen below)
                 uint4 seen = make_uint4(0, 0, 0, 0);
-                if (FORM != ATTN_SELF && p.qseen) seen = p.qseen[qt0 + qi0];
+                if (FORM != ATTN_SELF && p.qseen && N > 0) seen = p.qseen[qt0 + qi0];  // (none: qt0 may be past the last tile)
                 for (int hh = hh0; ok && (kShares ? no < (uint32_t)N : hh < n); ++hh)
                     for (int qt = qt0 + (hh == hh0 ? qi0 : 0); qt < qt0 + nt && (!kShares || no < (uint32_t)N); ++qt) {
                         const int h = g * n + hh;
