@@ -1,5 +1,6 @@
 // C ABI of the layer operators: argument validation, workspace layout and the kernel sequence of
 // each entry point.  See include/lora_layer.h for the contract.
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -734,7 +735,9 @@ lm_status check_qkrope(const lm_qkrope* r, int32_t hk, int32_t d) {
         LL_TRY(must_be_null(r->axis, "axis", "with rot = 0"));
     }
     if (r->norm) {
-        if (!(r->eps > 0.f) || !std::isfinite(r->eps)) return report_error(LM_ERR_SHAPE, "eps = %g must be positive", r->eps);
+        // (the kernels' reciprocal root takes subnormals for 0, and a head of zeros would be 0 x inf)
+        if (!(r->eps >= FLT_MIN) || !std::isfinite(r->eps))
+            return report_error(LM_ERR_SHAPE, "eps = %g must be at least 2^-126", r->eps);
         if (!std::isfinite(r->w_offset)) return report_error(LM_ERR_SHAPE, "w_offset is not finite");
         LL_TRY(want(r->w_q, r->w_dtype == LM_F32 ? 4 : 2, "w_q"));
         LL_TRY(want(r->w_k, r->w_dtype == LM_F32 ? 4 : 2, "w_k"));

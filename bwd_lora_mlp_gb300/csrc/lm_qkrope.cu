@@ -1,6 +1,7 @@
 // Norms of query and key heads with the rotation by position in the same pass (include/lora_layer.h).
 //   n = x r w,  r = rsqrt(mean x^2 + eps);    (a, b) -> f (a cos - b sin, b cos + a sin)
-//   backward: g the rotation's transpose of dy,  dw = sum g x r,  dx = r (g w - x r^2 mean(g w x))
+//   backward: g the rotation's transpose of dy,  dw = sum g x r,  dx = r (g w - x r^2 mean(g w x))  (multiplied in this order:
+//   r^3 overflows where a head and eps are tiny)
 // A head is taken by up to 32 lanes, each two vectors of 8 (or 4) dims that hold whole pairs, so the rotation
 // needs no other lane and a mean a few shuffles.  A warp takes one token at a time: its angles, formed by a lane each
 // and exchanged in shared memory, serve all of the token's heads.  The next heads are on their way to shared memory
@@ -276,7 +277,7 @@ __device__ __forceinline__ void wait_for() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float rsqrt_fast(float x) {  // (2^-22.9 of itself; x > 0)
+__device__ __forceinline__ float rsqrt_fast(float x) {  // (2^-22.9 of itself; x at least eps, which is no subnormal)
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
                 dt += __shfl_xor_sync(0xffffffffu, dt, o);
             }
             const float r = rsqrt_fast(fmaf(q, inv_d, p.eps));
-            const float2 r2 = both2(r), m = both2(-dt * inv_d * r * r * r);
+            const float2 r2 = both2(r), m = both2(-dt * inv_d * r * r);
             if (mine)  // (a slot that no copy came to holds anything)
 #pragma unroll
                 for (int i = 0; i < VEC / 2; ++i) {
@@ -468,8 +469,8 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas) qkrope_bwd_kernel(cons
                 }
 #pragma unroll
             for (int i = 0; i < VEC / 2; ++i) {
-                g.a[i] = __ffma2_rn(n.a[i], m, __fmul2_rn(g.a[i], __fmul2_rn(wa[i], r2)));
-                g.b[i] = __ffma2_rn(n.b[i], m, __fmul2_rn(g.b[i], __fmul2_rn(wb[i], r2)));
+                g.a[i] = __fmul2_rn(__ffma2_rn(n.a[i], m, __fmul2_rn(g.a[i], wa[i])), r2);
+                g.b[i] = __fmul2_rn(__ffma2_rn(n.b[i], m, __fmul2_rn(g.b[i], wb[i])), r2);
             }
         }
         g.to(u, INTER);

@@ -456,7 +456,7 @@ class QkRope:
     None: no rotation): pair p turns by pos[axis[p]][token] * inv_freq[p], and the rotated dims are multiplied
     by ``factor``.  Pairs are dims (p, p + len) or, ``interleaved``, (2p, 2p + 1).  inv_freq: float32; pos: int32 or
     int64, (T), or (axes, T) with axis (int32, an axis for each pair; numbers outside are clamped); None: the
-    token's index."""
+    token's index.  eps: at least 2^-126."""
     inv_freq: Optional[torch.Tensor] = None
     pos: Optional[torch.Tensor] = None
     axis: Optional[torch.Tensor] = None

@@ -202,7 +202,7 @@ typedef struct lm_qkrope {
     const void* w_q;
     const void* w_k;
     float factor;
-    float eps; /* > 0 */
+    float eps; /* at least 2^-126 (no subnormal) */
     float w_offset;
     int32_t rot;
     int32_t axes;
