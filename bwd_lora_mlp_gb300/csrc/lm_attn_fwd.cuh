@@ -127,6 +127,24 @@ __device__ __forceinline__ int rounds_of(const AttnParams& p) {
     return (n + (int)gridDim.x - 1) / (int)gridDim.x;
 }
 
+// The keys [lo, hi) that some query of an item sees (hi past every place where they end with the last one), and whether
+// all of its queries see the same.
+struct ItemKeys {
+    int lo, hi;
+    bool alike;
+    // the rows of key tile j that are in there
+    __device__ __forceinline__ uint4 of_tile(int j) const {
+        const int a = lo - j * kTile, z = hi - j * kTile;
+        if (a <= 0 && z >= kTile) return make_uint4(~0u, ~0u, ~0u, ~0u);
+        return make_uint4(bits_between(a, z), bits_between(a - 32, z - 32), bits_between(a - 64, z - 64), bits_between(a - 96, z - 96));
+    }
+};
+template <int FORM>
+__device__ __forceinline__ ItemKeys keys_of(const AttnParams& p, int q0, int tokens) {
+    const TokRange a = query_range<FORM>(p, q0), b = query_range<FORM>(p, min(q0 + tokens, p.T) - 1);
+    return ItemKeys{a.lo, b.hi == p.Tk ? 1 << 30 : b.hi, a.lo == b.lo && a.hi == b.hi};
+}
+
 // The key tiles that a CTA takes, in order.
 struct FewTiles {
     int n, first;          // first of them, or < 0: they are listed
@@ -177,6 +195,79 @@ __device__ __forceinline__ FewTiles few_setup(const AttnParams& p, uint16_t* lis
     return FewTiles{z - a, -1, list};
 }
 
+// O of query i and head h again, from its own keys alone, by a warp: dims [c0, c0 + 32 N), N a lane.  Where the queries
+// of an item are of several documents its products multiply the others' values by weights of 0, which leaves a NaN where
+// such a value is not finite; the weights and their sums are of the query's own keys in any case.  So what is finite stands,
+// and the rest is formed again and written where that is finite.  (Nothing but an infinity or NaN among
+// the values comes here, so it is simple: a lane a key, then a lane N dims.  A batch of 64 sequences of 1024 states with one
+// NaN 0.7 ms instead of 58 us; 4097 queries in nine documents, 32 heads, 3.5 ms instead of 97 us.)
+template <int MODE, int N>
+__device__ __forceinline__ void own_row(const AttnParams& p, int i, int h, int c0) {
+    const int lane = threadIdx.x & 31, g = h / (p.hq / p.hk), c = c0 + lane * N;
+    const float lse = p.lse[(int64_t)h * p.T + i];
+    if (!(fabsf(lse) < INFINITY)) return;  // (it sees nothing, or its own scores are not finite)
+    uint16_t* out = p.out + ((int64_t)i * p.hq + h) * p.d;
+    bool open[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) open[e] = c + e < p.d && (out[c + e] & 0x7F80u) == 0x7F80u;
+    const TokRange t = query_range<ATTN_CROSS>(p, i);
+    const uint16_t *q = p.q.p + (int64_t)i * p.q.ts + (int64_t)h * p.q.hs, *k = p.k.p + (int64_t)g * p.k.hs, *v = p.v.p + (int64_t)g * p.v.hs;
+    const float sc = capped(MODE) ? 2.f * kLog2e * p.scale / p.cap : p.scale * kLog2e, sx = capped(MODE) ? 2.f * p.cap * kLog2e : sc;
+    float m = -INFINITY, l = 0.f, o[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) o[e] = 0.f;
+#pragma unroll 1
+    for (int j0 = t.lo; j0 < t.hi; j0 += 32) {
+        bool left = false;
+#pragma unroll
+        for (int e = 0; e < N; ++e) left |= open[e] && fabsf(o[e]) < INFINITY;
+        if (!__any_sync(0xffffffffu, left)) return;  // its own values are not finite either
+        float x = 0.f;
+        if (j0 + lane < t.hi) {
+            const uint16_t* kj = k + (int64_t)(j0 + lane) * p.k.ts;
+#pragma unroll 1
+            for (int b = 0; b < p.d; b += 8) {
+                const uint4 a = *reinterpret_cast<const uint4*>(q + b), w = *reinterpret_cast<const uint4*>(kj + b);
+                x = fmaf(bf16lo(a.x), bf16lo(w.x), fmaf(bf16hi(a.x), bf16hi(w.x), x));
+                x = fmaf(bf16lo(a.y), bf16lo(w.y), fmaf(bf16hi(a.y), bf16hi(w.y), x));
+                x = fmaf(bf16lo(a.z), bf16lo(w.z), fmaf(bf16hi(a.z), bf16hi(w.z), x));
+                x = fmaf(bf16lo(a.w), bf16lo(w.w), fmaf(bf16hi(a.w), bf16hi(w.w), x));
+            }
+        }
+        x = j0 + lane < t.hi ? (capped(MODE) ? cap_n(two(x * sc)).x : x) * sx : -INFINITY;
+        float top = x;
+#pragma unroll
+        for (int b = 16; b; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+        if (top > m) {
+            const float f = ex2(m - top);  // (0 for the first keys)
+            m = top;
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] *= f;
+        }
+        const float w = x == -INFINITY ? 0.f : ex2(x - m);
+        l += w;
+#pragma unroll 4
+        for (int b = 0; b < 32; ++b) {
+            const float wb = __shfl_sync(0xffffffffu, w, b);
+            const uint16_t* vj = v + (int64_t)(j0 + b) * p.v.ts + c;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (j0 + b < t.hi && c + e < p.d) o[e] = fmaf(wb, bf16lo(vj[e]), o[e]);
+        }
+    }
+#pragma unroll
+    for (int b = 16; b; b >>= 1) l += __shfl_xor_sync(0xffffffffu, l, b);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (open[e] && fabsf(o[e]) < INFINITY) {
+            const float y = o[e] / l;
+            const uint32_t bits = pack_bf16x2(y, 0.f) & 0xFFFFu;
+            out[c + e] = (uint16_t)bits;
+            if (p.out_lo) p.out_lo[((int64_t)i * p.hq + h) * p.d16 + c + e] = (int8_t)bits_left(y, bits);
+        }
+}
+
 template <int DP, int MODE, int FORM>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     attn_fwd_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ FwdMaps maps) {
@@ -194,7 +285,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint64_t* drain = lready + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint4* s_seen = reinterpret_cast<uint4*>(smem + 768);   // [slot] the tile's keys that somebody sees (not SELF)
+    volatile int* s_odd = s_abort + 1;  // an infinity or NaN was written (not SELF)
+    uint4* s_seen = reinterpret_cast<uint4*>(smem + 768);   // [slot] the tile's keys that some query of the item sees (not SELF)
     uint64_t* clean = reinterpret_cast<uint64_t*>(smem + 896);  // [slot] and the others have been cleared
     uint16_t* s_tiles = reinterpret_cast<uint16_t*>(smem + 2048);  // (few queries) this CTA's key tiles
     float* s_inv = reinterpret_cast<float*>(smem + 1024);  // [2][128] 1 / l
@@ -221,7 +313,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int q = 0; q < 4; ++q) mbar_init(smem_u32(&lready[4 * w + q]), 2);
         }
         mbar_init(smem_u32(drain), 1);
-        *s_abort = 0;
+        *s_abort = *s_odd = 0;
         fence_mbar_init();
         tma_prefetch_map(&maps.q);
         tma_prefetch_map(&maps.k);
@@ -251,6 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 uint32_t n = 0, nq[2] = {0, 0};  // tiles and queries asked for
                 // (which keys are seen is asked for a tile ahead: a wait for memory here is a wait of every tile's)
                 uint4 seen = make_uint4(0, 0, 0, 0);
+                ItemKeys keys{0, 0, true};
                 auto look = [&](int j) {
                     if (FORM != ATTN_SELF && p.kseen) seen = p.kseen[j];
                 };
@@ -259,7 +352,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         const uint32_t s = n % C::kSlots, ph = (n / C::kSlots) & 1u;
                         if (!mbar_wait(smem_u32(&empty[s]), ph ^ 1u, s_abort, p.wait_ns)) return false;
                         if (FORM != ATTN_SELF && kv && p.kseen) {
-                            s_seen[s] = seen;
+                            const uint4 here = keys.of_tile(j);  // (values of other documents are zeros here)
+                            s_seen[s] = make_uint4(seen.x & here.x, seen.y & here.y, seen.z & here.z, seen.w & here.w);
                             look(then);
                         }
                         mbar_expect_tx(smem_u32(&full[s]), C::kTileBytes);
@@ -286,6 +380,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         return true;
                     };
                     ok = query(0);  // then K, then the other queries: the first scores wait for what they need
+                    if (FORM != ATTN_SELF && p.kseen && it.J0 < it.J1) keys = keys_of<FORM>(p, it.q0, p.rows);
                     if constexpr (FORM == ATTN_FEW) {
                         if (tiles > 0) look(mine[0]);
                         for (int i = 0; ok && i < tiles; ++i)
@@ -315,7 +410,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (FORM == ATTN_SELF) inside_tokens(p, in0, in1);
             bool ok = true;
             uint32_t n = 0, nt[2] = {0, 0}, nq[2] = {0, 0};  // ring position of K_{J0}; tiles, items of each query tile
-            // V's rows that nobody sees are zeros
+            // V's rows that no query of the item sees are zeros
             auto values = [&](uint32_t nv) {
                 uint64_t* bar = FORM != ATTN_SELF && p.kseen ? clean : full;
                 return mbar_wait(smem_u32(&bar[nv % C::kSlots]), (nv / C::kSlots) & 1u, s_abort, p.wait_ns);
@@ -432,7 +527,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             volatile int never = 0;
             mbar_wait(smem_u32(drain), 0, &never, p.wait_ns);
         }
-        if (FORM != ATTN_SELF && warp == kFwdMath + 2 && p.kseen) {  // ---------------- clears values that nobody sees
+        if (FORM != ATTN_SELF && warp == kFwdMath + 2 && p.kseen) {  // ---------------- clears values that no query of the item sees
             bool ok = true;
             uint32_t n = 0;
             auto pair_of = [&] {
@@ -703,6 +798,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     tmem_ld_wait16(raw);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = inv == 0.f ? 0.f : __uint_as_float(raw[e]) * inv;
+                    if (FORM != ATTN_SELF && p.qrange && i < p.T) {
+                        float zero = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) zero = fmaf(o[e], 0.f, zero);
+                        if (zero != zero) *s_odd = 1;
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0.f;
@@ -736,6 +837,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             attn_error(p, 5, 3);
             *s_abort = 1;
         }
+        // at the end, when nothing waits for these warps: the rows of this one that are not finite
+        if (FORM != ATTN_SELF && ok && __any_sync(0xffffffffu, *s_odd))
+#pragma unroll 1
+            for (int k = 0; k < rounds; ++k) {
+                const Item it = item_of<FORM>(p, k);
+                if (!it.valid || (FORM == ATTN_FEW ? w : w * kTile >= p.rows) || keys_of<FORM>(p, it.q0, p.rows).alike) continue;
+#pragma unroll 1
+                for (int row = quarter * 32; row < quarter * 32 + 32; ++row) {
+                    const int i = FORM != ATTN_FEW ? it.q0 + w * kTile + row : row < p.rows * group ? it.q0 + row / group : p.T;
+                    if (i < p.T) own_row<MODE, DP / 64>(p, i, FORM != ATTN_FEW ? it.h : it.h * group + row % group, sub * (DP / 2));
+                }
+            }
         tc_fence_before();
     }
     __syncthreads();

@@ -150,6 +150,13 @@ __global__ void __launch_bounds__(WARPS * 32) cross_join_kernel(const __grid_con
         for (int e = 0; e < 4; ++e) w |= (uint32_t)(bits_left(x[e], b[e]) & 255) << (8 * e);
         *reinterpret_cast<uint32_t*>(p.out_lo + row * p.d16 + c) = w;
     }
+    if (!p.qrange) return;
+    const float zero = fmaf(x[0], 0.f, fmaf(x[1], 0.f, fmaf(x[2], 0.f, x[3] * 0.f)));
+    if (__any_sync(0xffffffffu, c < p.d && zero != zero)) {  // (another document's values?)
+        const int i = (int)(row / p.hq);
+        __syncwarp();
+        if (!keys_of<ATTN_FEW>(p, i / p.rows * p.rows, p.rows).alike) own_row<CAP ? ATTN_CAP : ATTN_PLAIN, 4>(p, i, (int)(row % p.hq), 0);
+    }
 }
 
 // ------------------------------------------------------------------ launches

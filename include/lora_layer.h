@@ -94,7 +94,9 @@ LM_API lm_status attn_bwd(int64_t T, int32_t hq, int32_t hk, int32_t d, const lm
  * seen by nothing.  As in attn_fwd a query that sees nothing has O = 0, lse = -inf and no part in any gradient, a key
  * that nothing sees has gradient 0, and both may hold anything, NaN included; offsets must not decrease and are
  * device values; with others results are unspecified, and no access leaves its buffer.  A value that is
- * not finite among those that are seen can besides reach queries and keys of documents that share its 128 tokens.
+ * not finite among those that are seen has no part in the forward's results of other documents (rows that it reaches in
+ * a tile are formed again, from their own keys); in the backward it can reach gradients of documents that share
+ * 128 queries or 128 keys, from a multiple of 128 on, with its own.
  * scale > 0.  Tq, Tk <= 2^20; q (Tq x hq x d), k and v (Tk x hk x d), strided as in attn_fwd, O, O_lo and lse as there.
  * The backward writes dQ (Tq x hq x d), dK and dV (Tk x hk x d) bf16, contiguous.  Rounding as in attn_fwd and
  * attn_bwd.  Few queries (one new token of each sequence) split the keys among CTAs, whose sums are joined in fp32.
