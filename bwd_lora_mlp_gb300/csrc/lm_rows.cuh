@@ -31,45 +31,14 @@ struct Row {
     }
 };
 
-// f(v, index of vector 0) over [j0, j1) in batches of U whole vectors of a thread (vector u lies
-// u kThreads vectors on; n of them are there), the next batch loading meanwhile, and one(x, index) for
-// the single elements before the first and after the last 16-byte boundary.
-template <int U, bool F32, typename F, typename G>
-__device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1, F f, G one) {
-    constexpr int W = Row<F32>::kVec;
-    const int64_t a = min(j1, j0 + row.head(j0));
-    const int nv = (int)((j1 - a) / W);
-    const char* base = row.p + a * (F32 ? 4 : 2);
-    uint4 next[U];
-    auto load = [&](int v) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u * kThreads < nv) next[u] = *reinterpret_cast<const uint4*>(base + (int64_t)(v + u * kThreads) * 16);
-    };
-    load(threadIdx.x);
-    for (int v = threadIdx.x; v < nv; v += U * kThreads) {
-        uint32_t w[U][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) w[u][0] = next[u].x, w[u][1] = next[u].y, w[u][2] = next[u].z, w[u][3] = next[u].w;
-        if (v + (U - 1) * kThreads >= nv)  // (the last batch of some threads: what is not there counts nothing)
-#pragma unroll
-            for (int u = 1; u < U; ++u)
-                if (v + u * kThreads >= nv)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[u][e] = F32 ? 0xFF800000u : 0xFF80FF80u;
-        load(v + U * kThreads);
-        f(w, a + (int64_t)v * W, nv - v);
-    }
-    const int64_t b = a + (int64_t)nv * W;
-    const int64_t j = threadIdx.x < W ? j0 + threadIdx.x : b + (threadIdx.x - W);
-    if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
-}
-// The same pass by a CTA of N threads, in two steps: the first batch's loads are under way from the beginning, run(f, one)
-// does the rest.
+// f(v, index of vector 0, whole vectors from there on) over [j0, j1) in batches of U whole vectors of a thread of N
+// (vector u lies u N vectors on), the next batch loading meanwhile, and one(x, index) for the single elements before the
+// first and after the last 16-byte boundary.  In two steps: the first batch's loads are under way from the
+// beginning, run(f, one) does the rest.
 template <int U, bool F32, int N>
 struct Scan {
     static constexpr int W = Row<F32>::kVec;
-    const Row<F32>& row;
+    const Row<F32> row;
     int64_t j0, j1, a;  // a: the first boundary
     int nv;
     const char* base;
@@ -105,6 +74,10 @@ struct Scan {
         if (threadIdx.x < 2 * W && (threadIdx.x < W ? j < a : j < j1)) one(row.at(j), j);
     }
 };
+template <int U, bool F32, typename F, typename G>
+__device__ __forceinline__ void scan(const Row<F32>& row, int64_t j0, int64_t j1, F f, G one) {
+    Scan<U, F32, kThreads>(row, j0, j1).run(f, one);
+}
 // logit e of a vector
 template <bool F32>
 __device__ __forceinline__ float logit(const uint32_t (&w)[4], int e) {
