@@ -257,9 +257,14 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     }
     __syncthreads();
     const float E = total_of(0), rest = s.S * brought(s.m, top, c), total = REST ? rest + total_of(1) : rest, log_total = logf(total);
-    // sum p (log p - log q); each log p - log q is formed before it is weighed: their sum is far smaller than its parts
+    // sum p (log p - log q); each log p - log q is formed before it is weighed: their sum is far smaller than its parts.
+    // (But for a logit that the scale takes out of fp32, the lowest numbers of a type, whose share may be small enough.)
+    auto weighed = [&](float pk, float lp, float z, float l) {  // l: log q = scale (z - top) + l
+        const float dz = z - top, dx = dz * p.scale;
+        return dx == -INFINITY && dz != dx ? pk * p.scale * -dz : pk * (lp - (dx + l));
+    };
     const float log_E = REST ? 0.f : logf(E), p_k = e == 0.f ? 0.f : REST ? e : e / E;
-    over_entries(p_k == 0.f ? 0.f : p_k * ((ly - log_E) - ((x - top) * p.scale - log_total)), 3);
+    over_entries(p_k == 0.f ? 0.f : weighed(p_k, ly - log_E, x, -log_total), 3);
     __syncthreads();
     if (tid) return;
 
@@ -277,8 +282,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         const float pr = E != E ? E : others ? fmaxf(1.f - E, 0.f) : 0.f, lr = logf(s.S);
         // log (p_r / q_r): of the quotient, whose logarithm is small, where q_r is a number of ordinary size
         const float qr = rest / total;
-        const float far = qr >= 1e-30f || !(qr == qr) ? logf(pr / qr) : logf(pr) - ((s.m - top) * p.scale + (lr - log_total));
-        if (any) kl += pr > 0.f ? pr * far : pr;
+        if (any) kl += !(pr > 0.f) ? pr : qr >= 1e-30f || !(qr == qr) ? pr * logf(pr / qr) : weighed(pr, logf(pr), s.m, lr - log_total);
         o.W = E + pr;
         o.m = others ? s.m : 0.f;
         o.ml2 = others ? lr * kL2e : INFINITY;
