@@ -29,9 +29,8 @@ constexpr int kEntryWarps = kMaxEntries / 32;
 // value a sum's logarithm is nothing beside the maximum.
 struct Saved {
     float top, l2, l1;  // the row's largest logit; log2 of sum e^{(z - top) scale}, of sum e^{z - top}
-    float m, ml2;       // with rest: the same over the logits that are not entries, at scale; else the teacher's largest value
-                        // and log sum e^{(y - m) scale} over the row's entries
-    float coef, W;      // others: coef times their share of e^x; entries: W q - p
+    float m, ml2;       // with rest: the same over the logits that are not entries, at scale; else m is the teacher's largest
+    float coef, W, tl;  // others: coef times their share of e^x; entries: W q - p,  p = e^{y - tl}, or e^{(y - m) scale - tl}
 };
 
 __device__ __forceinline__ float teacher_at(const DistillParams& p, int64_t t, int k) {
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         const float r1 = s.S1 * brought(s.m, top, kL2e);
         log_total1 = logf(REST ? r1 + total_of(2) : r1);
     }
-    Saved o{top, log_total * kL2e, log_total1 * kL2e, 0.f, 0.f, 1.f, 1.f};
+    Saved o{top, log_total * kL2e, log_total1 * kL2e, 0.f, 0.f, 1.f, 1.f, 0.f};
     float kl = any ? total_of(3) : 0.f;
     if (REST) {
         const bool others = s.m != -INFINITY;  // some logit outside the entries weighs something
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
         o.coef = any && others ? fmaf(o.W, qr, -pr) : 0.f;
     } else {
         o.m = yref;
-        o.ml2 = any && E != 0.f ? log_E : INFINITY;
+        o.tl = any && E != 0.f ? log_E : INFINITY;
         if (!any || E == 0.f) o.coef = o.W = 0.f;
     }
     if (empty) kl = any && E > 0.f ? INFINITY : 0.f;  // no distribution: what the teacher expects is infinitely far
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(N, 1024 / N) distill_fwd_kernel(const __grid_c
     if (p.logp) p.logp[t] = target < 0 ? 0.f : empty ? -INFINITY : zt - top - log_total1;
     float4* out = reinterpret_cast<float4*>(p.saved + t * 8);
     out[0] = make_float4(o.top, o.l2, o.l1, o.m);
-    out[1] = make_float4(o.ml2, o.coef, o.W, 0.f);
+    out[1] = make_float4(o.ml2, o.coef, o.W, o.tl);
 }
 
 template <bool F32, bool REST, bool TWO, int N>
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
         else reinterpret_cast<uint16_t*>(out)[j] = (uint16_t)(pack_bf16x2(d, 0.f) & 0xFFFFu);
     };
     const float4 s_a = reinterpret_cast<const float4*>(p.saved + t * 8)[0], s_b = reinterpret_cast<const float4*>(p.saved + t * 8)[1];
-    const Saved s{s_a.x, s_a.y, s_a.z, s_a.w, s_b.x, s_b.y, s_b.z};
+    const Saved s{s_a.x, s_a.y, s_a.z, s_a.w, s_b.x, s_b.y, s_b.z, s_b.w};
     const float m = REST ? s.m : s.top, ml2 = REST ? s.ml2 : s.l2;  // of the logits that coef is a factor of
     const float c = p.scale * kL2e;
     const bool none = (gk == 0.f && gh == 0.f) || s.top == -INFINITY;  // the row's gradient is 0, whatever it holds
@@ -382,7 +381,10 @@ __global__ void __launch_bounds__(kDbThreads) distill_bwd_kernel(const __grid_co
             if (id < from || id >= s1) id = -1;
             if (id >= 0) {
                 x = row.at(id);
-                if (gk != 0.f) pk = expf(teacher_log<REST>(teacher_at(p, t, tid), s.m, p.scale) - (REST ? 0.f : s.ml2));
+                // (with rest tl is 0, but this load then waits for the row's scalars, behind the stretch's own loads: 4096 x
+                // 131072 321 us instead of 336)
+                const float e = expf(teacher_log<REST>(teacher_at(p, t, tid), s.m, p.scale) - s.tl);
+                pk = gk == 0.f ? 0.f : e;
             }
         }
         if (tid < kMaxEntries) ids[tid] = id, ps[tid] = pk;
