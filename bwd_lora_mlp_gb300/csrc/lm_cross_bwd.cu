@@ -10,7 +10,7 @@ namespace lm {
 // Few key tiles (short states under long texts) are shared by more CTAs than a cluster has, and few query tiles under many
 // keys are split along them; the parts' sums are joined in order.  Both where what one CTA walks would be long beside
 // what an SM has in all: a step is a pair of tiles.  (A training step in
-// a graph, with parts and without: 12000 queries on 78 states, 4 heads on 1, 45 and 278 us; 3700 on 651 in documents 58 and
+// a graph, with parts and without: 12000 queries on 78 states, 4 heads on 1 of 64, 46 and 278 us; 3700 on 651 in documents 58 and
 // 87; 160 on 27000, 40 heads on 8, 627 and 689.  The joins take 6 us of the first.)
 static int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 constexpr int kLeastPairs = 4, kLeastTiles = 16;  // (an item begins and ends for five tiles' time)
