@@ -838,6 +838,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             *s_abort = 1;
         }
         // at the end, when nothing waits for these warps: the rows of this one that are not finite
+        __syncwarp();  // (lanes read what others of them wrote)
         if (FORM != ATTN_SELF && ok && __any_sync(0xffffffffu, *s_odd))
 #pragma unroll 1
             for (int k = 0; k < rounds; ++k) {
